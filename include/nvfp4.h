@@ -23,8 +23,8 @@
  * rowwise outputs of x transposed, optionally after a 16-point random Hadamard transform.
  *
  * Execution: every call is asynchronous on the caller's stream (a cudaStream_t passed as
- * void*; NULL is the legacy default stream). The quantize, amax and MX kernels are launched
- * with programmatic dependent launch: each waits for the previous kernel in the stream before
+ * void*; NULL is the legacy default stream). The quantize, amax, MX, routing and checkpoint
+ * kernels are launched with programmatic dependent launch: each waits for the previous kernel in the stream before
  * it touches memory, and lets the next kernel launched that way start early, so a kernel of
  * the caller's launched after them with programmatic dependent launch must wait
  * (cudaGridDependencySynchronize) before it reads their outputs, as that mechanism requires. Pointers marked (device) must be device (or
@@ -73,6 +73,8 @@ typedef enum nvfp4_rounding {
                                           or padded token total above the column capacity */
 #define NVFP4_DEVICE_TIMEOUT     0x2u  /* the wait for every CTA's amax or a copy wait passed
                                           its limit */
+#define NVFP4_DEVICE_BAD_ROUTE   0x4u  /* an expert id that is not below E, or a plan's row
+                                          outside the packed tensor; the slot was skipped */
 
 /* Options of one quantization. Zero-initialise and set what is needed. */
 typedef struct nvfp4_config {
@@ -343,6 +345,106 @@ nvfp4_status nvfp4_mx_quantize(const void* x, int64_t M, int64_t N, int32_t form
  * 16-byte aligned. */
 nvfp4_status nvfp4_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t format,
                                  int64_t R, int64_t C, float* out, void* stream);
+
+/* ---- Token routing around the grouped quantizer -------------------------------------------
+ * A batch of T tokens, K choices each: slot s = t * K + k holds the expert of token t's choice k.
+ * A plan gives every held slot a row of the packed tensor [T*K][H] that nvfp4_quantize_grouped
+ * takes: rows sorted by expert, slots of one expert in ascending order (a stable sort).
+ * 1 <= K <= 32 (above: NVFP4_ERR_UNSUPPORTED), 1 <= E <= 256, T * K below 2^31 - 65536. BF16
+ * tensors, H % 8 == 0, 16-byte aligned. Rows past the last expert's end belong to dropped slots:
+ * outputs have zeros there, inputs are not read there. */
+
+/* Make the plan.
+ *   expert_ids   (device) [T][K], id_bytes 4 (int32) or 8 (int64) each. A negative id drops the
+ *                slot; an id >= E drops it too and sets NVFP4_DEVICE_BAD_ROUTE.
+ *   row_of_slot  (device) int32 [T][K]: the slot's row, -1 for a dropped slot.
+ *   slot_of_row  (device) int32 [T*K]: the row's slot, -1 past the last expert's end.
+ *   offsets      (device) int32 [E]: cumulative expert ends, as nvfp4_quantize_grouped reads them.
+ * One launch. T == 0 writes offsets alone. */
+nvfp4_status nvfp4_moe_plan(const void* expert_ids, int32_t id_bytes, int64_t T, int32_t K,
+                            int32_t E, int32_t* row_of_slot, int32_t* slot_of_row,
+                            int32_t* offsets, void* stream);
+
+/* packed[row_of_slot[t][k]] = x[t] for every held slot, zeros in the rows past offsets[E-1].
+ *   x (device) BF16 [T][H], packed (device) BF16 [T*K][H]; row_of_slot and offsets of a plan.
+ *   amax (device) float [E] or NULL: max |.| of each expert's rows (0 for an empty expert), the
+ *   amax_row that nvfp4_quantize_grouped takes. */
+nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
+                                int64_t T, int64_t H, int32_t K, int32_t E, void* packed,
+                                float* amax, void* stream);
+
+/* The gradient of dispatch: grad_x[t] = sum over k of grad_packed[row_of_slot[t][k]], dropped
+ * slots left out, summed in binary32 in the order of k and rounded once. */
+nvfp4_status nvfp4_moe_dispatch_backward(const void* grad_packed, const int32_t* row_of_slot,
+                                         int64_t T, int64_t H, int32_t K, void* grad_x,
+                                         void* stream);
+
+/* out[t] = sum over k of weights[t][k] * y[row_of_slot[t][k]], as above. The weight of a dropped
+ * slot is not read into the sum (it may be NaN); a token without held slots gets zeros.
+ *   y (device) BF16 [T*K][H], weights (device) float [T][K], out (device) BF16 [T][H]. */
+nvfp4_status nvfp4_moe_combine(const void* y, const float* weights, const int32_t* row_of_slot,
+                               int64_t T, int64_t H, int32_t K, void* out, void* stream);
+
+/* The gradients of combine: grad_y[row] = weights[t][k] * grad_out[t] (zeros past offsets[E-1])
+ * and grad_weights[t][k] = <grad_out[t], y[row]> in binary32, 0 for a dropped slot.
+ *   grad_y (device) BF16 [T*K][H], grad_weights (device) float [T][K]. */
+nvfp4_status nvfp4_moe_combine_backward(const void* grad_out, const void* y, const float* weights,
+                                        const int32_t* row_of_slot, const int32_t* offsets,
+                                        int64_t T, int64_t H, int32_t K, int32_t E, void* grad_y,
+                                        float* grad_weights, void* stream);
+
+/* ---- Operators that keep their inputs in 8 bits for the backward pass ---------------------
+ * A kept tensor [R][C] is E4M3 codes [R][C] and E8M0 scales [R][C/32], the layout
+ * nvfp4_mx_dequantize reads (NVFP4_MX_E4M3). Its scale differs from nvfp4_mx_quantize's: the
+ * smallest 2^e, e >= -127, with the block's largest finite magnitude <= 448 * 2^e, so no element
+ * saturates. Elements are rounded to nearest-even, those that would round to 2^128 to 1.875 * 2^127
+ * (what is finite stays finite); infinities and NaN become NaN codes and do not
+ * count for the scale. An all-zero block has scale byte 0. The backward passes take the kept
+ * values for the inputs. Row lengths are multiples of 32, buffers 16-byte aligned (scales: any). */
+
+/* y = silu(g) * u of h = [g | u], and h kept.
+ *   h (device) BF16 [M][2F]: F gate columns, then F up columns; F % 32 == 0.
+ *   offsets (device) int32 [E] or NULL (then E = 1 and every row counts): expert ends; the rows
+ *     past offsets[E-1] are not read and their outputs are zeros. Offsets that are not
+ *     non-decreasing within [0, M] set NVFP4_DEVICE_BAD_OFFSETS.
+ *   y (device) BF16 [M][F]; codes [M][2F], scales [M][2F/32]; amax (device) float [E] or NULL:
+ *     max |y| over each expert's rows. */
+nvfp4_status nvfp4_swiglu_checkpoint(const void* h, int64_t M, int64_t F, const int32_t* offsets,
+                                     int32_t E, void* y, uint8_t* codes, uint8_t* scales,
+                                     float* amax, void* stream);
+
+/* grad_h [M][2F] from grad_y [M][F] and the kept h: with s = sigmoid(g),
+ * dg = dy * u * s * (1 + g * (1 - s)), du = dy * g * s, binary32 and rounded once to BF16. */
+nvfp4_status nvfp4_swiglu_checkpoint_backward(const void* grad_y, const uint8_t* codes,
+                                              const uint8_t* scales, int64_t M, int64_t F,
+                                              const int32_t* offsets, int32_t E, void* grad_h,
+                                              void* stream);
+
+/* y = bf16((weight + weight_bias) * (x * rstd)), rstd = rsqrt(mean(x^2) + eps) per row in
+ * binary32, and x kept.
+ *   x, y (device) BF16 [M][N], weight (device) BF16 [N]; N % 32 == 0, N <= 32768 (above:
+ *   NVFP4_ERR_UNSUPPORTED); codes [M][N], scales [M][N/32]; rstd (device) float [M]; amax
+ *   (device) float [1]: max |y|, for nvfp4_quantize. */
+nvfp4_status nvfp4_rmsnorm_checkpoint(const void* x, const void* weight, int64_t M, int64_t N,
+                                      float eps, float weight_bias, void* y, uint8_t* codes,
+                                      uint8_t* scales, float* rstd, float* amax, void* stream);
+
+/* Bytes of workspace that nvfp4_rmsnorm_checkpoint_backward takes for these sizes. */
+nvfp4_status nvfp4_rmsnorm_checkpoint_workspace(int64_t M, int64_t N, size_t* bytes);
+
+/* With xh = x * rstd of the kept x and g = (weight + weight_bias) * dy:
+ * grad_x = rstd * (g - xh * mean(g * xh)) (+ grad_residual when given: the gradient that reaches
+ * x past the norm), grad_weight = sum over rows of dy * xh in binary32, in an order that depends
+ * on the sizes and the device alone.
+ *   grad_residual (device) BF16 [M][N] or NULL; grad_x (device) BF16 [M][N]; grad_weight (device)
+ *   float [N]; workspace (device) of at least the bytes above, free for other use afterwards in
+ *   stream order. M == 0 writes zeros into grad_weight. */
+nvfp4_status nvfp4_rmsnorm_checkpoint_backward(const void* grad_y, const uint8_t* codes,
+                                               const uint8_t* scales, const float* rstd,
+                                               const void* weight, int64_t M, int64_t N,
+                                               float weight_bias, const void* grad_residual,
+                                               void* grad_x, float* grad_weight, void* workspace,
+                                               size_t workspace_bytes, void* stream);
 
 /* The per-device workspace: the status word the kernels report to, and the counts, maxima and
  * claim bits of the single-launch amax. By default the library allocates it with cudaMalloc

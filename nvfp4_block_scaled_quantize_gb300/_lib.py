@@ -18,6 +18,7 @@ ROUND_RN = 0
 ROUND_SR = 1
 DEVICE_BAD_OFFSETS = 0x1
 DEVICE_TIMEOUT = 0x2
+DEVICE_BAD_ROUTE = 0x4
 
 EXPORTED = ["nvfp4_status_string", "nvfp4_amax", "nvfp4_quantize", "nvfp4_quantize_grouped",
             "nvfp4_dequantize", "nvfp4_get_status", "nvfp4_quantize_noalloc",
@@ -28,7 +29,11 @@ EXPORTED = ["nvfp4_status_string", "nvfp4_amax", "nvfp4_quantize", "nvfp4_quanti
             "nvfp4_rmsnorm_amax", "nvfp4_rmsnorm_quantize", "nvfp4_set_workspace",
             "nvfp4_amax_grouped", "nvfp4_debug_fused_extra_arrivals",
             "nvfp4_debug_fail_next_launch", "nvfp4_noalloc_get_status",
-            "nvfp4_debug_fused_late_ctas", "nvfp4_debug_fused_takeovers"]
+            "nvfp4_debug_fused_late_ctas", "nvfp4_debug_fused_takeovers",
+            "nvfp4_moe_plan", "nvfp4_moe_dispatch", "nvfp4_moe_dispatch_backward",
+            "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_swiglu_checkpoint",
+            "nvfp4_swiglu_checkpoint_backward", "nvfp4_rmsnorm_checkpoint",
+            "nvfp4_rmsnorm_checkpoint_workspace", "nvfp4_rmsnorm_checkpoint_backward"]
 
 
 class Config(ctypes.Structure):
@@ -133,5 +138,22 @@ def load(build_if_missing: bool = False):
     L.nvfp4_debug_fused_late_ctas.argtypes = [i32]
     L.nvfp4_debug_fused_takeovers.restype = ctypes.c_int
     L.nvfp4_debug_fused_takeovers.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+    for name, args in (
+            ("nvfp4_moe_plan", [vp, i32, i64, i32, i32, vp, vp, vp, vp]),
+            ("nvfp4_moe_dispatch", [vp, vp, vp, i64, i64, i32, i32, vp, vp, vp]),
+            ("nvfp4_moe_dispatch_backward", [vp, vp, i64, i64, i32, vp, vp]),
+            ("nvfp4_moe_combine", [vp, vp, vp, i64, i64, i32, vp, vp]),
+            ("nvfp4_moe_combine_backward",
+             [vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, vp, vp]),
+            ("nvfp4_swiglu_checkpoint", [vp, i64, i64, vp, i32, vp, vp, vp, vp, vp]),
+            ("nvfp4_swiglu_checkpoint_backward", [vp, vp, vp, i64, i64, vp, i32, vp, vp]),
+            ("nvfp4_rmsnorm_checkpoint",
+             [vp, vp, i64, i64, f32, f32, vp, vp, vp, vp, vp, vp]),
+            ("nvfp4_rmsnorm_checkpoint_workspace", [i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
+            ("nvfp4_rmsnorm_checkpoint_backward",
+             [vp, vp, vp, vp, vp, i64, i64, f32, vp, vp, vp, vp, ctypes.c_size_t, vp])):
+        fn = getattr(L, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = args
     _lib = L
     return L

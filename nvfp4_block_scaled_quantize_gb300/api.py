@@ -304,6 +304,244 @@ def nvfp4_mx_dequantize(codes, scales, fmt="e4m3"):
     return out
 
 
+def _check(t, name, dtype, shape, device):
+    """Refuse a tensor that is not a contiguous `dtype` tensor of `shape` on `device`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError("%s must be a %s tensor" % (name, dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous (row-major)" % name)
+
+
+def _out(t, name, dtype, shape, device):
+    """`t` checked, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _check(t, name, dtype, shape, device)
+    return t
+
+
+def nvfp4_moe_plan(expert_ids, num_experts, out=None):
+    """Sort the (token, choice) slots of expert_ids (int32 or int64 [T, K], negative: dropped) by
+    expert. Returns a plan, a dict of int32 tensors: row_of_slot [T, K] (-1: dropped),
+    slot_of_row [T * K] (-1 past the last expert's end) and offsets [num_experts] (expert ends,
+    as nvfp4_quantize_grouped takes them). `out` reuses the tensors of a plan of these sizes."""
+    if not isinstance(expert_ids, torch.Tensor) or expert_ids.dim() != 2 or \
+            expert_ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("expert_ids must be a 2-D int32 or int64 tensor")
+    if not expert_ids.is_cuda:
+        raise TypeError("expert_ids must live on a CUDA device")
+    if not expert_ids.is_contiguous():
+        raise ValueError("expert_ids must be contiguous (row-major)")
+    L = _lib.load()
+    T, K = expert_ids.shape
+    E, dev, g = int(num_experts), expert_ids.device, (out or {}).get
+    plan = {"row_of_slot": _out(g("row_of_slot"), "row_of_slot", torch.int32, (T, K), dev),
+            "slot_of_row": _out(g("slot_of_row"), "slot_of_row", torch.int32, (T * K,), dev),
+            "offsets": _out(g("offsets"), "offsets", torch.int32, (max(E, 0),), dev)}
+    _raise_if(L.nvfp4_moe_plan(_ptr(expert_ids), expert_ids.element_size(), T, K, E,
+                               _ptr(plan["row_of_slot"]), _ptr(plan["slot_of_row"]),
+                               _ptr(plan["offsets"]), _stream(dev)), "nvfp4_moe_plan")
+    return plan
+
+
+def _plan_sizes(plan, device):
+    """(row_of_slot, offsets, T, K, E) of a plan, checked."""
+    rows, offsets = plan["row_of_slot"], plan["offsets"]
+    if rows.dim() != 2 or offsets.dim() != 1:
+        raise ValueError("plan: row_of_slot must be [T, K] and offsets [E]")
+    _check(rows, "row_of_slot", torch.int32, rows.shape, device)
+    _check(offsets, "offsets", torch.int32, offsets.shape, device)
+    return rows, offsets, rows.shape[0], rows.shape[1], offsets.shape[0]
+
+
+def nvfp4_moe_dispatch(x, plan, out=None, amax=None):
+    """Copy the token rows of x (BF16 [T, H]) into the plan's packed order. Returns (packed BF16
+    [T * K, H], zeros past the last expert's end, and the per-expert amax float32 [E], the
+    amax_row of nvfp4_quantize_grouped)."""
+    _check_x(x)
+    L = _lib.load()
+    T, H = x.shape
+    rows, offsets, t, K, E = _plan_sizes(plan, x.device)
+    if t != T:
+        raise ValueError("the plan is for %d tokens, x has %d rows" % (t, T))
+    out = _out(out, "out", torch.bfloat16, (T * K, H), x.device)
+    amax = _out(amax, "amax", torch.float32, (E,), x.device)
+    _raise_if(L.nvfp4_moe_dispatch(_ptr(x), _ptr(rows), _ptr(offsets), T, H, K, E, _ptr(out),
+                                   _ptr(amax), _stream(x.device)), "nvfp4_moe_dispatch")
+    return out, amax
+
+
+def nvfp4_moe_dispatch_backward(grad_packed, plan, out=None):
+    """The gradient of nvfp4_moe_dispatch: BF16 [T, H], the sum of each token's packed gradients
+    (BF16 [T * K, H])."""
+    _check_x(grad_packed)
+    L = _lib.load()
+    rows, _, T, K, _ = _plan_sizes(plan, grad_packed.device)
+    H = grad_packed.shape[1]
+    _check(grad_packed, "grad_packed", torch.bfloat16, (T * K, H), grad_packed.device)
+    out = _out(out, "out", torch.bfloat16, (T, H), grad_packed.device)
+    _raise_if(L.nvfp4_moe_dispatch_backward(_ptr(grad_packed), _ptr(rows), T, H, K, _ptr(out),
+                                            _stream(out.device)), "nvfp4_moe_dispatch_backward")
+    return out
+
+
+def nvfp4_moe_combine(y, weights, plan, out=None):
+    """Weighted sum of each token's expert outputs: y BF16 [T * K, H] in packed order, weights
+    float32 [T, K] -> BF16 [T, H]. Dropped slots are left out."""
+    _check_x(y)
+    L = _lib.load()
+    rows, _, T, K, _ = _plan_sizes(plan, y.device)
+    H = y.shape[1]
+    _check(y, "y", torch.bfloat16, (T * K, H), y.device)
+    _check(weights, "weights", torch.float32, (T, K), y.device)
+    out = _out(out, "out", torch.bfloat16, (T, H), y.device)
+    _raise_if(L.nvfp4_moe_combine(_ptr(y), _ptr(weights), _ptr(rows), T, H, K, _ptr(out),
+                                  _stream(y.device)), "nvfp4_moe_combine")
+    return out
+
+
+def nvfp4_moe_combine_backward(grad_out, y, weights, plan, grad_y=None, grad_weights=None):
+    """The gradients of nvfp4_moe_combine from grad_out BF16 [T, H]: (grad_y BF16 [T * K, H],
+    zeros past the last expert's end, grad_weights float32 [T, K], 0 for dropped slots)."""
+    _check_x(grad_out)
+    L = _lib.load()
+    dev = grad_out.device
+    rows, offsets, T, K, E = _plan_sizes(plan, dev)
+    H = grad_out.shape[1]
+    _check(grad_out, "grad_out", torch.bfloat16, (T, H), dev)
+    _check(y, "y", torch.bfloat16, (T * K, H), dev)
+    _check(weights, "weights", torch.float32, (T, K), dev)
+    grad_y = _out(grad_y, "grad_y", torch.bfloat16, (T * K, H), dev)
+    grad_weights = _out(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    _raise_if(L.nvfp4_moe_combine_backward(_ptr(grad_out), _ptr(y), _ptr(weights), _ptr(rows),
+                                           _ptr(offsets), T, H, K, E, _ptr(grad_y),
+                                           _ptr(grad_weights), _stream(dev)),
+              "nvfp4_moe_combine_backward")
+    return grad_y, grad_weights
+
+
+def _segments(offsets, device):
+    """(pointer, E) of optional expert ends."""
+    if offsets is None:
+        return None, 1
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1-D int32 CUDA tensor")
+    _check(offsets, "offsets", torch.int32, offsets.shape, device)
+    return _ptr(offsets), offsets.shape[0]
+
+
+def nvfp4_swiglu_checkpoint(h, offsets=None, out=None):
+    """silu(gate) * up of h = [gate | up] (BF16 [M, 2F], F a multiple of 32), with h kept in 8 bits
+    for the backward pass. offsets (int32 [E] expert ends): the rows past the last end are not
+    read and their outputs are zeros. Returns y BF16 [M, F], codes uint8 (E4M3 bits) [M, 2F],
+    scales uint8 (E8M0) [M, 2F / 32] and amax float32 [E] ([1] without offsets): max |y| of each
+    expert's rows. `out` reuses such a dict."""
+    _check_x(h)
+    L = _lib.load()
+    M, N = h.shape
+    if N % 64 != 0:
+        raise ValueError("h must have 2F columns, F a multiple of 32")
+    offs, E = _segments(offsets, h.device)
+    g, dev = (out or {}).get, h.device
+    out = {"y": _out(g("y"), "y", torch.bfloat16, (M, N // 2), dev),
+           "codes": _out(g("codes"), "codes", torch.uint8, (M, N), dev),
+           "scales": _out(g("scales"), "scales", torch.uint8, (M, N // 32), dev),
+           "amax": _out(g("amax"), "amax", torch.float32, (E,), dev)}
+    _raise_if(L.nvfp4_swiglu_checkpoint(_ptr(h), M, N // 2, offs, E, _ptr(out["y"]),
+                                        _ptr(out["codes"]), _ptr(out["scales"]),
+                                        _ptr(out["amax"]), _stream(dev)),
+              "nvfp4_swiglu_checkpoint")
+    return out
+
+
+def nvfp4_swiglu_checkpoint_backward(grad_y, codes, scales, offsets=None, out=None):
+    """grad_h BF16 [M, 2F] of nvfp4_swiglu_checkpoint from grad_y BF16 [M, F] and the kept h."""
+    _check_x(grad_y)
+    L = _lib.load()
+    M, F = grad_y.shape
+    dev = grad_y.device
+    if F % 32 != 0:
+        raise ValueError("grad_y must have a multiple of 32 columns")
+    _check(codes, "codes", torch.uint8, (M, 2 * F), dev)
+    _check(scales, "scales", torch.uint8, (M, F // 16), dev)
+    offs, E = _segments(offsets, dev)
+    out = _out(out, "out", torch.bfloat16, (M, 2 * F), dev)
+    _raise_if(L.nvfp4_swiglu_checkpoint_backward(_ptr(grad_y), _ptr(codes), _ptr(scales), M, F,
+                                                 offs, E, _ptr(out), _stream(dev)),
+              "nvfp4_swiglu_checkpoint_backward")
+    return out
+
+
+def nvfp4_rmsnorm_checkpoint(x, weight, eps=1e-6, weight_bias=0.0, out=None):
+    """RMSNorm of x (BF16 [M, N], N a multiple of 32, at most 32768) with x kept in 8 bits for the
+    backward pass. Returns y BF16 [M, N], codes uint8 (E4M3 bits) [M, N], scales uint8 (E8M0)
+    [M, N / 32], rstd float32 [M] and amax float32 [1] (max |y|). `out` reuses such a dict."""
+    _check_x(x)
+    L = _lib.load()
+    M, N = x.shape
+    dev = x.device
+    _check(weight, "weight", torch.bfloat16, (N,), dev)
+    if N % 32 != 0:
+        raise ValueError("x must have a multiple of 32 columns")
+    g = (out or {}).get
+    out = {"y": _out(g("y"), "y", torch.bfloat16, (M, N), dev),
+           "codes": _out(g("codes"), "codes", torch.uint8, (M, N), dev),
+           "scales": _out(g("scales"), "scales", torch.uint8, (M, N // 32), dev),
+           "rstd": _out(g("rstd"), "rstd", torch.float32, (M,), dev),
+           "amax": _out(g("amax"), "amax", torch.float32, (1,), dev)}
+    _raise_if(L.nvfp4_rmsnorm_checkpoint(_ptr(x), _ptr(weight), M, N, float(eps),
+                                         float(weight_bias), _ptr(out["y"]), _ptr(out["codes"]),
+                                         _ptr(out["scales"]), _ptr(out["rstd"]),
+                                         _ptr(out["amax"]), _stream(dev)),
+              "nvfp4_rmsnorm_checkpoint")
+    return out
+
+
+def nvfp4_rmsnorm_checkpoint_workspace(M, N):
+    """Bytes of workspace of nvfp4_rmsnorm_checkpoint_backward."""
+    n = ctypes.c_size_t(0)
+    _raise_if(_lib.load().nvfp4_rmsnorm_checkpoint_workspace(M, N, ctypes.byref(n)),
+              "nvfp4_rmsnorm_checkpoint_workspace")
+    return n.value
+
+
+def nvfp4_rmsnorm_checkpoint_backward(grad_y, codes, scales, rstd, weight, weight_bias=0.0,
+                                      grad_residual=None, grad_x=None, grad_weight=None,
+                                      workspace=None):
+    """The gradients of nvfp4_rmsnorm_checkpoint from grad_y BF16 [M, N] and the kept x: (grad_x
+    BF16 [M, N], grad_weight float32 [N]). grad_residual (BF16 [M, N]) is added to grad_x: the
+    gradient that reaches x past the norm. workspace: a uint8 tensor of at least
+    nvfp4_rmsnorm_checkpoint_workspace(M, N) bytes."""
+    _check_x(grad_y)
+    L = _lib.load()
+    M, N = grad_y.shape
+    dev = grad_y.device
+    if N % 32 != 0:
+        raise ValueError("grad_y must have a multiple of 32 columns")
+    _check(codes, "codes", torch.uint8, (M, N), dev)
+    _check(scales, "scales", torch.uint8, (M, N // 32), dev)
+    _check(rstd, "rstd", torch.float32, (M,), dev)
+    _check(weight, "weight", torch.bfloat16, (N,), dev)
+    if grad_residual is not None:
+        _check(grad_residual, "grad_residual", torch.bfloat16, (M, N), dev)
+    grad_x = _out(grad_x, "grad_x", torch.bfloat16, (M, N), dev)
+    grad_weight = _out(grad_weight, "grad_weight", torch.float32, (N,), dev)
+    if workspace is None:
+        workspace = torch.empty(nvfp4_rmsnorm_checkpoint_workspace(M, N), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _raise_if(L.nvfp4_rmsnorm_checkpoint_backward(
+        _ptr(grad_y), _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(weight), M, N,
+        float(weight_bias), _ptr(grad_residual), _ptr(grad_x), _ptr(grad_weight),
+        _ptr(workspace), workspace.numel(), _stream(dev)), "nvfp4_rmsnorm_checkpoint_backward")
+    return grad_x, grad_weight
+
+
 WORKSPACE_BYTES = 16384
 
 

@@ -1,6 +1,6 @@
 // Internal declarations of the library's kernels other than the tile kernel (not part of the
-// C ABI): MX quantization, the RMSNorm producer, the flat amax, the scale swizzle and
-// dequantization. Kept apart from nvfp4_internal.h, whose contents the tile kernel depends on.
+// C ABI): MX quantization, the RMSNorm producer, token routing, the operators with 8-bit
+// checkpoints, the flat amax, the scale swizzle and dequantization. Kept apart from nvfp4_internal.h, whose contents the tile kernel depends on.
 #pragma once
 
 #include <cuda.h>
@@ -44,6 +44,49 @@ cudaError_t launch_mx_dequantize(int fmt, const uint8_t* codes, const uint8_t* s
 cudaError_t launch_rmsnorm_amax(const void* x, const void* w, int64_t M, int64_t N, float eps,
                                 float bias, void* y, float* amax, int grid, cudaStream_t s);
 int rmsnorm_rows_per_cta();
+
+// ---- token routing (moe_route.cu) ----
+constexpr int kMaxTopk = 32;  // choices of a token: one warp loads a token's rows
+// rows of `nv` 16-byte vectors; amax (zeroed by the caller) may be null
+cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
+                            int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
+                            cudaStream_t s);
+cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
+                                int64_t T, int32_t K, int32_t E, int64_t nv, void* packed,
+                                float* amax, uint32_t* status, int sm_count, cudaStream_t s);
+// weights null: all 1 (the gradient of dispatch)
+cudaError_t launch_moe_gather_sum(const void* y, const float* weights, const int32_t* row_of_slot,
+                                  int64_t T, int32_t K, int64_t nv, void* out, uint32_t* status,
+                                  int sm_count, cudaStream_t s);
+cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const float* weights,
+                                        const int32_t* row_of_slot, const int32_t* offsets,
+                                        int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
+                                        float* grad_w, uint32_t* status, cudaStream_t s);
+
+// ---- operators with 8-bit checkpoints (checkpoint.cu) ----
+cudaError_t launch_swiglu_checkpoint(const void* h, int64_t M, int64_t F, const int32_t* offsets,
+                                     int32_t E, void* y, void* codes, uint8_t* scales, float* amax,
+                                     uint32_t* status, int sm_count, cudaStream_t s);
+cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* codes,
+                                              const uint8_t* scales, int64_t M, int64_t F,
+                                              const int32_t* offsets, int32_t E, void* grad_h,
+                                              uint32_t* status, int sm_count, cudaStream_t s);
+constexpr int64_t kRmsMaxN = 32768;       // a row stays in one CTA's registers
+constexpr int64_t kRmsMaxPartials = 256;  // rows of the weight gradient's partial sums
+struct RmsArgs {
+  int64_t M, N;
+  float eps, bias;
+  const void *x, *weight, *grad, *residual;  // residual may be null
+  void *y, *codes, *grad_x;
+  uint8_t* scales;
+  float *rstd, *amax, *partial, *grad_weight;
+};
+cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s);
+cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s);
+
+// The current device's SM count and status word, set up on first need (nvfp4_api.cu); false when
+// a CUDA call failed.
+bool device_resources(int* sm_count, uint32_t** status);
 
 cudaError_t launch_amax_flat(const void* x, int64_t n_elems, float* out0, float* out1, int grid,
                              cudaStream_t s);

@@ -145,6 +145,14 @@ __global__ void gscale_fill_kernel(const float* amax, float* gscale, int n) {
 
 }  // namespace
 
+bool device_resources(int* sm_count, uint32_t** status) {
+  DeviceState* ds = nullptr;
+  if (device_state(&ds) != NVFP4_OK) return false;
+  *sm_count = ds->sm_count;
+  *status = ds->workspace;
+  return true;
+}
+
 void take_fuse_debug(QuantArgs& q) {
   q.fuse_extra = g_fuse_extra.exchange(0);
   q.fuse_late = g_fuse_late.exchange(0);
@@ -234,7 +242,7 @@ NVFP4_EXPORT const char* nvfp4_status_string(nvfp4_status s) {
     case NVFP4_ERR_ALIGN: return "pointer or row pitch not 16-byte aligned";
     case NVFP4_ERR_UNSUPPORTED: return "unsupported option combination";
     case NVFP4_ERR_CUDA: return "CUDA error";
-    case NVFP4_ERR_DEVICE_STATUS: return "device flagged its input (bad grouped offsets)";
+    case NVFP4_ERR_DEVICE_STATUS: return "device flagged its input (bad grouped offsets or routing)";
     case NVFP4_ERR_TIMEOUT: return "a bounded device wait gave up";
   }
   return "unknown status";
