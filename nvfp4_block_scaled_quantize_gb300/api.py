@@ -18,14 +18,21 @@ from ._lib import Config, NVFP4Error, ROUND_RN, ROUND_SR
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    """A c_void_p argument: ctypes takes the integer itself."""
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The device's current stream as an integer (the Stream object of torch.cuda.current_stream
+    costs 2 us a call on the host, as much as a small kernel)."""
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _check_x(x):
+    if isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.dim() == 2 and x.is_cuda \
+            and x.is_contiguous():
+        return
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("x must be a 2-D torch.bfloat16 tensor")
     if not x.is_cuda:
@@ -306,6 +313,9 @@ def nvfp4_mx_dequantize(codes, scales, fmt="e4m3"):
 
 def _check(t, name, dtype, shape, device):
     """Refuse a tensor that is not a contiguous `dtype` tensor of `shape` on `device`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError("%s must be a %s tensor" % (name, dtype))
     if t.device != device:
@@ -324,6 +334,13 @@ def _out(t, name, dtype, shape, device):
     return t
 
 
+def _outputs(out, wanted, device):
+    """Tensors for {name: (dtype, shape)}: those of the dict `out`, checked, else new ones."""
+    if out is None:
+        return {k: torch.empty(s, dtype=d, device=device) for k, (d, s) in wanted.items()}
+    return {k: _out(out.get(k), k, d, s, device) for k, (d, s) in wanted.items()}
+
+
 def nvfp4_moe_plan(expert_ids, num_experts, out=None):
     """Sort the (token, choice) slots of expert_ids (int32 or int64 [T, K], negative: dropped) by
     expert. Returns a plan, a dict of int32 tensors: row_of_slot [T, K] (-1: dropped),
@@ -338,10 +355,9 @@ def nvfp4_moe_plan(expert_ids, num_experts, out=None):
         raise ValueError("expert_ids must be contiguous (row-major)")
     L = _lib.load()
     T, K = expert_ids.shape
-    E, dev, g = int(num_experts), expert_ids.device, (out or {}).get
-    plan = {"row_of_slot": _out(g("row_of_slot"), "row_of_slot", torch.int32, (T, K), dev),
-            "slot_of_row": _out(g("slot_of_row"), "slot_of_row", torch.int32, (T * K,), dev),
-            "offsets": _out(g("offsets"), "offsets", torch.int32, (max(E, 0),), dev)}
+    E, dev, i32 = int(num_experts), expert_ids.device, torch.int32
+    shapes = {"row_of_slot": (T, K), "slot_of_row": (T * K,), "offsets": (max(E, 0),)}
+    plan = _outputs(out, {k: (i32, s) for k, s in shapes.items()}, dev)
     _raise_if(L.nvfp4_moe_plan(_ptr(expert_ids), expert_ids.element_size(), T, K, E,
                                _ptr(plan["row_of_slot"]), _ptr(plan["slot_of_row"]),
                                _ptr(plan["offsets"]), _stream(dev)), "nvfp4_moe_plan")
@@ -351,11 +367,12 @@ def nvfp4_moe_plan(expert_ids, num_experts, out=None):
 def _plan_sizes(plan, device):
     """(row_of_slot, offsets, T, K, E) of a plan, checked."""
     rows, offsets = plan["row_of_slot"], plan["offsets"]
-    if rows.dim() != 2 or offsets.dim() != 1:
+    shape, ends = rows.shape, offsets.shape
+    if len(shape) != 2 or len(ends) != 1:
         raise ValueError("plan: row_of_slot must be [T, K] and offsets [E]")
-    _check(rows, "row_of_slot", torch.int32, rows.shape, device)
-    _check(offsets, "offsets", torch.int32, offsets.shape, device)
-    return rows, offsets, rows.shape[0], rows.shape[1], offsets.shape[0]
+    _check(rows, "row_of_slot", torch.int32, shape, device)
+    _check(offsets, "offsets", torch.int32, ends, device)
+    return rows, offsets, shape[0], shape[1], ends[0]
 
 
 def nvfp4_moe_dispatch(x, plan, out=None, amax=None):
@@ -446,11 +463,9 @@ def nvfp4_swiglu_checkpoint(h, offsets=None, out=None):
     if N % 64 != 0:
         raise ValueError("h must have 2F columns, F a multiple of 32")
     offs, E = _segments(offsets, h.device)
-    g, dev = (out or {}).get, h.device
-    out = {"y": _out(g("y"), "y", torch.bfloat16, (M, N // 2), dev),
-           "codes": _out(g("codes"), "codes", torch.uint8, (M, N), dev),
-           "scales": _out(g("scales"), "scales", torch.uint8, (M, N // 32), dev),
-           "amax": _out(g("amax"), "amax", torch.float32, (E,), dev)}
+    dev = h.device
+    out = _outputs(out, {"y": (torch.bfloat16, (M, N // 2)), "codes": (torch.uint8, (M, N)),
+                         "scales": (torch.uint8, (M, N // 32)), "amax": (torch.float32, (E,))}, dev)
     _raise_if(L.nvfp4_swiglu_checkpoint(_ptr(h), M, N // 2, offs, E, _ptr(out["y"]),
                                         _ptr(out["codes"]), _ptr(out["scales"]),
                                         _ptr(out["amax"]), _stream(dev)),
@@ -487,12 +502,9 @@ def nvfp4_rmsnorm_checkpoint(x, weight, eps=1e-6, weight_bias=0.0, out=None):
     _check(weight, "weight", torch.bfloat16, (N,), dev)
     if N % 32 != 0:
         raise ValueError("x must have a multiple of 32 columns")
-    g = (out or {}).get
-    out = {"y": _out(g("y"), "y", torch.bfloat16, (M, N), dev),
-           "codes": _out(g("codes"), "codes", torch.uint8, (M, N), dev),
-           "scales": _out(g("scales"), "scales", torch.uint8, (M, N // 32), dev),
-           "rstd": _out(g("rstd"), "rstd", torch.float32, (M,), dev),
-           "amax": _out(g("amax"), "amax", torch.float32, (1,), dev)}
+    out = _outputs(out, {"y": (torch.bfloat16, (M, N)), "codes": (torch.uint8, (M, N)),
+                         "scales": (torch.uint8, (M, N // 32)), "rstd": (torch.float32, (M,)),
+                         "amax": (torch.float32, (1,))}, dev)
     _raise_if(L.nvfp4_rmsnorm_checkpoint(_ptr(x), _ptr(weight), M, N, float(eps),
                                          float(weight_bias), _ptr(out["y"]), _ptr(out["codes"]),
                                          _ptr(out["scales"]), _ptr(out["rstd"]),

@@ -48,6 +48,7 @@ int rmsnorm_rows_per_cta();
 // ---- token routing (moe_route.cu) ----
 constexpr int kMaxTopk = 32;  // choices of a token: one warp loads a token's rows
 // rows of `nv` 16-byte vectors; amax (zeroed by the caller) may be null
+cudaError_t prepare_moe_kernels();
 cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
                             int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
                             cudaStream_t s);
@@ -72,7 +73,7 @@ cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* code
                                               const int32_t* offsets, int32_t E, void* grad_h,
                                               uint32_t* status, int sm_count, cudaStream_t s);
 constexpr int64_t kRmsMaxN = 32768;       // a row stays in one CTA's registers
-constexpr int64_t kRmsMaxPartials = 256;  // rows of the weight gradient's partial sums
+constexpr int64_t kRmsMaxPartials = 512;  // rows of the weight gradient's partial sums
 struct RmsArgs {
   int64_t M, N;
   float eps, bias;

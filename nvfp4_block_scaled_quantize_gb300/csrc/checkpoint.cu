@@ -46,13 +46,45 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 constexpr uint32_t kRoundsToInf = 0x7F78u;  // BF16 bits of 1.9375 * 2^127
 
-// Codes of the lane's 16 values and the block's scale byte. With a = 2^(E-127) (1 + m/128) the
-// block's largest BF16 magnitude, a <= 448 * 2^e = 1.75 * 2^(8+e) first holds at e = E - 127 - 8
-// when m <= 96 and one above it otherwise, so the biased scale is ((bits + 31) >> 7) - 8, at least
-// 0. Scaling by a power of two is exact, so each code is rounded once. Infinities and NaN do not
-// count for the maximum and become E4M3 NaN (E4M3 has no infinity), so they reach the gradient.
+// The scale byte of a block whose largest magnitude has the BF16 bits `top`. With
+// a = 2^(E-127) (1 + m/128) that magnitude, a <= 448 * 2^e = 1.75 * 2^(8+e) first holds at
+// e = E - 127 - 8 when m <= 96 and one above it otherwise: ((top + 31) >> 7) - 8, at least 0.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const uint32_t biased = (top + 31u) >> 7;
+  return biased > 8u ? biased - 8u : 0u;
+}
+// 2^(127 - scale), exact for every byte that scale_byte gives
+__device__ __forceinline__ float inverse_scale(uint32_t scale) {
+  return __uint_as_float((254u - scale) << 23);
+}
+
+// The rare block with magnitudes from kRoundsToInf up. Infinities and NaN become NaN (E4M3 has no
+// infinity), so they reach the gradient, and do not count for the maximum, which is returned.
 // Finite magnitudes from 1.9375 * 2^127 up would round to 2^128, outside binary32: they are kept
-// as 1.875 * 2^127, so that what is finite stays finite. Called by both lanes of a pair (lane, lane ^ 1) at once.
+// as 1.875 * 2^127, so that what is finite stays finite.
+template <int COUNT>
+__device__ __forceinline__ uint32_t clean_values(float (&v)[COUNT]) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < COUNT; i++) {
+    const uint32_t b = (__float_as_uint(v[i]) >> 16) & 0x7FFFu;
+    if (b >= 0x7F80u) {
+      v[i] = __uint_as_float(0x7FC00000u);
+      continue;
+    }
+    top = max(top, b);
+    if (b >= kRoundsToInf) v[i] = copysignf(__uint_as_float(0x7F700000u), v[i]);
+  }
+  return top;
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t m, uint32_t quad) {
+  m = max(m, __shfl_xor_sync(quad, m, 1));
+  return max(m, __shfl_xor_sync(quad, m, 2));
+}
+
+// Codes of the lane's 16 values and the block's scale byte, called by both lanes of a pair
+// (lane, lane ^ 1) at once. Scaling by a power of two is exact, so each code is rounded once.
 __device__ __forceinline__ uint4 keep_half(const uint32_t (&w)[8], uint32_t& scale) {
   const int lane = threadIdx.x & 31;
   const uint32_t pair = 3u << (lane & 30);
@@ -68,22 +100,11 @@ __device__ __forceinline__ uint4 keep_half(const uint32_t (&w)[8], uint32_t& sca
     v[2 * i + 1] = bf16_hi(w[i]);
   }
   if (top >= kRoundsToInf) {  // both lanes of the pair
-    top = 0u;
-#pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const uint32_t b = (__float_as_uint(v[i]) >> 16) & 0x7FFFu;
-      if (b >= 0x7F80u) {
-        v[i] = __uint_as_float(0x7FC00000u);
-        continue;
-      }
-      top = max(top, b);
-      if (b >= kRoundsToInf) v[i] = copysignf(__uint_as_float(0x7F700000u), v[i]);
-    }
+    top = clean_values(v);
     top = max(top, __shfl_xor_sync(pair, top, 1));
   }
-  const uint32_t biased = (top + 31u) >> 7;
-  scale = biased > 8u ? biased - 8u : 0u;
-  const float inv = __uint_as_float((254u - scale) << 23);
+  scale = scale_byte(top);
+  const float inv = inverse_scale(scale);
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; i++)
@@ -92,16 +113,40 @@ __device__ __forceinline__ uint4 keep_half(const uint32_t (&w)[8], uint32_t& sca
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
+// The same for 8 values a lane, the block in the four lanes of a quad: two words of codes.
+__device__ __forceinline__ uint2 keep_quarter(const uint32_t (&w)[4], uint32_t& scale) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t quad = 15u << (lane & 28);
+  uint32_t top = pair_bits(vmax2(vmax2(abs2(w[0]), abs2(w[1])), vmax2(abs2(w[2]), abs2(w[3]))));
+  top = quad_max(top, quad);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    v[2 * i] = bf16_lo(w[i]);
+    v[2 * i + 1] = bf16_hi(w[i]);
+  }
+  if (top >= kRoundsToInf) top = quad_max(clean_values(v), quad);
+  scale = scale_byte(top);
+  const float inv = inverse_scale(scale);
+  uint32_t c[2];
+#pragma unroll
+  for (int i = 0; i < 2; i++)
+    c[i] = e4m3x2(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv)) |
+           (e4m3x2(__fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv)) << 16);
+  return make_uint2(c[0], c[1]);
+}
+
 // The binary32 value of a scale byte (255 is NaN).
 __device__ __forceinline__ float e8m0_value(uint32_t s) {
   return s == 0u ? __uint_as_float(0x00400000u)
                  : (s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23));
 }
 
-__device__ __forceinline__ void kept_values(const uint4& c, float scale, float (&v)[16]) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+template <int WORDS>
+__device__ __forceinline__ void kept_values(const uint32_t (&w)[WORDS], float scale,
+                                            float (&v)[4 * WORDS]) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
+  for (int i = 0; i < 2 * WORDS; i++) {
     const float2 f = e4m3x2_to_float2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
     v[2 * i] = __fmul_rn(f.x, scale);
     v[2 * i + 1] = __fmul_rn(f.y, scale);
@@ -232,9 +277,9 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
       uint32_t d[8];
       float g[16], u[16];
       words(load_half(grad + (r * nc + c) * 2), d);
-      kept_values(__ldg(codes + r * 2 * nc + c), e8m0_value(scales[r * nc + c / 2]), g);
-      kept_values(__ldg(codes + r * 2 * nc + nc + c),
-                  e8m0_value(scales[r * nc + nc / 2 + c / 2]), u);
+      const uint4 kg = __ldg(codes + r * 2 * nc + c), ku = __ldg(codes + r * 2 * nc + nc + c);
+      kept_values({kg.x, kg.y, kg.z, kg.w}, e8m0_value(scales[r * nc + c / 2]), g);
+      kept_values({ku.x, ku.y, ku.z, ku.w}, e8m0_value(scales[r * nc + nc / 2 + c / 2]), u);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         float dg[2], du[2];
@@ -262,86 +307,111 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
 
 // ---- RMSNorm -----------------------------------------------------------------------------
 
-// A group of WPR warps owns a row, ITEMS x 16 columns a thread: the row is read once and stays in
-// registers between its sum and its output. A CTA of 16 warps holds 16 / WPR groups.
-constexpr int kRmsWarps = 16;
-constexpr int kRmsThreads = 32 * kRmsWarps;
+// A group of `wpr` warps owns a row, ITEMS x 8 columns a thread (a vector of 16 bytes, neighbouring
+// threads neighbouring vectors): the row is read once and stays in registers between its sum and
+// its output. A CTA holds as many groups as fit in 16 warps, at least one. With ITEMS = 1 (rows up
+// to 8192 columns) the registers also hold the group's next row, which is loaded before the current
+// one is summed, so that the SM's loads do not stop at the barrier of the sum.
+constexpr int kRmsThreads = 1024;  // of the largest CTA
 
-// Sum over the group's threads: shuffles, then the warps' sums in order. `red` has two halves used
-// in turn, so one barrier a row is enough.
-template <int WPR>
-__device__ __forceinline__ float group_sum(float s, float (*red)[kRmsWarps], int turn) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (WPR == 1) return s;
-  const int warp = threadIdx.x >> 5, group = warp / WPR;
-  if ((threadIdx.x & 31) == 0) red[turn][warp] = s;
-  named_bar_sync(1 + group, WPR * 32);
-  s = red[turn][group * WPR];
-#pragma unroll
-  for (int i = 1; i < WPR; i++) s += red[turn][group * WPR + i];
+struct RmsShape {
+  int wpr, groups, items;
+};
+RmsShape rms_shape(int64_t N) {
+  RmsShape s;
+  s.items = N <= 8192 ? 1 : (N <= 16384 ? 2 : 4);
+  const int64_t per_warp = 256 * s.items;
+  s.wpr = (int)((N + per_warp - 1) / per_warp);
+  s.groups = s.wpr >= 16 ? 1 : 16 / s.wpr;
   return s;
 }
 
-template <int WPR, int ITEMS>
-__global__ void __launch_bounds__(kRmsThreads) rmsnorm_checkpoint_kernel(
-    const uint4* __restrict__ x, const uint4* __restrict__ weight, int64_t M, int64_t N, float eps,
-    float bias, uint4* y, uint4* codes, uint8_t* scales, float* rstd, uint32_t* amax) {
-  __shared__ float red[2][kRmsWarps];
-  __shared__ uint32_t top[kRmsWarps];
+// Sum over the group's threads: shuffles, then the warps' sums through shared memory, in an order
+// that does not depend on time. `red` has two halves used in turn, so one barrier a row is enough.
+__device__ __forceinline__ float group_sum(float s, float (*red)[32], int turn, int group, int wpr) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (wpr == 1) return s;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[turn][threadIdx.x >> 5] = s;
+  named_bar_sync(1 + group, wpr * 32);
+  s = lane < wpr ? red[turn][group * wpr + lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return s;
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_kernel(
+    const uint4* __restrict__ x, const uint4* __restrict__ weight, int64_t M, int32_t N, float eps,
+    float bias, int wpr, int groups, uint4* y, uint2* codes, uint8_t* scales, float* rstd,
+    uint32_t* amax) {
+  __shared__ float red[2][32];
+  __shared__ uint32_t top[32];
   pdl_wait();
   pdl_allow_next();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int group = warp / WPR, at = tid - group * WPR * 32;
-  const int64_t nc = N / 16;
-  constexpr int kGroups = kRmsWarps / WPR;
+  const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
+  const int nv = N / 8;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  constexpr bool kAhead = ITEMS == 1;
   uint32_t m = 0u;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * kGroups + group; r < M; r += (int64_t)gridDim.x * kGroups) {
-    uint32_t w[ITEMS][8];
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  uint4 next[ITEMS], g[ITEMS];
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++) {
+    next[j] = g[j] = make_uint4(0u, 0u, 0u, 0u);
+    const int c = at + j * threads;
+    if (c < nv) {
+      g[j] = __ldg(weight + c);
+      if (r < M) next[j] = __ldg(x + r * nv + c);
+    }
+  }
+  for (; r < M; r += step) {
+    uint32_t w[ITEMS][4];
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int64_t c = at + j * WPR * 32;
-      if (c < nc) words(load_half(x + (r * nc + c) * 2), w[j]);
+      const int c = at + j * threads;
+      w[j][0] = next[j].x; w[j][1] = next[j].y; w[j][2] = next[j].z; w[j][3] = next[j].w;
+      if (kAhead && c < nv && r + step < M) next[j] = __ldg(x + (r + step) * nv + c);
     }
 #pragma unroll
-    for (int j = 0; j < ITEMS; j++) {
-      if (at + j * WPR * 32 >= nc) break;
+    for (int j = 0; j < ITEMS; j++)  // (columns past the row hold zeros)
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
+      for (int i = 0; i < 4; i++) {
         s = __fmaf_rn(bf16_lo(w[j][i]), bf16_lo(w[j][i]), s);
         s = __fmaf_rn(bf16_hi(w[j][i]), bf16_hi(w[j][i]), s);
       }
-    }
-    s = group_sum<WPR>(s, red, turn);
+    s = group_sum(s, red, turn, group, wpr);
     turn ^= 1;
     const float rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, (float)N), eps));
     if (at == 0) rstd[r] = rs;
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int64_t c = at + j * WPR * 32;
-      if (c >= nc) break;
-      uint32_t g[8], o[8], sc;
-      words(load_half(weight + c * 2), g);
+      const int c = at + j * threads;
+      if (c >= nv) break;
+      const uint32_t ge[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+      uint32_t o[4], sc;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        o[i] = pack_bf16(__fmul_rn(__fadd_rn(bf16_lo(g[i]), bias), __fmul_rn(bf16_lo(w[j][i]), rs)),
-                         __fmul_rn(__fadd_rn(bf16_hi(g[i]), bias), __fmul_rn(bf16_hi(w[j][i]), rs)));
-        m = max(m, pair_bits(abs2(o[i])));
+      for (int i = 0; i < 4; i++) {
+        o[i] = pack_bf16(__fmul_rn(__fadd_rn(bf16_lo(ge[i]), bias), __fmul_rn(bf16_lo(w[j][i]), rs)),
+                         __fmul_rn(__fadd_rn(bf16_hi(ge[i]), bias), __fmul_rn(bf16_hi(w[j][i]), rs)));
+        m = vmax2(m, abs2(o[i]));
       }
-      y[(r * nc + c) * 2] = make_uint4(o[0], o[1], o[2], o[3]);
-      y[(r * nc + c) * 2 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-      codes[r * nc + c] = keep_half(w[j], sc);
-      if ((c & 1) == 0) scales[r * (nc / 2) + c / 2] = (uint8_t)sc;
+      y[r * nv + c] = make_uint4(o[0], o[1], o[2], o[3]);
+      codes[r * nv + c] = keep_quarter(w[j], sc);
+      if ((c & 3) == 0) scales[r * (nv / 4) + c / 4] = (uint8_t)sc;
+      if (!kAhead && r + step < M) next[j] = __ldg(x + (r + step) * nv + c);
     }
   }
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
   if (lane == 0) top[warp] = m;
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kRmsWarps; i++) m = max(m, top[i]);
-    atomicMax(amax, m << 16);
+  if (warp == 0) {
+    m = __reduce_max_sync(0xFFFFFFFFu, lane < (int)(blockDim.x >> 5) ? top[lane] : 0u);
+    if (lane == 0) atomicMax(amax, m << 16);
   }
 }
 
@@ -349,110 +419,127 @@ __global__ void __launch_bounds__(kRmsThreads) rmsnorm_checkpoint_kernel(
 // dw = sum over rows of dy xh. A thread keeps its columns' share of dw over all of its rows; the
 // groups of a CTA are added in shared memory in order and each CTA writes one row of `partial`, so
 // that the sum's order depends on the grid alone.
-template <int WPR, int ITEMS, bool RES>
+template <int ITEMS, bool RES>
 __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_kernel(
-    const uint4* __restrict__ grad, const uint4* __restrict__ codes,
+    const uint4* __restrict__ grad, const uint2* __restrict__ codes,
     const uint8_t* __restrict__ scales, const float* __restrict__ rstd,
-    const uint4* __restrict__ weight, int64_t M, int64_t N, float bias,
+    const uint4* __restrict__ weight, int64_t M, int32_t N, float bias, int wpr, int groups,
     const uint4* __restrict__ residual, uint4* grad_x, float* partial) {
-  constexpr int kGroups = kRmsWarps / WPR;
-  __shared__ float red[2][kRmsWarps];
-  __shared__ float4 cols[kGroups > 1 ? WPR * 32 * ITEMS * 4 : 1];
+  __shared__ float red[2][32];
+  __shared__ float4 cols[2048 / 4];  // the groups' joint sums: more than one group has N <= 2048
   pdl_wait();
   pdl_allow_next();
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int group = warp / WPR, at = tid - group * WPR * 32;
-  const int64_t nc = N / 16;
-  float dw[ITEMS][16];
+  const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
+  const int nv = N / 8;
+  const int64_t step = (int64_t)gridDim.x * groups;
+  float dw[ITEMS][8];
 #pragma unroll
   for (int j = 0; j < ITEMS; j++)
 #pragma unroll
-    for (int i = 0; i < 16; i++) dw[j][i] = 0.0f;
+    for (int i = 0; i < 8; i++) dw[j][i] = 0.0f;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * kGroups + group; r < M; r += (int64_t)gridDim.x * kGroups) {
-    uint32_t d[ITEMS][8], res[ITEMS][8];
-    uint4 k[ITEMS];
-    float sc[ITEMS];
-    const float rs = rstd[r];
+  constexpr bool kAhead = ITEMS == 1;
+  struct Row {
+    uint4 d[ITEMS], res[ITEMS];
+    uint2 k[ITEMS];
+    uint32_t sc[ITEMS];
+    float rs;
+  } next;
+  auto load = [&](int64_t r) {
+    next.rs = rstd[r];
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int64_t c = at + j * WPR * 32;
-      if (c < nc) {
-        words(load_half(grad + (r * nc + c) * 2), d[j]);
-        k[j] = __ldg(codes + r * nc + c);
-        sc[j] = e8m0_value(scales[r * (nc / 2) + c / 2]);
-        if (RES) words(load_half(residual + (r * nc + c) * 2), res[j]);
+      const int c = at + j * threads;
+      if (c < nv) {
+        next.d[j] = __ldg(grad + r * nv + c);
+        next.k[j] = __ldg(codes + r * nv + c);
+        next.sc[j] = __ldg(scales + r * (nv / 4) + c / 4);
+        if (RES) next.res[j] = __ldg(residual + r * nv + c);
       }
     }
+  };
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++) {
+    next.d[j] = next.res[j] = make_uint4(0u, 0u, 0u, 0u);
+    next.k[j] = make_uint2(0u, 0u);
+    next.sc[j] = 0u;
+  }
+  int64_t r = (int64_t)blockIdx.x * groups + group;
+  if (kAhead && r < M) load(r);
+  for (; r < M; r += step) {
+    if (!kAhead) load(r);
+    const Row row = next;
+    if (kAhead && r + step < M) load(r + step);
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int64_t c = at + j * WPR * 32;
-      if (c >= nc) break;
-      uint32_t g[8];
-      float v[16];
-      words(load_half(weight + c * 2), g);
-      kept_values(k[j], sc[j], v);
+      const int c = at + j * threads;
+      if (c >= nv) break;
+      const uint4 gw = __ldg(weight + c);
+      const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
+      const uint32_t d[4] = {row.d[j].x, row.d[j].y, row.d[j].z, row.d[j].w};
+      float v[8];
+      kept_values({row.k[j].x, row.k[j].y}, e8m0_value(row.sc[j]), v);
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        const float dy = (i & 1) ? bf16_hi(d[j][i >> 1]) : bf16_lo(d[j][i >> 1]);
+      for (int i = 0; i < 8; i++) {
+        const float dy = (i & 1) ? bf16_hi(d[i >> 1]) : bf16_lo(d[i >> 1]);
         const float w = __fadd_rn((i & 1) ? bf16_hi(g[i >> 1]) : bf16_lo(g[i >> 1]), bias);
-        const float t = __fmul_rn(dy, __fmul_rn(v[i], rs));
+        const float t = __fmul_rn(dy, __fmul_rn(v[i], row.rs));
         dw[j][i] = __fadd_rn(dw[j][i], t);
         s = __fmaf_rn(w, t, s);
       }
     }
-    s = group_sum<WPR>(s, red, turn);
+    s = group_sum(s, red, turn, group, wpr);
     turn ^= 1;
     const float mean = __fdiv_rn(s, (float)N);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int64_t c = at + j * WPR * 32;
-      if (c >= nc) break;
-      uint32_t g[8], o[8];
-      float v[16];
-      words(load_half(weight + c * 2), g);
-      kept_values(k[j], sc[j], v);
+      const int c = at + j * threads;
+      if (c >= nv) break;
+      const uint4 gw = __ldg(weight + c);
+      const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
+      const uint32_t d[4] = {row.d[j].x, row.d[j].y, row.d[j].z, row.d[j].w};
+      const uint32_t e[4] = {row.res[j].x, row.res[j].y, row.res[j].z, row.res[j].w};
+      uint32_t o[4];
+      float v[8];
+      kept_values({row.k[j].x, row.k[j].y}, e8m0_value(row.sc[j]), v);
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
+      for (int i = 0; i < 4; i++) {
         float q[2];
 #pragma unroll
         for (int b = 0; b < 2; b++) {
-          const float dy = b ? bf16_hi(d[j][i]) : bf16_lo(d[j][i]);
+          const float dy = b ? bf16_hi(d[i]) : bf16_lo(d[i]);
           const float w = __fadd_rn(b ? bf16_hi(g[i]) : bf16_lo(g[i]), bias);
-          const float xh = __fmul_rn(v[2 * i + b], rs);
-          q[b] = __fmul_rn(rs, __fmaf_rn(-xh, mean, __fmul_rn(w, dy)));
-          if (RES) q[b] = __fadd_rn(q[b], b ? bf16_hi(res[j][i]) : bf16_lo(res[j][i]));
+          const float xh = __fmul_rn(v[2 * i + b], row.rs);
+          q[b] = __fmul_rn(row.rs, __fmaf_rn(-xh, mean, __fmul_rn(w, dy)));
+          if (RES) q[b] = __fadd_rn(q[b], b ? bf16_hi(e[i]) : bf16_lo(e[i]));
         }
         o[i] = pack_bf16(q[0], q[1]);
       }
-      grad_x[(r * nc + c) * 2] = make_uint4(o[0], o[1], o[2], o[3]);
-      grad_x[(r * nc + c) * 2 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+      grad_x[r * nv + c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
   float4* out = reinterpret_cast<float4*>(partial + (int64_t)blockIdx.x * N);
-#pragma unroll 1
-  for (int g = 0; g < kGroups; g++) {
+  for (int g = 0; g < groups; g++) {
     if (group == g) {
 #pragma unroll
       for (int j = 0; j < ITEMS; j++) {
-        const int64_t c = at + j * WPR * 32;
-        if (c >= nc) break;
+        const int c = at + j * threads;
+        if (c >= nv) break;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < 2; i++) {
           float4 v = make_float4(dw[j][4 * i], dw[j][4 * i + 1], dw[j][4 * i + 2], dw[j][4 * i + 3]);
-          if (kGroups > 1) {
-            if (g > 0) {
-              const float4 p = cols[c * 4 + i];
-              v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
-            }
-            cols[c * 4 + i] = v;
+          if (g > 0) {
+            const float4 p = cols[c * 2 + i];
+            v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
           }
-          if (g == kGroups - 1) out[c * 4 + i] = v;
+          if (g == groups - 1) out[c * 2 + i] = v;
+          else cols[c * 2 + i] = v;
         }
       }
     }
-    if (kGroups > 1) __syncthreads();
+    if (groups > 1) __syncthreads();
   }
 }
 
@@ -485,30 +572,33 @@ int64_t glu_per_cta(int64_t items, int sm_count, int* grid) {
   return per;
 }
 
-template <int WPR, int ITEMS>
-cudaError_t rms_forward_t(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const int64_t groups = kRmsWarps / WPR;
-  const int64_t ctas = (a.M + groups - 1) / groups;
-  const int grid = (int)(ctas < sm_count ? ctas : sm_count);
-  return launch_pdl(rmsnorm_checkpoint_kernel<WPR, ITEMS>, dim3(grid), dim3(kRmsThreads), 0, s,
-                    static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.weight), a.M, a.N,
-                    a.eps, a.bias, static_cast<uint4*>(a.y), static_cast<uint4*>(a.codes),
-                    a.scales, a.rstd, reinterpret_cast<uint32_t*>(a.amax));
+// One wave: the CTAs that the registers of 1024 threads allow on every SM.
+int rms_grid(const RmsShape& f, int64_t M, int sm_count) {
+  const int64_t ctas = (M + f.groups - 1) / f.groups;
+  const int64_t wave = (int64_t)sm_count * (kRmsThreads / (f.wpr * f.groups * 32));
+  return (int)(ctas < wave ? ctas : wave);
 }
 
-template <int WPR, int ITEMS>
-cudaError_t rms_backward_t(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const int64_t groups = kRmsWarps / WPR;
-  const int64_t ctas = (a.M + groups - 1) / groups;
-  int grid = (int)(ctas < sm_count ? ctas : sm_count);
+template <int ITEMS>
+cudaError_t rms_forward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
+  return launch_pdl(rmsnorm_checkpoint_kernel<ITEMS>, dim3(rms_grid(f, a.M, sm_count)),
+                    dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.x),
+                    static_cast<const uint4*>(a.weight), a.M, (int32_t)a.N, a.eps, a.bias, f.wpr,
+                    f.groups, static_cast<uint4*>(a.y), static_cast<uint2*>(a.codes), a.scales,
+                    a.rstd, reinterpret_cast<uint32_t*>(a.amax));
+}
+
+template <int ITEMS>
+cudaError_t rms_backward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
+  int grid = rms_grid(f, a.M, sm_count);
   if (grid > kRmsMaxPartials) grid = kRmsMaxPartials;
   const cudaError_t e = launch_pdl(
-      a.residual ? rmsnorm_checkpoint_backward_kernel<WPR, ITEMS, true>
-                 : rmsnorm_checkpoint_backward_kernel<WPR, ITEMS, false>,
-      dim3(grid), dim3(kRmsThreads), 0, s, static_cast<const uint4*>(a.grad),
-      static_cast<const uint4*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
-      a.M, a.N, a.bias, static_cast<const uint4*>(a.residual), static_cast<uint4*>(a.grad_x),
-      a.partial);
+      a.residual ? rmsnorm_checkpoint_backward_kernel<ITEMS, true>
+                 : rmsnorm_checkpoint_backward_kernel<ITEMS, false>,
+      dim3(grid), dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.grad),
+      static_cast<const uint2*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
+      a.M, (int32_t)a.N, a.bias, f.wpr, f.groups, static_cast<const uint4*>(a.residual),
+      static_cast<uint4*>(a.grad_x), a.partial);
   if (e != cudaSuccess) return e;
   return launch_pdl(column_sum_kernel, dim3((unsigned)(a.N / 32)), dim3(32 * kSumWarps), 0, s,
                     a.partial, grid, a.N, a.grad_weight);
@@ -538,23 +628,17 @@ cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* code
 }
 
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  if (a.N <= 512) return rms_forward_t<1, 1>(a, sm_count, s);
-  if (a.N <= 1024) return rms_forward_t<1, 2>(a, sm_count, s);
-  if (a.N <= 2048) return rms_forward_t<2, 2>(a, sm_count, s);
-  if (a.N <= 4096) return rms_forward_t<4, 2>(a, sm_count, s);
-  if (a.N <= 8192) return rms_forward_t<8, 2>(a, sm_count, s);
-  if (a.N <= 16384) return rms_forward_t<16, 2>(a, sm_count, s);
-  return rms_forward_t<16, 4>(a, sm_count, s);
+  const RmsShape f = rms_shape(a.N);
+  if (f.items == 1) return rms_forward_t<1>(a, f, sm_count, s);
+  if (f.items == 2) return rms_forward_t<2>(a, f, sm_count, s);
+  return rms_forward_t<4>(a, f, sm_count, s);
 }
 
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  if (a.N <= 512) return rms_backward_t<1, 1>(a, sm_count, s);
-  if (a.N <= 1024) return rms_backward_t<1, 2>(a, sm_count, s);
-  if (a.N <= 2048) return rms_backward_t<2, 2>(a, sm_count, s);
-  if (a.N <= 4096) return rms_backward_t<4, 2>(a, sm_count, s);
-  if (a.N <= 8192) return rms_backward_t<8, 2>(a, sm_count, s);
-  if (a.N <= 16384) return rms_backward_t<16, 2>(a, sm_count, s);
-  return rms_backward_t<16, 4>(a, sm_count, s);
+  const RmsShape f = rms_shape(a.N);
+  if (f.items == 1) return rms_backward_t<1>(a, f, sm_count, s);
+  if (f.items == 2) return rms_backward_t<2>(a, f, sm_count, s);
+  return rms_backward_t<4>(a, f, sm_count, s);
 }
 
 }  // namespace nvfp4

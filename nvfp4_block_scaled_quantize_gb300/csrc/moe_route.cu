@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBatch = 8;  // groups of 32 slots whose ids a warp loads together
 constexpr int kRouteThreads = 128;
 constexpr uint32_t kBadRoute = 0x4u;  // NVFP4_DEVICE_BAD_ROUTE
 
@@ -47,12 +48,20 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(
   const int32_t begin = (int32_t)(first < n ? first : n);
   const int32_t end = n - begin < run ? n : begin + run;
   bool bad = false;
-  for (int32_t s = begin + lane; s < end; s += 32) {
-    const Id id = ids[s];
-    if (id >= 0 && id < E)
-      atomicAdd(&hist[warp][(int)id], 1u);
-    else if (id >= E)
-      bad = true;
+  for (int32_t s0 = begin; s0 < end; s0 += 32 * kPlanBatch) {
+    Id id[kPlanBatch];
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; j++) {
+      const int32_t s = s0 + 32 * j + lane;
+      id[j] = s < end ? ids[s] : (Id)-1;
+    }
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; j++) {
+      if (id[j] >= 0 && id[j] < E)
+        atomicAdd(&hist[warp][(int)id[j]], 1u);
+      else if (id[j] >= E)
+        bad = true;
+    }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(status, kBadRoute);
   __syncthreads();
@@ -93,23 +102,28 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(
   }
   __syncthreads();
   // the same number of steps for every lane: the match below takes the whole warp
-  for (int32_t s0 = begin; s0 < end; s0 += 32) {
-    const int32_t s = s0 + lane;
-    int32_t e = -1;
-    if (s < end) {
-      const Id id = ids[s];
-      if (id >= 0 && id < E) e = (int32_t)id;
+  for (int32_t s0 = begin; s0 < end; s0 += 32 * kPlanBatch) {
+    int32_t e[kPlanBatch];
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; j++) {
+      const int32_t s = s0 + 32 * j + lane;
+      const Id id = s < end ? ids[s] : (Id)-1;
+      e[j] = id >= 0 && id < E ? (int32_t)id : -1;
     }
-    const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e);
-    const int before_me = __popc(peers & ((1u << lane) - 1u));
-    int32_t row = -1;
-    if (e >= 0) row = (int32_t)(hist[warp][e] + before_me);
-    __syncwarp();
-    if (e >= 0 && before_me == 0) hist[warp][e] += __popc(peers);
-    __syncwarp();
-    if (s < end) {
-      row_of_slot[s] = row;
-      if (row >= 0) slot_of_row[row] = s;
+#pragma unroll
+    for (int j = 0; j < kPlanBatch; j++) {
+      const int32_t s = s0 + 32 * j + lane;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e[j]);
+      const int before_me = __popc(peers & ((1u << lane) - 1u));
+      int32_t row = -1;
+      if (e[j] >= 0) row = (int32_t)(hist[warp][e[j]] + before_me);
+      __syncwarp();
+      if (e[j] >= 0 && before_me == 0) hist[warp][e[j]] += __popc(peers);
+      __syncwarp();
+      if (s < end) {
+        row_of_slot[s] = row;
+        if (row >= 0) slot_of_row[row] = s;
+      }
     }
   }
   for (int64_t r = (int64_t)live + rank * kPlanThreads + tid; r < n;
@@ -303,10 +317,21 @@ __global__ void __launch_bounds__(kRouteThreads) moe_combine_backward_kernel(
 
 }  // namespace
 
+cudaError_t prepare_moe_kernels() {
+  cudaError_t e = cudaSuccess, r;
+  if ((r = cudaFuncSetAttribute(moe_plan_kernel<int32_t>,
+                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    e = r;
+  if ((r = cudaFuncSetAttribute(moe_plan_kernel<int64_t>,
+                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    e = r;
+  return e;
+}
+
 cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
                             int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
                             cudaStream_t s) {
-  const int ctas = n <= 4096 ? 1 : 8;
+  const int ctas = n <= 4096 ? 1 : 16;
   const int64_t warps = (int64_t)ctas * kPlanWarps;
   const int32_t run = (int32_t)((n + warps * 32 - 1) / (warps * 32) * 32);
   cudaLaunchConfig_t cfg = {};
