@@ -400,7 +400,8 @@ nvfp4_status nvfp4_moe_combine_backward(const void* grad_out, const void* y, con
  * saturates. Elements are rounded to nearest-even, those that would round to 2^128 to 1.875 * 2^127
  * (what is finite stays finite); infinities and NaN become NaN codes and do not
  * count for the scale. An all-zero block has scale byte 0. The backward passes take the kept
- * values for the inputs. Row lengths are multiples of 32, buffers 16-byte aligned (scales: any). */
+ * values for the inputs. Row lengths are multiples of 32; BF16 buffers are 32-byte aligned (one
+ * half block a load), the others 16-byte (scales: any). */
 
 /* y = silu(g) * u of h = [g | u], and h kept.
  *   h (device) BF16 [M][2F]: F gate columns, then F up columns; F % 32 == 0.

@@ -17,20 +17,21 @@ namespace {
 
 constexpr uint32_t kBadOffsets = 0x1u;  // NVFP4_DEVICE_BAD_OFFSETS
 
-// 16 BF16 values of one row: half a block of 32, the other half in the neighbouring lane.
+// 16 BF16 values of one row, half a block of 32 (the other half is in the neighbouring lane), by
+// one 32-byte load or store: a warp's request is whole 128-byte lines, with one address a lane.
 struct Half32 {
-  uint4 lo, hi;
+  uint32_t w[8];
 };
-
-__device__ __forceinline__ Half32 load_half(const uint4* p) {
+__device__ __forceinline__ Half32 load_half(const void* p) {
   Half32 h;
-  h.lo = __ldg(p);
-  h.hi = __ldg(p + 1);
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(h.w[0]), "=r"(h.w[1]), "=r"(h.w[2]), "=r"(h.w[3]), "=r"(h.w[4]), "=r"(h.w[5]),
+                 "=r"(h.w[6]), "=r"(h.w[7])
+               : "l"(p));
   return h;
 }
-__device__ __forceinline__ void words(const Half32& h, uint32_t (&w)[8]) {
-  w[0] = h.lo.x; w[1] = h.lo.y; w[2] = h.lo.z; w[3] = h.lo.w;
-  w[4] = h.hi.x; w[5] = h.hi.y; w[6] = h.hi.z; w[7] = h.hi.w;
+__device__ __forceinline__ void store_half(void* p, const uint32_t (&w)[8]) {
+  stg256(p, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -62,78 +63,53 @@ __device__ __forceinline__ float inverse_scale(uint32_t scale) {
 // infinity), so they reach the gradient, and do not count for the maximum, which is returned.
 // Finite magnitudes from 1.9375 * 2^127 up would round to 2^128, outside binary32: they are kept
 // as 1.875 * 2^127, so that what is finite stays finite.
-template <int COUNT>
-__device__ __forceinline__ uint32_t clean_values(float (&v)[COUNT]) {
+template <int WORDS>
+__device__ __forceinline__ uint32_t clean_words(uint32_t (&w)[WORDS]) {
   uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < COUNT; i++) {
-    const uint32_t b = (__float_as_uint(v[i]) >> 16) & 0x7FFFu;
-    if (b >= 0x7F80u) {
-      v[i] = __uint_as_float(0x7FC00000u);
-      continue;
-    }
-    top = max(top, b);
-    if (b >= kRoundsToInf) v[i] = copysignf(__uint_as_float(0x7F700000u), v[i]);
+  for (int i = 0; i < 2 * WORDS; i++) {
+    const int sh = 16 * (i & 1);
+    const uint32_t h = (w[i >> 1] >> sh) & 0xFFFFu, b = h & 0x7FFFu;
+    uint32_t c = h;
+    if (b >= 0x7F80u) c = 0x7FC0u;
+    else if (b >= kRoundsToInf) c = (h & 0x8000u) | 0x7F70u;
+    if (b < 0x7F80u) top = max(top, b);
+    w[i >> 1] = (w[i >> 1] & ~(0xFFFFu << sh)) | (c << sh);
   }
   return top;
 }
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t m, uint32_t quad) {
-  m = max(m, __shfl_xor_sync(quad, m, 1));
-  return max(m, __shfl_xor_sync(quad, m, 2));
-}
-
-// Codes of the lane's 16 values and the block's scale byte, called by both lanes of a pair
-// (lane, lane ^ 1) at once. Scaling by a power of two is exact, so each code is rounded once.
-__device__ __forceinline__ uint4 keep_half(const uint32_t (&w)[8], uint32_t& scale) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t pair = 3u << (lane & 30);
-  uint32_t m = abs2(w[0]);
+// E4M3 codes and the scale byte of a block of 32, 2 * WORDS values in each of 16 / WORDS
+// neighbouring lanes, which call it at once. Scaling by a power of two is exact, so each code is
+// rounded once.
+template <int WORDS>
+__device__ __forceinline__ void keep_block(const uint32_t (&words)[WORDS], uint32_t (&codes)[WORDS / 2],
+                                           uint32_t& scale) {
+  constexpr int kLanes = 16 / WORDS;
+  const uint32_t mates = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+  uint32_t m = abs2(words[0]);
 #pragma unroll
-  for (int i = 1; i < 8; i++) m = vmax2(m, abs2(w[i]));
+  for (int i = 1; i < WORDS; i++) m = vmax2(m, abs2(words[i]));
   uint32_t top = pair_bits(m);
-  top = max(top, __shfl_xor_sync(pair, top, 1));
-  float v[16];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-  if (top >= kRoundsToInf) {  // both lanes of the pair
-    top = clean_values(v);
-    top = max(top, __shfl_xor_sync(pair, top, 1));
+  for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
+  uint32_t w[WORDS];
+#pragma unroll
+  for (int i = 0; i < WORDS; i++) w[i] = words[i];
+  if (top >= kRoundsToInf) {  // all lanes of the block
+    top = clean_words(w);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
   }
   scale = scale_byte(top);
   const float inv = inverse_scale(scale);
-  uint32_t c[4];
+  const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-    c[i] = e4m3x2(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv)) |
-           (e4m3x2(__fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv)) << 16);
-  return make_uint4(c[0], c[1], c[2], c[3]);
-}
-
-// The same for 8 values a lane, the block in the four lanes of a quad: two words of codes.
-__device__ __forceinline__ uint2 keep_quarter(const uint32_t (&w)[4], uint32_t& scale) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t quad = 15u << (lane & 28);
-  uint32_t top = pair_bits(vmax2(vmax2(abs2(w[0]), abs2(w[1])), vmax2(abs2(w[2]), abs2(w[3]))));
-  top = quad_max(top, quad);
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
+  for (int i = 0; i < WORDS / 2; i++) {
+    const float2 lo = f2_unpack(f2_mul(f2_from_bf16x2(w[2 * i]), inv2));
+    const float2 hi = f2_unpack(f2_mul(f2_from_bf16x2(w[2 * i + 1]), inv2));
+    codes[i] = e4m3x2(lo.x, lo.y) | (e4m3x2(hi.x, hi.y) << 16);
   }
-  if (top >= kRoundsToInf) top = quad_max(clean_values(v), quad);
-  scale = scale_byte(top);
-  const float inv = inverse_scale(scale);
-  uint32_t c[2];
-#pragma unroll
-  for (int i = 0; i < 2; i++)
-    c[i] = e4m3x2(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv)) |
-           (e4m3x2(__fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv)) << 16);
-  return make_uint2(c[0], c[1]);
 }
 
 // The binary32 value of a scale byte (255 is NaN).
@@ -142,15 +118,25 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
                  : (s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23));
 }
 
+// Four codes a word times a factor, as packed pairs. The factor is the block's scale, alone or
+// times another number: E4M3 values times a power of two are exact, so the product is rounded once.
 template <int WORDS>
-__device__ __forceinline__ void kept_values(const uint32_t (&w)[WORDS], float scale,
-                                            float (&v)[4 * WORDS]) {
+__device__ __forceinline__ void kept_values(const uint32_t (&w)[WORDS], float factor,
+                                            uint64_t (&v)[2 * WORDS]) {
+  const uint64_t f2 = f2_pack(factor, factor);
 #pragma unroll
   for (int i = 0; i < 2 * WORDS; i++) {
     const float2 f = e4m3x2_to_float2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-    v[2 * i] = __fmul_rn(f.x, scale);
-    v[2 * i + 1] = __fmul_rn(f.y, scale);
+    v[i] = f2_mul(f2_pack(f.x, f.y), f2);
   }
+}
+__device__ __forceinline__ void unpack16(const Half32& h, uint64_t (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = f2_from_bf16x2(h.w[i]);
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  const float2 f = f2_unpack(v);
+  return pack_bf16(f.x, f.y);
 }
 
 // sigmoid(a) from exp(-|a|), which cannot overflow.
@@ -221,34 +207,31 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
   uint32_t m = 0u;
   for (GluWalk it(M, nc, per_cta); it.left > 0; it.next()) {
     const int64_t r = it.row, c = it.col;
-    uint4 yo[2], kg = make_uint4(0u, 0u, 0u, 0u), ku = kg;
-    uint32_t sg = 0u, su = 0u;
-    yo[0] = yo[1] = kg;
+    uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, kg[4] = {0u, 0u, 0u, 0u},
+             ku[4] = {0u, 0u, 0u, 0u}, sg = 0u, su = 0u;
     if (r < live) {
+      const Half32 g = load_half(h + (r * 2 * nc + c) * 2);
+      const Half32 u = load_half(h + (r * 2 * nc + nc + c) * 2);
       while (expert < E - 1 && r >= ends[expert]) {
         if (m) atomicMax(&top[expert], m);
         m = 0u;
         expert++;
       }
-      uint32_t g[8], u[8], o[8];
-      words(load_half(h + (r * 2 * nc + c) * 2), g);
-      words(load_half(h + (r * 2 * nc + nc + c) * 2), u);
+      uint32_t mm = 0u;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float a0 = bf16_lo(g[i]), a1 = bf16_hi(g[i]);
-        o[i] = pack_bf16(__fmul_rn(__fmul_rn(a0, sigmoid(a0)), bf16_lo(u[i])),
-                         __fmul_rn(__fmul_rn(a1, sigmoid(a1)), bf16_hi(u[i])));
-        m = max(m, pair_bits(abs2(o[i])));
+        const float a0 = bf16_lo(g.w[i]), a1 = bf16_hi(g.w[i]);
+        o[i] = pack_bf16(__fmul_rn(__fmul_rn(a0, sigmoid(a0)), bf16_lo(u.w[i])),
+                         __fmul_rn(__fmul_rn(a1, sigmoid(a1)), bf16_hi(u.w[i])));
+        mm = vmax2(mm, abs2(o[i]));
       }
-      yo[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      yo[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      kg = keep_half(g, sg);
-      ku = keep_half(u, su);
+      m = max(m, pair_bits(mm));
+      keep_block(g.w, kg, sg);
+      keep_block(u.w, ku, su);
     }
-    y[(r * nc + c) * 2] = yo[0];
-    y[(r * nc + c) * 2 + 1] = yo[1];
-    codes[r * 2 * nc + c] = kg;
-    codes[r * 2 * nc + nc + c] = ku;
+    store_half(y + (r * nc + c) * 2, o);
+    codes[r * 2 * nc + c] = make_uint4(kg[0], kg[1], kg[2], kg[3]);
+    codes[r * 2 * nc + nc + c] = make_uint4(ku[0], ku[1], ku[2], ku[3]);
     if ((c & 1) == 0) {
       scales[r * nc + c / 2] = (uint8_t)sg;
       scales[r * nc + nc / 2 + c / 2] = (uint8_t)su;
@@ -274,9 +257,8 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
     const int64_t r = it.row, c = it.col;
     uint32_t og[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, ou[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
     if (r < live) {
-      uint32_t d[8];
-      float g[16], u[16];
-      words(load_half(grad + (r * nc + c) * 2), d);
+      uint64_t g[8], u[8];
+      const Half32 d = load_half(grad + (r * nc + c) * 2);
       const uint4 kg = __ldg(codes + r * 2 * nc + c), ku = __ldg(codes + r * 2 * nc + nc + c);
       kept_values({kg.x, kg.y, kg.z, kg.w}, e8m0_value(scales[r * nc + c / 2]), g);
       kept_values({ku.x, ku.y, ku.z, ku.w}, e8m0_value(scales[r * nc + nc / 2 + c / 2]), u);
@@ -285,8 +267,9 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
         float dg[2], du[2];
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-          const float dy = j ? bf16_hi(d[i]) : bf16_lo(d[i]);
-          const float a = g[2 * i + j], b = u[2 * i + j];
+          const float dy = j ? bf16_hi(d.w[i]) : bf16_lo(d.w[i]);
+          const float2 av = f2_unpack(g[i]), bv = f2_unpack(u[i]);
+          const float a = j ? av.y : av.x, b = j ? bv.y : bv.x;
           const float s = sigmoid(a);
           const float slope = __fmul_rn(s, __fmaf_rn(a, __fsub_rn(1.0f, s), 1.0f));
           dg[j] = __fmul_rn(__fmul_rn(dy, b), slope);
@@ -296,23 +279,22 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
         ou[i] = pack_bf16(du[0], du[1]);
       }
     }
-    uint4* pg = grad_h + (r * 2 * nc + c) * 2;
-    uint4* pu = grad_h + (r * 2 * nc + nc + c) * 2;
-    pg[0] = make_uint4(og[0], og[1], og[2], og[3]);
-    pg[1] = make_uint4(og[4], og[5], og[6], og[7]);
-    pu[0] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-    pu[1] = make_uint4(ou[4], ou[5], ou[6], ou[7]);
+    store_half(grad_h + (r * 2 * nc + c) * 2, og);
+    store_half(grad_h + (r * 2 * nc + nc + c) * 2, ou);
   }
 }
 
 // ---- RMSNorm -----------------------------------------------------------------------------
 
-// A group of `wpr` warps owns a row, ITEMS x 8 columns a thread (a vector of 16 bytes, neighbouring
-// threads neighbouring vectors): the row is read once and stays in registers between its sum and
-// its output. A CTA holds as many groups as fit in 16 warps, at least one. With ITEMS = 1 (rows up
-// to 8192 columns) the registers also hold the group's next row, which is loaded before the current
-// one is summed, so that the SM's loads do not stop at the barrier of the sum.
-constexpr int kRmsThreads = 1024;  // of the largest CTA
+// A group of `wpr` warps owns a row, ITEMS x 16 columns a thread: the row is read once and stays in
+// registers between its sum and its output. A CTA holds as many groups as fit in 16 warps. With
+// ITEMS = 1 (rows up to 8192 columns) the registers also hold the weights and the group's next row,
+// which is loaded before the current one is summed, so that the SM's loads do not stop at the
+// barrier of the sum.
+constexpr int kRmsWarps = 16;
+constexpr int kRmsThreads = 32 * kRmsWarps;
+
+constexpr int kMaxJointN = 4096;  // a CTA with more than one group has rows up to this
 
 struct RmsShape {
   int wpr, groups, items;
@@ -320,15 +302,18 @@ struct RmsShape {
 RmsShape rms_shape(int64_t N) {
   RmsShape s;
   s.items = N <= 8192 ? 1 : (N <= 16384 ? 2 : 4);
-  const int64_t per_warp = 256 * s.items;
+  const int64_t per_warp = 512 * s.items;
   s.wpr = (int)((N + per_warp - 1) / per_warp);
-  s.groups = s.wpr >= 16 ? 1 : 16 / s.wpr;
+  s.groups = kRmsWarps / s.wpr;
   return s;
 }
 
 // Sum over the group's threads: shuffles, then the warps' sums through shared memory, in an order
 // that does not depend on time. `red` has two halves used in turn, so one barrier a row is enough.
-__device__ __forceinline__ float group_sum(float s, float (*red)[32], int turn, int group, int wpr) {
+__device__ __forceinline__ float group_sum(uint64_t pair, float (*red)[kRmsWarps], int turn,
+                                           int group, int wpr) {
+  const float2 f = f2_unpack(pair);
+  float s = __fadd_rn(f.x, f.y);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (wpr == 1) return s;
@@ -337,73 +322,88 @@ __device__ __forceinline__ float group_sum(float s, float (*red)[32], int turn, 
   named_bar_sync(1 + group, wpr * 32);
   s = lane < wpr ? red[turn][group * wpr + lane] : 0.0f;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  return s;
+  for (int o = 8; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  return __shfl_sync(0xFFFFFFFFu, s, 0);
+}
+
+// w + bias of 16 columns as packed pairs
+__device__ __forceinline__ void biased_weight(const Half32& weight, float bias, uint64_t (&w)[8]) {
+  unpack16(weight, w);
+  const uint64_t b2 = f2_pack(bias, bias);
+#pragma unroll
+  for (int i = 0; i < 8; i++) w[i] = f2_add(w[i], b2);
 }
 
 template <int ITEMS>
-__global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_kernel(
+__global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_checkpoint_kernel(
     const uint4* __restrict__ x, const uint4* __restrict__ weight, int64_t M, int32_t N, float eps,
-    float bias, int wpr, int groups, uint4* y, uint2* codes, uint8_t* scales, float* rstd,
+    float bias, int wpr, int groups, uint4* y, uint4* codes, uint8_t* scales, float* rstd,
     uint32_t* amax) {
-  __shared__ float red[2][32];
-  __shared__ uint32_t top[32];
+  __shared__ float red[2][kRmsWarps];
+  __shared__ uint32_t top[kRmsWarps];
   pdl_wait();
   pdl_allow_next();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
-  const int nv = N / 8;
+  const int nc = N / 16;
   const int64_t step = (int64_t)gridDim.x * groups;
   constexpr bool kAhead = ITEMS == 1;
+  const float inv_n = 1.0f / (float)N;
   uint32_t m = 0u;
   int turn = 0;
   int64_t r = (int64_t)blockIdx.x * groups + group;
-  uint4 next[ITEMS], g[ITEMS];
+  int64_t pos = r * nc + at;  // of the thread's first 16 columns, in units of 16
+  Half32 next[ITEMS], weights;
+  auto load = [&](int64_t p) {
 #pragma unroll
-  for (int j = 0; j < ITEMS; j++) {
-    next[j] = g[j] = make_uint4(0u, 0u, 0u, 0u);
-    const int c = at + j * threads;
-    if (c < nv) {
-      g[j] = __ldg(weight + c);
-      if (r < M) next[j] = __ldg(x + r * nv + c);
-    }
+    for (int j = 0; j < ITEMS; j++)
+      if (at + j * threads < nc) next[j] = load_half(x + 2 * (p + j * threads));
+  };
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++)
+#pragma unroll
+    for (int i = 0; i < 8; i++) next[j].w[i] = 0u;
+  if (kAhead) {
+    if (at < nc) weights = load_half(weight + 2 * at);
+    if (r < M) load(pos);
   }
-  for (; r < M; r += step) {
-    uint32_t w[ITEMS][4];
-    float s = 0.0f;
+  for (; r < M; r += step, pos += step * nc) {
+    if (!kAhead) load(pos);
+    Half32 w[ITEMS];
 #pragma unroll
-    for (int j = 0; j < ITEMS; j++) {
-      const int c = at + j * threads;
-      w[j][0] = next[j].x; w[j][1] = next[j].y; w[j][2] = next[j].z; w[j][3] = next[j].w;
-      if (kAhead && c < nv && r + step < M) next[j] = __ldg(x + (r + step) * nv + c);
+    for (int j = 0; j < ITEMS; j++) w[j] = next[j];
+    if (kAhead && r + step < M) load(pos + step * nc);
+    uint64_t s = f2_pack(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < ITEMS; j++) {  // (columns past the row hold zeros)
+      uint64_t v[8];
+      unpack16(w[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; i++) s = f2_fma(v[i], v[i], s);
     }
-#pragma unroll
-    for (int j = 0; j < ITEMS; j++)  // (columns past the row hold zeros)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        s = __fmaf_rn(bf16_lo(w[j][i]), bf16_lo(w[j][i]), s);
-        s = __fmaf_rn(bf16_hi(w[j][i]), bf16_hi(w[j][i]), s);
-      }
-    s = group_sum(s, red, turn, group, wpr);
+    const float sum = group_sum(s, red, turn, group, wpr);
     turn ^= 1;
-    const float rs = __frsqrt_rn(__fadd_rn(__fdiv_rn(s, (float)N), eps));
+    const float rs = rsqrtf(__fmaf_rn(sum, inv_n, eps));
+    const uint64_t rs2 = f2_pack(rs, rs);
     if (at == 0) rstd[r] = rs;
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
-      if (c >= nv) break;
-      const uint32_t ge[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
-      uint32_t o[4], sc;
+      if (c >= nc) break;
+      const int64_t p = pos + j * threads;
+      uint64_t v[8], g[8];
+      uint32_t o[8], k[4], sc;
+      unpack16(w[j], v);
+      biased_weight(kAhead ? weights : load_half(weight + 2 * c), bias, g);
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        o[i] = pack_bf16(__fmul_rn(__fadd_rn(bf16_lo(ge[i]), bias), __fmul_rn(bf16_lo(w[j][i]), rs)),
-                         __fmul_rn(__fadd_rn(bf16_hi(ge[i]), bias), __fmul_rn(bf16_hi(w[j][i]), rs)));
+      for (int i = 0; i < 8; i++) {
+        o[i] = pack_bf16(f2_mul(g[i], f2_mul(v[i], rs2)));
         m = vmax2(m, abs2(o[i]));
       }
-      y[r * nv + c] = make_uint4(o[0], o[1], o[2], o[3]);
-      codes[r * nv + c] = keep_quarter(w[j], sc);
-      if ((c & 3) == 0) scales[r * (nv / 4) + c / 4] = (uint8_t)sc;
-      if (!kAhead && r + step < M) next[j] = __ldg(x + (r + step) * nv + c);
+      store_half(y + 2 * p, o);
+      keep_block(w[j].w, k, sc);
+      codes[p] = make_uint4(k[0], k[1], k[2], k[3]);
+      if ((c & 1) == 0) scales[p / 2] = (uint8_t)sc;  // (rows are an even number of halves)
     }
   }
   m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
@@ -421,103 +421,93 @@ __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_kernel(
 // that the sum's order depends on the grid alone.
 template <int ITEMS, bool RES>
 __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_kernel(
-    const uint4* __restrict__ grad, const uint2* __restrict__ codes,
+    const uint4* __restrict__ grad, const uint4* __restrict__ codes,
     const uint8_t* __restrict__ scales, const float* __restrict__ rstd,
     const uint4* __restrict__ weight, int64_t M, int32_t N, float bias, int wpr, int groups,
     const uint4* __restrict__ residual, uint4* grad_x, float* partial) {
-  __shared__ float red[2][32];
-  __shared__ float4 cols[2048 / 4];  // the groups' joint sums: more than one group has N <= 2048
+  __shared__ float red[2][kRmsWarps];
+  __shared__ float4 cols[kMaxJointN / 4];  // the groups' joint sums
   pdl_wait();
   pdl_allow_next();
   const int tid = threadIdx.x, warp = tid >> 5;
   const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
-  const int nv = N / 8;
+  const int nc = N / 16;
   const int64_t step = (int64_t)gridDim.x * groups;
-  float dw[ITEMS][8];
-#pragma unroll
-  for (int j = 0; j < ITEMS; j++)
-#pragma unroll
-    for (int i = 0; i < 8; i++) dw[j][i] = 0.0f;
-  int turn = 0;
   constexpr bool kAhead = ITEMS == 1;
+  const float inv_n = 1.0f / (float)N;
   struct Row {
-    uint4 d[ITEMS], res[ITEMS];
-    uint2 k[ITEMS];
+    Half32 d[ITEMS], res[RES ? ITEMS : 1];
+    uint4 k[ITEMS];
     uint32_t sc[ITEMS];
     float rs;
   } next;
-  auto load = [&](int64_t r) {
-    next.rs = rstd[r];
+  uint64_t dw[ITEMS][8], w[8], h[8];
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++)
+#pragma unroll
+    for (int i = 0; i < 8; i++) dw[j][i] = f2_pack(0.0f, 0.0f);
+  if (kAhead && at < nc) biased_weight(load_half(weight + 2 * at), bias, w);
+  auto load = [&](int64_t r, int64_t pos) {
+    next.rs = __ldg(rstd + r);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
-      const int c = at + j * threads;
-      if (c < nv) {
-        next.d[j] = __ldg(grad + r * nv + c);
-        next.k[j] = __ldg(codes + r * nv + c);
-        next.sc[j] = __ldg(scales + r * (nv / 4) + c / 4);
-        if (RES) next.res[j] = __ldg(residual + r * nv + c);
+      const int64_t p = pos + j * threads;
+      if (at + j * threads < nc) {
+        next.d[j] = load_half(grad + 2 * p);
+        next.k[j] = __ldg(codes + p);
+        next.sc[j] = __ldg(scales + p / 2);
+        if (RES) next.res[j] = load_half(residual + 2 * p);
       }
     }
   };
-#pragma unroll
-  for (int j = 0; j < ITEMS; j++) {
-    next.d[j] = next.res[j] = make_uint4(0u, 0u, 0u, 0u);
-    next.k[j] = make_uint2(0u, 0u);
-    next.sc[j] = 0u;
-  }
+  auto kept = [&](const uint4& k, uint32_t sc, float rs) {
+    kept_values({k.x, k.y, k.z, k.w}, __fmul_rn(e8m0_value(sc), rs), h);
+  };
+  int turn = 0;
   int64_t r = (int64_t)blockIdx.x * groups + group;
-  if (kAhead && r < M) load(r);
-  for (; r < M; r += step) {
-    if (!kAhead) load(r);
+  int64_t pos = r * nc + at;  // of the thread's first 16 columns, in units of 16
+  if (kAhead && r < M) load(r, pos);
+  for (; r < M; r += step, pos += step * nc) {
+    if (!kAhead) load(r, pos);
     const Row row = next;
-    if (kAhead && r + step < M) load(r + step);
-    float s = 0.0f;
+    if (kAhead && r + step < M) load(r + step, pos + step * nc);
+    uint64_t s = f2_pack(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
-      if (c >= nv) break;
-      const uint4 gw = __ldg(weight + c);
-      const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
-      const uint32_t d[4] = {row.d[j].x, row.d[j].y, row.d[j].z, row.d[j].w};
-      float v[8];
-      kept_values({row.k[j].x, row.k[j].y}, e8m0_value(row.sc[j]), v);
+      if (c >= nc) break;
+      if (!kAhead) biased_weight(load_half(weight + 2 * c), bias, w);
+      uint64_t d[8];
+      unpack16(row.d[j], d);
+      kept(row.k[j], row.sc[j], row.rs);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const float dy = (i & 1) ? bf16_hi(d[i >> 1]) : bf16_lo(d[i >> 1]);
-        const float w = __fadd_rn((i & 1) ? bf16_hi(g[i >> 1]) : bf16_lo(g[i >> 1]), bias);
-        const float t = __fmul_rn(dy, __fmul_rn(v[i], row.rs));
-        dw[j][i] = __fadd_rn(dw[j][i], t);
-        s = __fmaf_rn(w, t, s);
+        const uint64_t t = f2_mul(d[i], h[i]);
+        dw[j][i] = f2_add(dw[j][i], t);
+        s = f2_fma(w[i], t, s);
       }
     }
-    s = group_sum(s, red, turn, group, wpr);
+    const float mean = __fmul_rn(group_sum(s, red, turn, group, wpr), inv_n);
     turn ^= 1;
-    const float mean = __fdiv_rn(s, (float)N);
+    const uint64_t rs2 = f2_pack(row.rs, row.rs), minus = f2_pack(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
-      if (c >= nv) break;
-      const uint4 gw = __ldg(weight + c);
-      const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
-      const uint32_t d[4] = {row.d[j].x, row.d[j].y, row.d[j].z, row.d[j].w};
-      const uint32_t e[4] = {row.res[j].x, row.res[j].y, row.res[j].z, row.res[j].w};
-      uint32_t o[4];
-      float v[8];
-      kept_values({row.k[j].x, row.k[j].y}, e8m0_value(row.sc[j]), v);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float q[2];
-#pragma unroll
-        for (int b = 0; b < 2; b++) {
-          const float dy = b ? bf16_hi(d[i]) : bf16_lo(d[i]);
-          const float w = __fadd_rn(b ? bf16_hi(g[i]) : bf16_lo(g[i]), bias);
-          const float xh = __fmul_rn(v[2 * i + b], row.rs);
-          q[b] = __fmul_rn(row.rs, __fmaf_rn(-xh, mean, __fmul_rn(w, dy)));
-          if (RES) q[b] = __fadd_rn(q[b], b ? bf16_hi(e[i]) : bf16_lo(e[i]));
-        }
-        o[i] = pack_bf16(q[0], q[1]);
+      if (c >= nc) break;
+      if (!kAhead) {
+        biased_weight(load_half(weight + 2 * c), bias, w);
+        kept(row.k[j], row.sc[j], row.rs);
       }
-      grad_x[r * nv + c] = make_uint4(o[0], o[1], o[2], o[3]);
+      uint64_t d[8], e[8];
+      uint32_t o[8];
+      unpack16(row.d[j], d);
+      if (RES) unpack16(row.res[RES ? j : 0], e);
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const uint64_t q = f2_fma(h[i], minus, f2_mul(w[i], d[i]));
+        o[i] = pack_bf16(RES ? f2_fma(rs2, q, e[i]) : f2_mul(rs2, q));
+      }
+      store_half(grad_x + 2 * (pos + j * threads), o);
     }
   }
   float4* out = reinterpret_cast<float4*>(partial + (int64_t)blockIdx.x * N);
@@ -526,16 +516,17 @@ __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_ke
 #pragma unroll
       for (int j = 0; j < ITEMS; j++) {
         const int c = at + j * threads;
-        if (c >= nv) break;
+        if (c >= nc) break;
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          float4 v = make_float4(dw[j][4 * i], dw[j][4 * i + 1], dw[j][4 * i + 2], dw[j][4 * i + 3]);
+        for (int i = 0; i < 4; i++) {
+          const float2 lo = f2_unpack(dw[j][2 * i]), hi = f2_unpack(dw[j][2 * i + 1]);
+          float4 v = make_float4(lo.x, lo.y, hi.x, hi.y);
           if (g > 0) {
-            const float4 p = cols[c * 2 + i];
+            const float4 p = cols[c * 4 + i];
             v = make_float4(p.x + v.x, p.y + v.y, p.z + v.z, p.w + v.w);
           }
-          if (g == groups - 1) out[c * 2 + i] = v;
-          else cols[c * 2 + i] = v;
+          if (g == groups - 1) out[c * 4 + i] = v;
+          else cols[c * 4 + i] = v;
         }
       }
     }
@@ -572,31 +563,31 @@ int64_t glu_per_cta(int64_t items, int sm_count, int* grid) {
   return per;
 }
 
-// One wave: the CTAs that the registers of 1024 threads allow on every SM.
-int rms_grid(const RmsShape& f, int64_t M, int sm_count) {
+// One wave of CTAs that share an SM's registers: 512 threads of `regs` = 128, 1024 of 64.
+int rms_grid(const RmsShape& f, int64_t M, int sm_count, int threads_per_sm) {
   const int64_t ctas = (M + f.groups - 1) / f.groups;
-  const int64_t wave = (int64_t)sm_count * (kRmsThreads / (f.wpr * f.groups * 32));
+  const int64_t wave = (int64_t)sm_count * (threads_per_sm / (f.wpr * f.groups * 32));
   return (int)(ctas < wave ? ctas : wave);
 }
 
 template <int ITEMS>
 cudaError_t rms_forward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
-  return launch_pdl(rmsnorm_checkpoint_kernel<ITEMS>, dim3(rms_grid(f, a.M, sm_count)),
+  return launch_pdl(rmsnorm_checkpoint_kernel<ITEMS>, dim3(rms_grid(f, a.M, sm_count, ITEMS == 1 ? 1024 : 512)),
                     dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.x),
                     static_cast<const uint4*>(a.weight), a.M, (int32_t)a.N, a.eps, a.bias, f.wpr,
-                    f.groups, static_cast<uint4*>(a.y), static_cast<uint2*>(a.codes), a.scales,
+                    f.groups, static_cast<uint4*>(a.y), static_cast<uint4*>(a.codes), a.scales,
                     a.rstd, reinterpret_cast<uint32_t*>(a.amax));
 }
 
 template <int ITEMS>
 cudaError_t rms_backward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
-  int grid = rms_grid(f, a.M, sm_count);
+  int grid = rms_grid(f, a.M, sm_count, 512);
   if (grid > kRmsMaxPartials) grid = kRmsMaxPartials;
   const cudaError_t e = launch_pdl(
       a.residual ? rmsnorm_checkpoint_backward_kernel<ITEMS, true>
                  : rmsnorm_checkpoint_backward_kernel<ITEMS, false>,
       dim3(grid), dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.grad),
-      static_cast<const uint2*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
+      static_cast<const uint4*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
       a.M, (int32_t)a.N, a.bias, f.wpr, f.groups, static_cast<const uint4*>(a.residual),
       static_cast<uint4*>(a.grad_x), a.partial);
   if (e != cudaSuccess) return e;

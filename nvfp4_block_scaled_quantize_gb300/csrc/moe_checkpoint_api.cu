@@ -165,7 +165,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_swiglu_checkpoint(const void* h, int64_t M, int6
   const bool empty = M * F == 0;
   if (!empty && (h == nullptr || y == nullptr || codes == nullptr || scales == nullptr))
     return NVFP4_ERR_INVALID_ARG;
-  if ((!empty && (!aligned(h, 16) || !aligned(y, 16) || !aligned(codes, 16))) || !aligned(amax, 4))
+  if ((!empty && (!aligned(h, 32) || !aligned(y, 32) || !aligned(codes, 16))) || !aligned(amax, 4))
     return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;
@@ -187,7 +187,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_swiglu_checkpoint_backward(const void* grad_y,
   if (M * F == 0) return NVFP4_OK;
   if (grad_y == nullptr || codes == nullptr || scales == nullptr || grad_h == nullptr)
     return NVFP4_ERR_INVALID_ARG;
-  if (!aligned(grad_y, 16) || !aligned(codes, 16) || !aligned(grad_h, 16)) return NVFP4_ERR_ALIGN;
+  if (!aligned(grad_y, 32) || !aligned(codes, 16) || !aligned(grad_h, 32)) return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
@@ -209,7 +209,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_rmsnorm_checkpoint(const void* x, const void* we
   if (!empty && (x == nullptr || weight == nullptr || y == nullptr || codes == nullptr ||
                  scales == nullptr || rstd == nullptr))
     return NVFP4_ERR_INVALID_ARG;
-  if ((!empty && (!aligned(x, 16) || !aligned(weight, 16) || !aligned(y, 16) ||
+  if ((!empty && (!aligned(x, 32) || !aligned(weight, 32) || !aligned(y, 32) ||
                   !aligned(codes, 16) || !aligned(rstd, 4))) ||
       !aligned(amax, 4))
     return NVFP4_ERR_ALIGN;
@@ -248,8 +248,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_rmsnorm_checkpoint_backward(
                  weight == nullptr || grad_x == nullptr || workspace == nullptr ||
                  workspace_bytes < need))
     return NVFP4_ERR_INVALID_ARG;
-  if ((!empty && (!aligned(grad_y, 16) || !aligned(codes, 16) || !aligned(rstd, 4) ||
-                  !aligned(weight, 16) || !aligned(grad_residual, 16) || !aligned(grad_x, 16) ||
+  if ((!empty && (!aligned(grad_y, 32) || !aligned(codes, 16) || !aligned(rstd, 4) ||
+                  !aligned(weight, 32) || !aligned(grad_residual, 32) || !aligned(grad_x, 32) ||
                   !aligned(workspace, 16))) ||
       !aligned(grad_weight, 16))
     return NVFP4_ERR_ALIGN;
