@@ -47,7 +47,9 @@ int rmsnorm_rows_per_cta();
 
 // ---- token routing (moe_route.cu) ----
 constexpr int kMaxTopk = 32;  // choices of a token: one warp loads a token's rows
-// rows of `nv` 16-byte vectors; amax (zeroed by the caller) may be null
+// rows of `nv` 16-byte vectors; amax may be null, and the caller zeroes it unless
+// moe_dispatch_clears_amax(T)
+bool moe_dispatch_clears_amax(int64_t T);
 cudaError_t prepare_moe_kernels();
 cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
                             int32_t* slot_of_row, int32_t* offsets, uint32_t* status,

@@ -139,10 +139,14 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
   return pack_bf16(f.x, f.y);
 }
 
-// sigmoid(a) from exp(-|a|), which cannot overflow.
+// sigmoid(a) from t = exp(-|a|), which cannot overflow. t is the square of 2^(-|a| log2(e) / 2):
+// the approximate instruction flushes subnormal results, and the half exponent keeps t exact in
+// kind down to binary32's smallest subnormal for two instructions fewer than the unflushed one.
 __device__ __forceinline__ float sigmoid(float a) {
-  const float t = __expf(-fabsf(a));
-  const float r = __fdividef(1.0f, __fadd_rn(1.0f, t));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(fabsf(a), -0.72134752f)));
+  const float t = __fmul_rn(e, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, t)));
   return a >= 0.0f ? r : __fmul_rn(t, r);
 }
 
@@ -203,9 +207,14 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
   }
   __syncthreads();
   const int64_t nc = F / 16;
-  int expert = 0;
+  GluWalk it(M, nc, per_cta);
+  int expert = 0;  // of the thread's current row: the first whose end is past it, at most E - 1
+  for (int hi = E - 1; expert < hi;) {
+    const int mid = (expert + hi) >> 1;
+    if (ends[mid] > it.row) hi = mid; else expert = mid + 1;
+  }
   uint32_t m = 0u;
-  for (GluWalk it(M, nc, per_cta); it.left > 0; it.next()) {
+  for (; it.left > 0; it.next()) {
     const int64_t r = it.row, c = it.col;
     uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, kg[4] = {0u, 0u, 0u, 0u},
              ku[4] = {0u, 0u, 0u, 0u}, sg = 0u, su = 0u;
@@ -287,25 +296,30 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
 // ---- RMSNorm -----------------------------------------------------------------------------
 
 // A group of `wpr` warps owns a row, ITEMS x 16 columns a thread: the row is read once and stays in
-// registers between its sum and its output. A CTA holds as many groups as fit in 16 warps. With
-// ITEMS = 1 (rows up to 8192 columns) the registers also hold the weights and the group's next row,
-// which is loaded before the current one is summed, so that the SM's loads do not stop at the
-// barrier of the sum.
+// registers between its sum and its output. A CTA holds as many groups as fit in 16 warps.
 constexpr int kRmsWarps = 16;
 constexpr int kRmsThreads = 32 * kRmsWarps;
-
-constexpr int kMaxJointN = 4096;  // a CTA with more than one group has rows up to this
+constexpr int kMaxJointN = 4096;  // backward: a CTA with more than one group has rows up to this
 
 struct RmsShape {
   int wpr, groups, items;
 };
-RmsShape rms_shape(int64_t N) {
+RmsShape rms_shape(int64_t N, int items) {
   RmsShape s;
-  s.items = N <= 8192 ? 1 : (N <= 16384 ? 2 : 4);
-  const int64_t per_warp = 512 * s.items;
+  s.items = items;
+  const int64_t per_warp = 512 * items;
   s.wpr = (int)((N + per_warp - 1) / per_warp);
   s.groups = kRmsWarps / s.wpr;
   return s;
+}
+// Forward: as many columns a thread as the registers hold, so that few warps meet at a barrier (none
+// up to 4096 columns) and the sum's shuffles are spread over more columns.
+RmsShape rms_forward_shape(int64_t N) {
+  return rms_shape(N, N <= 512 ? 1 : (N <= 1024 ? 2 : 4));
+}
+// Backward: the weight gradient takes a register a column, so 16 columns a thread up to 8192.
+RmsShape rms_backward_shape(int64_t N) {
+  return rms_shape(N, N <= 8192 ? 1 : (N <= 16384 ? 2 : 4));
 }
 
 // Sum over the group's threads: shuffles, then the warps' sums through shared memory, in an order
@@ -334,6 +348,17 @@ __device__ __forceinline__ void biased_weight(const Half32& weight, float bias, 
   for (int i = 0; i < 8; i++) w[i] = f2_add(w[i], b2);
 }
 
+// Keeps the packed words in registers, not their widened values, from the sum to the output.
+template <int ITEMS>
+__device__ __forceinline__ void hold_packed(Half32 (&h)[ITEMS]) {
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++)
+#pragma unroll
+    for (int i = 0; i < 8; i++) asm volatile("" : "+r"(h[j].w[i]));
+}
+
+// Up to 1024 columns the registers also hold the group's next row, which is loaded before the
+// current one is summed.
 template <int ITEMS>
 __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_checkpoint_kernel(
     const uint4* __restrict__ x, const uint4* __restrict__ weight, int64_t M, int32_t N, float eps,
@@ -347,13 +372,14 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
   const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
   const int nc = N / 16;
   const int64_t step = (int64_t)gridDim.x * groups;
-  constexpr bool kAhead = ITEMS == 1;
+  constexpr bool kAhead = ITEMS <= 2;
   const float inv_n = 1.0f / (float)N;
   uint32_t m = 0u;
   int turn = 0;
-  int64_t r = (int64_t)blockIdx.x * groups + group;
+  // a CTA's groups take rows gridDim.x apart, so that a last partial round is spread over the SMs
+  int64_t r = (int64_t)blockIdx.x + (int64_t)group * gridDim.x;
   int64_t pos = r * nc + at;  // of the thread's first 16 columns, in units of 16
-  Half32 next[ITEMS], weights;
+  Half32 next[ITEMS];
   auto load = [&](int64_t p) {
 #pragma unroll
     for (int j = 0; j < ITEMS; j++)
@@ -363,10 +389,7 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
   for (int j = 0; j < ITEMS; j++)
 #pragma unroll
     for (int i = 0; i < 8; i++) next[j].w[i] = 0u;
-  if (kAhead) {
-    if (at < nc) weights = load_half(weight + 2 * at);
-    if (r < M) load(pos);
-  }
+  if (kAhead && r < M) load(pos);
   for (; r < M; r += step, pos += step * nc) {
     if (!kAhead) load(pos);
     Half32 w[ITEMS];
@@ -383,6 +406,7 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
     }
     const float sum = group_sum(s, red, turn, group, wpr);
     turn ^= 1;
+    hold_packed(w);
     const float rs = rsqrtf(__fmaf_rn(sum, inv_n, eps));
     const uint64_t rs2 = f2_pack(rs, rs);
     if (at == 0) rstd[r] = rs;
@@ -394,7 +418,7 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
       uint64_t v[8], g[8];
       uint32_t o[8], k[4], sc;
       unpack16(w[j], v);
-      biased_weight(kAhead ? weights : load_half(weight + 2 * c), bias, g);
+      biased_weight(load_half(weight + 2 * c), bias, g);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         o[i] = pack_bf16(f2_mul(g[i], f2_mul(v[i], rs2)));
@@ -418,7 +442,9 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
 // With xh = x * rstd and g = (w + bias) dy: dx = rstd (g - xh mean(g xh)) [+ residual], and
 // dw = sum over rows of dy xh. A thread keeps its columns' share of dw over all of its rows; the
 // groups of a CTA are added in shared memory in order and each CTA writes one row of `partial`, so
-// that the sum's order depends on the grid alone.
+// that the sum's order depends on the grid alone. Up to 8192 columns the registers also hold the
+// weights and the group's next row, which is loaded before the current one is summed, so that the
+// SM's loads do not stop at the barrier of the sum.
 template <int ITEMS, bool RES>
 __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_kernel(
     const uint4* __restrict__ grad, const uint4* __restrict__ codes,
@@ -619,14 +645,14 @@ cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* code
 }
 
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const RmsShape f = rms_shape(a.N);
+  const RmsShape f = rms_forward_shape(a.N);
   if (f.items == 1) return rms_forward_t<1>(a, f, sm_count, s);
   if (f.items == 2) return rms_forward_t<2>(a, f, sm_count, s);
   return rms_forward_t<4>(a, f, sm_count, s);
 }
 
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const RmsShape f = rms_shape(a.N);
+  const RmsShape f = rms_backward_shape(a.N);
   if (f.items == 1) return rms_backward_t<1>(a, f, sm_count, s);
   if (f.items == 2) return rms_backward_t<2>(a, f, sm_count, s);
   return rms_backward_t<4>(a, f, sm_count, s);

@@ -92,7 +92,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* row_o
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = zero(amax, 4 * (size_t)E, s);
+  const cudaError_t e =
+      !empty && moe_dispatch_clears_amax(T) ? cudaSuccess : zero(amax, 4 * (size_t)E, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
   return cuda_status(launch_moe_dispatch(x, row_of_slot, offsets, T, K, E, H / 8, packed, amax,
                                          status, sms, s));

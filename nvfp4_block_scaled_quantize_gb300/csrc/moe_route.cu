@@ -15,7 +15,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanMaxCtas = 16;  // one cluster of the opt-in size
+constexpr int kPlanMaxRun = 832;  // slots of a warp's run that is sorted in shared memory
 constexpr int kPlanBatch = 8;  // groups of 32 slots whose ids a warp loads together
 constexpr int kRouteThreads = 128;
 constexpr uint32_t kBadRoute = 0x4u;  // NVFP4_DEVICE_BAD_ROUTE
@@ -27,24 +28,42 @@ constexpr uint32_t kBadRoute = 0x4u;  // NVFP4_DEVICE_BAD_ROUTE
 // distributed shared memory, and the exclusive prefix (expert, CTA, warp) is the row of the first
 // slot of that expert in that run; a second walk over the run hands the rows out in slot order.
 // So the order is that of a stable sort, whatever the timing.
-template <typename Id>
+//
+// Rows of one expert in one run are consecutive. STAGED: the warp sorts its run in shared memory
+// and writes slot_of_row in row order, so that a store instruction touches a few sectors instead
+// of 32 scattered ones.
+
+// Expert e's word of a warp's counters: padded so that lanes 8 experts apart meet no bank twice.
+__device__ __forceinline__ int plan_word(int e) { return e + (e >> 3); }
+constexpr int kPlanWords = kMaxSegments + kMaxSegments / 8;
+
+template <typename Id, bool STAGED>
 __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(
     const Id* __restrict__ ids, int32_t n, int32_t run, int32_t E, int32_t* row_of_slot,
     int32_t* slot_of_row, int32_t* offsets, uint32_t* status) {
   namespace cg = cooperative_groups;
-  __shared__ uint32_t hist[kPlanWarps][kMaxSegments];
-  __shared__ uint32_t total[kMaxSegments];
+  extern __shared__ uint32_t plan_smem[];
+  __shared__ uint32_t total[kMaxSegments], base[kPlanWords];
   __shared__ uint32_t scan[kMaxSegments / 32];
   __shared__ uint32_t live;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kPlanWarps * kMaxSegments; i += kPlanThreads) (&hist[0][0])[i] = 0;
+  const int threads = blockDim.x, warps = threads / 32;
+  // per warp and expert: next position in the run's order (STAGED) or next row, and what turns the
+  // first into the second
+  uint32_t* const all_next = plan_smem;
+  uint32_t* const all_shift = plan_smem + warps * kPlanWords;
+  uint32_t* const next = all_next + warp * kPlanWords;
+  uint32_t* const shift = all_shift + warp * kPlanWords;
+  uint32_t* const peers_of = plan_smem + (2 * warps + warp) * kPlanWords;
+  uint32_t* const sorted = plan_smem + 3 * warps * kPlanWords + (size_t)warp * run;
+  for (int i = tid; i < 3 * warps * kPlanWords; i += threads) plan_smem[i] = 0;
   __syncthreads();
   pdl_wait();
   pdl_allow_next();
 
-  const int64_t first = ((int64_t)rank * kPlanWarps + warp) * run;
+  const int64_t first = ((int64_t)rank * warps + warp) * run;
   const int32_t begin = (int32_t)(first < n ? first : n);
   const int32_t end = n - begin < run ? n : begin + run;
   bool bad = false;
@@ -58,28 +77,28 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(
 #pragma unroll
     for (int j = 0; j < kPlanBatch; j++) {
       if (id[j] >= 0 && id[j] < E)
-        atomicAdd(&hist[warp][(int)id[j]], 1u);
+        atomicAdd(&next[plan_word((int)id[j])], 1u);
       else if (id[j] >= E)
         bad = true;
     }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(status, kBadRoute);
   __syncthreads();
-  if (tid < kMaxSegments) {  // counts -> exclusive prefixes over this CTA's warps
+  if (tid < kMaxSegments) {  // exclusive prefixes of the counts over this CTA's warps
     uint32_t sum = 0;
 #pragma unroll 8
-    for (int w = 0; w < kPlanWarps; w++) {
-      const uint32_t c = hist[w][tid];
-      hist[w][tid] = sum;
-      sum += c;
+    for (int w = 0; w < warps; w++) {
+      all_shift[w * kPlanWords + plan_word(tid)] = sum;
+      sum += all_next[w * kPlanWords + plan_word(tid)];
     }
     total[tid] = sum;
   }
   cluster.sync();
   uint32_t before = 0, all = 0, incl = 0;
   if (tid < kMaxSegments) {
-    for (int c = 0; c < ctas; c++) {
-      const uint32_t v = cluster.map_shared_rank(total, c)[tid];
+#pragma unroll
+    for (int c = 0; c < kPlanMaxCtas; c++) {
+      const uint32_t v = c < ctas ? cluster.map_shared_rank(total, c)[tid] : 0u;
       if (c < rank) before += v;
       all += v;
     }
@@ -91,74 +110,115 @@ __global__ void __launch_bounds__(kPlanThreads) moe_plan_kernel(
     }
     if (lane == 31) scan[warp] = incl;
   }
-  __syncthreads();
+  cluster.sync();  // also: every CTA has read the others' totals, so none may have ended
   if (tid < kMaxSegments) {
     for (int w = 0; w < warp; w++) incl += scan[w];
     if (rank == 0 && tid < E) offsets[tid] = (int32_t)incl;
     if (tid == kMaxSegments - 1) live = incl;
-    const uint32_t base = incl - all + before;
-#pragma unroll 8
-    for (int w = 0; w < kPlanWarps; w++) hist[w][tid] += base;
+    base[plan_word(tid)] = incl - all + before;
   }
   __syncthreads();
-  // the same number of steps for every lane: the match below takes the whole warp
+  uint32_t placed = 0;  // STAGED: the run's held slots
+  if (STAGED) {         // counts -> exclusive prefixes over the experts; shift = row - position
+    constexpr int kEach = kMaxSegments / 32;
+    uint32_t c[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      c[i] = next[plan_word(lane * kEach + i)];
+      sum += c[i];
+    }
+    uint32_t to = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, to, o);
+      if (lane >= o) to += v;
+    }
+    placed = __shfl_sync(0xFFFFFFFFu, to, 31);
+    to -= sum;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+      next[plan_word(lane * kEach + i)] = to;
+      shift[plan_word(lane * kEach + i)] += base[plan_word(lane * kEach + i)] - to;
+      to += c[i];
+    }
+  } else {
+    for (int e = lane; e < kMaxSegments; e += 32)
+      next[plan_word(e)] = shift[plan_word(e)] + base[plan_word(e)];
+  }
+  __syncwarp();
+  // Slots that share an expert find each other through a word of shared memory for the expert, one
+  // bit a lane (__match_any_sync takes a step for each distinct expert, and a ballot for each bit
+  // of the expert about 75 instructions).
   for (int32_t s0 = begin; s0 < end; s0 += 32 * kPlanBatch) {
     int32_t e[kPlanBatch];
 #pragma unroll
     for (int j = 0; j < kPlanBatch; j++) {
       const int32_t s = s0 + 32 * j + lane;
       const Id id = s < end ? ids[s] : (Id)-1;
-      e[j] = id >= 0 && id < E ? (int32_t)id : -1;
+      e[j] = id >= 0 && id < E ? plan_word((int32_t)id) : -1;
     }
 #pragma unroll
     for (int j = 0; j < kPlanBatch; j++) {
       const int32_t s = s0 + 32 * j + lane;
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, e[j]);
-      const int before_me = __popc(peers & ((1u << lane) - 1u));
-      int32_t row = -1;
-      if (e[j] >= 0) row = (int32_t)(hist[warp][e[j]] + before_me);
+      if (s0 + 32 * j >= end) break;
+      if (e[j] >= 0) atomicOr(&peers_of[e[j]], 1u << lane);
       __syncwarp();
-      if (e[j] >= 0 && before_me == 0) hist[warp][e[j]] += __popc(peers);
+      uint32_t peers = 0, at = 0;
+      if (e[j] >= 0) {
+        peers = peers_of[e[j]];
+        at = next[e[j]] + __popc(peers & ((1u << lane) - 1u));
+      }
+      __syncwarp();
+      if (e[j] >= 0 && (peers >> lane) == 1u) {  // the expert's last lane
+        next[e[j]] = at + 1;
+        peers_of[e[j]] = 0;
+      }
       __syncwarp();
       if (s < end) {
+        int32_t row = -1;
+        if (e[j] >= 0) {
+          row = (int32_t)(STAGED ? at + shift[e[j]] : at);
+          if (STAGED) sorted[at] = ((uint32_t)(s - begin) << 9) | (uint32_t)e[j];
+          else slot_of_row[row] = s;
+        }
         row_of_slot[s] = row;
-        if (row >= 0) slot_of_row[row] = s;
       }
     }
   }
-  for (int64_t r = (int64_t)live + rank * kPlanThreads + tid; r < n;
-       r += (int64_t)ctas * kPlanThreads)
+  if (STAGED) {
+    __syncwarp();
+    for (uint32_t i = lane; i < placed; i += 32) {
+      const uint32_t v = sorted[i];
+      slot_of_row[i + shift[v & 511u]] = begin + (int32_t)(v >> 9);
+    }
+  }
+  for (int64_t r = (int64_t)live + rank * threads + tid; r < n; r += (int64_t)ctas * threads)
     slot_of_row[r] = -1;
-  cluster.sync();  // `total` stays until every CTA has read it
 }
 
 // ---- rows of a token ---------------------------------------------------------------------
 
-// The token's rows that are held, in the order of its choices; whole CTA calls it, warp 0 works.
+// A warp owns a token (or a range of its row's vectors): lane i holds the token's i-th held row and
+// that slot's choice, in the order of the choices.
 struct TokenRows {
-  int32_t row[kMaxTopk];
-  int32_t slot[kMaxTopk];
-  int32_t count;
+  int32_t row, slot;
+  int count;
 };
 
-__device__ __forceinline__ void load_token_rows(TokenRows& r, const int32_t* row_of_slot,
-                                                int64_t token, int32_t K, int64_t P,
-                                                uint32_t* status) {
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int32_t row = lane < K ? row_of_slot[token * K + lane] : -1;
-    if (row >= P) {
-      atomicOr(status, kBadRoute);
-      row = -1;
-    }
-    const uint32_t held = __ballot_sync(0xFFFFFFFFu, row >= 0);
-    if (row >= 0) {
-      const int at = __popc(held & ((1u << lane) - 1u));
-      r.row[at] = row;
-      r.slot[at] = lane;
-    }
-    if (lane == 0) r.count = __popc(held);
+__device__ __forceinline__ TokenRows load_token_rows(const int32_t* row_of_slot, int64_t token,
+                                                     int32_t K, int64_t P, int2 (*scratch)[32],
+                                                     uint32_t* status) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int32_t row = lane < K ? row_of_slot[token * K + lane] : -1;
+  if (row >= P) {
+    atomicOr(status, kBadRoute);
+    row = -1;
   }
+  const uint32_t held = __ballot_sync(0xFFFFFFFFu, row >= 0);
+  if (row >= 0) scratch[warp][__popc(held & ((1u << lane) - 1u))] = make_int2(row, lane);
+  __syncwarp();
+  const int2 v = scratch[warp][lane];
+  return {v.x, v.y, __popc(held)};
 }
 
 __device__ __forceinline__ int64_t live_rows(const int32_t* offsets, int32_t E, int64_t P) {
@@ -166,177 +226,243 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* offsets, int32_t E, 
   return v < 0 ? 0 : (v < P ? v : P);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  const float2 f = f2_unpack(v);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 // ---- dispatch ----------------------------------------------------------------------------
 
-// grid.x: tokens, grid.y: ranges of `span` 16-byte vectors of a row.
-__global__ void __launch_bounds__(kRouteThreads) moe_dispatch_kernel(
+// `tw` warps (a power of two) per token, neighbouring ones taking neighbouring 32 vectors of its
+// row; a CTA holds its warps / tw tokens. The token's maximum is joined in shared memory, so that
+// it costs one atomic for each of its experts. ONE: the grid is one cluster, which joins the
+// experts' maxima in its first CTA's shared memory and writes all of amax itself, so that a small
+// call needs no clearing of amax before it.
+constexpr int kCopyBatch = 4;  // vectors a lane holds between their load and their K stores
+constexpr int kCopyMaxWarps = 32;
+constexpr int64_t kOneClusterTokens = 16;  // 8 CTAs of two tokens, 16 warps each
+template <bool ONE>
+__global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ row_of_slot,
-    const int32_t* __restrict__ offsets, int32_t K, int32_t E, int64_t nv, int64_t span,
+    const int32_t* __restrict__ offsets, int64_t T, int32_t K, int32_t E, int64_t nv, int tw,
     uint4* packed, uint32_t* amax, uint32_t* status) {
-  __shared__ TokenRows rows;
+  namespace cg = cooperative_groups;
+  __shared__ int2 scratch[kCopyMaxWarps][32];
   __shared__ int32_t ends[kMaxSegments];
-  __shared__ uint32_t red[kRouteThreads / 32];
+  __shared__ uint32_t top[kCopyMaxWarps], joint[ONE ? kMaxSegments : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int mine = warp / tw, sub = warp - mine * tw;  // the CTA's token, the warp's part of it
+  if (lane == 0) top[warp] = 0u;
+  if (ONE)
+    for (int e = tid; e < kMaxSegments; e += blockDim.x) joint[e] = 0u;
   pdl_wait();
   pdl_allow_next();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t token = blockIdx.x, P = (int64_t)gridDim.x * K;
-  const int64_t v0 = (int64_t)blockIdx.y * span, v1 = v0 + span < nv ? v0 + span : nv;
-  load_token_rows(rows, row_of_slot, token, K, P, status);
-  for (int e = tid; e < E; e += kRouteThreads) ends[e] = offsets[e];
-  __syncthreads();
-  const int count = rows.count;
-  uint32_t m = 0;
-  for (int64_t v = v0 + tid; v < v1; v += kRouteThreads) {
-    const uint4 q = x[token * nv + v];
-    m = vmax2(m, vmax2(vmax2(abs2(q.x), abs2(q.y)), vmax2(abs2(q.z), abs2(q.w))));
-    for (int k = 0; k < count; k++) packed[rows.row[k] * nv + v] = q;
+  const int64_t token = (int64_t)blockIdx.x * (blockDim.x / 32 / tw) + mine, P = T * K;
+  for (int e = tid; e < E; e += blockDim.x) ends[e] = offsets[e];
+  if (ONE) cg::this_cluster().sync();
+  else __syncthreads();
+  TokenRows rows = {0, 0, 0};
+  if (token < T) {
+    rows = load_token_rows(row_of_slot, token, K, P, scratch, status);
+    uint32_t m = 0;
+    for (int64_t at = sub * 32; at < nv; at += 32 * tw * kCopyBatch) {  // every lane: shuffles
+      const int64_t v = at + lane;
+      uint4 q[kCopyBatch];
+#pragma unroll
+      for (int j = 0; j < kCopyBatch; j++)
+        q[j] = v + 32 * tw * j < nv ? __ldg(x + token * nv + v + 32 * tw * j)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int j = 0; j < kCopyBatch; j++)
+        m = vmax2(m, vmax2(vmax2(abs2(q[j].x), abs2(q[j].y)), vmax2(abs2(q[j].z), abs2(q[j].w))));
+      for (int k = 0; k < rows.count; k++) {
+        uint4* to = packed + __shfl_sync(0xFFFFFFFFu, rows.row, k) * nv + v;
+#pragma unroll
+        for (int j = 0; j < kCopyBatch; j++)
+          if (v + 32 * tw * j < nv) to[32 * tw * j] = q[j];
+      }
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if (lane == 0 && m != 0u) atomicMax(&top[mine], m);
   }
-  m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-  if (lane == 0) red[warp] = m;
   __syncthreads();
-  if (amax != nullptr && tid < count) {
-    for (int w = 0; w < kRouteThreads / 32; w++) m = max(m, red[w]);
-    const int32_t row = rows.row[tid];
+  if (amax != nullptr && sub == 0 && lane < rows.count) {
     int lo = 0, hi = E;  // the expert of the row: the first whose end is past it
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (ends[mid] > row) hi = mid; else lo = mid + 1;
+      if (ends[mid] > rows.row) hi = mid; else lo = mid + 1;
     }
-    if (lo < E) atomicMax(amax + lo, m << 16);
+    const uint32_t m = top[mine] << 16;
+    if (lo < E) atomicMax(ONE ? cg::this_cluster().map_shared_rank(joint, 0) + lo : amax + lo, m);
   }
-  int64_t live = ends[E - 1];
-  live = live < 0 ? 0 : live;
-  for (int64_t r = live + token; r < P; r += gridDim.x)
-    for (int64_t v = v0 + tid; v < v1; v += kRouteThreads)
-      packed[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+  const int64_t live = ends[E - 1] < 0 ? 0 : ends[E - 1];
+  if (token < T)
+    for (int64_t r = live + token; r < P; r += T)
+      for (int64_t v = sub * 32 + lane; v < nv; v += 32 * tw)
+        packed[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+  if (ONE) {
+    cg::this_cluster().sync();
+    if (amax != nullptr && blockIdx.x == 0)
+      for (int e = tid; e < E; e += blockDim.x) amax[e] = joint[e];
+  }
 }
 
 // ---- combine and the gradient of dispatch ------------------------------------------------
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-// out[t] = sum over the token's held rows of w * y[row], in the order of its choices, in binary32.
-template <bool WEIGHTED>
+// out[t] = sum over the token's held rows of w * y[row], in the order of its choices, in binary32;
+// a warp per token and range of its row. A lane has 8 loads in flight: VECS vectors of 8 / VECS rows.
+template <bool WEIGHTED, int VECS>
 __global__ void __launch_bounds__(kRouteThreads) moe_gather_sum_kernel(
     const uint4* __restrict__ y, const float* __restrict__ weights,
-    const int32_t* __restrict__ row_of_slot, int32_t K, int64_t nv, int64_t span, uint4* out,
-    uint32_t* status) {
-  __shared__ TokenRows rows;
+    const int32_t* __restrict__ row_of_slot, int64_t T, int32_t K, int64_t nv, int64_t span,
+    uint4* out, uint32_t* status) {
+  __shared__ int2 scratch[kRouteThreads / 32][32];
   pdl_wait();
   pdl_allow_next();
-  const int64_t token = blockIdx.x, P = (int64_t)gridDim.x * K;
+  const int lane = threadIdx.x & 31;
+  const int64_t token = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5), P = T * K;
+  if (token >= T) return;
+  const TokenRows rows = load_token_rows(row_of_slot, token, K, P, scratch, status);
+  const float weight = WEIGHTED && lane < rows.count ? weights[token * K + rows.slot] : 0.0f;
   const int64_t v0 = (int64_t)blockIdx.y * span, v1 = v0 + span < nv ? v0 + span : nv;
-  load_token_rows(rows, row_of_slot, token, K, P, status);
-  __syncthreads();
-  const int count = rows.count;
-  for (int64_t v = v0 + threadIdx.x; v < v1; v += kRouteThreads) {
-    float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int k = 0; k < count; k++) {
-      const uint4 q = y[rows.row[k] * nv + v];
-      const uint32_t e[4] = {q.x, q.y, q.z, q.w};
-      const float w = WEIGHTED ? weights[token * K + rows.slot[k]] : 1.0f;
+  constexpr int kRows = 8 / VECS;
+  for (int64_t at = v0; at < v1; at += 32 * VECS) {  // every lane, for the shuffles
+    const int64_t v = at + lane;
+    uint64_t acc[VECS][4];
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        acc[2 * i] = __fmaf_rn(w, bf16_lo(e[i]), acc[2 * i]);
-        acc[2 * i + 1] = __fmaf_rn(w, bf16_hi(e[i]), acc[2 * i + 1]);
+    for (int u = 0; u < VECS; u++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[u][i] = f2_pack(0.0f, 0.0f);
+    for (int k0 = 0; k0 < rows.count; k0 += kRows) {
+      uint4 q[kRows][VECS];
+#pragma unroll
+      for (int j = 0; j < kRows; j++) {
+        const int32_t row = __shfl_sync(0xFFFFFFFFu, rows.row, k0 + j);
+#pragma unroll
+        for (int u = 0; u < VECS; u++)
+          q[j][u] = k0 + j < rows.count && v + 32 * u < v1 ? __ldg(y + row * nv + v + 32 * u)
+                                                           : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int j = 0; j < kRows; j++) {
+        if (k0 + j < rows.count) {
+          const float w = WEIGHTED ? __shfl_sync(0xFFFFFFFFu, weight, k0 + j) : 1.0f;
+          const uint64_t w2 = f2_pack(w, w);
+#pragma unroll
+          for (int u = 0; u < VECS; u++) {
+            const uint32_t e[4] = {q[j][u].x, q[j][u].y, q[j][u].z, q[j][u].w};
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              acc[u][i] = WEIGHTED ? f2_fma(w2, f2_from_bf16x2(e[i]), acc[u][i])
+                                   : f2_add(f2_from_bf16x2(e[i]), acc[u][i]);
+          }
+        }
       }
     }
-    out[token * nv + v] = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
-                                     pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+#pragma unroll
+    for (int u = 0; u < VECS; u++)
+      if (v + 32 * u < v1)
+        out[token * nv + v + 32 * u] =
+            make_uint4(pack_bf16(acc[u][0]), pack_bf16(acc[u][1]), pack_bf16(acc[u][2]),
+                       pack_bf16(acc[u][3]));
   }
 }
 
 // ---- the gradient of combine -------------------------------------------------------------
 
-// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: one CTA per token, kGroup of
-// its rows at a time; rows past the last expert's end become zero.
-constexpr int kGroup = 8;
-__global__ void __launch_bounds__(kRouteThreads) moe_combine_backward_kernel(
+// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: a warp per slot, so that the
+// product needs no sum across warps; the warps of a CTA mostly share a token, whose gradient row
+// then comes from L1. Slot i also clears row i when it lies past the last expert's end.
+constexpr int kSlotThreads = 256;
+constexpr int kDotBatch = 4;
+__global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(
     const uint4* __restrict__ grad, const uint4* __restrict__ y, const float* __restrict__ weights,
-    const int32_t* __restrict__ row_of_slot, const int32_t* __restrict__ offsets, int32_t K,
-    int32_t E, int64_t nv, uint4* grad_y, float* grad_w, uint32_t* status) {
-  __shared__ TokenRows rows;
-  __shared__ float red[kRouteThreads / 32][kGroup];
+    const int32_t* __restrict__ row_of_slot, const int32_t* __restrict__ offsets, int64_t T,
+    int32_t K, int32_t E, int64_t nv, uint4* grad_y, float* grad_w, uint32_t* status) {
   pdl_wait();
   pdl_allow_next();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t token = blockIdx.x, P = (int64_t)gridDim.x * K;
-  load_token_rows(rows, row_of_slot, token, K, P, status);
-  if (tid < K) grad_w[token * K + tid] = 0.0f;  // the dropped slots keep it
-  __syncthreads();
-  const int count = rows.count;
-  for (int k0 = 0; k0 < count; k0 += kGroup) {
-    float dot[kGroup], w[kGroup];
+  const int lane = threadIdx.x & 31;
+  const int64_t P = T * K;
+  const int64_t slot = (int64_t)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5);
+  if (slot >= P) return;
+  const int64_t token = (uint32_t)slot / (uint32_t)K;
+  int64_t row = row_of_slot[slot];
+  if (row >= P) {
+    if (lane == 0) atomicOr(status, kBadRoute);
+    row = -1;
+  }
+  float dot = 0.0f;
+  if (row >= 0) {
+    const float w = weights[slot];
+    const uint64_t w2 = f2_pack(w, w);
+    uint64_t s = f2_pack(0.0f, 0.0f);
+    const uint4 *g = grad + token * nv, *from = y + row * nv;
+    uint4* to = grad_y + row * nv;
+    for (int64_t v = lane; v < nv; v += 32 * kDotBatch) {
+      uint4 a[kDotBatch], b[kDotBatch];
 #pragma unroll
-    for (int j = 0; j < kGroup; j++) {
-      dot[j] = 0.0f;
-      w[j] = k0 + j < count ? weights[token * K + rows.slot[k0 + j]] : 0.0f;
-    }
-    for (int64_t v = tid; v < nv; v += kRouteThreads) {
-      const uint4 g = grad[token * nv + v];
-      const uint32_t ge[4] = {g.x, g.y, g.z, g.w};
+      for (int j = 0; j < kDotBatch; j++) {
+        const bool in = v + 32 * j < nv;
+        b[j] = in ? __ldg(from + v + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+        a[j] = in ? __ldg(g + v + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
+      }
 #pragma unroll
-      for (int j = 0; j < kGroup; j++) {
-        if (k0 + j < count) {
-          const int64_t at = rows.row[k0 + j] * nv + v;
-          const uint4 q = y[at];
-          const uint32_t qe[4] = {q.x, q.y, q.z, q.w};
-          uint32_t o[4];
+      for (int j = 0; j < kDotBatch; j++) {
+        const uint32_t ae[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+        const uint32_t be[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+        uint32_t o[4];
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            dot[j] = __fmaf_rn(bf16_lo(ge[i]), bf16_lo(qe[i]), dot[j]);
-            dot[j] = __fmaf_rn(bf16_hi(ge[i]), bf16_hi(qe[i]), dot[j]);
-            o[i] = pack_bf16(__fmul_rn(w[j], bf16_lo(ge[i])), __fmul_rn(w[j], bf16_hi(ge[i])));
-          }
-          grad_y[at] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 4; i++) {
+          const uint64_t d = f2_from_bf16x2(ae[i]);
+          s = f2_fma(d, f2_from_bf16x2(be[i]), s);
+          o[i] = pack_bf16(f2_mul(w2, d));
         }
+        if (v + 32 * j < nv) to[v + 32 * j] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-#pragma unroll
-    for (int j = 0; j < kGroup; j++) {
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-      if (lane == 0) red[warp][j] = dot[j];
-    }
-    __syncthreads();
-    if (tid < kGroup && k0 + tid < count) {
-      float s = red[0][tid];
-      for (int i = 1; i < kRouteThreads / 32; i++) s += red[i][tid];
-      grad_w[token * K + rows.slot[k0 + tid]] = s;
-    }
-    __syncthreads();
+    const float2 f = f2_unpack(s);
+    dot = __fadd_rn(f.x, f.y);
   }
-  for (int64_t r = live_rows(offsets, E, P) + token; r < P; r += gridDim.x)
-    for (int64_t v = tid; v < nv; v += kRouteThreads)
-      grad_y[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  if (lane == 0) grad_w[slot] = dot;
+  if (slot >= live_rows(offsets, E, P))
+    for (int64_t v = lane; v < nv; v += 32) grad_y[slot * nv + v] = make_uint4(0u, 0u, 0u, 0u);
 }
 
 }  // namespace
 
+constexpr int plan_smem_bytes(int warps, int32_t run, bool staged) {
+  return 4 * (3 * warps * kPlanWords + (staged ? warps * run : 0));
+}
+
+template <typename Id, bool STAGED>
+static cudaError_t prepare_plan() {
+  const void* f = reinterpret_cast<const void*>(moe_plan_kernel<Id, STAGED>);
+  const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              plan_smem_bytes(kPlanThreads / 32, kPlanMaxRun, STAGED));
+}
+
 cudaError_t prepare_moe_kernels() {
   cudaError_t e = cudaSuccess, r;
-  if ((r = cudaFuncSetAttribute(moe_plan_kernel<int32_t>,
-                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-    e = r;
-  if ((r = cudaFuncSetAttribute(moe_plan_kernel<int64_t>,
-                                cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-    e = r;
+  if ((r = prepare_plan<int32_t, false>()) != cudaSuccess) e = r;
+  if ((r = prepare_plan<int32_t, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_plan<int64_t, false>()) != cudaSuccess) e = r;
+  if ((r = prepare_plan<int64_t, true>()) != cudaSuccess) e = r;
   return e;
 }
 
-cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
-                            int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
-                            cudaStream_t s) {
-  const int ctas = n <= 4096 ? 1 : 16;
-  const int64_t warps = (int64_t)ctas * kPlanWarps;
-  const int32_t run = (int32_t)((n + warps * 32 - 1) / (warps * 32) * 32);
+// A launch of one cluster (the grid is the cluster) with programmatic dependent launch.
+template <typename... KernelArgs, typename... Args>
+static cudaError_t launch_cluster(void (*kernel)(KernelArgs...), int ctas, int threads, size_t smem,
+                                  cudaStream_t s, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPlanThreads);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -347,45 +473,100 @@ cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, in
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (wide)
-    return cudaLaunchKernelEx(&cfg, moe_plan_kernel<int64_t>, static_cast<const int64_t*>(ids), n,
-                              run, E, row_of_slot, slot_of_row, offsets, status);
-  return cudaLaunchKernelEx(&cfg, moe_plan_kernel<int32_t>, static_cast<const int32_t*>(ids), n,
-                            run, E, row_of_slot, slot_of_row, offsets, status);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
-// Ranges of a row: whole rows when there are tokens enough for every SM, else 128 vectors each.
-static int64_t row_span(int64_t tokens, int64_t nv, int sm_count) {
-  return tokens >= 4 * (int64_t)sm_count ? nv : kRouteThreads;
+template <typename Id>
+static cudaError_t launch_plan(const void* ids, int32_t n, int32_t E, int32_t* row_of_slot,
+                               int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
+                               cudaStream_t s) {
+  // one CTA against the cluster, 256 threads: 4.1 and 4.2 us at 1024 slots, 5.1 and 4.4 at 2048;
+  // the cluster with 256 and with 1024 threads: 5.0 and 6.3 us at 16384
+  const int threads = n <= 16384 ? kMaxSegments : kPlanThreads, ctas = n <= 1024 ? 1 : kPlanMaxCtas;
+  const int warps = threads / 32;
+  const int64_t lanes = (int64_t)ctas * threads;
+  const int32_t run = (int32_t)((n + lanes - 1) / lanes * 32);
+  // sorted in shared memory against scattered stores: 14.1 and 17.3 us at 262144 slots of 64 experts
+  // (eight slots an expert in a run), 17.7 and 17.3 us with 256 experts (two)
+  const bool staged = ctas > 1 && run >= 4 * E && run <= kPlanMaxRun;
+  return launch_cluster(staged ? moe_plan_kernel<Id, true> : moe_plan_kernel<Id, false>, ctas,
+                        threads, plan_smem_bytes(warps, run, staged), s,
+                        static_cast<const Id*>(ids), n, run, E, row_of_slot, slot_of_row, offsets,
+                        status);
 }
+
+cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
+                            int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
+                            cudaStream_t s) {
+  return wide ? launch_plan<int64_t>(ids, n, E, row_of_slot, slot_of_row, offsets, status, s)
+              : launch_plan<int32_t>(ids, n, E, row_of_slot, slot_of_row, offsets, status, s);
+}
+
+// Grid of a warp per token and range of its row: whole rows when the tokens alone give every SM
+// about 64 warps, else ranges of at least 32 vectors.
+static dim3 token_grid(int64_t tokens, int64_t nv, int sm_count, int64_t* span) {
+  const int64_t want = (int64_t)sm_count * 64;
+  int64_t ranges = (want + tokens - 1) / tokens;
+  const int64_t most = (nv + 31) / 32;
+  if (ranges > most) ranges = most;
+  *span = ((nv + ranges - 1) / ranges + 31) / 32 * 32;
+  constexpr int kTokens = kRouteThreads / 32;
+  return dim3((unsigned)((tokens + kTokens - 1) / kTokens), (unsigned)((nv + *span - 1) / *span));
+}
+
+bool moe_dispatch_clears_amax(int64_t T) { return T <= kOneClusterTokens; }
 
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
                                 int64_t T, int32_t K, int32_t E, int64_t nv, void* packed,
                                 float* amax, uint32_t* status, int sm_count, cudaStream_t s) {
-  const int64_t span = row_span(T, nv, sm_count);
-  return launch_pdl(moe_dispatch_kernel, dim3((unsigned)T, (unsigned)((nv + span - 1) / span)),
-                    dim3(kRouteThreads), 0, s, static_cast<const uint4*>(x), row_of_slot, offsets,
-                    K, E, nv, span, static_cast<uint4*>(packed),
-                    reinterpret_cast<uint32_t*>(amax), status);
+  // warps per token: about 64 for every SM in all, no more than the row has vectors for
+  const int64_t want = (int64_t)sm_count * 64;
+  int tw = 1;
+  while (tw < 16 && tw * 32 < nv && T * tw < want) tw *= 2;
+  const bool one = moe_dispatch_clears_amax(T);
+  if (one) {
+    const int ctas = (int)(T < 8 ? T : 8), tokens = (int)((T + ctas - 1) / ctas);
+    return launch_cluster(moe_dispatch_kernel<true>, ctas, 32 * tw * tokens, 0, s,
+                          static_cast<const uint4*>(x), row_of_slot, offsets, T, K, E, nv, tw,
+                          static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax), status);
+  }
+  const int warps = tw < 4 ? 4 : tw;
+  const int64_t tokens = warps / tw;
+  return launch_pdl(moe_dispatch_kernel<false>, dim3((unsigned)((T + tokens - 1) / tokens)),
+                    dim3(32 * warps), 0, s, static_cast<const uint4*>(x), row_of_slot, offsets, T,
+                    K, E, nv, tw, static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax),
+                    status);
+}
+
+template <int VECS>
+static cudaError_t launch_gather(const void* y, const float* weights, const int32_t* row_of_slot,
+                                 int64_t T, int32_t K, int64_t nv, void* out, uint32_t* status,
+                                 int sm_count, cudaStream_t s) {
+  int64_t span = 0;
+  const dim3 grid = token_grid(T, nv, sm_count, &span);
+  return launch_pdl(
+      weights ? moe_gather_sum_kernel<true, VECS> : moe_gather_sum_kernel<false, VECS>, grid,
+      dim3(kRouteThreads), 0, s, static_cast<const uint4*>(y), weights, row_of_slot, T, K, nv, span,
+      static_cast<uint4*>(out), status);
 }
 
 cudaError_t launch_moe_gather_sum(const void* y, const float* weights, const int32_t* row_of_slot,
                                   int64_t T, int32_t K, int64_t nv, void* out, uint32_t* status,
                                   int sm_count, cudaStream_t s) {
-  const int64_t span = row_span(T, nv, sm_count);
-  const dim3 grid((unsigned)T, (unsigned)((nv + span - 1) / span));
-  return launch_pdl(weights ? moe_gather_sum_kernel<true> : moe_gather_sum_kernel<false>, grid,
-                    dim3(kRouteThreads), 0, s, static_cast<const uint4*>(y), weights, row_of_slot,
-                    K, nv, span, static_cast<uint4*>(out), status);
+  if (K <= 2) return launch_gather<4>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
+  if (K <= 4) return launch_gather<2>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
+  return launch_gather<1>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
 }
 
 cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const float* weights,
                                         const int32_t* row_of_slot, const int32_t* offsets,
                                         int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
                                         float* grad_w, uint32_t* status, cudaStream_t s) {
-  return launch_pdl(moe_combine_backward_kernel, dim3((unsigned)T), dim3(kRouteThreads), 0, s,
-                    static_cast<const uint4*>(grad), static_cast<const uint4*>(y), weights,
-                    row_of_slot, offsets, K, E, nv, static_cast<uint4*>(grad_y), grad_w, status);
+  constexpr int kSlots = kSlotThreads / 32;
+  return launch_pdl(moe_combine_backward_kernel, dim3((unsigned)((T * K + kSlots - 1) / kSlots)),
+                    dim3(kSlotThreads), 0, s, static_cast<const uint4*>(grad),
+                    static_cast<const uint4*>(y), weights, row_of_slot, offsets, T, K, E, nv,
+                    static_cast<uint4*>(grad_y), grad_w, status);
 }
 
 }  // namespace nvfp4
