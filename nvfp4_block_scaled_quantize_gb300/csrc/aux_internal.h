@@ -64,7 +64,8 @@ cudaError_t launch_moe_gather_sum(const void* y, const float* weights, const int
 cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const float* weights,
                                         const int32_t* row_of_slot, const int32_t* offsets,
                                         int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
-                                        float* grad_w, uint32_t* status, cudaStream_t s);
+                                        float* grad_w, uint32_t* status, int sm_count,
+                                        cudaStream_t s);
 
 // ---- operators with 8-bit checkpoints (checkpoint.cu) ----
 cudaError_t launch_swiglu_checkpoint(const void* h, int64_t M, int64_t F, const int32_t* offsets,

@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(
 int64_t glu_per_cta(int64_t items, int sm_count, int* grid) {
   const int64_t most = (int64_t)sm_count * 8;
   int64_t per = (items + most - 1) / most;
+  if (per > 4 * kGluThreads) per = 4 * kGluThreads;
   per = (per + kGluThreads - 1) / kGluThreads * kGluThreads;
   *grid = (int)((items + per - 1) / per);
   return per;

@@ -154,7 +154,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_combine_backward(const void* grad_out, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (H == 0) return cuda_status(zero(grad_weights, 4 * (size_t)(T * K), s));
   return cuda_status(launch_moe_combine_backward(grad_out, y, weights, row_of_slot, offsets, T, K,
-                                                 E, H / 8, grad_y, grad_weights, status, s));
+                                                 E, H / 8, grad_y, grad_weights, status, sms, s));
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_swiglu_checkpoint(const void* h, int64_t M, int64_t F,

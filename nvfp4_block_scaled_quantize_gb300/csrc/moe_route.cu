@@ -234,31 +234,30 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 
 // ---- dispatch ----------------------------------------------------------------------------
 
-// `tw` warps (a power of two) per token, neighbouring ones taking neighbouring 32 vectors of its
-// row; a CTA holds its warps / tw tokens. The token's maximum is joined in shared memory, so that
+// TW warps per token, neighbouring ones taking neighbouring 32 vectors of its row; a CTA holds its
+// warps / TW tokens. The token's maximum is joined in shared memory, so that
 // it costs one atomic for each of its experts. ONE: the grid is one cluster, which joins the
 // experts' maxima in its first CTA's shared memory and writes all of amax itself, so that a small
 // call needs no clearing of amax before it.
-constexpr int kCopyBatch = 4;  // vectors a lane holds between their load and their K stores
 constexpr int kCopyMaxWarps = 32;
 constexpr int64_t kOneClusterTokens = 16;  // 8 CTAs of two tokens, 16 warps each
-template <bool ONE>
+template <int TW, int BATCH, bool ONE>
 __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ row_of_slot,
-    const int32_t* __restrict__ offsets, int64_t T, int32_t K, int32_t E, int64_t nv, int tw,
-    uint4* packed, uint32_t* amax, uint32_t* status) {
+    const int32_t* __restrict__ offsets, int64_t T, int32_t K, int32_t E, int64_t nv, uint4* packed,
+    uint32_t* amax, uint32_t* status) {
   namespace cg = cooperative_groups;
   __shared__ int2 scratch[kCopyMaxWarps][32];
   __shared__ int32_t ends[kMaxSegments];
   __shared__ uint32_t top[kCopyMaxWarps], joint[ONE ? kMaxSegments : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int mine = warp / tw, sub = warp - mine * tw;  // the CTA's token, the warp's part of it
+  const int mine = warp / TW, sub = warp % TW;  // the CTA's token, the warp's part of it
   if (lane == 0) top[warp] = 0u;
   if (ONE)
     for (int e = tid; e < kMaxSegments; e += blockDim.x) joint[e] = 0u;
   pdl_wait();
   pdl_allow_next();
-  const int64_t token = (int64_t)blockIdx.x * (blockDim.x / 32 / tw) + mine, P = T * K;
+  const int64_t token = (int64_t)blockIdx.x * (blockDim.x / 32 / TW) + mine, P = T * K;
   for (int e = tid; e < E; e += blockDim.x) ends[e] = offsets[e];
   if (ONE) cg::this_cluster().sync();
   else __syncthreads();
@@ -266,21 +265,21 @@ __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
   if (token < T) {
     rows = load_token_rows(row_of_slot, token, K, P, scratch, status);
     uint32_t m = 0;
-    for (int64_t at = sub * 32; at < nv; at += 32 * tw * kCopyBatch) {  // every lane: shuffles
+    for (int64_t at = sub * 32; at < nv; at += 32 * TW * BATCH) {  // every lane: shuffles
       const int64_t v = at + lane;
-      uint4 q[kCopyBatch];
+      uint4 q[BATCH];
 #pragma unroll
-      for (int j = 0; j < kCopyBatch; j++)
-        q[j] = v + 32 * tw * j < nv ? __ldg(x + token * nv + v + 32 * tw * j)
+      for (int j = 0; j < BATCH; j++)
+        q[j] = v + 32 * TW * j < nv ? __ldg(x + token * nv + v + 32 * TW * j)
                                     : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j = 0; j < kCopyBatch; j++)
+      for (int j = 0; j < BATCH; j++)
         m = vmax2(m, vmax2(vmax2(abs2(q[j].x), abs2(q[j].y)), vmax2(abs2(q[j].z), abs2(q[j].w))));
       for (int k = 0; k < rows.count; k++) {
         uint4* to = packed + __shfl_sync(0xFFFFFFFFu, rows.row, k) * nv + v;
 #pragma unroll
-        for (int j = 0; j < kCopyBatch; j++)
-          if (v + 32 * tw * j < nv) to[32 * tw * j] = q[j];
+        for (int j = 0; j < BATCH; j++)
+          if (v + 32 * TW * j < nv) to[32 * TW * j] = q[j];
       }
     }
     m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
@@ -299,7 +298,7 @@ __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
   const int64_t live = ends[E - 1] < 0 ? 0 : ends[E - 1];
   if (token < T)
     for (int64_t r = live + token; r < P; r += T)
-      for (int64_t v = sub * 32 + lane; v < nv; v += 32 * tw)
+      for (int64_t v = sub * 32 + lane; v < nv; v += 32 * TW)
         packed[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
   if (ONE) {
     cg::this_cluster().sync();
@@ -371,64 +370,75 @@ __global__ void __launch_bounds__(kRouteThreads) moe_gather_sum_kernel(
 
 // ---- the gradient of combine -------------------------------------------------------------
 
-// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: a warp per slot, so that the
-// product needs no sum across warps; the warps of a CTA mostly share a token, whose gradient row
-// then comes from L1. Slot i also clears row i when it lies past the last expert's end.
+// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: TW warps per slot;
+// the slots of a CTA mostly share a token, whose gradient row then comes from L1. Slot i also
+// clears row i when it lies past the last expert's end.
 constexpr int kSlotThreads = 256;
 constexpr int kDotBatch = 4;
+template <int TW>
 __global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(
     const uint4* __restrict__ grad, const uint4* __restrict__ y, const float* __restrict__ weights,
     const int32_t* __restrict__ row_of_slot, const int32_t* __restrict__ offsets, int64_t T,
     int32_t K, int32_t E, int64_t nv, uint4* grad_y, float* grad_w, uint32_t* status) {
+  __shared__ float red[kSlotThreads / 32];
   pdl_wait();
   pdl_allow_next();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kThreads = 32 * TW;
+  const int mine = warp / TW, sub = warp % TW;
   const int64_t P = T * K;
-  const int64_t slot = (int64_t)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5);
-  if (slot >= P) return;
-  const int64_t token = (uint32_t)slot / (uint32_t)K;
-  int64_t row = row_of_slot[slot];
-  if (row >= P) {
-    if (lane == 0) atomicOr(status, kBadRoute);
-    row = -1;
-  }
+  const int64_t slot = (int64_t)blockIdx.x * (kSlotThreads / kThreads) + mine;
+  const int64_t v0 = sub * 32 + lane;
   float dot = 0.0f;
-  if (row >= 0) {
-    const float w = weights[slot];
-    const uint64_t w2 = f2_pack(w, w);
-    uint64_t s = f2_pack(0.0f, 0.0f);
-    const uint4 *g = grad + token * nv, *from = y + row * nv;
-    uint4* to = grad_y + row * nv;
-    for (int64_t v = lane; v < nv; v += 32 * kDotBatch) {
-      uint4 a[kDotBatch], b[kDotBatch];
-#pragma unroll
-      for (int j = 0; j < kDotBatch; j++) {
-        const bool in = v + 32 * j < nv;
-        b[j] = in ? __ldg(from + v + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
-        a[j] = in ? __ldg(g + v + 32 * j) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int j = 0; j < kDotBatch; j++) {
-        const uint32_t ae[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
-        const uint32_t be[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint64_t d = f2_from_bf16x2(ae[i]);
-          s = f2_fma(d, f2_from_bf16x2(be[i]), s);
-          o[i] = pack_bf16(f2_mul(w2, d));
-        }
-        if (v + 32 * j < nv) to[v + 32 * j] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+  if (slot < P) {
+    const int64_t token = (uint32_t)slot / (uint32_t)K;
+    int64_t row = row_of_slot[slot];
+    if (row >= P) {
+      if (lane == 0) atomicOr(status, kBadRoute);
+      row = -1;
     }
-    const float2 f = f2_unpack(s);
-    dot = __fadd_rn(f.x, f.y);
+    if (row >= 0) {
+      const float w = weights[slot];
+      const uint64_t w2 = f2_pack(w, w);
+      uint64_t s = f2_pack(0.0f, 0.0f);
+      const uint4 *g = grad + token * nv, *from = y + row * nv;
+      uint4* to = grad_y + row * nv;
+      for (int64_t v = v0; v < nv; v += kThreads * kDotBatch) {
+        uint4 a[kDotBatch], b[kDotBatch];
+#pragma unroll
+        for (int j = 0; j < kDotBatch; j++) {
+          const bool in = v + kThreads * j < nv;
+          b[j] = in ? __ldg(from + v + kThreads * j) : make_uint4(0u, 0u, 0u, 0u);
+          a[j] = in ? __ldg(g + v + kThreads * j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < kDotBatch; j++) {
+          const uint32_t ae[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+          const uint32_t be[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const uint64_t d = f2_from_bf16x2(ae[i]);
+            s = f2_fma(d, f2_from_bf16x2(be[i]), s);
+            o[i] = pack_bf16(f2_mul(w2, d));
+          }
+          if (v + kThreads * j < nv) to[v + kThreads * j] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      const float2 f = f2_unpack(s);
+      dot = __fadd_rn(f.x, f.y);
+    }
+    if (slot >= live_rows(offsets, E, P))
+      for (int64_t v = v0; v < nv; v += kThreads) grad_y[slot * nv + v] = make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-  if (lane == 0) grad_w[slot] = dot;
-  if (slot >= live_rows(offsets, E, P))
-    for (int64_t v = lane; v < nv; v += 32) grad_y[slot * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+  if (TW > 1) {
+    if (lane == 0) red[warp] = dot;
+    __syncthreads();
+    for (int i = 1; i < TW; i++) dot += red[mine * TW + i];  // (of the first warp's lanes)
+  }
+  if (lane == 0 && sub == 0 && slot < P) grad_w[slot] = dot;
 }
 
 }  // namespace
@@ -516,26 +526,36 @@ static dim3 token_grid(int64_t tokens, int64_t nv, int sm_count, int64_t* span) 
 
 bool moe_dispatch_clears_amax(int64_t T) { return T <= kOneClusterTokens; }
 
+template <int TW, int BATCH>
+static cudaError_t launch_dispatch(const void* x, const int32_t* row_of_slot,
+                                   const int32_t* offsets, int64_t T, int32_t K, int32_t E,
+                                   int64_t nv, void* packed, float* amax, uint32_t* status,
+                                   cudaStream_t s) {
+  constexpr int kWarps = TW < 4 ? 4 : TW;
+  constexpr int64_t kTokens = kWarps / TW;
+  return launch_pdl(moe_dispatch_kernel<TW, BATCH, false>,
+                    dim3((unsigned)((T + kTokens - 1) / kTokens)), dim3(32 * kWarps), 0, s,
+                    static_cast<const uint4*>(x), row_of_slot, offsets, T, K, E, nv,
+                    static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax), status);
+}
+
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
                                 int64_t T, int32_t K, int32_t E, int64_t nv, void* packed,
                                 float* amax, uint32_t* status, int sm_count, cudaStream_t s) {
-  // warps per token: about 64 for every SM in all, no more than the row has vectors for
-  const int64_t want = (int64_t)sm_count * 64;
-  int tw = 1;
-  while (tw < 16 && tw * 32 < nv && T * tw < want) tw *= 2;
-  const bool one = moe_dispatch_clears_amax(T);
-  if (one) {
+  if (moe_dispatch_clears_amax(T)) {
     const int ctas = (int)(T < 8 ? T : 8), tokens = (int)((T + ctas - 1) / ctas);
-    return launch_cluster(moe_dispatch_kernel<true>, ctas, 32 * tw * tokens, 0, s,
-                          static_cast<const uint4*>(x), row_of_slot, offsets, T, K, E, nv, tw,
+    return launch_cluster(moe_dispatch_kernel<16, 2, true>, ctas, 32 * 16 * tokens, 0, s,
+                          static_cast<const uint4*>(x), row_of_slot, offsets, T, K, E, nv,
                           static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax), status);
   }
-  const int warps = tw < 4 ? 4 : tw;
-  const int64_t tokens = warps / tw;
-  return launch_pdl(moe_dispatch_kernel<false>, dim3((unsigned)((T + tokens - 1) / tokens)),
-                    dim3(32 * warps), 0, s, static_cast<const uint4*>(x), row_of_slot, offsets, T,
-                    K, E, nv, tw, static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax),
-                    status);
+  // warps per token: a row in one batch of 8 vectors a lane, so that each destination row is
+  // written in one burst, and more warps when the tokens do not give every SM 64
+  const int64_t want = (int64_t)sm_count * 64;
+  if (nv <= 128 && T >= want)
+    return launch_dispatch<1, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
+  if (T * 4 >= want)
+    return launch_dispatch<4, 8>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
+  return launch_dispatch<8, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
 }
 
 template <int VECS>
@@ -558,15 +578,30 @@ cudaError_t launch_moe_gather_sum(const void* y, const float* weights, const int
   return launch_gather<1>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
 }
 
+template <int TW>
+static cudaError_t launch_combine_backward(const void* grad, const void* y, const float* weights,
+                                           const int32_t* row_of_slot, const int32_t* offsets,
+                                           int64_t T, int32_t K, int32_t E, int64_t nv,
+                                           void* grad_y, float* grad_w, uint32_t* status,
+                                           cudaStream_t s) {
+  constexpr int64_t kSlots = kSlotThreads / 32 / TW;
+  return launch_pdl(moe_combine_backward_kernel<TW>,
+                    dim3((unsigned)((T * K + kSlots - 1) / kSlots)), dim3(kSlotThreads), 0, s,
+                    static_cast<const uint4*>(grad), static_cast<const uint4*>(y), weights,
+                    row_of_slot, offsets, T, K, E, nv, static_cast<uint4*>(grad_y), grad_w, status);
+}
+
 cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const float* weights,
                                         const int32_t* row_of_slot, const int32_t* offsets,
                                         int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
-                                        float* grad_w, uint32_t* status, cudaStream_t s) {
-  constexpr int kSlots = kSlotThreads / 32;
-  return launch_pdl(moe_combine_backward_kernel, dim3((unsigned)((T * K + kSlots - 1) / kSlots)),
-                    dim3(kSlotThreads), 0, s, static_cast<const uint4*>(grad),
-                    static_cast<const uint4*>(y), weights, row_of_slot, offsets, T, K, E, nv,
-                    static_cast<uint4*>(grad_y), grad_w, status);
+                                        float* grad_w, uint32_t* status, int sm_count,
+                                        cudaStream_t s) {
+  // several warps per slot when the slots alone do not give every SM 64 warps
+  if (T * K < (int64_t)sm_count * 64 && nv > 32 * kDotBatch)
+    return launch_combine_backward<4>(grad, y, weights, row_of_slot, offsets, T, K, E, nv, grad_y,
+                                      grad_w, status, s);
+  return launch_combine_backward<1>(grad, y, weights, row_of_slot, offsets, T, K, E, nv, grad_y,
+                                    grad_w, status, s);
 }
 
 }  // namespace nvfp4
