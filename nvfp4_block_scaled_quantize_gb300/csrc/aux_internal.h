@@ -68,6 +68,7 @@ cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const f
                                         cudaStream_t s);
 
 // ---- operators with 8-bit checkpoints (checkpoint.cu) ----
+cudaError_t prepare_checkpoint_kernels();
 cudaError_t launch_swiglu_checkpoint(const void* h, int64_t M, int64_t F, const int32_t* offsets,
                                      int32_t E, void* y, void* codes, uint8_t* scales, float* amax,
                                      uint32_t* status, int sm_count, cudaStream_t s);
@@ -84,6 +85,7 @@ struct RmsArgs {
   void *y, *codes, *grad_x;
   uint8_t* scales;
   float *rstd, *amax, *partial, *grad_weight;
+  uint32_t* status;
 };
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s);

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "nvfp4_device.cuh"
 #include "aux_internal.h"
@@ -295,48 +296,82 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
 
 // ---- RMSNorm -----------------------------------------------------------------------------
 
-// A group of `wpr` warps owns a row, ITEMS x 16 columns a thread: the row is read once and stays in
-// registers between its sum and its output. A CTA holds as many groups as fit in 16 warps.
-constexpr int kRmsWarps = 16;
-constexpr int kRmsThreads = 32 * kRmsWarps;
-constexpr int kMaxJointN = 4096;  // backward: a CTA with more than one group has rows up to this
+// A group of `wpr` warps owns a row, ITEMS x 16 columns a thread; a CTA of at most WARPS warps works
+// on tiles of `groups` consecutive rows. A tile is contiguous in memory: one thread fetches it by
+// bulk copies into a ring of STAGES tiles in shared memory, ahead of the tile that is summed, so
+// that neither the loads nor their addresses cost the other threads instructions, and DRAM stays
+// busy across the barrier of the sum. Two CTAs an SM up to 8192 columns: while one waits at its
+// barrier the other computes.
+constexpr int kMaxJointN = 2048;  // a CTA with more than one group has rows up to this
+constexpr uint64_t kTileWaitNs = 2000000000ull;
+constexpr uint32_t kTimeout = 0x2u;  // NVFP4_DEVICE_TIMEOUT
 
 struct RmsShape {
-  int wpr, groups, items;
+  int wpr, groups;
 };
-RmsShape rms_shape(int64_t N, int items) {
+RmsShape rms_shape(int64_t N, int warps, int items) {
   RmsShape s;
-  s.items = items;
   const int64_t per_warp = 512 * items;
   s.wpr = (int)((N + per_warp - 1) / per_warp);
-  s.groups = kRmsWarps / s.wpr;
+  s.groups = warps / s.wpr;
   return s;
 }
-// Forward: as many columns a thread as the registers hold, so that few warps meet at a barrier (none
-// up to 4096 columns) and the sum's shuffles are spread over more columns.
-RmsShape rms_forward_shape(int64_t N) {
-  return rms_shape(N, N <= 512 ? 1 : (N <= 1024 ? 2 : 4));
-}
-// Backward: the weight gradient takes a register a column, so 16 columns a thread up to 8192.
-RmsShape rms_backward_shape(int64_t N) {
-  return rms_shape(N, N <= 8192 ? 1 : (N <= 16384 ? 2 : 4));
+
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(to)),
+      "l"(from), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
-// Sum over the group's threads: shuffles, then the warps' sums through shared memory, in an order
-// that does not depend on time. `red` has two halves used in turn, so one barrier a row is enough.
-__device__ __forceinline__ float group_sum(uint64_t pair, float (*red)[kRmsWarps], int turn,
-                                           int group, int wpr) {
+// One thread's waits for the CTA's tiles. A wait that gives up is reported and the thread's later
+// ones are skipped, so that every thread still reaches every barrier of the CTA; thread 0 then
+// fetches no more, and the CTA leaves only once the copies in flight have landed (bounded too).
+template <int STAGES>
+struct TileWaits {
+  uint64_t* full;
+  uint32_t* status;
+  int stage = 0;
+  uint32_t parity = 0;
+  bool dead = false;
+  __device__ void wait() {
+    if (!dead && !mbar_wait_bounded(&full[stage], parity, kTileWaitNs)) {
+      dead = true;
+      atomicOr(status, kTimeout);
+    }
+  }
+  __device__ void next() {
+    if (++stage == STAGES) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+  __device__ void drain() {
+    if (dead)
+      for (int i = 0; i < STAGES; i++)
+        mbar_wait_bounded(&full[i], i < stage ? parity : parity ^ 1u, kTileWaitNs);
+  }
+};
+
+// Sum over each group's threads: shuffles, then the warps' sums through shared memory, in an order
+// that does not depend on time; `red` has two halves used in turn. The barrier is the CTA's, so that
+// after it every thread has left the previous tile.
+template <int WARPS>
+__device__ __forceinline__ float group_sum(uint64_t pair, float (*red)[WARPS], int turn, int group,
+                                           int wpr) {
   const float2 f = f2_unpack(pair);
   float s = __fadd_rn(f.x, f.y);
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (wpr == 1) return s;
   const int lane = threadIdx.x & 31;
   if (lane == 0) red[turn][threadIdx.x >> 5] = s;
-  named_bar_sync(1 + group, wpr * 32);
+  __syncthreads();
+  if (wpr == 1) return s;
   s = lane < wpr ? red[turn][group * wpr + lane] : 0.0f;
 #pragma unroll
-  for (int o = 8; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  for (int o = WARPS / 2; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   return __shfl_sync(0xFFFFFFFFu, s, 0);
 }
 
@@ -357,55 +392,71 @@ __device__ __forceinline__ void hold_packed(Half32 (&h)[ITEMS]) {
     for (int i = 0; i < 8; i++) asm volatile("" : "+r"(h[j].w[i]));
 }
 
-// Up to 1024 columns the registers also hold the group's next row, which is loaded before the
-// current one is summed.
-template <int ITEMS>
-__global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_checkpoint_kernel(
+__device__ __forceinline__ Half32 shared_half(const uint8_t* at) {
+  const uint4* p = reinterpret_cast<const uint4*>(at);
+  const uint4 a = p[0], b = p[1];
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// WARPS warps a CTA, ITEMS x 16 columns a thread, STAGES tiles in the ring, CTAS CTAs an SM.
+template <int WARPS, int ITEMS, int STAGES, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_kernel(
     const uint4* __restrict__ x, const uint4* __restrict__ weight, int64_t M, int32_t N, float eps,
     float bias, int wpr, int groups, uint4* y, uint4* codes, uint8_t* scales, float* rstd,
-    uint32_t* amax) {
-  __shared__ float red[2][kRmsWarps];
-  __shared__ uint32_t top[kRmsWarps];
-  pdl_wait();
-  pdl_allow_next();
+    uint32_t* amax, uint32_t* status) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[STAGES];
+  __shared__ float red[2][WARPS];
+  __shared__ uint32_t top[WARPS];
+  constexpr int kStage = WARPS * 32 * ITEMS * 32;  // bytes
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
   const int nc = N / 16;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  constexpr bool kAhead = ITEMS <= 2;
   const float inv_n = 1.0f / (float)N;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; i++) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_allow_next();
+  const int64_t step = (int64_t)gridDim.x * groups;
+  auto fetch = [&](int stage, int64_t row) {  // thread 0
+    if (row >= M) return;
+    const int64_t rows = M - row < groups ? M - row : groups;
+    const uint32_t bytes = (uint32_t)(rows * N * 2);
+    mbar_expect_tx(&full[stage], bytes);
+    bulk_load(ring + stage * kStage, x + row * nc * 2, bytes, &full[stage]);
+  };
+  int64_t first = (int64_t)blockIdx.x * groups;  // of the tile
+  if (tid == 0)
+    for (int i = 0; i < STAGES - 1; i++) fetch(i, first + i * step);
+  TileWaits<STAGES> tiles{full, status};
   uint32_t m = 0u;
   int turn = 0;
-  // a CTA's groups take rows gridDim.x apart, so that a last partial round is spread over the SMs
-  int64_t r = (int64_t)blockIdx.x + (int64_t)group * gridDim.x;
-  int64_t pos = r * nc + at;  // of the thread's first 16 columns, in units of 16
-  Half32 next[ITEMS];
-  auto load = [&](int64_t p) {
-#pragma unroll
-    for (int j = 0; j < ITEMS; j++)
-      if (at + j * threads < nc) next[j] = load_half(x + 2 * (p + j * threads));
-  };
-#pragma unroll
-  for (int j = 0; j < ITEMS; j++)
-#pragma unroll
-    for (int i = 0; i < 8; i++) next[j].w[i] = 0u;
-  if (kAhead && r < M) load(pos);
-  for (; r < M; r += step, pos += step * nc) {
-    if (!kAhead) load(pos);
+  const uint8_t* const mine = ring + ((size_t)group * nc + at) * 32;
+  for (; first < M; first += step) {
+    const int64_t r = first + group, pos = r * nc + at;
+    const bool live = r < M;
+    tiles.wait();
     Half32 w[ITEMS];
-#pragma unroll
-    for (int j = 0; j < ITEMS; j++) w[j] = next[j];
-    if (kAhead && r + step < M) load(pos + step * nc);
     uint64_t s = f2_pack(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < ITEMS; j++) {  // (columns past the row hold zeros)
+    for (int j = 0; j < ITEMS; j++) {
+      if (!live || at + j * threads >= nc) break;
+      w[j] = shared_half(mine + tiles.stage * kStage + j * threads * 32);
       uint64_t v[8];
       unpack16(w[j], v);
 #pragma unroll
       for (int i = 0; i < 8; i++) s = f2_fma(v[i], v[i], s);
     }
-    const float sum = group_sum(s, red, turn, group, wpr);
+    const float sum = group_sum<WARPS>(s, red, turn, group, wpr);
+    // every thread has read this tile into registers: its stage and all before it are free
+    if (tid == 0 && !tiles.dead)
+      fetch(tiles.stage == 0 ? STAGES - 1 : tiles.stage - 1, first + (STAGES - 1) * step);
+    tiles.next();
     turn ^= 1;
+    if (!live) continue;
     hold_packed(w);
     const float rs = rsqrtf(__fmaf_rn(sum, inv_n, eps));
     const uint64_t rs2 = f2_pack(rs, rs);
@@ -430,6 +481,7 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
       if ((c & 1) == 0) scales[p / 2] = (uint8_t)sc;  // (rows are an even number of halves)
     }
   }
+  tiles.drain();
   m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
   if (lane == 0) top[warp] = m;
   __syncthreads();
@@ -442,70 +494,94 @@ __global__ void __launch_bounds__(kRmsThreads, ITEMS == 1 ? 2 : 1) rmsnorm_check
 // With xh = x * rstd and g = (w + bias) dy: dx = rstd (g - xh mean(g xh)) [+ residual], and
 // dw = sum over rows of dy xh. A thread keeps its columns' share of dw over all of its rows; the
 // groups of a CTA are added in shared memory in order and each CTA writes one row of `partial`, so
-// that the sum's order depends on the grid alone. Up to 8192 columns the registers also hold the
-// weights and the group's next row, which is loaded before the current one is summed, so that the
-// SM's loads do not stop at the barrier of the sum.
-template <int ITEMS, bool RES>
-__global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_kernel(
+// that the sum's order depends on the grid alone.
+__host__ __device__ constexpr int rms_column_bytes(bool res) { return res ? 5 : 3; }
+
+template <int WARPS, int ITEMS, int STAGES, int CTAS, bool RES>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_kernel(
     const uint4* __restrict__ grad, const uint4* __restrict__ codes,
     const uint8_t* __restrict__ scales, const float* __restrict__ rstd,
     const uint4* __restrict__ weight, int64_t M, int32_t N, float bias, int wpr, int groups,
-    const uint4* __restrict__ residual, uint4* grad_x, float* partial) {
-  __shared__ float red[2][kRmsWarps];
+    const uint4* __restrict__ residual, uint4* grad_x, float* partial, uint32_t* status) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[STAGES];
+  __shared__ float red[2][WARPS];
   __shared__ float4 cols[kMaxJointN / 4];  // the groups' joint sums
-  pdl_wait();
-  pdl_allow_next();
+  constexpr int kColumns = WARPS * 32 * ITEMS * 16;
+  constexpr int kStage = kColumns * rms_column_bytes(RES);  // grad, residual, codes
+  constexpr int kCodes = kColumns * (RES ? 4 : 2);
   const int tid = threadIdx.x, warp = tid >> 5;
   const int group = warp / wpr, at = tid - group * wpr * 32, threads = wpr * 32;
   const int nc = N / 16;
-  const int64_t step = (int64_t)gridDim.x * groups;
-  constexpr bool kAhead = ITEMS == 1;
   const float inv_n = 1.0f / (float)N;
-  struct Row {
-    Half32 d[ITEMS], res[RES ? ITEMS : 1];
-    uint4 k[ITEMS];
-    uint32_t sc[ITEMS];
-    float rs;
-  } next;
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; i++) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_allow_next();
   uint64_t dw[ITEMS][8], w[8], h[8];
 #pragma unroll
   for (int j = 0; j < ITEMS; j++)
 #pragma unroll
     for (int i = 0; i < 8; i++) dw[j][i] = f2_pack(0.0f, 0.0f);
-  if (kAhead && at < nc) biased_weight(load_half(weight + 2 * at), bias, w);
-  auto load = [&](int64_t r, int64_t pos) {
-    next.rs = __ldg(rstd + r);
+  if (ITEMS == 1 && at < nc) biased_weight(load_half(weight + 2 * at), bias, w);
+  const int64_t step = (int64_t)gridDim.x * groups;
+  auto fetch = [&](int stage, int64_t row) {  // thread 0
+    if (row >= M) return;
+    const int64_t rows = M - row < groups ? M - row : groups;
+    const uint32_t n = (uint32_t)(rows * N);
+    uint8_t* to = ring + stage * kStage;
+    mbar_expect_tx(&full[stage], n * rms_column_bytes(RES));
+    bulk_load(to, grad + row * nc * 2, 2 * n, &full[stage]);
+    bulk_load(to + kCodes, codes + row * nc, n, &full[stage]);
+    if (RES) bulk_load(to + kColumns * 2, residual + row * nc * 2, 2 * n, &full[stage]);
+  };
+  // the scale bytes and the row's rstd come one tile ahead, in registers
+  uint32_t next_sc[ITEMS];
+  float next_rs = 0.0f;
+  auto fetch_scales = [&](int64_t row) {
+    if (row < M) {
+      next_rs = __ldg(rstd + row);
 #pragma unroll
-    for (int j = 0; j < ITEMS; j++) {
-      const int64_t p = pos + j * threads;
-      if (at + j * threads < nc) {
-        next.d[j] = load_half(grad + 2 * p);
-        next.k[j] = __ldg(codes + p);
-        next.sc[j] = __ldg(scales + p / 2);
-        if (RES) next.res[j] = load_half(residual + 2 * p);
+      for (int j = 0; j < ITEMS; j++) {
+        const int c = at + j * threads;
+        if (c < nc) next_sc[j] = __ldg(scales + (row * nc + c) / 2);
       }
     }
   };
-  auto kept = [&](const uint4& k, uint32_t sc, float rs) {
-    kept_values({k.x, k.y, k.z, k.w}, __fmul_rn(e8m0_value(sc), rs), h);
-  };
+  int64_t first = (int64_t)blockIdx.x * groups;  // of the tile
+  if (tid == 0)
+    for (int i = 0; i < (STAGES > 1 ? STAGES - 1 : 1); i++) fetch(i, first + i * step);
+  fetch_scales(first + group);
+  TileWaits<STAGES> tiles{full, status};
   int turn = 0;
-  int64_t r = (int64_t)blockIdx.x * groups + group;
-  int64_t pos = r * nc + at;  // of the thread's first 16 columns, in units of 16
-  if (kAhead && r < M) load(r, pos);
-  for (; r < M; r += step, pos += step * nc) {
-    if (!kAhead) load(r, pos);
-    const Row row = next;
-    if (kAhead && r + step < M) load(r + step, pos + step * nc);
+  const uint8_t* const mine = ring + ((size_t)group * nc + at) * 32;
+  const uint8_t* const mine8 = ring + kCodes + ((size_t)group * nc + at) * 16;
+  for (; first < M; first += step) {
+    const int64_t r = first + group;
+    const bool live = r < M;
+    const float rs = next_rs;
+    float factor[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; j++) factor[j] = __fmul_rn(e8m0_value(next_sc[j]), rs);
+    fetch_scales(r + step);
+    tiles.wait();
+    const int at_stage = tiles.stage * kStage;
+    auto kept = [&](int j) {
+      const uint4 k = *reinterpret_cast<const uint4*>(mine8 + at_stage + j * threads * 16);
+      kept_values({k.x, k.y, k.z, k.w}, factor[j], h);
+    };
     uint64_t s = f2_pack(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
-      if (c >= nc) break;
-      if (!kAhead) biased_weight(load_half(weight + 2 * c), bias, w);
+      if (!live || c >= nc) break;
+      if (ITEMS > 1) biased_weight(load_half(weight + 2 * c), bias, w);
       uint64_t d[8];
-      unpack16(row.d[j], d);
-      kept(row.k[j], row.sc[j], row.rs);
+      unpack16(shared_half(mine + at_stage + j * threads * 32), d);
+      kept(j);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const uint64_t t = f2_mul(d[i], h[i]);
@@ -513,29 +589,38 @@ __global__ void __launch_bounds__(kRmsThreads, 1) rmsnorm_checkpoint_backward_ke
         s = f2_fma(w[i], t, s);
       }
     }
-    const float mean = __fmul_rn(group_sum(s, red, turn, group, wpr), inv_n);
+    const float mean = __fmul_rn(group_sum<WARPS>(s, red, turn, group, wpr), inv_n);
     turn ^= 1;
-    const uint64_t rs2 = f2_pack(row.rs, row.rs), minus = f2_pack(-mean, -mean);
+    // every thread has left the previous tile: its stage takes the tile STAGES - 1 ahead
+    if (STAGES > 1 && tid == 0 && !tiles.dead)
+      fetch(tiles.stage == 0 ? STAGES - 1 : tiles.stage - 1, first + (STAGES - 1) * step);
+    tiles.next();
+    const uint64_t rs2 = f2_pack(rs, rs), minus = f2_pack(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
-      if (c >= nc) break;
-      if (!kAhead) {
+      if (!live || c >= nc) break;
+      if (ITEMS > 1) {
         biased_weight(load_half(weight + 2 * c), bias, w);
-        kept(row.k[j], row.sc[j], row.rs);
+        kept(j);
       }
       uint64_t d[8], e[8];
       uint32_t o[8];
-      unpack16(row.d[j], d);
-      if (RES) unpack16(row.res[RES ? j : 0], e);
+      unpack16(shared_half(mine + at_stage + j * threads * 32), d);
+      if (RES) unpack16(shared_half(mine + at_stage + kColumns * 2 + j * threads * 32), e);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         const uint64_t q = f2_fma(h[i], minus, f2_mul(w[i], d[i]));
         o[i] = pack_bf16(RES ? f2_fma(rs2, q, e[i]) : f2_mul(rs2, q));
       }
-      store_half(grad_x + 2 * (pos + j * threads), o);
+      store_half(grad_x + 2 * (r * nc + c), o);
+    }
+    if (STAGES == 1) {
+      __syncthreads();
+      if (tid == 0 && !tiles.dead) fetch(0, first + step);
     }
   }
+  tiles.drain();
   float4* out = reinterpret_cast<float4*>(partial + (int64_t)blockIdx.x * N);
   for (int g = 0; g < groups; g++) {
     if (group == g) {
@@ -590,36 +675,70 @@ int64_t glu_per_cta(int64_t items, int sm_count, int* grid) {
   return per;
 }
 
-// One wave of CTAs that share an SM's registers: 512 threads of `regs` = 128, 1024 of 64.
-int rms_grid(const RmsShape& f, int64_t M, int sm_count, int threads_per_sm) {
+int rms_grid(const RmsShape& f, int64_t M, int64_t wave) {
   const int64_t ctas = (M + f.groups - 1) / f.groups;
-  const int64_t wave = (int64_t)sm_count * (threads_per_sm / (f.wpr * f.groups * 32));
   return (int)(ctas < wave ? ctas : wave);
 }
 
-template <int ITEMS>
-cudaError_t rms_forward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
-  return launch_pdl(rmsnorm_checkpoint_kernel<ITEMS>, dim3(rms_grid(f, a.M, sm_count, ITEMS == 1 ? 1024 : 512)),
-                    dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.x),
-                    static_cast<const uint4*>(a.weight), a.M, (int32_t)a.N, a.eps, a.bias, f.wpr,
-                    f.groups, static_cast<uint4*>(a.y), static_cast<uint4*>(a.codes), a.scales,
-                    a.rstd, reinterpret_cast<uint32_t*>(a.amax));
-}
+// One kernel's shape, as template arguments of both directions.
+template <int WARPS, int ITEMS, int STAGES, int CTAS>
+struct RmsForward {
+  static constexpr int kSmem = STAGES * WARPS * 32 * ITEMS * 32;
+  static cudaError_t prepare() {
+    return cudaFuncSetAttribute(rmsnorm_checkpoint_kernel<WARPS, ITEMS, STAGES, CTAS>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  }
+  static cudaError_t launch(const RmsArgs& a, int sm_count, cudaStream_t s) {
+    const RmsShape f = rms_shape(a.N, WARPS, ITEMS);
+    return launch_pdl(rmsnorm_checkpoint_kernel<WARPS, ITEMS, STAGES, CTAS>,
+                      dim3(rms_grid(f, a.M, (int64_t)sm_count * CTAS)),
+                      dim3(f.wpr * f.groups * 32), kSmem, s, static_cast<const uint4*>(a.x),
+                      static_cast<const uint4*>(a.weight), a.M, (int32_t)a.N, a.eps, a.bias, f.wpr,
+                      f.groups, static_cast<uint4*>(a.y), static_cast<uint4*>(a.codes), a.scales,
+                      a.rstd, reinterpret_cast<uint32_t*>(a.amax), a.status);
+  }
+};
 
-template <int ITEMS>
-cudaError_t rms_backward_t(const RmsArgs& a, const RmsShape& f, int sm_count, cudaStream_t s) {
-  int grid = rms_grid(f, a.M, sm_count, 512);
-  if (grid > kRmsMaxPartials) grid = kRmsMaxPartials;
-  const cudaError_t e = launch_pdl(
-      a.residual ? rmsnorm_checkpoint_backward_kernel<ITEMS, true>
-                 : rmsnorm_checkpoint_backward_kernel<ITEMS, false>,
-      dim3(grid), dim3(f.wpr * f.groups * 32), 0, s, static_cast<const uint4*>(a.grad),
-      static_cast<const uint4*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
-      a.M, (int32_t)a.N, a.bias, f.wpr, f.groups, static_cast<const uint4*>(a.residual),
-      static_cast<uint4*>(a.grad_x), a.partial);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(column_sum_kernel, dim3((unsigned)(a.N / 32)), dim3(32 * kSumWarps), 0, s,
-                    a.partial, grid, a.N, a.grad_weight);
+template <int WARPS, int ITEMS, int STAGES, int CTAS, bool RES>
+struct RmsBackward {
+  static constexpr int kSmem = STAGES * WARPS * 32 * ITEMS * 16 * rms_column_bytes(RES);
+  static cudaError_t prepare() {
+    return cudaFuncSetAttribute(rmsnorm_checkpoint_backward_kernel<WARPS, ITEMS, STAGES, CTAS, RES>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  }
+  static cudaError_t launch(const RmsArgs& a, int sm_count, cudaStream_t s) {
+    const RmsShape f = rms_shape(a.N, WARPS, ITEMS);
+    int64_t wave = (int64_t)sm_count * CTAS;
+    if (wave > kRmsMaxPartials) wave = kRmsMaxPartials;
+    const int grid = rms_grid(f, a.M, wave);
+    const cudaError_t e = launch_pdl(
+        rmsnorm_checkpoint_backward_kernel<WARPS, ITEMS, STAGES, CTAS, RES>, dim3(grid),
+        dim3(f.wpr * f.groups * 32), kSmem, s, static_cast<const uint4*>(a.grad),
+        static_cast<const uint4*>(a.codes), a.scales, a.rstd, static_cast<const uint4*>(a.weight),
+        a.M, (int32_t)a.N, a.bias, f.wpr, f.groups, static_cast<const uint4*>(a.residual),
+        static_cast<uint4*>(a.grad_x), a.partial, a.status);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(column_sum_kernel, dim3((unsigned)(a.N / 32)), dim3(32 * kSumWarps), 0, s,
+                      a.partial, grid, a.N, a.grad_weight);
+  }
+};
+
+// By the row's columns: up to 4096, 8192, 16384, 32768.
+using RmsForward0 = RmsForward<8, 1, 4, 3>;
+using RmsForward1 = RmsForward<8, 2, 4, 2>;
+using RmsForward2 = RmsForward<16, 2, 4, 1>;
+using RmsForward3 = RmsForward<16, 4, 3, 1>;
+template <bool RES> using RmsBackward0 = RmsBackward<8, 1, 4, 2, RES>;
+template <bool RES> using RmsBackward1 = RmsBackward<8, 2, 2, 2, RES>;
+template <bool RES> using RmsBackward2 = RmsBackward<16, 2, 2, 1, RES>;
+template <bool RES> using RmsBackward3 = RmsBackward<16, 4, 1, 1, RES>;
+
+template <bool RES>
+cudaError_t rms_backward(const RmsArgs& a, int sm_count, cudaStream_t s) {
+  if (a.N <= 4096) return RmsBackward0<RES>::launch(a, sm_count, s);
+  if (a.N <= 8192) return RmsBackward1<RES>::launch(a, sm_count, s);
+  if (a.N <= 16384) return RmsBackward2<RES>::launch(a, sm_count, s);
+  return RmsBackward3<RES>::launch(a, sm_count, s);
 }
 
 }  // namespace
@@ -645,18 +764,27 @@ cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* code
                     F, offsets, E, per, static_cast<uint4*>(grad_h), status);
 }
 
+cudaError_t prepare_checkpoint_kernels() {
+  cudaError_t e = cudaSuccess;
+  for (const cudaError_t r :
+       {RmsForward0::prepare(), RmsForward1::prepare(), RmsForward2::prepare(),
+        RmsForward3::prepare(), RmsBackward0<false>::prepare(), RmsBackward0<true>::prepare(),
+        RmsBackward1<false>::prepare(), RmsBackward1<true>::prepare(),
+        RmsBackward2<false>::prepare(), RmsBackward2<true>::prepare(),
+        RmsBackward3<false>::prepare(), RmsBackward3<true>::prepare()})
+    if (r != cudaSuccess) e = r;
+  return e;
+}
+
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const RmsShape f = rms_forward_shape(a.N);
-  if (f.items == 1) return rms_forward_t<1>(a, f, sm_count, s);
-  if (f.items == 2) return rms_forward_t<2>(a, f, sm_count, s);
-  return rms_forward_t<4>(a, f, sm_count, s);
+  if (a.N <= 4096) return RmsForward0::launch(a, sm_count, s);
+  if (a.N <= 8192) return RmsForward1::launch(a, sm_count, s);
+  if (a.N <= 16384) return RmsForward2::launch(a, sm_count, s);
+  return RmsForward3::launch(a, sm_count, s);
 }
 
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s) {
-  const RmsShape f = rms_backward_shape(a.N);
-  if (f.items == 1) return rms_backward_t<1>(a, f, sm_count, s);
-  if (f.items == 2) return rms_backward_t<2>(a, f, sm_count, s);
-  return rms_backward_t<4>(a, f, sm_count, s);
+  return a.residual ? rms_backward<true>(a, sm_count, s) : rms_backward<false>(a, sm_count, s);
 }
 
 }  // namespace nvfp4

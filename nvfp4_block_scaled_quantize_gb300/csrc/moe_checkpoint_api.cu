@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "nvfp4.h"
+#include "nvfp4_device.cuh"
 #include "aux_internal.h"
 #include "nvfp4_internal.h"
 
@@ -47,8 +48,17 @@ nvfp4_status check_segments(const int32_t* offsets, int32_t E) {
   return aligned(offsets, 4) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
-cudaError_t zero(void* p, size_t bytes, cudaStream_t s) {
-  return p == nullptr || bytes == 0 ? cudaSuccess : cudaMemsetAsync(p, 0, bytes, s);
+__global__ void zero_kernel(float* p, int64_t n) {
+  pdl_wait();
+  pdl_allow_next();
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0.0f;
+}
+
+// Clears n words by a kernel: a memset in the stream ends the overlap of the launches on both of
+// its sides (with one before dispatch, 300 x 8 x 7168 takes 10.4 us, with this 7.2).
+cudaError_t zero(void* p, int64_t n, cudaStream_t s) {
+  if (p == nullptr || n == 0) return cudaSuccess;
+  return launch_pdl(zero_kernel, dim3(1), dim3(256), 0, s, static_cast<float*>(p), n);
 }
 
 }  // namespace
@@ -70,7 +80,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_plan(const void* expert_ids, int32_t id_byte
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (n == 0) return cuda_status(zero(offsets, 4 * (size_t)E, s));
+  if (n == 0) return cuda_status(zero(offsets, E, s));
   return cuda_status(launch_moe_plan(expert_ids, id_bytes == 8, (int32_t)n, E, row_of_slot,
                                      slot_of_row, offsets, status, s));
 }
@@ -93,7 +103,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* row_o
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      !empty && moe_dispatch_clears_amax(T) ? cudaSuccess : zero(amax, 4 * (size_t)E, s);
+      !empty && moe_dispatch_clears_amax(T) ? cudaSuccess : zero(amax, E, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
   return cuda_status(launch_moe_dispatch(x, row_of_slot, offsets, T, K, E, H / 8, packed, amax,
                                          status, sms, s));
@@ -152,7 +162,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_combine_backward(const void* grad_out, const
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (H == 0) return cuda_status(zero(grad_weights, 4 * (size_t)(T * K), s));
+  if (H == 0) return cuda_status(zero(grad_weights, T * K, s));
   return cuda_status(launch_moe_combine_backward(grad_out, y, weights, row_of_slot, offsets, T, K,
                                                  E, H / 8, grad_y, grad_weights, status, sms, s));
 }
@@ -172,7 +182,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_swiglu_checkpoint(const void* h, int64_t M, int6
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = zero(amax, 4 * (size_t)E, s);
+  const cudaError_t e = zero(amax, E, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
   return cuda_status(launch_swiglu_checkpoint(h, M, F, offsets, E, y, codes, scales, amax, status,
                                               sms, s));
@@ -218,12 +228,12 @@ NVFP4_EXPORT nvfp4_status nvfp4_rmsnorm_checkpoint(const void* x, const void* we
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = zero(amax, 4, s);
+  const cudaError_t e = zero(amax, 1, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
   RmsArgs a = {};
   a.M = M; a.N = N; a.eps = eps; a.bias = weight_bias;
   a.x = x; a.weight = weight; a.y = y; a.codes = codes; a.scales = scales; a.rstd = rstd;
-  a.amax = amax;
+  a.amax = amax; a.status = status;
   return cuda_status(launch_rmsnorm_checkpoint(a, sms, s));
 }
 
@@ -258,11 +268,12 @@ NVFP4_EXPORT nvfp4_status nvfp4_rmsnorm_checkpoint_backward(
   uint32_t* status = nullptr;
   if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (empty) return cuda_status(zero(grad_weight, 4 * (size_t)N, s));
+  if (empty) return cuda_status(zero(grad_weight, N, s));
   RmsArgs a = {};
   a.M = M; a.N = N; a.bias = weight_bias;
   a.grad = grad_y; a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
   a.rstd = const_cast<float*>(rstd); a.weight = weight; a.residual = grad_residual;
   a.grad_x = grad_x; a.grad_weight = grad_weight; a.partial = static_cast<float*>(workspace);
+  a.status = status;
   return cuda_status(launch_rmsnorm_checkpoint_backward(a, sms, s));
 }

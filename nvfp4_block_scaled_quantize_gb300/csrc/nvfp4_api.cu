@@ -179,6 +179,7 @@ cudaError_t prepare_quantize_kernels() {
   if ((r = prepare_amax_tiles()) != cudaSuccess) e = r;
   if ((r = prepare_mx_kernels()) != cudaSuccess) e = r;
   if ((r = prepare_moe_kernels()) != cudaSuccess) e = r;
+  if ((r = prepare_checkpoint_kernels()) != cudaSuccess) e = r;
   return e;
 }
 
