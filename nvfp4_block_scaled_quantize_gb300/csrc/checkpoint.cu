@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
   __syncthreads();
   pdl_wait();
   pdl_allow_next();
-  uint64_t dw[ITEMS][8], w[8], h[8];
+  constexpr bool kHold = ITEMS == 1;  // xh and g stay in registers from the sum to the output
+  uint64_t dw[ITEMS][8], w[8], h[8], g[8];
 #pragma unroll
   for (int j = 0; j < ITEMS; j++)
 #pragma unroll
@@ -569,24 +570,25 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
     fetch_scales(r + step);
     tiles.wait();
     const int at_stage = tiles.stage * kStage;
-    auto kept = [&](int j) {
+    auto prepare = [&](int j, uint64_t (&d)[8]) {  // dy, xh and g of the thread's j-th columns
       const uint4 k = *reinterpret_cast<const uint4*>(mine8 + at_stage + j * threads * 16);
       kept_values({k.x, k.y, k.z, k.w}, factor[j], h);
+      unpack16(shared_half(mine + at_stage + j * threads * 32), d);
+      if (ITEMS > 1) biased_weight(load_half(weight + 2 * (at + j * threads)), bias, w);
+#pragma unroll
+      for (int i = 0; i < 8; i++) g[i] = f2_mul(w[i], d[i]);
     };
     uint64_t s = f2_pack(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
       if (!live || c >= nc) break;
-      if (ITEMS > 1) biased_weight(load_half(weight + 2 * c), bias, w);
       uint64_t d[8];
-      unpack16(shared_half(mine + at_stage + j * threads * 32), d);
-      kept(j);
+      prepare(j, d);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const uint64_t t = f2_mul(d[i], h[i]);
-        dw[j][i] = f2_add(dw[j][i], t);
-        s = f2_fma(w[i], t, s);
+        dw[j][i] = f2_fma(d[i], h[i], dw[j][i]);
+        s = f2_fma(g[i], h[i], s);
       }
     }
     const float mean = __fmul_rn(group_sum<WARPS>(s, red, turn, group, wpr), inv_n);
@@ -600,17 +602,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
     for (int j = 0; j < ITEMS; j++) {
       const int c = at + j * threads;
       if (!live || c >= nc) break;
-      if (ITEMS > 1) {
-        biased_weight(load_half(weight + 2 * c), bias, w);
-        kept(j);
-      }
       uint64_t d[8], e[8];
       uint32_t o[8];
-      unpack16(shared_half(mine + at_stage + j * threads * 32), d);
+      if (!kHold) prepare(j, d);
       if (RES) unpack16(shared_half(mine + at_stage + kColumns * 2 + j * threads * 32), e);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
-        const uint64_t q = f2_fma(h[i], minus, f2_mul(w[i], d[i]));
+        const uint64_t q = f2_fma(h[i], minus, g[i]);
         o[i] = pack_bf16(RES ? f2_fma(rs2, q, e[i]) : f2_mul(rs2, q));
       }
       store_half(grad_x + 2 * (r * nc + c), o);
@@ -725,11 +723,11 @@ struct RmsBackward {
 
 // By the row's columns: up to 4096, 8192, 16384, 32768.
 using RmsForward0 = RmsForward<8, 1, 4, 3>;
-using RmsForward1 = RmsForward<8, 2, 4, 2>;
+using RmsForward1 = RmsForward<16, 1, 4, 2>;
 using RmsForward2 = RmsForward<16, 2, 4, 1>;
 using RmsForward3 = RmsForward<16, 4, 3, 1>;
 template <bool RES> using RmsBackward0 = RmsBackward<8, 1, 4, 2, RES>;
-template <bool RES> using RmsBackward1 = RmsBackward<8, 2, 2, 2, RES>;
+template <bool RES> using RmsBackward1 = RmsBackward<16, 1, 4, 1, RES>;
 template <bool RES> using RmsBackward2 = RmsBackward<16, 2, 2, 1, RES>;
 template <bool RES> using RmsBackward3 = RmsBackward<16, 4, 1, 1, RES>;
 
