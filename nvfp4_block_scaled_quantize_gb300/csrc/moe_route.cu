@@ -234,13 +234,23 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 
 // ---- dispatch ----------------------------------------------------------------------------
 
+// The expert of a packed row: the first whose end is past it (E when there is none).
+__device__ __forceinline__ int expert_of(const int32_t* ends, int32_t E, int32_t row) {
+  int lo = 0, hi = E;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (ends[mid] > row) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
 // TW warps per token, neighbouring ones taking neighbouring 32 vectors of its row; a CTA holds its
-// warps / TW tokens. The token's maximum is joined in shared memory, so that
-// it costs one atomic for each of its experts. ONE: the grid is one cluster, which joins the
+// warps / TW tokens. The token's maximum is joined in shared memory, so that it costs one atomic for
+// each of its experts. ONE: the grid is one cluster, which joins the
 // experts' maxima in its first CTA's shared memory and writes all of amax itself, so that a small
 // call needs no clearing of amax before it.
 constexpr int kCopyMaxWarps = 32;
-constexpr int64_t kOneClusterTokens = 16;  // 8 CTAs of two tokens, 16 warps each
+constexpr int64_t kOneClusterTokens = 8;  // a CTA of 16 warps each
 template <int TW, int BATCH, bool ONE>
 __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ row_of_slot,
@@ -287,17 +297,12 @@ __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
   }
   __syncthreads();
   if (amax != nullptr && sub == 0 && lane < rows.count) {
-    int lo = 0, hi = E;  // the expert of the row: the first whose end is past it
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > rows.row) hi = mid; else lo = mid + 1;
-    }
+    const int e = expert_of(ends, E, rows.row);
     const uint32_t m = top[mine] << 16;
-    if (lo < E) atomicMax(ONE ? cg::this_cluster().map_shared_rank(joint, 0) + lo : amax + lo, m);
+    if (e < E) atomicMax(ONE ? cg::this_cluster().map_shared_rank(joint, 0) + e : amax + e, m);
   }
-  const int64_t live = ends[E - 1] < 0 ? 0 : ends[E - 1];
   if (token < T)
-    for (int64_t r = live + token; r < P; r += T)
+    for (int64_t r = live_rows(ends, E, P) + token; r < P; r += T)
       for (int64_t v = sub * 32 + lane; v < nv; v += 32 * TW)
         packed[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
   if (ONE) {
@@ -305,6 +310,62 @@ __global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
     if (amax != nullptr && blockIdx.x == 0)
       for (int e = tid; e < E; e += blockDim.x) amax[e] = joint[e];
   }
+}
+
+// Short rows, at most kNarrowVecs vectors: a warp per token, CTAs that stay for many tokens and join
+// the experts' maxima in shared memory. One atomic a slot into the few lines of amax runs at 2 per ns:
+// 16384 x 8 slots of 512 columns take 68.4 us that way and 30.5 us this way.
+constexpr int kNarrowVecs = 128;
+constexpr int kNarrowThreads = 512;
+__global__ void __launch_bounds__(kNarrowThreads, 2) moe_dispatch_narrow_kernel(
+    const uint4* __restrict__ x, const int32_t* __restrict__ row_of_slot,
+    const int32_t* __restrict__ offsets, int64_t T, int32_t K, int32_t E, int64_t nv, uint4* packed,
+    uint32_t* amax, uint32_t* status) {
+  constexpr int kWarps = kNarrowThreads / 32, kBatch = kNarrowVecs / 32;
+  __shared__ int2 scratch[kWarps][32];
+  __shared__ int32_t ends[kMaxSegments];
+  __shared__ uint32_t joint[kMaxSegments];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t P = T * K;
+  pdl_wait();
+  pdl_allow_next();
+  for (int e = tid; e < E; e += kNarrowThreads) {
+    ends[e] = offsets[e];
+    joint[e] = 0u;
+  }
+  __syncthreads();
+  const int64_t live = live_rows(ends, E, P);
+  for (int64_t token = (int64_t)blockIdx.x * kWarps + warp; token < T;
+       token += (int64_t)gridDim.x * kWarps) {
+    uint4 q[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; j++)
+      q[j] = lane + 32 * j < nv ? __ldg(x + token * nv + lane + 32 * j)
+                                : make_uint4(0u, 0u, 0u, 0u);
+    const TokenRows rows = load_token_rows(row_of_slot, token, K, P, scratch, status);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kBatch; j++)
+      m = vmax2(m, vmax2(vmax2(abs2(q[j].x), abs2(q[j].y)), vmax2(abs2(q[j].z), abs2(q[j].w))));
+    for (int k = 0; k < rows.count; k++) {
+      uint4* to = packed + __shfl_sync(0xFFFFFFFFu, rows.row, k) * nv + lane;
+#pragma unroll
+      for (int j = 0; j < kBatch; j++)
+        if (lane + 32 * j < nv) to[32 * j] = q[j];
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    if (lane < rows.count) {
+      const int e = expert_of(ends, E, rows.row);
+      if (e < E) atomicMax(&joint[e], m << 16);
+    }
+    for (int64_t r = live + token; r < P; r += T)
+      for (int64_t v = lane; v < nv; v += 32) packed[r * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+    __syncwarp();  // `scratch` has been read
+  }
+  __syncthreads();
+  if (amax != nullptr)
+    for (int e = tid; e < E; e += kNarrowThreads)
+      if (joint[e]) atomicMax(amax + e, joint[e]);
 }
 
 // ---- combine and the gradient of dispatch ------------------------------------------------
@@ -374,8 +435,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_gather_sum_kernel(
 // the slots of a CTA mostly share a token, whose gradient row then comes from L1. Slot i also
 // clears row i when it lies past the last expert's end.
 constexpr int kSlotThreads = 256;
-constexpr int kDotBatch = 4;
-template <int TW>
+template <int TW, int BATCH>
 __global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(
     const uint4* __restrict__ grad, const uint4* __restrict__ y, const float* __restrict__ weights,
     const int32_t* __restrict__ row_of_slot, const int32_t* __restrict__ offsets, int64_t T,
@@ -403,16 +463,16 @@ __global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(
       uint64_t s = f2_pack(0.0f, 0.0f);
       const uint4 *g = grad + token * nv, *from = y + row * nv;
       uint4* to = grad_y + row * nv;
-      for (int64_t v = v0; v < nv; v += kThreads * kDotBatch) {
-        uint4 a[kDotBatch], b[kDotBatch];
+      for (int64_t v = v0; v < nv; v += kThreads * BATCH) {
+        uint4 a[BATCH], b[BATCH];
 #pragma unroll
-        for (int j = 0; j < kDotBatch; j++) {
+        for (int j = 0; j < BATCH; j++) {
           const bool in = v + kThreads * j < nv;
           b[j] = in ? __ldg(from + v + kThreads * j) : make_uint4(0u, 0u, 0u, 0u);
           a[j] = in ? __ldg(g + v + kThreads * j) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int j = 0; j < kDotBatch; j++) {
+        for (int j = 0; j < BATCH; j++) {
           const uint32_t ae[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
           const uint32_t be[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
           uint32_t o[4];
@@ -542,20 +602,28 @@ static cudaError_t launch_dispatch(const void* x, const int32_t* row_of_slot,
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
                                 int64_t T, int32_t K, int32_t E, int64_t nv, void* packed,
                                 float* amax, uint32_t* status, int sm_count, cudaStream_t s) {
-  if (moe_dispatch_clears_amax(T)) {
-    const int ctas = (int)(T < 8 ? T : 8), tokens = (int)((T + ctas - 1) / ctas);
-    return launch_cluster(moe_dispatch_kernel<16, 2, true>, ctas, 32 * 16 * tokens, 0, s,
+  // up to 8 tokens: 4.5 us and one launch, against 4.7 us and two (8 experts each, 7168 columns)
+  if (moe_dispatch_clears_amax(T))
+    return launch_cluster(moe_dispatch_kernel<16, 2, true>, (int)T, 32 * 16, 0, s,
                           static_cast<const uint4*>(x), row_of_slot, offsets, T, K, E, nv,
                           static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax), status);
+  constexpr int64_t kNarrowTokens = kNarrowThreads / 32;
+  const int64_t wave = (int64_t)sm_count * 2;
+  // short rows this way and the other: 5.3 and 10.6 us at 2000 x 8 rows of 64 vectors, 13.9 and 31.0
+  // at 16384 x 1 of 128, 57.3 and 56.0 at 16384 x 8 of 128 with 256 experts
+  if (nv <= kNarrowVecs) {
+    const int64_t ctas = (T + kNarrowTokens - 1) / kNarrowTokens;
+    return launch_pdl(moe_dispatch_narrow_kernel, dim3((unsigned)(ctas < wave ? ctas : wave)),
+                      dim3(kNarrowThreads), 0, s, static_cast<const uint4*>(x), row_of_slot,
+                      offsets, T, K, E, nv, static_cast<uint4*>(packed),
+                      reinterpret_cast<uint32_t*>(amax), status);
   }
-  // warps per token: a row in one batch of 8 vectors a lane, so that each destination row is
-  // written in one burst, and more warps when the tokens do not give every SM 64
-  const int64_t want = (int64_t)sm_count * 64;
-  if (nv <= 128 && T >= want)
-    return launch_dispatch<1, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
-  if (T * 4 >= want)
-    return launch_dispatch<4, 8>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
-  return launch_dispatch<8, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
+  // a row in one batch of the lanes' vectors, so that each destination row is written in one burst:
+  // eight warps of 4 vectors against four of 8, 81.5 and 83.0 us at 4096 x 8 rows of 896 vectors,
+  // 58.9 and 53.4 us at 8192 x 4 rows of 512
+  if (nv > 512)
+    return launch_dispatch<8, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
+  return launch_dispatch<4, 8>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
 }
 
 template <int VECS>
@@ -573,19 +641,23 @@ static cudaError_t launch_gather(const void* y, const float* weights, const int3
 cudaError_t launch_moe_gather_sum(const void* y, const float* weights, const int32_t* row_of_slot,
                                   int64_t T, int32_t K, int64_t nv, void* out, uint32_t* status,
                                   int sm_count, cudaStream_t s) {
-  if (K <= 2) return launch_gather<4>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
-  if (K <= 4) return launch_gather<2>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
+  // vectors a lane, 1 / 2 / 4: 58.3 / 50.5 / 51.4 us at 8192 x 4 rows of 512 vectors, 80.4 / 77.5 /
+  // 80.9 at 4096 x 8 of 896, 22.5 / 14.4 / 13.3 at 16384 x 1 of 128; with few tokens one vector
+  // leaves more warps: 8.0 / 8.9 / 13.8 at 300 x 8 of 896
+  if (K == 1) return launch_gather<4>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
+  if (K <= 4 || T >= (int64_t)sm_count * 24)
+    return launch_gather<2>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
   return launch_gather<1>(y, weights, row_of_slot, T, K, nv, out, status, sm_count, s);
 }
 
-template <int TW>
+template <int TW, int BATCH>
 static cudaError_t launch_combine_backward(const void* grad, const void* y, const float* weights,
                                            const int32_t* row_of_slot, const int32_t* offsets,
                                            int64_t T, int32_t K, int32_t E, int64_t nv,
                                            void* grad_y, float* grad_w, uint32_t* status,
                                            cudaStream_t s) {
   constexpr int64_t kSlots = kSlotThreads / 32 / TW;
-  return launch_pdl(moe_combine_backward_kernel<TW>,
+  return launch_pdl(moe_combine_backward_kernel<TW, BATCH>,
                     dim3((unsigned)((T * K + kSlots - 1) / kSlots)), dim3(kSlotThreads), 0, s,
                     static_cast<const uint4*>(grad), static_cast<const uint4*>(y), weights,
                     row_of_slot, offsets, T, K, E, nv, static_cast<uint4*>(grad_y), grad_w, status);
@@ -596,12 +668,14 @@ cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const f
                                         int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
                                         float* grad_w, uint32_t* status, int sm_count,
                                         cudaStream_t s) {
-  // several warps per slot when the slots alone do not give every SM 64 warps
-  if (T * K < (int64_t)sm_count * 64 && nv > 32 * kDotBatch)
-    return launch_combine_backward<4>(grad, y, weights, row_of_slot, offsets, T, K, E, nv, grad_y,
-                                      grad_w, status, s);
-  return launch_combine_backward<1>(grad, y, weights, row_of_slot, offsets, T, K, E, nv, grad_y,
-                                    grad_w, status, s);
+  // four warps of 4 vectors per slot when the slots alone do not give every SM 64 warps, else one of
+  // one vector: 3.5 and 5.5 us at 64 x 8 rows of 896 vectors, 42.4 and 43.5 at 1000 x 8, 159.1 and
+  // 147.3 at 4096 x 8 (one warp of 4 vectors: 152.4; more warps in flight beat more loads a warp)
+  if (T * K < (int64_t)sm_count * 64 && nv > 128)
+    return launch_combine_backward<4, 4>(grad, y, weights, row_of_slot, offsets, T, K, E, nv,
+                                         grad_y, grad_w, status, s);
+  return launch_combine_backward<1, 1>(grad, y, weights, row_of_slot, offsets, T, K, E, nv, grad_y,
+                                       grad_w, status, s);
 }
 
 }  // namespace nvfp4
