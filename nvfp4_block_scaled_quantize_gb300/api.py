@@ -312,33 +312,24 @@ def nvfp4_mx_dequantize(codes, scales, fmt="e4m3"):
 
 
 def _check(t, name, dtype, shape, device):
-    """Refuse a tensor that is not a contiguous `dtype` tensor of `shape` on `device`."""
+    """Refuse a tensor that is not a contiguous `dtype` tensor of `shape` on `device`; return it."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
             t.device == device and t.is_contiguous():
-        return
+        return t
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError("%s must be a %s tensor" % (name, dtype))
     if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous (row-major)" % name)
+    raise ValueError("%s must be contiguous (row-major)" % name)
 
 
 def _out(t, name, dtype, shape, device):
     """`t` checked, or a new tensor."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _check(t, name, dtype, shape, device)
-    return t
-
-
-def _outputs(out, wanted, device):
-    """Tensors for {name: (dtype, shape)}: those of the dict `out`, checked, else new ones."""
-    if out is None:
-        return {k: torch.empty(s, dtype=d, device=device) for k, (d, s) in wanted.items()}
-    return {k: _out(out.get(k), k, d, s, device) for k, (d, s) in wanted.items()}
+    return _check(t, name, dtype, shape, device)
 
 
 def nvfp4_moe_plan(expert_ids, num_experts, out=None):
@@ -355,24 +346,34 @@ def nvfp4_moe_plan(expert_ids, num_experts, out=None):
         raise ValueError("expert_ids must be contiguous (row-major)")
     L = _lib.load()
     T, K = expert_ids.shape
-    E, dev, i32 = int(num_experts), expert_ids.device, torch.int32
-    shapes = {"row_of_slot": (T, K), "slot_of_row": (T * K,), "offsets": (max(E, 0),)}
-    plan = _outputs(out, {k: (i32, s) for k, s in shapes.items()}, dev)
-    _raise_if(L.nvfp4_moe_plan(_ptr(expert_ids), expert_ids.element_size(), T, K, E,
-                               _ptr(plan["row_of_slot"]), _ptr(plan["slot_of_row"]),
-                               _ptr(plan["offsets"]), _stream(dev)), "nvfp4_moe_plan")
-    return plan
+    E, dev = int(num_experts), expert_ids.device
+    get = {}.get if out is None else out.get
+    rows = _out(get("row_of_slot"), "row_of_slot", torch.int32, (T, K), dev)
+    slots = _out(get("slot_of_row"), "slot_of_row", torch.int32, (T * K,), dev)
+    offsets = _out(get("offsets"), "offsets", torch.int32, (max(E, 0),), dev)
+    status = L.nvfp4_moe_plan(expert_ids.data_ptr(), expert_ids.element_size(), T, K, E,
+                              rows.data_ptr(), slots.data_ptr(), offsets.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_moe_plan")
+    return {"row_of_slot": rows, "slot_of_row": slots, "offsets": offsets}
 
 
-def _plan_sizes(plan, device):
-    """(row_of_slot, offsets, T, K, E) of a plan, checked."""
-    rows, offsets = plan["row_of_slot"], plan["offsets"]
-    shape, ends = rows.shape, offsets.shape
-    if len(shape) != 2 or len(ends) != 1:
-        raise ValueError("plan: row_of_slot must be [T, K] and offsets [E]")
+def _plan_rows(plan, device):
+    """(row_of_slot, T, K) of a plan, checked."""
+    rows = plan["row_of_slot"]
+    shape = rows.shape
+    if len(shape) != 2:
+        raise ValueError("plan: row_of_slot must be [T, K]")
     _check(rows, "row_of_slot", torch.int32, shape, device)
-    _check(offsets, "offsets", torch.int32, ends, device)
-    return rows, offsets, shape[0], shape[1], ends[0]
+    return rows, shape[0], shape[1]
+
+
+def _plan_offsets(plan, device):
+    """(offsets, E) of a plan, checked."""
+    offsets = plan["offsets"]
+    shape = offsets.shape
+    if len(shape) != 1:
+        raise ValueError("plan: offsets must be [E]")
+    return _check(offsets, "offsets", torch.int32, shape, device), shape[0]
 
 
 def nvfp4_moe_dispatch(x, plan, out=None, amax=None):
@@ -382,13 +383,16 @@ def nvfp4_moe_dispatch(x, plan, out=None, amax=None):
     _check_x(x)
     L = _lib.load()
     T, H = x.shape
-    rows, offsets, t, K, E = _plan_sizes(plan, x.device)
+    dev = x.device
+    rows, t, K = _plan_rows(plan, dev)
+    offsets, E = _plan_offsets(plan, dev)
     if t != T:
         raise ValueError("the plan is for %d tokens, x has %d rows" % (t, T))
-    out = _out(out, "out", torch.bfloat16, (T * K, H), x.device)
-    amax = _out(amax, "amax", torch.float32, (E,), x.device)
-    _raise_if(L.nvfp4_moe_dispatch(_ptr(x), _ptr(rows), _ptr(offsets), T, H, K, E, _ptr(out),
-                                   _ptr(amax), _stream(x.device)), "nvfp4_moe_dispatch")
+    out = _out(out, "out", torch.bfloat16, (T * K, H), dev)
+    amax = _out(amax, "amax", torch.float32, (E,), dev)
+    status = L.nvfp4_moe_dispatch(x.data_ptr(), rows.data_ptr(), offsets.data_ptr(), T, H, K, E,
+                                  out.data_ptr(), amax.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_moe_dispatch")
     return out, amax
 
 
@@ -397,12 +401,15 @@ def nvfp4_moe_dispatch_backward(grad_packed, plan, out=None):
     (BF16 [T * K, H])."""
     _check_x(grad_packed)
     L = _lib.load()
-    rows, _, T, K, _ = _plan_sizes(plan, grad_packed.device)
-    H = grad_packed.shape[1]
-    _check(grad_packed, "grad_packed", torch.bfloat16, (T * K, H), grad_packed.device)
-    out = _out(out, "out", torch.bfloat16, (T, H), grad_packed.device)
-    _raise_if(L.nvfp4_moe_dispatch_backward(_ptr(grad_packed), _ptr(rows), T, H, K, _ptr(out),
-                                            _stream(out.device)), "nvfp4_moe_dispatch_backward")
+    dev = grad_packed.device
+    rows, T, K = _plan_rows(plan, dev)
+    P, H = grad_packed.shape
+    if P != T * K:
+        raise ValueError("grad_packed must have %d rows, not %d" % (T * K, P))
+    out = _out(out, "out", torch.bfloat16, (T, H), dev)
+    status = L.nvfp4_moe_dispatch_backward(grad_packed.data_ptr(), rows.data_ptr(), T, H, K,
+                                           out.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_moe_dispatch_backward")
     return out
 
 
@@ -411,13 +418,16 @@ def nvfp4_moe_combine(y, weights, plan, out=None):
     float32 [T, K] -> BF16 [T, H]. Dropped slots are left out."""
     _check_x(y)
     L = _lib.load()
-    rows, _, T, K, _ = _plan_sizes(plan, y.device)
-    H = y.shape[1]
-    _check(y, "y", torch.bfloat16, (T * K, H), y.device)
-    _check(weights, "weights", torch.float32, (T, K), y.device)
-    out = _out(out, "out", torch.bfloat16, (T, H), y.device)
-    _raise_if(L.nvfp4_moe_combine(_ptr(y), _ptr(weights), _ptr(rows), T, H, K, _ptr(out),
-                                  _stream(y.device)), "nvfp4_moe_combine")
+    dev = y.device
+    rows, T, K = _plan_rows(plan, dev)
+    P, H = y.shape
+    if P != T * K:
+        raise ValueError("y must have %d rows, not %d" % (T * K, P))
+    _check(weights, "weights", torch.float32, (T, K), dev)
+    out = _out(out, "out", torch.bfloat16, (T, H), dev)
+    status = L.nvfp4_moe_combine(y.data_ptr(), weights.data_ptr(), rows.data_ptr(), T, H, K,
+                                 out.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_moe_combine")
     return out
 
 
@@ -427,17 +437,20 @@ def nvfp4_moe_combine_backward(grad_out, y, weights, plan, grad_y=None, grad_wei
     _check_x(grad_out)
     L = _lib.load()
     dev = grad_out.device
-    rows, offsets, T, K, E = _plan_sizes(plan, dev)
-    H = grad_out.shape[1]
-    _check(grad_out, "grad_out", torch.bfloat16, (T, H), dev)
-    _check(y, "y", torch.bfloat16, (T * K, H), dev)
+    rows, T, K = _plan_rows(plan, dev)
+    offsets, E = _plan_offsets(plan, dev)
+    t, H = grad_out.shape
+    if t != T:
+        raise ValueError("grad_out must have %d rows, not %d" % (T, t))
+    packed = (T * K, H)
+    _check(y, "y", torch.bfloat16, packed, dev)
     _check(weights, "weights", torch.float32, (T, K), dev)
-    grad_y = _out(grad_y, "grad_y", torch.bfloat16, (T * K, H), dev)
+    grad_y = _out(grad_y, "grad_y", torch.bfloat16, packed, dev)
     grad_weights = _out(grad_weights, "grad_weights", torch.float32, (T, K), dev)
-    _raise_if(L.nvfp4_moe_combine_backward(_ptr(grad_out), _ptr(y), _ptr(weights), _ptr(rows),
-                                           _ptr(offsets), T, H, K, E, _ptr(grad_y),
-                                           _ptr(grad_weights), _stream(dev)),
-              "nvfp4_moe_combine_backward")
+    status = L.nvfp4_moe_combine_backward(grad_out.data_ptr(), y.data_ptr(), weights.data_ptr(),
+                                          rows.data_ptr(), offsets.data_ptr(), T, H, K, E,
+                                          grad_y.data_ptr(), grad_weights.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_moe_combine_backward")
     return grad_y, grad_weights
 
 
@@ -448,7 +461,7 @@ def _segments(offsets, device):
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         raise TypeError("offsets must be a 1-D int32 CUDA tensor")
     _check(offsets, "offsets", torch.int32, offsets.shape, device)
-    return _ptr(offsets), offsets.shape[0]
+    return offsets.data_ptr(), offsets.shape[0]
 
 
 def nvfp4_swiglu_checkpoint(h, offsets=None, out=None):
@@ -462,15 +475,18 @@ def nvfp4_swiglu_checkpoint(h, offsets=None, out=None):
     M, N = h.shape
     if N % 64 != 0:
         raise ValueError("h must have 2F columns, F a multiple of 32")
-    offs, E = _segments(offsets, h.device)
     dev = h.device
-    out = _outputs(out, {"y": (torch.bfloat16, (M, N // 2)), "codes": (torch.uint8, (M, N)),
-                         "scales": (torch.uint8, (M, N // 32)), "amax": (torch.float32, (E,))}, dev)
-    _raise_if(L.nvfp4_swiglu_checkpoint(_ptr(h), M, N // 2, offs, E, _ptr(out["y"]),
-                                        _ptr(out["codes"]), _ptr(out["scales"]),
-                                        _ptr(out["amax"]), _stream(dev)),
-              "nvfp4_swiglu_checkpoint")
-    return out
+    offs, E = _segments(offsets, dev)
+    get = {}.get if out is None else out.get
+    y = _out(get("y"), "y", torch.bfloat16, (M, N // 2), dev)
+    codes = _out(get("codes"), "codes", torch.uint8, (M, N), dev)
+    scales = _out(get("scales"), "scales", torch.uint8, (M, N // 32), dev)
+    amax = _out(get("amax"), "amax", torch.float32, (E,), dev)
+    status = L.nvfp4_swiglu_checkpoint(h.data_ptr(), M, N // 2, offs, E, y.data_ptr(),
+                                       codes.data_ptr(), scales.data_ptr(), amax.data_ptr(),
+                                       _stream(dev))
+    _raise_if(status, "nvfp4_swiglu_checkpoint")
+    return {"y": y, "codes": codes, "scales": scales, "amax": amax}
 
 
 def nvfp4_swiglu_checkpoint_backward(grad_y, codes, scales, offsets=None, out=None):
@@ -485,9 +501,10 @@ def nvfp4_swiglu_checkpoint_backward(grad_y, codes, scales, offsets=None, out=No
     _check(scales, "scales", torch.uint8, (M, F // 16), dev)
     offs, E = _segments(offsets, dev)
     out = _out(out, "out", torch.bfloat16, (M, 2 * F), dev)
-    _raise_if(L.nvfp4_swiglu_checkpoint_backward(_ptr(grad_y), _ptr(codes), _ptr(scales), M, F,
-                                                 offs, E, _ptr(out), _stream(dev)),
-              "nvfp4_swiglu_checkpoint_backward")
+    status = L.nvfp4_swiglu_checkpoint_backward(grad_y.data_ptr(), codes.data_ptr(),
+                                                scales.data_ptr(), M, F, offs, E, out.data_ptr(),
+                                                _stream(dev))
+    _raise_if(status, "nvfp4_swiglu_checkpoint_backward")
     return out
 
 
@@ -502,15 +519,17 @@ def nvfp4_rmsnorm_checkpoint(x, weight, eps=1e-6, weight_bias=0.0, out=None):
     _check(weight, "weight", torch.bfloat16, (N,), dev)
     if N % 32 != 0:
         raise ValueError("x must have a multiple of 32 columns")
-    out = _outputs(out, {"y": (torch.bfloat16, (M, N)), "codes": (torch.uint8, (M, N)),
-                         "scales": (torch.uint8, (M, N // 32)), "rstd": (torch.float32, (M,)),
-                         "amax": (torch.float32, (1,))}, dev)
-    _raise_if(L.nvfp4_rmsnorm_checkpoint(_ptr(x), _ptr(weight), M, N, float(eps),
-                                         float(weight_bias), _ptr(out["y"]), _ptr(out["codes"]),
-                                         _ptr(out["scales"]), _ptr(out["rstd"]),
-                                         _ptr(out["amax"]), _stream(dev)),
-              "nvfp4_rmsnorm_checkpoint")
-    return out
+    get = {}.get if out is None else out.get
+    y = _out(get("y"), "y", torch.bfloat16, (M, N), dev)
+    codes = _out(get("codes"), "codes", torch.uint8, (M, N), dev)
+    scales = _out(get("scales"), "scales", torch.uint8, (M, N // 32), dev)
+    rstd = _out(get("rstd"), "rstd", torch.float32, (M,), dev)
+    amax = _out(get("amax"), "amax", torch.float32, (1,), dev)
+    status = L.nvfp4_rmsnorm_checkpoint(x.data_ptr(), weight.data_ptr(), M, N, eps, weight_bias,
+                                        y.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                        rstd.data_ptr(), amax.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_rmsnorm_checkpoint")
+    return {"y": y, "codes": codes, "scales": scales, "rstd": rstd, "amax": amax}
 
 
 def nvfp4_rmsnorm_checkpoint_workspace(M, N):
@@ -530,27 +549,29 @@ def nvfp4_rmsnorm_checkpoint_backward(grad_y, codes, scales, rstd, weight, weigh
     nvfp4_rmsnorm_checkpoint_workspace(M, N) bytes."""
     _check_x(grad_y)
     L = _lib.load()
-    M, N = grad_y.shape
+    shape = grad_y.shape
+    M, N = shape
     dev = grad_y.device
     if N % 32 != 0:
         raise ValueError("grad_y must have a multiple of 32 columns")
-    _check(codes, "codes", torch.uint8, (M, N), dev)
+    _check(codes, "codes", torch.uint8, shape, dev)
     _check(scales, "scales", torch.uint8, (M, N // 32), dev)
     _check(rstd, "rstd", torch.float32, (M,), dev)
     _check(weight, "weight", torch.bfloat16, (N,), dev)
     if grad_residual is not None:
-        _check(grad_residual, "grad_residual", torch.bfloat16, (M, N), dev)
-    grad_x = _out(grad_x, "grad_x", torch.bfloat16, (M, N), dev)
+        _check(grad_residual, "grad_residual", torch.bfloat16, shape, dev)
+    grad_x = _out(grad_x, "grad_x", torch.bfloat16, shape, dev)
     grad_weight = _out(grad_weight, "grad_weight", torch.float32, (N,), dev)
     if workspace is None:
         workspace = torch.empty(nvfp4_rmsnorm_checkpoint_workspace(M, N), dtype=torch.uint8,
                                 device=dev)
     else:
         _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    _raise_if(L.nvfp4_rmsnorm_checkpoint_backward(
-        _ptr(grad_y), _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(weight), M, N,
-        float(weight_bias), _ptr(grad_residual), _ptr(grad_x), _ptr(grad_weight),
-        _ptr(workspace), workspace.numel(), _stream(dev)), "nvfp4_rmsnorm_checkpoint_backward")
+    status = L.nvfp4_rmsnorm_checkpoint_backward(
+        grad_y.data_ptr(), codes.data_ptr(), scales.data_ptr(), rstd.data_ptr(), weight.data_ptr(),
+        M, N, weight_bias, _ptr(grad_residual), grad_x.data_ptr(), grad_weight.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream(dev))
+    _raise_if(status, "nvfp4_rmsnorm_checkpoint_backward")
     return grad_x, grad_weight
 
 

@@ -1,6 +1,12 @@
 // Token routing around the grouped quantizer: the plan (a stable counting sort of the (token,
 // choice) slots by expert), the dispatch of token rows into that packed order, the weighted sum
 // of expert outputs back into token order, and the gradients of both.
+//
+// The plan is bound by the shared memory and the stores of the 16 SMs that one cluster has (14.9 us
+// at 262144 slots, whose bytes would take 0.5 us); it stays one launch, which small calls need. The
+// other four are bound by DRAM: at the measured copy rate of 6787 GB/s their bytes take 96% of
+// dispatch's time (4096 x 8 rows of 7168, 80.9 us), 98% of combine's (8192 x 4 of 4096, 50.6 us),
+// 98% of its gradient's (4096 x 8 of 7168, 148.2 us) and 83% to 100% of the gradient of dispatch's.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -431,9 +437,10 @@ __global__ void __launch_bounds__(kRouteThreads) moe_gather_sum_kernel(
 
 // ---- the gradient of combine -------------------------------------------------------------
 
-// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: TW warps per slot;
-// the slots of a CTA mostly share a token, whose gradient row then comes from L1. Slot i also
-// clears row i when it lies past the last expert's end.
+// grad_y[row] = w * grad[t] and grad_w[t, k] = <grad[t], y[row]>: TW warps per slot, so that the
+// product is summed within a warp or two; the slots of a CTA mostly share a token, whose gradient
+// row then comes from L1 (a CTA per token with the row in registers took 170 us at 4096 x 8 rows of
+// 7168 columns). Slot i also clears row i when it lies past the last expert's end.
 constexpr int kSlotThreads = 256;
 template <int TW, int BATCH>
 __global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(

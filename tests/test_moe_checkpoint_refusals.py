@@ -143,5 +143,7 @@ def test_binding_refuses_before_it_calls_the_library():
     with pytest.raises(ValueError):
         api._check(x, "x", torch.bfloat16, (4, 64), torch.device("cuda"))
     with pytest.raises(ValueError):
-        api._plan_sizes(dict(plan, offsets=torch.zeros(2, 4, dtype=torch.int32)), cpu)
+        api._plan_offsets(dict(plan, offsets=torch.zeros(2, 4, dtype=torch.int32)), cpu)
+    with pytest.raises(ValueError):
+        api._plan_rows(dict(plan, row_of_slot=torch.zeros(8, dtype=torch.int32)), cpu)
     assert api.nvfp4_rmsnorm_checkpoint_workspace(2, 96) == 2 * 96 * 4
