@@ -70,11 +70,10 @@ __device__ __forceinline__ float inverse_scale(uint32_t scale) {
 // infinity), so they reach the gradient, and do not count for the maximum, which is returned.
 // Finite magnitudes from 1.9375 * 2^127 up would round to 2^128, outside binary32: they are kept
 // as 1.875 * 2^127, so that what is finite stays finite.
-template <int WORDS>
-__device__ __forceinline__ uint32_t clean_words(uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ uint32_t clean_words(uint32_t (&w)[8]) {
   uint32_t top = 0u;
 #pragma unroll
-  for (int i = 0; i < 2 * WORDS; i++) {
+  for (int i = 0; i < 16; i++) {
     const int sh = 16 * (i & 1);
     const uint32_t h = (w[i >> 1] >> sh) & 0xFFFFu, b = h & 0x7FFFu;
     uint32_t c = h;
@@ -86,33 +85,29 @@ __device__ __forceinline__ uint32_t clean_words(uint32_t (&w)[WORDS]) {
   return top;
 }
 
-// E4M3 codes and the scale byte of a block of 32, 2 * WORDS values in each of 16 / WORDS
-// neighbouring lanes, which call it at once. Scaling by a power of two is exact, so each code is
-// rounded once.
-template <int WORDS>
-__device__ __forceinline__ void keep_block(const uint32_t (&words)[WORDS], uint32_t (&codes)[WORDS / 2],
-                                           uint32_t& scale) {
-  constexpr int kLanes = 16 / WORDS;
-  const uint32_t mates = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
-  uint32_t m = abs2(words[0]);
+// E4M3 codes of the lane's half of a block of 32 and the block's scale byte, called by both lanes
+// of the pair (lane, lane ^ 1) at once. Scaling by a power of two is exact, so each code is rounded
+// once.
+__device__ __forceinline__ void keep_half(const Half32& half, uint32_t (&codes)[4],
+                                          uint32_t& scale) {
+  const uint32_t pair = 3u << (threadIdx.x & 30);
+  uint32_t m = abs2(half.w[0]);
 #pragma unroll
-  for (int i = 1; i < WORDS; i++) m = vmax2(m, abs2(words[i]));
+  for (int i = 1; i < 8; i++) m = vmax2(m, abs2(half.w[i]));
   uint32_t top = pair_bits(m);
+  top = max(top, __shfl_xor_sync(pair, top, 1));
+  uint32_t w[8];
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
-  uint32_t w[WORDS];
-#pragma unroll
-  for (int i = 0; i < WORDS; i++) w[i] = words[i];
-  if (top >= kRoundsToInf) {  // all lanes of the block
+  for (int i = 0; i < 8; i++) w[i] = half.w[i];
+  if (top >= kRoundsToInf) {  // both lanes of the block
     top = clean_words(w);
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(mates, top, o));
+    top = max(top, __shfl_xor_sync(pair, top, 1));
   }
   scale = scale_byte(top);
   const float inv = inverse_scale(scale);
   const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
-  for (int i = 0; i < WORDS / 2; i++) {
+  for (int i = 0; i < 4; i++) {
     const float2 lo = f2_unpack(f2_mul(f2_from_bf16x2(w[2 * i]), inv2));
     const float2 hi = f2_unpack(f2_mul(f2_from_bf16x2(w[2 * i + 1]), inv2));
     codes[i] = e4m3x2(lo.x, lo.y) | (e4m3x2(hi.x, hi.y) << 16);
@@ -125,14 +120,13 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
                  : (s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s << 23));
 }
 
-// Four codes a word times a factor, as packed pairs. The factor is the block's scale, alone or
-// times another number: E4M3 values times a power of two are exact, so the product is rounded once.
-template <int WORDS>
-__device__ __forceinline__ void kept_values(const uint32_t (&w)[WORDS], float factor,
-                                            uint64_t (&v)[2 * WORDS]) {
+// 16 codes times a factor, as packed pairs. The factor is the block's scale, alone or times another
+// number: E4M3 values times a power of two are exact, so the product is rounded once.
+__device__ __forceinline__ void kept_values(const uint4& codes, float factor, uint64_t (&v)[8]) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
   const uint64_t f2 = f2_pack(factor, factor);
 #pragma unroll
-  for (int i = 0; i < 2 * WORDS; i++) {
+  for (int i = 0; i < 8; i++) {
     const float2 f = e4m3x2_to_float2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
     v[i] = f2_mul(f2_pack(f.x, f.y), f2);
   }
@@ -242,8 +236,8 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
         mm = vmax2(mm, abs2(o[i]));
       }
       m = max(m, pair_bits(mm));
-      keep_block(g.w, kg, sg);
-      keep_block(u.w, ku, su);
+      keep_half(g, kg, sg);
+      keep_half(u, ku, su);
     }
     store_half(y + (r * nc + c) * 2, o);
     codes[r * 2 * nc + c] = make_uint4(kg[0], kg[1], kg[2], kg[3]);
@@ -276,8 +270,8 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
       uint64_t g[8], u[8];
       const Half32 d = load_half(grad + (r * nc + c) * 2);
       const uint4 kg = __ldg(codes + r * 2 * nc + c), ku = __ldg(codes + r * 2 * nc + nc + c);
-      kept_values({kg.x, kg.y, kg.z, kg.w}, e8m0_value(scales[r * nc + c / 2]), g);
-      kept_values({ku.x, ku.y, ku.z, ku.w}, e8m0_value(scales[r * nc + nc / 2 + c / 2]), u);
+      kept_values(kg, e8m0_value(scales[r * nc + c / 2]), g);
+      kept_values(ku, e8m0_value(scales[r * nc + nc / 2 + c / 2]), u);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         float dg[2], du[2];
@@ -482,7 +476,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_kernel(
         m = vmax2(m, abs2(o[i]));
       }
       store_half(y + 2 * p, o);
-      keep_block(w[j].w, k, sc);
+      keep_half(w[j], k, sc);
       codes[p] = make_uint4(k[0], k[1], k[2], k[3]);
       if ((c & 1) == 0) scales[p / 2] = (uint8_t)sc;  // (rows are an even number of halves)
     }
@@ -578,7 +572,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
     const int at_stage = tiles.stage * kStage;
     auto prepare = [&](int j, uint64_t (&d)[8]) {  // dy, xh and g of the thread's j-th columns
       const uint4 k = *reinterpret_cast<const uint4*>(mine8 + at_stage + j * threads * 16);
-      kept_values({k.x, k.y, k.z, k.w}, factor[j], h);
+      kept_values(k, factor[j], h);
       unpack16(shared_half(mine + at_stage + j * threads * 32), d);
       if (ITEMS > 1) biased_weight(load_half(weight + 2 * (at + j * threads)), bias, w);
 #pragma unroll

@@ -11,6 +11,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "nvfp4_device.cuh"
@@ -21,7 +22,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanMaxCtas = 16;  // one cluster of the opt-in size
+constexpr int kPlanMaxCtas = 16;  // one cluster of the opt-in size (8 where 16 SMs do not fit)
 constexpr int kPlanMaxRun = 832;  // slots of a warp's run that is sorted in shared memory
 constexpr int kPlanBatch = 8;  // groups of 32 slots whose ids a warp loads together
 constexpr int kRouteThreads = 128;
@@ -255,10 +256,10 @@ __device__ __forceinline__ int expert_of(const int32_t* ends, int32_t E, int32_t
 // each of its experts. ONE: the grid is one cluster, which joins the
 // experts' maxima in its first CTA's shared memory and writes all of amax itself, so that a small
 // call needs no clearing of amax before it.
-constexpr int kCopyMaxWarps = 32;
+constexpr int kCopyMaxWarps = 16;
 constexpr int64_t kOneClusterTokens = 8;  // a CTA of 16 warps each
 template <int TW, int BATCH, bool ONE>
-__global__ void __launch_bounds__(32 * kCopyMaxWarps, 1) moe_dispatch_kernel(
+__global__ void __launch_bounds__(32 * kCopyMaxWarps, 2) moe_dispatch_kernel(
     const uint4* __restrict__ x, const int32_t* __restrict__ row_of_slot,
     const int32_t* __restrict__ offsets, int64_t T, int32_t K, int32_t E, int64_t nv, uint4* packed,
     uint32_t* amax, uint32_t* status) {
@@ -523,12 +524,32 @@ static cudaError_t prepare_plan() {
                               plan_smem_bytes(kPlanThreads / 32, kPlanMaxRun, STAGED));
 }
 
+static std::atomic<int> g_plan_ctas{kPlanMaxCtas};
+
 cudaError_t prepare_moe_kernels() {
   cudaError_t e = cudaSuccess, r;
   if ((r = prepare_plan<int32_t, false>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int32_t, true>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int64_t, false>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int64_t, true>()) != cudaSuccess) e = r;
+  // a context with fewer SMs (a green context, a reduced share) may not hold the large cluster
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPlanMaxCtas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_smem_bytes(kPlanThreads / 32, kPlanMaxRun, true);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kPlanMaxCtas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, moe_plan_kernel<int64_t, true>, &cfg) !=
+          cudaSuccess ||
+      clusters < 1) {
+    (void)cudaGetLastError();
+    g_plan_ctas.store(8);
+  }
   return e;
 }
 
@@ -559,7 +580,7 @@ static cudaError_t launch_plan(const void* ids, int32_t n, int32_t E, int32_t* r
                                cudaStream_t s) {
   // one CTA against the cluster, 256 threads: 4.1 and 4.2 us at 1024 slots, 5.1 and 4.4 at 2048;
   // the cluster with 256 and with 1024 threads: 5.0 and 6.3 us at 16384
-  const int threads = n <= 16384 ? kMaxSegments : kPlanThreads, ctas = n <= 1024 ? 1 : kPlanMaxCtas;
+  const int threads = n <= 16384 ? kMaxSegments : kPlanThreads, ctas = n <= 1024 ? 1 : g_plan_ctas.load();
   const int warps = threads / 32;
   const int64_t lanes = (int64_t)ctas * threads;
   const int32_t run = (int32_t)((n + lanes - 1) / lanes * 32);
