@@ -286,6 +286,38 @@ def test_rmsnorm_backward(M, N, residual, bias):
     assert bool(((gw.cpu().double() - ref_w).abs() <= off_w).all())
 
 
+@pytest.mark.parametrize("M,N", [(22000, 512), (9001, 1056), (3100, 4096), (2100, 8192), (1000, 16384)])
+def test_rmsnorm_many_tiles(M, N):
+    """Rows enough that every CTA goes round its ring of tiles several times: each row equals the
+    same row of a call whose CTAs have one tile each."""
+    dev = _cuda()
+    g = torch.Generator(device=dev).manual_seed(N)
+    draw = lambda *s: torch.randn(*s, generator=g, device=dev)
+    x, res = draw(M, N).to(torch.bfloat16), (draw(M, N) * 1e-3).to(torch.bfloat16)
+    dy, w = (draw(M, N) * 1e-3).to(torch.bfloat16), (1 + 0.3 * draw(N)).to(torch.bfloat16)
+    a = api.nvfp4_rmsnorm_checkpoint(x, w)
+    for r in (None, res):
+        gx, gw = api.nvfp4_rmsnorm_checkpoint_backward(dy, a["codes"], a["scales"], a["rstd"], w,
+                                                       grad_residual=r)
+        for i in range(0, M, 140):
+            s = slice(i, min(i + 140, M))
+            if r is None:
+                b = api.nvfp4_rmsnorm_checkpoint(x[s], w)
+                for k in ("y", "codes", "scales", "rstd"):
+                    assert torch.equal(a[k][s], b[k]), (k, i)
+            gb, _ = api.nvfp4_rmsnorm_checkpoint_backward(
+                dy[s], a["codes"][s], a["scales"][s], a["rstd"][s], w,
+                grad_residual=None if r is None else r[s])
+            assert torch.equal(gx[s], gb), i
+        xh = (a["codes"].view(torch.float8_e4m3fn).double() *
+              torch.exp2(a["scales"].double() - 127).repeat_interleave(32, 1) *
+              a["rstd"].double().unsqueeze(1))
+        prod = dy.double() * xh
+        assert bool(((gw.double() - prod.sum(0)).abs() <=
+                     (M + 64) * U32 * prod.abs().sum(0)).all())
+    assert a["amax"].item() == float(a["y"].abs().max())
+
+
 def test_rmsnorm_gradient_against_differences():
     dev = _cuda()
     M, N, step, eps = 5, 96, 2.0 ** -12, 1e-5

@@ -47,10 +47,12 @@ def _check_plan(plan, ids, E):
     assert np.array_equal(plan["offsets"].cpu().numpy(), offsets)
 
 
-# one slot; one warp's run; a run's edge and one past it; one CTA and the cluster; odd sizes
+# one slot; one warp's run; a run's edge and one past it; one CTA and the cluster; odd sizes; runs
+# that are sorted before they are written and runs too long for it
 PLANS = [(1, 1, 1, 0.0), (1, 8, 256, 0.0), (4, 8, 8, 0.0), (33, 1, 2, 0.0), (16, 32, 5, 0.5),
          (1000, 3, 37, 0.1), (1024, 1, 256, 0.0), (1025, 4, 64, 0.0), (4096, 1, 3, 0.0),
-         (4097, 1, 3, 0.02), (5003, 6, 256, 0.06), (9999, 7, 61, 0.3), (40000, 8, 64, 0.01)]
+         (4097, 1, 3, 0.02), (5003, 6, 256, 0.06), (9999, 7, 61, 0.3), (40000, 8, 64, 0.01),
+         (60000, 8, 20, 0.01)]
 
 
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64], ids=["int32", "int64"])
@@ -87,7 +89,8 @@ def test_plan_flags_and_drops_ids_past_the_experts(value):
 
 # T, K, E, H, drop: single tokens, one vector a row, odd vectors, more than 128 vectors, many tokens
 SIZES = [(1, 1, 1, 8, 0.0), (1, 8, 256, 7168, 0.0), (3, 32, 5, 24, 0.3), (7, 2, 4, 1032, 0.0),
-         (33, 6, 37, 2056, 0.2), (700, 3, 11, 136, 0.1), (1300, 4, 64, 1040, 0.0), (50, 4, 8, 64, 1.0)]
+         (33, 6, 37, 2056, 0.2), (700, 3, 11, 136, 0.1), (1300, 4, 64, 1040, 0.0), (50, 4, 8, 64, 1.0),
+         (20, 8, 64, 7168, 0.1), (500, 1, 9, 2056, 0.1), (3700, 5, 16, 264, 0.02)]
 
 
 def _setup(T, K, E, H, drop, seed=0):
