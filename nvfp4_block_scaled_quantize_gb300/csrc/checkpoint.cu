@@ -730,7 +730,10 @@ struct RmsBackward {
 // thread, 106.5 with two of 16 warps and 16. Backward, 16384 x 8192 with the residual: 158.7 with two
 // of 8 warps and 32 columns a thread (which decode every code twice), 141.3 with one of 16 warps and
 // 16; 32768 x 4096: 115.6 with two of 8 warps, 117.4 with one of 16. Beyond 8192 columns the weight
-// gradient's accumulators leave no registers to keep xh in, and the codes are decoded twice.
+// gradient's accumulators leave no registers to keep xh in, and the codes are decoded twice; the
+// weights are read for every row, so the ring must leave them L1: 8192 x 16384 takes 145 us with two
+// stages and 167 with four. 4096 x 32768: 152 us with two stages, 162 with one (all that fits with the
+// residual).
 using RmsForward0 = RmsForward<8, 1, 4, 3>;
 using RmsForward1 = RmsForward<16, 1, 4, 2>;
 using RmsForward2 = RmsForward<16, 2, 4, 1>;
@@ -738,7 +741,7 @@ using RmsForward3 = RmsForward<16, 4, 3, 1>;
 template <bool RES> using RmsBackward0 = RmsBackward<8, 1, 4, 2, RES>;
 template <bool RES> using RmsBackward1 = RmsBackward<16, 1, 4, 1, RES>;
 template <bool RES> using RmsBackward2 = RmsBackward<16, 2, 2, 1, RES>;
-template <bool RES> using RmsBackward3 = RmsBackward<16, 4, 1, 1, RES>;
+template <bool RES> using RmsBackward3 = RmsBackward<16, 4, RES ? 1 : 2, 1, RES>;
 
 template <bool RES>
 cudaError_t rms_backward(const RmsArgs& a, int sm_count, cudaStream_t s) {
