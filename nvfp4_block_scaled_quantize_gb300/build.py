@@ -20,7 +20,7 @@ SOURCES = ["quantize_row.cu", "quantize_col.cu", "quantize_rowcol.cu", "quantize
            "host_pipeline.cu", "amax_pass.cu", "mx_kernel.cu", "producer.cu",
            "moe_route.cu", "checkpoint.cu", "moe_checkpoint_api.cu"]
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "aux_internal.h", "quantize_kernel.cuh",
-           "fused_amax.cuh"]
+           "fused_amax.cuh", "tile_ring.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -18,6 +18,7 @@
 #include "nvfp4_device.cuh"
 #include "aux_internal.h"
 #include "nvfp4_internal.h"
+#include "tile_ring.h"
 
 namespace nvfp4 {
 namespace {
@@ -317,41 +318,23 @@ RmsShape rms_shape(int64_t N, int warps, int items) {
   return s;
 }
 
-__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(to)),
-      "l"(from), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// One thread's waits for the CTA's tiles. A wait that gives up is reported and the thread's later
-// ones are skipped, so that every thread still reaches every barrier of the CTA; thread 0 then
-// fetches no more, and the CTA leaves only once the copies in flight have landed (bounded too).
+// A thread's waits for the CTA's tiles (thread 0 is the ring's owner). A wait that gives up is
+// reported.
 template <int STAGES>
-struct TileWaits {
+struct TileWaits : TileRing<STAGES> {
   uint64_t* full;
   uint32_t* status;
-  int stage = 0;
-  uint32_t parity = 0;
-  bool dead = false;
-  __device__ void wait() {
-    if (!dead && !mbar_wait_bounded(&full[stage], parity, kTileWaitNs)) {
-      dead = true;
-      atomicOr(status, kTimeout);
-    }
-  }
-  __device__ void next() {
-    if (++stage == STAGES) {
-      stage = 0;
-      parity ^= 1u;
-    }
-  }
-  __device__ void drain() {
-    if (dead)
-      for (int i = 0; i < STAGES; i++)
-        mbar_wait_bounded(&full[i], i < stage ? parity : parity ^ 1u, kTileWaitNs);
+  __device__ TileWaits(uint64_t* full_, uint32_t* status_) : full(full_), status(status_) {}
+  // `first` is the tile's first row; the next tiles start `step` rows on, below M.
+  __device__ void wait(int64_t first, int64_t step, int64_t M) {
+    TileRing<STAGES>::wait(
+        threadIdx.x == 0,
+        [&](int stage, uint32_t parity) {
+          if (mbar_wait_bounded(&full[stage], parity, kTileWaitNs)) return true;
+          atomicOr(status, kTimeout);
+          return false;
+        },
+        [&](int i) { return first + i * step < M; });
   }
 };
 
@@ -430,15 +413,15 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_kernel(
   };
   int64_t first = (int64_t)blockIdx.x * groups;  // of the tile
   if (tid == 0)
-    for (int i = 0; i < STAGES - 1; i++) fetch(i, first + i * step);
-  TileWaits<STAGES> tiles{full, status};
+    for (int i = 0; i < TileRing<STAGES>::kAhead; i++) fetch(i, first + i * step);
+  TileWaits<STAGES> tiles(full, status);
   uint32_t m = 0u;
   int turn = 0;
   const uint8_t* const mine = ring + ((size_t)group * nc + at) * 32;
   for (; first < M; first += step) {
     const int64_t r = first + group, pos = r * nc + at;
     const bool live = r < M;
-    tiles.wait();
+    tiles.wait(first, step, M);
     Half32 w[ITEMS];
     uint64_t s = f2_pack(0.0f, 0.0f);
 #pragma unroll
@@ -481,7 +464,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_kernel(
       if ((c & 1) == 0) scales[p / 2] = (uint8_t)sc;  // (rows are an even number of halves)
     }
   }
-  tiles.drain();
   m = __reduce_max_sync(0xFFFFFFFFu, pair_bits(m));
   if (lane == 0) top[warp] = m;
   __syncthreads();
@@ -554,9 +536,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
   };
   int64_t first = (int64_t)blockIdx.x * groups;  // of the tile
   if (tid == 0)
-    for (int i = 0; i < (STAGES > 1 ? STAGES - 1 : 1); i++) fetch(i, first + i * step);
+    for (int i = 0; i < TileRing<STAGES>::kAhead; i++) fetch(i, first + i * step);
   fetch_scales(first + group);
-  TileWaits<STAGES> tiles{full, status};
+  TileWaits<STAGES> tiles(full, status);
   int turn = 0;
   const uint8_t* const mine = ring + ((size_t)group * nc + at) * 32;
   const uint8_t* const mine8 = ring + kCodes + ((size_t)group * nc + at) * 16;
@@ -568,7 +550,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
 #pragma unroll
     for (int j = 0; j < ITEMS; j++) factor[j] = __fmul_rn(e8m0_value(next_sc[j]), rs);
     fetch_scales(r + step);
-    tiles.wait();
+    tiles.wait(first, step, M);
     const int at_stage = tiles.stage * kStage;
     auto prepare = [&](int j, uint64_t (&d)[8]) {  // dy, xh and g of the thread's j-th columns
       const uint4 k = *reinterpret_cast<const uint4*>(mine8 + at_stage + j * threads * 16);
@@ -618,7 +600,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) rmsnorm_checkpoint_backward_
       if (tid == 0 && !tiles.dead) fetch(0, first + step);
     }
   }
-  tiles.drain();
   float4* out = reinterpret_cast<float4*>(partial + (int64_t)blockIdx.x * N);
   for (int g = 0; g < groups; g++) {
     if (group == g) {

@@ -429,6 +429,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// Untiled bulk copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`; both
+// addresses are 16-byte aligned.
+__device__ __forceinline__ void bulk_load(void* to, const void* from, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(to)),
+      "l"(from), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 2D tiled TMA load of the box at (x = innermost element index, y = row) into shared memory,
 // completing on `bar`. Out-of-range rows and columns are filled with zeros.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tensor_map, int32_t x,
