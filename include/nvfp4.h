@@ -415,7 +415,8 @@ nvfp4_status nvfp4_swiglu_checkpoint(const void* h, int64_t M, int64_t F, const 
                                      float* amax, void* stream);
 
 /* grad_h [M][2F] from grad_y [M][F] and the kept h: with s = sigmoid(g),
- * dg = dy * u * s * (1 + g * (1 - s)), du = dy * g * s, binary32 and rounded once to BF16. */
+ * dg = dy * u * s * (1 + g * (1 - s)), du = dy * g * s, binary32 and rounded once to BF16.
+ * offsets as above: rows past the last end are not read and get zeros, bad offsets are flagged. */
 nvfp4_status nvfp4_swiglu_checkpoint_backward(const void* grad_y, const uint8_t* codes,
                                               const uint8_t* scales, int64_t M, int64_t F,
                                               const int32_t* offsets, int32_t E, void* grad_h,

@@ -183,11 +183,17 @@ struct GluWalk {
   }
 };
 
+// Rows before the last expert's end, within [0, M]. The first CTA flags ends that do not ascend from 0
+// to M.
 __device__ __forceinline__ int64_t live_of(const int32_t* offsets, int32_t E, int64_t M,
                                            uint32_t* status) {
   if (offsets == nullptr) return M;
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e < E; e += kGluThreads) {
+      const int32_t v = offsets[e];
+      if (v < (e > 0 ? offsets[e - 1] : 0) || v > M) atomicOr(status, kBadOffsets);
+    }
   const int64_t v = offsets[E - 1];
-  if ((v < 0 || v > M) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kBadOffsets);
   return v < 0 ? 0 : (v < M ? v : M);
 }
 
@@ -204,8 +210,6 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
   for (int e = tid; e < E; e += kGluThreads) {
     ends[e] = offsets ? offsets[e] : (int32_t)M;
     top[e] = 0u;
-    if (blockIdx.x == 0 && offsets && e > 0 && offsets[e] < offsets[e - 1])
-      atomicOr(status, kBadOffsets);
   }
   __syncthreads();
   const int64_t nc = F / 16;
