@@ -332,6 +332,9 @@ def _out(t, name, dtype, shape, device):
     return _check(t, name, dtype, shape, device)
 
 
+MAX_EXPERTS = 256
+
+
 def nvfp4_moe_plan(expert_ids, num_experts, out=None):
     """Sort the (token, choice) slots of expert_ids (int32 or int64 [T, K], negative: dropped) by
     expert. Returns a plan, a dict of int32 tensors: row_of_slot [T, K] (-1: dropped),
@@ -346,11 +349,12 @@ def nvfp4_moe_plan(expert_ids, num_experts, out=None):
         raise ValueError("expert_ids must be contiguous (row-major)")
     L = _lib.load()
     T, K = expert_ids.shape
-    E, dev = int(num_experts), expert_ids.device
+    # the library refuses what lies outside 1 .. MAX_EXPERTS; a C int would wrap around before it
+    E, dev = max(0, min(int(num_experts), MAX_EXPERTS + 1)), expert_ids.device
     get = {}.get if out is None else out.get
     rows = _out(get("row_of_slot"), "row_of_slot", torch.int32, (T, K), dev)
     slots = _out(get("slot_of_row"), "slot_of_row", torch.int32, (T * K,), dev)
-    offsets = _out(get("offsets"), "offsets", torch.int32, (max(E, 0),), dev)
+    offsets = _out(get("offsets"), "offsets", torch.int32, (E,), dev)
     status = L.nvfp4_moe_plan(expert_ids.data_ptr(), expert_ids.element_size(), T, K, E,
                               rows.data_ptr(), slots.data_ptr(), offsets.data_ptr(), _stream(dev))
     _raise_if(status, "nvfp4_moe_plan")
