@@ -499,6 +499,11 @@ nvfp4_status nvfp4_debug_fused_takeovers(void* stream, uint32_t* count);
  * Errors: NVFP4_ERR_INVALID_ARG (on not 0 or 1). */
 nvfp4_status nvfp4_debug_fail_next_launch(int32_t on);
 
+/* Test hook for the set-up of the routing and checkpoint kernels (shared memory and cluster
+ * size, once per device). fault = 1: it counts as failed; those calls return NVFP4_ERR_CUDA and
+ * every other call runs. 0 clears it. Not for production use. Errors: NVFP4_ERR_INVALID_ARG (any other fault). */
+nvfp4_status nvfp4_debug_setup_fault(int32_t fault);
+
 /* Host pipeline: quantization of tensors that live in host memory, with the copies of
  * consecutive submissions overlapped (the input of one on the host-to-device link while the
  * outputs of the previous one use the device-to-host direction). Runtime plumbing around

@@ -30,6 +30,7 @@ EXPORTED = ["nvfp4_status_string", "nvfp4_amax", "nvfp4_quantize", "nvfp4_quanti
             "nvfp4_amax_grouped", "nvfp4_debug_fused_extra_arrivals",
             "nvfp4_debug_fail_next_launch", "nvfp4_noalloc_get_status",
             "nvfp4_debug_fused_late_ctas", "nvfp4_debug_fused_takeovers",
+            "nvfp4_debug_setup_fault",
             "nvfp4_moe_plan", "nvfp4_moe_dispatch", "nvfp4_moe_dispatch_backward",
             "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_swiglu_checkpoint",
             "nvfp4_swiglu_checkpoint_backward", "nvfp4_rmsnorm_checkpoint",
@@ -132,6 +133,8 @@ def load(build_if_missing: bool = False):
     L.nvfp4_debug_fused_extra_arrivals.argtypes = [i32]
     L.nvfp4_debug_fail_next_launch.restype = ctypes.c_int
     L.nvfp4_debug_fail_next_launch.argtypes = [i32]
+    L.nvfp4_debug_setup_fault.restype = ctypes.c_int
+    L.nvfp4_debug_setup_fault.argtypes = [i32]
     L.nvfp4_noalloc_get_status.restype = ctypes.c_int
     L.nvfp4_noalloc_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
     L.nvfp4_debug_fused_late_ctas.restype = ctypes.c_int

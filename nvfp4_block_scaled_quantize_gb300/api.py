@@ -643,6 +643,12 @@ def nvfp4_debug_fail_next_launch(on=True):
               "nvfp4_debug_fail_next_launch")
 
 
+def nvfp4_debug_setup_fault(fault=0):
+    """Test hook: with fault = 1 the set-up of the routing and checkpoint kernels counts as failed,
+    so their calls raise NVFP4Error(NVFP4_ERR_CUDA); 0 clears it."""
+    _raise_if(_lib.load().nvfp4_debug_setup_fault(int(fault)), "nvfp4_debug_setup_fault")
+
+
 def quantize_from_host(x_host, pinned_out=None, **kw):
     """End-to-end call for host data: copy a pinned host BF16 tensor to the device, quantize,
     and copy every output back into pinned host tensors (all on the current stream)."""

@@ -90,8 +90,8 @@ struct RmsArgs {
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s);
 
-// The current device's SM count and status word, set up on first need (nvfp4_api.cu); false when
-// a CUDA call failed.
+// The current device's SM count and status word, with the kernels of these two groups set up
+// (nvfp4_api.cu); false when a CUDA call failed.
 bool device_resources(int* sm_count, uint32_t** status);
 
 cudaError_t launch_amax_flat(const void* x, int64_t n_elems, float* out0, float* out1, int grid,

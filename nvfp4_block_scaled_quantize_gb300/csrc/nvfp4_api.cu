@@ -26,6 +26,7 @@ static_assert((kFuseWsOffset + kFuseWsWords) * 4 <= (int)kWorkspaceBytes, "works
 
 struct DeviceState {
   bool ready = false;
+  bool aux_ready = false;         // the routing and checkpoint kernels' attributes are set
   int sm_count = 0;
   uint32_t* workspace = nullptr;  // [0] status word; the library's own or the caller's
   uint32_t* own = nullptr;        // the library's own workspace, allocated on first need
@@ -38,6 +39,8 @@ std::atomic<int32_t> g_fuse_extra{0};
 // CTAs of the next single-launch amax that hold back until every rank has arrived
 // (nvfp4_debug_fused_late_ctas)
 std::atomic<int32_t> g_fuse_late{0};
+// nvfp4_debug_setup_fault
+std::atomic<int32_t> g_setup_fault{0};
 // Set: the next quantize call launches an empty grid, which the runtime rejects
 // (nvfp4_debug_fail_next_launch)
 std::atomic<int32_t> g_fail_next{0};
@@ -48,6 +51,18 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
+
+// Sets up the routing and checkpoint kernels (under g_mutex): with the quantizer's, so that a capture
+// after any first call finds them ready, but without failing those where they cannot be (a device
+// share without their shared memory or cluster size); their own calls then try again.
+bool prepare_aux(DeviceState& st) {
+  if (g_setup_fault.load() == 1) return false;
+  if (st.aux_ready) return true;
+  st.aux_ready =
+      prepare_moe_kernels() == cudaSuccess && prepare_checkpoint_kernels() == cudaSuccess;
+  if (!st.aux_ready) (void)cudaGetLastError();
+  return st.aux_ready;
+}
 
 // Everything of a device's state but its workspace (under g_mutex).
 nvfp4_status init_device(DeviceState& st, int dev) {
@@ -64,6 +79,7 @@ nvfp4_status init_device(DeviceState& st, int dev) {
       return NVFP4_ERR_CUDA;
     g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   }
+  (void)prepare_aux(st);
   st.ready = true;
   return NVFP4_OK;
 }
@@ -148,6 +164,10 @@ __global__ void gscale_fill_kernel(const float* amax, float* gscale, int n) {
 bool device_resources(int* sm_count, uint32_t** status) {
   DeviceState* ds = nullptr;
   if (device_state(&ds) != NVFP4_OK) return false;
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!prepare_aux(*ds)) return false;
+  }
   *sm_count = ds->sm_count;
   *status = ds->workspace;
   return true;
@@ -178,8 +198,6 @@ cudaError_t prepare_quantize_kernels() {
   if ((r = prepare_quantize_2d()) != cudaSuccess) e = r;
   if ((r = prepare_amax_tiles()) != cudaSuccess) e = r;
   if ((r = prepare_mx_kernels()) != cudaSuccess) e = r;
-  if ((r = prepare_moe_kernels()) != cudaSuccess) e = r;
-  if ((r = prepare_checkpoint_kernels()) != cudaSuccess) e = r;
   return e;
 }
 
@@ -701,6 +719,12 @@ NVFP4_EXPORT nvfp4_status nvfp4_debug_fused_takeovers(void* stream, uint32_t* co
 NVFP4_EXPORT nvfp4_status nvfp4_debug_fail_next_launch(int32_t on) {
   if (on != 0 && on != 1) return NVFP4_ERR_INVALID_ARG;
   g_fail_next.store(on);
+  return NVFP4_OK;
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_debug_setup_fault(int32_t fault) {
+  if (fault < 0 || fault > 1) return NVFP4_ERR_INVALID_ARG;
+  g_setup_fault.store(fault);
   return NVFP4_OK;
 }
 
