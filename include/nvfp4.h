@@ -501,7 +501,9 @@ nvfp4_status nvfp4_debug_fail_next_launch(int32_t on);
 
 /* Test hook for the set-up of the routing and checkpoint kernels (shared memory and cluster
  * size, once per device). fault = 1: it counts as failed; those calls return NVFP4_ERR_CUDA and
- * every other call runs. 0 clears it. Not for production use. Errors: NVFP4_ERR_INVALID_ARG (any other fault). */
+ * every other call runs. fault = 2: launches of the plan's cluster of 16 CTAs count as rejected, as
+ * where the stream's context holds too few SMs, and the call launches 8. 0 clears it. Not for
+ * production use. Errors: NVFP4_ERR_INVALID_ARG (any other fault). */
 nvfp4_status nvfp4_debug_setup_fault(int32_t fault);
 
 /* Host pipeline: quantization of tensors that live in host memory, with the copies of

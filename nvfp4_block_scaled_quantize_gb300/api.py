@@ -645,7 +645,8 @@ def nvfp4_debug_fail_next_launch(on=True):
 
 def nvfp4_debug_setup_fault(fault=0):
     """Test hook: with fault = 1 the set-up of the routing and checkpoint kernels counts as failed,
-    so their calls raise NVFP4Error(NVFP4_ERR_CUDA); 0 clears it."""
+    so their calls raise NVFP4Error(NVFP4_ERR_CUDA); with fault = 2 launches of the plan's cluster of
+    16 CTAs count as rejected and it takes 8; 0 clears it."""
     _raise_if(_lib.load().nvfp4_debug_setup_fault(int(fault)), "nvfp4_debug_setup_fault")
 
 

@@ -50,10 +50,11 @@ constexpr int kMaxTopk = 32;  // choices of a token: one warp loads a token's ro
 // rows of `nv` 16-byte vectors; amax may be null, and the caller zeroes it unless
 // moe_dispatch_clears_amax(T)
 bool moe_dispatch_clears_amax(int64_t T);
-cudaError_t prepare_moe_kernels();
+// plan_ctas: the largest cluster of the plan that the current device holds
+cudaError_t prepare_moe_kernels(int* plan_ctas);
 cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
                             int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
-                            cudaStream_t s);
+                            int plan_ctas, cudaStream_t s);
 cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const int32_t* offsets,
                                 int64_t T, int32_t K, int32_t E, int64_t nv, void* packed,
                                 float* amax, uint32_t* status, int sm_count, cudaStream_t s);
@@ -90,9 +91,10 @@ struct RmsArgs {
 cudaError_t launch_rmsnorm_checkpoint(const RmsArgs& a, int sm_count, cudaStream_t s);
 cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, cudaStream_t s);
 
-// The current device's SM count and status word, with the kernels of these two groups set up
-// (nvfp4_api.cu); false when a CUDA call failed.
-bool device_resources(int* sm_count, uint32_t** status);
+// The current device's SM count, status word and largest cluster of the plan, with the kernels of
+// these two groups set up (nvfp4_api.cu); false when a CUDA call failed.
+bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas = nullptr);
+int setup_fault();  // nvfp4_debug_setup_fault
 
 cudaError_t launch_amax_flat(const void* x, int64_t n_elems, float* out0, float* out1, int grid,
                              cudaStream_t s);

@@ -76,13 +76,13 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_plan(const void* expert_ids, int32_t id_byte
   if (!aligned(offsets, 4) || (n > 0 && (!aligned(expert_ids, (uintptr_t)id_bytes) ||
                                          !aligned(row_of_slot, 4) || !aligned(slot_of_row, 4))))
     return NVFP4_ERR_ALIGN;
-  int sms = 0;
+  int sms = 0, ctas = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_resources(&sms, &status, &ctas)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n == 0) return cuda_status(zero(offsets, E, s));
   return cuda_status(launch_moe_plan(expert_ids, id_bytes == 8, (int32_t)n, E, row_of_slot,
-                                     slot_of_row, offsets, status, s));
+                                     slot_of_row, offsets, status, ctas, s));
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_moe_dispatch(const void* x, const int32_t* row_of_slot,

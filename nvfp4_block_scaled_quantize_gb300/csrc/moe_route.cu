@@ -11,7 +11,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "nvfp4_device.cuh"
@@ -22,7 +21,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanMaxCtas = 16;  // one cluster of the opt-in size (8 where 16 SMs do not fit)
+constexpr int kPlanMaxCtas = 16;  // one cluster of the opt-in size
+constexpr int kPlanPortableCtas = 8;  // where that does not fit
 constexpr int kPlanMaxRun = 832;  // slots of a warp's run that is sorted in shared memory
 constexpr int kPlanBatch = 8;  // groups of 32 slots whose ids a warp loads together
 constexpr int kRouteThreads = 128;
@@ -524,15 +524,13 @@ static cudaError_t prepare_plan() {
                               plan_smem_bytes(kPlanThreads / 32, kPlanMaxRun, STAGED));
 }
 
-static std::atomic<int> g_plan_ctas{kPlanMaxCtas};
-
-cudaError_t prepare_moe_kernels() {
+cudaError_t prepare_moe_kernels(int* plan_ctas) {
   cudaError_t e = cudaSuccess, r;
   if ((r = prepare_plan<int32_t, false>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int32_t, true>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int64_t, false>()) != cudaSuccess) e = r;
   if ((r = prepare_plan<int64_t, true>()) != cudaSuccess) e = r;
-  // a context with fewer SMs (a green context, a reduced share) may not hold the large cluster
+  // a device with fewer SMs in every GPC (a reduced share) does not hold the large cluster
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPlanMaxCtas);
   cfg.blockDim = dim3(kPlanThreads);
@@ -544,11 +542,12 @@ cudaError_t prepare_moe_kernels() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int clusters = 0;
+  *plan_ctas = kPlanMaxCtas;
   if (cudaOccupancyMaxActiveClusters(&clusters, moe_plan_kernel<int64_t, true>, &cfg) !=
           cudaSuccess ||
       clusters < 1) {
     (void)cudaGetLastError();
-    g_plan_ctas.store(8);
+    *plan_ctas = kPlanPortableCtas;
   }
   return e;
 }
@@ -577,10 +576,11 @@ static cudaError_t launch_cluster(void (*kernel)(KernelArgs...), int ctas, int t
 template <typename Id>
 static cudaError_t launch_plan(const void* ids, int32_t n, int32_t E, int32_t* row_of_slot,
                                int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
-                               cudaStream_t s) {
+                               int plan_ctas, cudaStream_t s) {
   // one CTA against the cluster, 256 threads: 4.1 and 4.2 us at 1024 slots, 5.1 and 4.4 at 2048;
   // the cluster with 256 and with 1024 threads: 5.0 and 6.3 us at 16384
-  const int threads = n <= 16384 ? kMaxSegments : kPlanThreads, ctas = n <= 1024 ? 1 : g_plan_ctas.load();
+  const int threads = n <= 16384 ? kMaxSegments : kPlanThreads;
+  const int ctas = n <= 1024 ? 1 : plan_ctas;
   const int warps = threads / 32;
   const int64_t lanes = (int64_t)ctas * threads;
   const int32_t run = (int32_t)((n + lanes - 1) / lanes * 32);
@@ -595,9 +595,18 @@ static cudaError_t launch_plan(const void* ids, int32_t n, int32_t E, int32_t* r
 
 cudaError_t launch_moe_plan(const void* ids, bool wide, int32_t n, int32_t E, int32_t* row_of_slot,
                             int32_t* slot_of_row, int32_t* offsets, uint32_t* status,
-                            cudaStream_t s) {
-  return wide ? launch_plan<int64_t>(ids, n, E, row_of_slot, slot_of_row, offsets, status, s)
-              : launch_plan<int32_t>(ids, n, E, row_of_slot, slot_of_row, offsets, status, s);
+                            int plan_ctas, cudaStream_t s) {
+  const auto launch = wide ? launch_plan<int64_t> : launch_plan<int32_t>;
+  cudaError_t e = plan_ctas > kPlanPortableCtas && setup_fault() == 2
+                      ? cudaErrorInvalidValue
+                      : launch(ids, n, E, row_of_slot, slot_of_row, offsets, status, plan_ctas, s);
+  // The stream's own context may hold fewer SMs than the device (a green context). Its rejection
+  // comes before anything is enqueued; a capture records the launch unchecked.
+  if (e != cudaSuccess && plan_ctas > kPlanPortableCtas) {
+    (void)cudaGetLastError();
+    e = launch(ids, n, E, row_of_slot, slot_of_row, offsets, status, kPlanPortableCtas, s);
+  }
+  return e;
 }
 
 // Grid of a warp per token and range of its row: whole rows when the tokens alone give every SM

@@ -28,6 +28,7 @@ struct DeviceState {
   bool ready = false;
   bool aux_ready = false;         // the routing and checkpoint kernels' attributes are set
   int sm_count = 0;
+  int plan_ctas = 0;              // the largest cluster of the routing plan
   uint32_t* workspace = nullptr;  // [0] status word; the library's own or the caller's
   uint32_t* own = nullptr;        // the library's own workspace, allocated on first need
 };
@@ -58,8 +59,8 @@ EncodeTiledFn g_encode = nullptr;
 bool prepare_aux(DeviceState& st) {
   if (g_setup_fault.load() == 1) return false;
   if (st.aux_ready) return true;
-  st.aux_ready =
-      prepare_moe_kernels() == cudaSuccess && prepare_checkpoint_kernels() == cudaSuccess;
+  st.aux_ready = prepare_moe_kernels(&st.plan_ctas) == cudaSuccess &&
+                 prepare_checkpoint_kernels() == cudaSuccess;
   if (!st.aux_ready) (void)cudaGetLastError();
   return st.aux_ready;
 }
@@ -161,7 +162,9 @@ __global__ void gscale_fill_kernel(const float* amax, float* gscale, int n) {
 
 }  // namespace
 
-bool device_resources(int* sm_count, uint32_t** status) {
+int setup_fault() { return g_setup_fault.load(); }
+
+bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas) {
   DeviceState* ds = nullptr;
   if (device_state(&ds) != NVFP4_OK) return false;
   {
@@ -170,6 +173,7 @@ bool device_resources(int* sm_count, uint32_t** status) {
   }
   *sm_count = ds->sm_count;
   *status = ds->workspace;
+  if (plan_ctas) *plan_ctas = ds->plan_ctas;
   return true;
 }
 
@@ -723,7 +727,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_debug_fail_next_launch(int32_t on) {
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_debug_setup_fault(int32_t fault) {
-  if (fault < 0 || fault > 1) return NVFP4_ERR_INVALID_ARG;
+  if (fault < 0 || fault > 2) return NVFP4_ERR_INVALID_ARG;
   g_setup_fault.store(fault);
   return NVFP4_OK;
 }
