@@ -56,7 +56,8 @@ typedef enum nvfp4_status {
   NVFP4_OK = 0,
   NVFP4_ERR_INVALID_ARG = 1,   /* NULL pointer where one is required, negative size, bad enum */
   NVFP4_ERR_SHAPE = 2,         /* a dimension is not a multiple of 16 where blocks need it */
-  NVFP4_ERR_ALIGN = 3,         /* a pointer or row pitch is not 16-byte aligned */
+  NVFP4_ERR_ALIGN = 3,         /* a pointer or row pitch is not aligned as its declaration asks
+                                (16 bytes where it does not say) */
   NVFP4_ERR_UNSUPPORTED = 4,   /* an option combination the method does not define */
   NVFP4_ERR_CUDA = 5,          /* a CUDA runtime call or a kernel launch failed */
   NVFP4_ERR_DEVICE_STATUS = 6, /* the device flagged its input (nvfp4_get_status) */

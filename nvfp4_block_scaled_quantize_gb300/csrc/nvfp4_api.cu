@@ -263,7 +263,7 @@ NVFP4_EXPORT const char* nvfp4_status_string(nvfp4_status s) {
     case NVFP4_OK: return "ok";
     case NVFP4_ERR_INVALID_ARG: return "invalid argument";
     case NVFP4_ERR_SHAPE: return "shape not a multiple of 16 where blocks need it";
-    case NVFP4_ERR_ALIGN: return "pointer or row pitch not 16-byte aligned";
+    case NVFP4_ERR_ALIGN: return "pointer or row pitch not aligned as its declaration asks";
     case NVFP4_ERR_UNSUPPORTED: return "unsupported option combination";
     case NVFP4_ERR_CUDA: return "CUDA error";
     case NVFP4_ERR_DEVICE_STATUS: return "device flagged its input (bad grouped offsets or routing)";
