@@ -1,11 +1,15 @@
-"""The checkpoint operators at their edges: offsets that are not what the header asks, and buffers
-with no more alignment than it asks for."""
+"""The checkpoint operators at their edges: offsets that are not what the header asks, buffers
+with no more alignment than it asks for, and gates far from zero in the gradient."""
 import pytest
 import torch
 
 from nvfp4_block_scaled_quantize_gb300 import _lib, api, workloads
 
 pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24   # half a binary32 step
+UBF = 2.0 ** -8    # half a BF16 step
+TINY = 2.0 ** -133
 
 
 def _cuda():
@@ -87,3 +91,39 @@ def test_buffers_with_the_least_alignment_and_with_less():
             call()
         assert "NVFP4_ERR_ALIGN" in str(e.value)
     assert api.nvfp4_get_status() == (0, 0)
+
+
+def test_gradient_at_gates_far_from_zero():
+    dev = _cuda()
+    # all of them E4M3 values times a power of two; sigmoid(-88), (-96) and (-104) are binary32
+    # subnormals or below, and from 17 up sigmoid rounds to 1
+    gates = [0.0, -0.0, 1.25, -1.25, -1.375, 5.5, -5.5, 16.0, 18.0, -18.0, 80.0, -80.0, 88.0, -88.0,
+             -96.0, -104.0, 112.0, 1.25 * 2.0 ** 13, -1.25 * 2.0 ** 13, 1.75 * 2.0 ** 127,
+             -1.75 * 2.0 ** 127, 2.0 ** -126, -2.0 ** -126]
+    F = 32 * len(gates)
+    pairs = [(1.0, 1.0), (-0.75, 3.0), (2.0 ** -10, 2.0 ** 100), (1.0, 2.0 ** -100)]  # dy, u
+    M = len(pairs)
+    h = torch.zeros(M, 2 * F, dtype=torch.bfloat16)
+    h[:, :F] = torch.tensor(gates).repeat_interleave(32).to(torch.bfloat16)
+    dy = torch.zeros(M, F, dtype=torch.bfloat16)
+    for i, (d, u) in enumerate(pairs):
+        h[i, F:], dy[i] = u, d
+    kept = api.nvfp4_swiglu_checkpoint(h.to(dev))
+    back = api.nvfp4_mx_dequantize(kept["codes"], kept["scales"], "e4m3").cpu().double()
+    assert torch.equal(back, h.double())
+    got = api.nvfp4_swiglu_checkpoint_backward(dy.to(dev), kept["codes"], kept["scales"])
+    g, u = h.double().split(F, 1)
+    d, s = dy.double(), torch.sigmoid(g)
+    slope = s * (1 + g * (1 - s))
+    ref = torch.cat([d * u * slope, d * g * s], 1)
+    # t = exp(-|g|) is off by 10 + 1.173 |g| steps of 2^-23 of itself and, where it is subnormal, by
+    # 2^-149; past 200 it is 0 in both, and for g > 17 so is 1 - s
+    near = g.abs().clamp(max=200.0)
+    n = torch.where(g > 0, near.clamp(max=17.0), near)
+    rel = (10 + 1.173 * n) * 2 * U32 + 8 * U32
+    under = 2.0 ** -149 * (2 + near)
+    off = torch.cat([(d * u).abs() * (s * (1 + n) * rel + under) + 2.0 ** -149,
+                     (d * g * s).abs() * rel + d.abs() * under], 1)
+    diff = (got.cpu().double() - ref).abs()
+    lim = UBF * (ref.abs() + off) + off + TINY
+    assert bool((diff <= lim).all()), (diff - lim).max()
