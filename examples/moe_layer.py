@@ -3,9 +3,10 @@
     out = x + sum_k w_k * expert_k(rmsnorm(x)),   expert(v) = (silu(v W1g) * (v W1u)) W2
 
 The norm and the SwiGLU keep their inputs in 8 bits for the backward pass; tokens are packed by
-expert, quantized to NVFP4 with the amax that the dispatch already found (the operands of the
-block-scaled GEMMs), and summed back with the router's weights. This library has no GEMM: the
-experts' products below are plain torch products over each expert's rows.
+expert and summed back with the router's weights. The rows that enter each of the experts' products
+are quantized to NVFP4 with the amax that the dispatch and the SwiGLU already found: the operands of
+block-scaled GEMMs. This library has no GEMM: the experts' products below are plain torch products
+over each expert's BF16 rows, and main() shows how far the operands are from those.
 
     python examples/moe_layer.py [--tokens 512 --hidden 1024 --width 512 --experts 8 --topk 2]
 """
@@ -38,6 +39,18 @@ def expert_weight_gradients(rows, grads, ends):
     return torch.stack(out)
 
 
+def operand_values(operands, ends):
+    """What the NVFP4 operands of packed rows stand for: float32, the last expert's end rows."""
+    out, begin = [], 0
+    for e, end in enumerate(ends):
+        if end > begin:
+            out.append(api.nvfp4_dequantize(operands["row_codes"][begin:end],
+                                            operands["row_scales"][begin:end],
+                                            operands["row_gscale"][e]))
+        begin = end
+    return torch.cat(out)
+
+
 class MoELayer:
     def __init__(self, hidden, width, experts, topk, device, seed=0):
         g = torch.Generator(device=device).manual_seed(seed)
@@ -59,12 +72,15 @@ class MoELayer:
         ends = plan["offsets"].tolist()
         act = api.nvfp4_swiglu_checkpoint(expert_products(packed, self.w1, ends),
                                           offsets=plan["offsets"])
+        act_operands = api.nvfp4_quantize_grouped(act["y"], plan["offsets"], columnwise=False,
+                                                  amax_row=act["amax"])
         y = expert_products(act["y"], self.w2, ends)
         out = x + api.nvfp4_moe_combine(y, weights, plan)
         # what the backward pass needs; the norm's and the SwiGLU's inputs in 8 bits
         self.saved = dict(norm={k: n[k] for k in ("codes", "scales", "rstd")}, n=n["y"], ids=ids,
                           weights=weights, plan=plan, ends=ends, packed=packed, y=y,
-                          glu={k: act[k] for k in ("codes", "scales")}, act=act["y"])
+                          glu={k: act[k] for k in ("codes", "scales")}, act=act["y"],
+                          operands={"packed": operands, "act": act_operands})
         return out, operands
 
     def backward(self, grad_out):
@@ -101,6 +117,10 @@ def main():
     out, operands = layer.forward(x)
     grads = layer.backward(torch.ones_like(out))
     print("out", tuple(out.shape), "operands", {k: tuple(v.shape) for k, v in operands.items()})
+    for k, q in layer.saved["operands"].items():
+        rows = layer.saved[k][:layer.saved["ends"][-1]].float()
+        off = (operand_values(q, layer.saved["ends"]) - rows).norm() / rows.norm()
+        print("operands of %-6s off by %.3f" % (k, off.item()))
     for k, v in grads.items():
         print("grad %-6s %s, norm %.4g" % (k, tuple(v.shape), v.float().norm().item()))
     bits = api.nvfp4_get_status()
