@@ -183,18 +183,17 @@ struct GluWalk {
   }
 };
 
-// Rows before the last expert's end, within [0, M]. The first CTA flags ends that do not ascend from 0
-// to M.
+// Rows before the last expert's end, within [0, M]; an end outside it is flagged.
 __device__ __forceinline__ int64_t live_of(const int32_t* offsets, int32_t E, int64_t M,
                                            uint32_t* status) {
   if (offsets == nullptr) return M;
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e < E; e += kGluThreads) {
-      const int32_t v = offsets[e];
-      if (v < (e > 0 ? offsets[e - 1] : 0) || v > M) atomicOr(status, kBadOffsets);
-    }
   const int64_t v = offsets[E - 1];
+  if ((v < 0 || v > M) && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kBadOffsets);
   return v < 0 ? 0 : (v < M ? v : M);
+}
+// Whether an expert's end lies before the previous one's (the first one's: before 0).
+__device__ __forceinline__ bool descends(const int32_t* offsets, int e) {
+  return offsets[e] < (e > 0 ? offsets[e - 1] : 0);
 }
 
 __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
@@ -210,6 +209,7 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_kernel(
   for (int e = tid; e < E; e += kGluThreads) {
     ends[e] = offsets ? offsets[e] : (int32_t)M;
     top[e] = 0u;
+    if (blockIdx.x == 0 && offsets && descends(offsets, e)) atomicOr(status, kBadOffsets);
   }
   __syncthreads();
   const int64_t nc = F / 16;
@@ -267,6 +267,9 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
   pdl_wait();
   pdl_allow_next();
   const int64_t live = live_of(offsets, E, M, status);
+  if (blockIdx.x == 0 && offsets)
+    for (int e = threadIdx.x; e < E; e += kGluThreads)
+      if (descends(offsets, e)) atomicOr(status, kBadOffsets);
   const int64_t nc = F / 16;
   for (GluWalk it(M, nc, per_cta); it.left > 0; it.next()) {
     const int64_t r = it.row, c = it.col;
