@@ -24,11 +24,12 @@
  *
  * Execution: every call is asynchronous on the caller's stream (a cudaStream_t passed as
  * void*; NULL is the legacy default stream). The quantize, amax, MX, routing and checkpoint
- * kernels are launched with programmatic dependent launch: each waits for the previous kernel in the stream before
- * it touches memory, and lets the next kernel launched that way start early, so a kernel of
- * the caller's launched after them with programmatic dependent launch must wait
- * (cudaGridDependencySynchronize) before it reads their outputs, as that mechanism requires. Pointers marked (device) must be device (or
- * managed) memory, 16-byte aligned. The return value reports argument checks and launch
+ * kernels are launched with programmatic dependent launch: each waits for the previous kernel in
+ * the stream before it touches memory, and lets the next kernel launched that way start early, so a
+ * kernel of the caller's launched after them with programmatic dependent launch must wait
+ * (cudaGridDependencySynchronize) before it reads their outputs, as that mechanism requires.
+ * Pointers marked (device) must be device (or managed) memory, aligned as the declaration says (16
+ * bytes where it does not). The return value reports argument checks and launch
  * errors only; problems the device detects (bad grouped offsets, a bounded wait that gave up)
  * are recorded in a per-device status word read by nvfp4_get_status. A call rejected by its
  * argument checks launched nothing and wrote nothing. NVFP4_ERR_CUDA reports a CUDA call or

@@ -1,6 +1,7 @@
 // Internal declarations of the library's kernels other than the tile kernel (not part of the
 // C ABI): MX quantization, the RMSNorm producer, token routing, the operators with 8-bit
-// checkpoints, the flat amax, the scale swizzle and dequantization. Kept apart from nvfp4_internal.h, whose contents the tile kernel depends on.
+// checkpoints, the flat amax, the scale swizzle and dequantization. Kept apart from
+// nvfp4_internal.h, whose contents the tile kernel depends on.
 #pragma once
 
 #include <cuda.h>
@@ -77,7 +78,9 @@ cudaError_t launch_swiglu_checkpoint_backward(const void* grad, const void* code
                                               const uint8_t* scales, int64_t M, int64_t F,
                                               const int32_t* offsets, int32_t E, void* grad_h,
                                               uint32_t* status, int sm_count, cudaStream_t s);
-constexpr int64_t kRmsMaxN = 32768;       // a row stays in one CTA's registers
+// a row stays in one CTA from the sum to the output: in registers (forward; backward as xh and g up
+// to 8192 columns), or in the ring's shared memory (backward above that)
+constexpr int64_t kRmsMaxN = 32768;
 constexpr int64_t kRmsMaxPartials = 512;  // rows of the weight gradient's partial sums
 struct RmsArgs {
   int64_t M, N;

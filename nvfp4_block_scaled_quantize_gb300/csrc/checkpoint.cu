@@ -4,11 +4,16 @@
 // magnitude within 448: unlike the MX conversion of mx_kernel.cu nothing saturates, so every normal
 // element is off by at most half an E4M3 step (2^-4 of itself).
 //
-// All four passes are bound by DRAM: at the measured copy rate of 6787 GB/s their bytes, each read
-// or written once, take 94% (SwiGLU 32768 x 2048, 83.6 us), 98% (its gradient, 80.3 us), 83%
-// (RMSNorm 8192 x 4096, 29.8 us; 93% at 16384 x 8192) and 98% (its gradient with the residual,
-// 16384 x 8192, 141.3 us) of the time. What they had to shed for that was instructions (47 an
-// element in the first norm gradient): packed binary32 pairs, 32-byte accesses, bulk copies.
+// The four passes are bound by DRAM, the norms so above 512 columns and their gradient up to
+// 8192: at the measured copy rate of 6787 GB/s their bytes, each read or written once, take 94%
+// (SwiGLU 32768 x 2048, 83.9 us), 98% (its gradient, 80.3 us), 84% (RMSNorm 8192 x 4096, 29.8 us;
+// 93% at 16384 x 8192) and 98% (its gradient with the residual, 16384 x 8192, 141.3 us) of the
+// time. What they had to shed for that was instructions (47 an element in the first norm gradient):
+// packed binary32 pairs, 32-byte accesses, bulk copies. Outside that range: a row of up to 512
+// columns is a warp's, most of whose lanes idle below 512, and a CTA's barrier serves 8 rows (65536
+// x 512: 30.4 us forward, 82%, and 36.6 backward, 68%; 131072 x 256: 48.6 and 54.2; 262144 x 128:
+// 91.0 and 98.8, 28% and 25%). The gradient beyond 8192 columns decodes every code twice (8192 x
+// 16384: 145 us, 69%; 4096 x 32768: 153 us, 65%).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -142,8 +147,8 @@ __device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
 }
 
 // sigmoid(a) from t = exp(-|a|), which cannot overflow. t is the square of 2^(-|a| log2(e) / 2):
-// the approximate instruction flushes subnormal results, and the half exponent keeps t exact in
-// kind down to binary32's smallest subnormal for two instructions fewer than the unflushed one.
+// the approximate instruction flushes subnormal results, which that square root only reaches where
+// t itself is below binary32's smallest subnormal.
 __device__ __forceinline__ float sigmoid(float a) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(fabsf(a), -0.72134752f)));
@@ -183,7 +188,7 @@ struct GluWalk {
   }
 };
 
-// Rows before the last expert's end, within [0, M]; an end outside it is flagged.
+// Rows before the last expert's end, within [0, M]; an end outside that range is flagged.
 __device__ __forceinline__ int64_t live_of(const int32_t* offsets, int32_t E, int64_t M,
                                            uint32_t* status) {
   if (offsets == nullptr) return M;
@@ -304,12 +309,13 @@ __global__ void __launch_bounds__(kGluThreads) swiglu_checkpoint_backward_kernel
 
 // ---- RMSNorm -----------------------------------------------------------------------------
 
-// A group of `wpr` warps owns a row, ITEMS x 16 columns a thread; a CTA of at most WARPS warps works
-// on tiles of `groups` consecutive rows. A tile is contiguous in memory: one thread fetches it by
-// bulk copies into a ring of STAGES tiles in shared memory, ahead of the tile that is summed, so
-// that neither the loads nor their addresses cost the other threads instructions, and DRAM stays
-// busy across the barrier of the sum. Two CTAs an SM up to 8192 columns: while one waits at its
-// barrier the other computes.
+// A group of `wpr` warps owns a row, ITEMS x 16 columns a thread; a CTA of at most WARPS warps
+// works on tiles of `groups` consecutive rows. A tile is contiguous in memory: one thread fetches
+// it by bulk copies into a ring of STAGES tiles in shared memory, ahead of the tile that is summed,
+// so that neither the loads nor their addresses cost the other threads instructions, and DRAM stays
+// busy across the barrier of the sum. Where registers and shared memory leave room, several CTAs
+// share an SM, one computing while another waits at its barrier: forward 3, 2, 1 and 1 by width
+// (RmsForward0 to 3), backward 2, 1, 1 and 1.
 constexpr int kMaxJointN = 2048;  // a CTA with more than one group has rows up to this
 constexpr uint64_t kTileWaitNs = 2000000000ull;
 constexpr uint32_t kTimeout = 0x2u;  // NVFP4_DEVICE_TIMEOUT
@@ -346,8 +352,8 @@ struct TileWaits : TileRing<STAGES> {
 };
 
 // Sum over each group's threads: shuffles, then the warps' sums through shared memory, in an order
-// that does not depend on time; `red` has two halves used in turn. The barrier is the CTA's, so that
-// after it every thread has left the previous tile.
+// that does not depend on time; `red` has two halves used in turn. The barrier is the CTA's, so
+// that after it every thread has left the previous tile.
 template <int WARPS>
 __device__ __forceinline__ float group_sum(uint64_t pair, float (*red)[WARPS], int turn, int group,
                                            int wpr) {
@@ -652,8 +658,8 @@ __global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(
   }
 }
 
-// Items of a CTA: about eight CTAs an SM, and at most four items a thread, so that the resident CTAs
-// sweep the tensors in address order: one long range for each of eight CTAs an SM took 97.6 us
+// Items of a CTA: about eight CTAs an SM, and at most four items a thread, so that the resident
+// CTAs sweep the tensors in address order: one long range for each of eight CTAs an SM took 97.6 us
 // instead of 86.3 forward and 83.2 instead of 80.3 backward at 32768 x 2048.
 int64_t glu_per_cta(int64_t items, int sm_count, int* grid) {
   const int64_t most = (int64_t)sm_count * 8;
@@ -713,15 +719,17 @@ struct RmsBackward {
   }
 };
 
-// By the row's columns: up to 4096, 8192, 16384, 32768. Forward, 8192 x 4096: 29.7 us with three CTAs
-// of 8 warps an SM, 31.0 with two of 16; 16384 x 8192: 112.5 with two of 8 warps and 32 columns a
-// thread, 106.5 with two of 16 warps and 16. Backward, 16384 x 8192 with the residual: 158.7 with two
-// of 8 warps and 32 columns a thread (which decode every code twice), 141.3 with one of 16 warps and
-// 16; 32768 x 4096: 115.6 with two of 8 warps, 117.4 with one of 16. Beyond 8192 columns the weight
-// gradient's accumulators leave no registers to keep xh in, and the codes are decoded twice; the
-// weights are read for every row, so the ring must leave them L1: 8192 x 16384 takes 145 us with two
-// stages and 167 with four. 4096 x 32768: 152 us with two stages, 162 with one (all that fits with the
-// residual).
+// By the row's columns: up to 4096, 8192, 16384, 32768. Forward, 8192 x 4096: 29.7 us with three
+// CTAs of 8 warps an SM, 31.0 with two of 16; 16384 x 8192: 112.5 with two of 8 warps and 32
+// columns a thread, 106.5 with two of 16 warps and 16. Backward, 16384 x 8192 with the residual:
+// 158.7 with two of 8 warps and 32 columns a thread (which decode every code twice), 141.3 with one
+// of 16 warps and 16; 32768 x 4096: 115.6 with two of 8 warps, 117.4 with one of 16. Beyond 8192
+// columns xh and g are not kept from the sum to the output beside the weight gradient's
+// accumulators (kept together they took longer; xh alone was not tried), so the codes are decoded
+// twice. The weights are read for every row, so the ring must leave them L1: 8192 x 16384 takes 145
+// us with two stages and 167 with four (with the residual 170 us, 82%). 4096 x 32768: 153 us with
+// two stages, 162 with one; with the residual one is all that fits, and no load overlaps the
+// computation (211 us, 66%).
 using RmsForward0 = RmsForward<8, 1, 4, 3>;
 using RmsForward1 = RmsForward<16, 1, 4, 2>;
 using RmsForward2 = RmsForward<16, 2, 4, 1>;

@@ -253,7 +253,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_rmsnorm_checkpoint_backward(
   size_t need = 0;
   nvfp4_status st = nvfp4_rmsnorm_checkpoint_workspace(M, N, &need);
   if (st != NVFP4_OK) return st;
-  if (!std::isfinite(weight_bias) || (N > 0 && grad_weight == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if (!std::isfinite(weight_bias) || (N > 0 && grad_weight == nullptr))
+    return NVFP4_ERR_INVALID_ARG;
   const bool empty = M * N == 0;
   if (!empty && (grad_y == nullptr || codes == nullptr || scales == nullptr || rstd == nullptr ||
                  weight == nullptr || grad_x == nullptr || workspace == nullptr ||

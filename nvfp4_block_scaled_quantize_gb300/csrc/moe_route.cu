@@ -3,10 +3,13 @@
 // of expert outputs back into token order, and the gradients of both.
 //
 // The plan is bound by the shared memory and the stores of the 16 SMs that one cluster has (14.9 us
-// at 262144 slots, whose bytes would take 0.5 us); it stays one launch, which small calls need. The
-// other four are bound by DRAM: at the measured copy rate of 6787 GB/s their bytes take 96% of
-// dispatch's time (4096 x 8 rows of 7168, 80.9 us), 98% of combine's (8192 x 4 of 4096, 50.6 us),
-// 98% of its gradient's (4096 x 8 of 7168, 148.2 us) and 83% to 100% of the gradient of dispatch's.
+// at 262144 slots, whose bytes would take 0.5 us; 25.0 at 524288, 42.0 at 1048576): one launch
+// without scratch memory, whatever the size. The other four are bound by DRAM: at the measured copy
+// rate of 6787 GB/s their bytes take 97% of dispatch's time (4096 x 8 rows of 7168, 80.1 us), 98%
+// of combine's (8192 x 4 of 4096, 50.6 us), 98% of its gradient's (4096 x 8 of 7168, 148.0 us) and
+// 81% (3001 x 6 of 2056) to 100% of the gradient of dispatch's. Dispatch of many rows of 129 to
+// about 256 vectors is bound by its maxima, one atomic a slot: 16384 x 8 rows of 130 vectors take
+// 74.6 us with 64 experts (60%), of 192 83.0 (80%), of 256 96.4 (92%).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -252,10 +255,10 @@ __device__ __forceinline__ int expert_of(const int32_t* ends, int32_t E, int32_t
 }
 
 // TW warps per token, neighbouring ones taking neighbouring 32 vectors of its row; a CTA holds its
-// warps / TW tokens. The token's maximum is joined in shared memory, so that it costs one atomic for
-// each of its experts. ONE: the grid is one cluster, which joins the
-// experts' maxima in its first CTA's shared memory and writes all of amax itself, so that a small
-// call needs no clearing of amax before it.
+// warps / TW tokens. The token's maximum is joined in shared memory, so that it costs one atomic
+// for each of its experts. ONE: the grid is one cluster, which joins the experts' maxima in its
+// first CTA's shared memory and writes all of amax itself, so that a small call needs no clearing
+// of amax before it.
 constexpr int kCopyMaxWarps = 16;
 constexpr int64_t kOneClusterTokens = 8;  // a CTA of 16 warps each
 template <int TW, int BATCH, bool ONE>
@@ -319,9 +322,9 @@ __global__ void __launch_bounds__(32 * kCopyMaxWarps, 2) moe_dispatch_kernel(
   }
 }
 
-// Short rows, at most kNarrowVecs vectors: a warp per token, CTAs that stay for many tokens and join
-// the experts' maxima in shared memory. One atomic a slot into the few lines of amax runs at 2 per ns:
-// 16384 x 8 slots of 512 columns take 68.4 us that way and 30.5 us this way.
+// Short rows, at most kNarrowVecs vectors: a warp per token, CTAs that stay for many tokens and
+// join the experts' maxima in shared memory. One atomic a slot into the few lines of amax runs at 2
+// per ns: 16384 x 8 slots of 512 columns and 64 experts take 66.0 us that way and 24.9 us this way.
 constexpr int kNarrowVecs = 128;
 constexpr int kNarrowThreads = 512;
 __global__ void __launch_bounds__(kNarrowThreads, 2) moe_dispatch_narrow_kernel(
@@ -378,7 +381,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) moe_dispatch_narrow_kernel(
 // ---- combine and the gradient of dispatch ------------------------------------------------
 
 // out[t] = sum over the token's held rows of w * y[row], in the order of its choices, in binary32;
-// a warp per token and range of its row. A lane has 8 loads in flight: VECS vectors of 8 / VECS rows.
+// a warp per token and range of its row. A lane has 8 loads in flight: VECS vectors of 8 / VECS
+// rows.
 template <bool WEIGHTED, int VECS>
 __global__ void __launch_bounds__(kRouteThreads) moe_gather_sum_kernel(
     const uint4* __restrict__ y, const float* __restrict__ weights,
@@ -497,7 +501,8 @@ __global__ void __launch_bounds__(kSlotThreads) moe_combine_backward_kernel(
       dot = __fadd_rn(f.x, f.y);
     }
     if (slot >= live_rows(offsets, E, P))
-      for (int64_t v = v0; v < nv; v += kThreads) grad_y[slot * nv + v] = make_uint4(0u, 0u, 0u, 0u);
+      for (int64_t v = v0; v < nv; v += kThreads)
+        grad_y[slot * nv + v] = make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
@@ -584,8 +589,8 @@ static cudaError_t launch_plan(const void* ids, int32_t n, int32_t E, int32_t* r
   const int warps = threads / 32;
   const int64_t lanes = (int64_t)ctas * threads;
   const int32_t run = (int32_t)((n + lanes - 1) / lanes * 32);
-  // sorted in shared memory against scattered stores: 14.1 and 17.3 us at 262144 slots of 64 experts
-  // (eight slots an expert in a run), 17.7 and 17.3 us with 256 experts (two)
+  // sorted in shared memory against scattered stores: 14.1 and 17.3 us at 262144 slots of 64
+  // experts (eight slots an expert in a run), 17.7 and 17.3 us with 256 experts (two)
   const bool staged = ctas > 1 && run >= 4 * E && run <= kPlanMaxRun;
   return launch_cluster(staged ? moe_plan_kernel<Id, true> : moe_plan_kernel<Id, false>, ctas,
                         threads, plan_smem_bytes(warps, run, staged), s,
@@ -646,8 +651,8 @@ cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const
                           static_cast<uint4*>(packed), reinterpret_cast<uint32_t*>(amax), status);
   constexpr int64_t kNarrowTokens = kNarrowThreads / 32;
   const int64_t wave = (int64_t)sm_count * 2;
-  // short rows this way and the other: 5.3 and 10.6 us at 2000 x 8 rows of 64 vectors, 13.9 and 31.0
-  // at 16384 x 1 of 128, 57.3 and 56.0 at 16384 x 8 of 128 with 256 experts
+  // short rows this way and the other: 5.1 and 10.4 us at 2000 x 8 rows of 64 vectors, 10.9 and
+  // 31.3 at 16384 x 1 of 128, 52.4 and 63.3 at 16384 x 8 of 128 with 256 experts
   if (nv <= kNarrowVecs) {
     const int64_t ctas = (T + kNarrowTokens - 1) / kNarrowTokens;
     return launch_pdl(moe_dispatch_narrow_kernel, dim3((unsigned)(ctas < wave ? ctas : wave)),
@@ -656,8 +661,9 @@ cudaError_t launch_moe_dispatch(const void* x, const int32_t* row_of_slot, const
                       reinterpret_cast<uint32_t*>(amax), status);
   }
   // a row in one batch of the lanes' vectors, so that each destination row is written in one burst:
-  // eight warps of 4 vectors against four of 8, 81.5 and 83.0 us at 4096 x 8 rows of 896 vectors,
-  // 58.9 and 53.4 us at 8192 x 4 rows of 512
+  // eight warps of 4 vectors against four of 8, 4096 x 8 rows of 512, 640, 896 and 1024 vectors:
+  // 46.4 and 47.3, 57.2 and 58.5, 80.2 and 81.7, 91.7 and 93.5 us; 8192 x 4 rows of 256, 512, 640
+  // and 896: 38.3 and 29.6, 57.4 and 51.4, 67.0 and 64.0, 88.4 and 89.2 us
   if (nv > 512)
     return launch_dispatch<8, 4>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
   return launch_dispatch<4, 8>(x, row_of_slot, offsets, T, K, E, nv, packed, amax, status, s);
@@ -705,9 +711,10 @@ cudaError_t launch_moe_combine_backward(const void* grad, const void* y, const f
                                         int64_t T, int32_t K, int32_t E, int64_t nv, void* grad_y,
                                         float* grad_w, uint32_t* status, int sm_count,
                                         cudaStream_t s) {
-  // four warps of 4 vectors per slot when the slots alone do not give every SM 64 warps, else one of
-  // one vector: 3.5 and 5.5 us at 64 x 8 rows of 896 vectors, 42.4 and 43.5 at 1000 x 8, 159.1 and
-  // 147.3 at 4096 x 8 (one warp of 4 vectors: 152.4; more warps in flight beat more loads a warp)
+  // four warps of 4 vectors per slot when the slots alone do not give every SM 64 warps, else one
+  // of one vector: 3.5 and 5.5 us at 64 x 8 rows of 896 vectors, 42.4 and 43.5 at 1000 x 8, 159.1
+  // and 147.3 at 4096 x 8 (one warp of 4 vectors: 152.4; more warps in flight beat more loads a
+  // warp)
   if (T * K < (int64_t)sm_count * 64 && nv > 128)
     return launch_combine_backward<4, 4>(grad, y, weights, row_of_slot, offsets, T, K, E, nv,
                                          grad_y, grad_w, status, s);

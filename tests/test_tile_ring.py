@@ -59,22 +59,22 @@ def test_nothing_is_in_flight_after_a_wait_that_gave_up(sim, stages):
                 delay[late + 1:] = after
                 delay[late] = LIMIT + LIMIT // 2
                 r = sim(stages, delay)
-                assert r["gave_up"] == late and r["in_flight"] == 0 and r["wrong"] == 0, (tiles, late, r)
-                assert r["timeouts"] == 1 and r["idle"] == 0, (tiles, late, r)
+                assert r == dict(gave_up=late, in_flight=0, timeouts=1, idle=0,
+                                 wrong=0), (tiles, late, r)
 
 
 @pytest.mark.parametrize("stages", [1, 2, 3, 4])
 def test_later_copies_that_outlast_the_lost_one_are_waited_for(sim, stages):
-    """A tile that never lands, and the tiles fetched with it landing only during the drain: the lost
-    copy alone is left, and only its own two waits run out."""
+    """A tile that never lands, and the tiles fetched with it landing only during the drain: the
+    lost copy alone is left, and only its own two waits run out."""
     for tiles in range(1, 20):
         for lost in range(tiles):
             delay = np.zeros(tiles, np.int64)
             delay[lost + 1:] = 2 * LIMIT + LIMIT // 2
             delay[lost] = -1
             r = sim(stages, delay)
-            assert r["gave_up"] == lost and r["in_flight"] == 1 and r["wrong"] == 0, (tiles, lost, r)
-            assert r["timeouts"] == 2 and r["idle"] == 0, (tiles, lost, r)
+            assert r == dict(gave_up=lost, in_flight=1, timeouts=2, idle=0,
+                             wrong=0), (tiles, lost, r)
 
 
 @pytest.mark.gpu
