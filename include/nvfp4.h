@@ -450,6 +450,167 @@ nvfp4_status nvfp4_rmsnorm_checkpoint_backward(const void* grad_y, const uint8_t
                                                void* grad_x, float* grad_weight, void* workspace,
                                                size_t workspace_bytes, void* stream);
 
+/* ---- The router ------------------------------------------------------------------------------
+ * Experts and weights of T tokens from logits [T][E], in front of nvfp4_moe_plan and
+ * nvfp4_moe_combine. 1 <= E <= 256, 1 <= K <= 32 (above: NVFP4_ERR_UNSUPPORTED), T * E below 2^40. */
+typedef enum {
+  NVFP4_SCORE_SOFTMAX = 0, /* p = softmax over the token's E logits */
+  NVFP4_SCORE_SIGMOID = 1  /* p = 1 / (1 + exp(-logit)) */
+} nvfp4_score;
+
+/* Choose K experts a token.
+ *   logits   (device) [T][E], float (logit_bytes 4) or BF16 (2).
+ *   bias     (device) float [E] or NULL: added to p for the choice alone, not to the weights.
+ *   groups, top_groups  the experts form `groups` groups of E / groups neighbours, of which the
+ *            top_groups with the largest sum of their two largest p + bias are kept (one where a
+ *            group has one expert); 1 <= top_groups <= groups, E % groups == 0,
+ *            K <= top_groups * E / groups.
+ *   expert_ids (device) int32 [T][K]: the K experts with the largest p + bias, in that order.
+ *   weights  (device) float [T][K]: scale * p of the chosen, with renormalize divided by the sum of
+ *            the chosen p.
+ * The order is that of the exact values (equal ones: the lower index first): where binary32 cannot
+ * tell two candidates apart the row is ranked in binary64. Without a bias it is that of the logits.
+ * A logit or a bias of -inf masks an expert: it is never chosen; slots for which nothing is left get
+ * id -1 and weight 0, which nvfp4_moe_plan takes as dropped, and so does every slot of a row with a
+ * NaN or +inf logit or p + bias, which sets NVFP4_DEVICE_BAD_ROUTE. */
+nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_bytes, const float* bias, int64_t T,
+                              int32_t E, int32_t K, int32_t score, int32_t groups,
+                              int32_t top_groups, int32_t renormalize, float scale,
+                              int32_t* expert_ids, float* weights, void* stream);
+
+/* The gradient of the logits, in their type: from grad_weights (device) float [T][K] and the same
+ * logits, ids and options. The choice is constant. Slots with an id outside [0, E) have no part (an
+ * id >= E sets NVFP4_DEVICE_BAD_ROUTE); an id that stands twice in a row counts twice. */
+nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, const void* logits,
+                                       int32_t logit_bytes, const int32_t* expert_ids, int64_t T,
+                                       int32_t E, int32_t K, int32_t score, int32_t renormalize,
+                                       float scale, void* grad_logits, void* stream);
+
+/* ---- Matrix products of NVFP4 operands ---------------------------------------------------------
+ * An operand is what the quantize calls write: codes [rows][K/2] and row-major scales [rows][K/16],
+ * K the dimension that is summed over (rowwise outputs: K = N; columnwise outputs: rows = N, K = M),
+ * with gscale {amax, S_dec}. Pitches are bytes from a row to the next and, for the experts of a
+ * stacked operand, from an expert to the next; rows themselves are contiguous. codes 16-byte aligned,
+ * their pitches multiples of 16; scales and their pitches any (multiples of 16 are fastest).
+ * K % 32 == 0. gscale 4-byte aligned. Products are exact, sums binary32. */
+typedef struct nvfp4_operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* gscale;
+  int64_t code_pitch, scale_pitch;
+  int64_t code_batch, scale_batch; /* stacked operands only */
+} nvfp4_operand;
+
+typedef enum {
+  NVFP4_ACT_NONE = 0,
+  NVFP4_ACT_RELU = 1,
+  NVFP4_ACT_RELU2 = 2, /* max(z, 0)^2 */
+  NVFP4_ACT_GELU = 3,  /* z / 2 * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) */
+  NVFP4_ACT_SILU = 4   /* z / (1 + exp(-z)) */
+} nvfp4_activation;
+
+/* z = S_dec(a) * S_dec(b) * sum + bias, out = act(z) + residual, binary32 and rounded once.
+ * Zero-initialise and set what is needed; out is row-major [M][N] without gaps. */
+typedef struct nvfp4_epilogue {
+  int32_t activation;    /* nvfp4_activation */
+  int32_t out_bytes;     /* 2: out and residual are BF16, 4: float */
+  int32_t bias_bytes;    /* 2: bias is BF16, 4: float; not read without a bias */
+  const void* bias;      /* [N] (grouped: [E][N]) or NULL */
+  const void* residual;  /* [M][N] or NULL; may be out itself */
+  void* preact;          /* BF16 [M][N] or NULL: receives z, for the backward pass */
+  float* amax;           /* float [1] (grouped: [E]) or NULL: receives max |out| as it is stored, the
+                            amax_row of the next quantization */
+} nvfp4_epilogue;
+
+/* out [M][N] from a [M][K] and b [N][K] (both with K innermost): a b^T through the epilogue.
+ * The other products of a training step are this call again: the input's gradient from the rowwise
+ * gradient and the columnwise weights, the weights' gradient from two columnwise operands (both
+ * transformed with the same signs, or neither). K == 0: the sum is 0. */
+nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t M, int64_t N,
+                        int64_t K, const nvfp4_epilogue* epilogue, void* out, void* stream);
+
+/* The experts' products of packed rows: for every expert e, out[rows of e] = a[rows of e] b[e]^T
+ * through the epilogue.
+ *   a [T][K] with gscale [E][2], as nvfp4_quantize_grouped writes it; offsets (device) int32 [E]
+ *   expert ends; b E stacked operands [N][K] with gscale [E][2]: the rowwise outputs of stacked
+ *   weights (code_batch = N * code_pitch), or the columnwise ones for the products of the backward
+ *   pass (code_batch = bytes of one expert's columns in a row). 1 <= E <= 256.
+ * Rows past the last end are not read and get zeros in out and preact. Offsets that are not
+ * non-decreasing within [0, T] set NVFP4_DEVICE_BAD_OFFSETS; out is undefined then. */
+nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4_operand* b,
+                                const int32_t* offsets, int32_t E, int64_t T, int64_t N, int64_t K,
+                                const nvfp4_epilogue* epilogue, void* out, void* stream);
+
+/* The experts' weight gradients: out[e] = a[:, tokens of e] b[:, tokens of e]^T, out [E][M][N].
+ *   a [M][capacity], b [N][capacity]: the columnwise outputs that nvfp4_quantize_grouped writes for
+ *   two packed tensors of these offsets (expert e's tokens from column sum of pad16(n_j), j < e),
+ *   gscale [E][2] each; capacity % 32 == 0, at least that sum over all experts (less sets
+ *   NVFP4_DEVICE_BAD_OFFSETS).
+ *   out_bytes 2 (BF16) or 4 (float); accumulate = 1 adds to out, which then holds the gradient so
+ *   far. An expert without tokens gets zeros (with accumulate: keeps what it has). */
+nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const nvfp4_operand* b,
+                                      const int32_t* offsets, int32_t E, int64_t M, int64_t N,
+                                      int64_t capacity, int32_t out_bytes, int32_t accumulate,
+                                      void* out, void* stream);
+
+/* The gradient through an epilogue: grad_preact = grad_out * act'(preact) in BF16 (rounded once), the
+ * column sums of its binary32 values, and its amax: what the quantizations and products of the
+ * backward pass take. (The residual's gradient is grad_out.)
+ *   grad_out, preact (device) BF16 [M][N], 16-byte aligned; activation; grad_preact (device) BF16
+ *   [M][N], 16-byte aligned, may be grad_out; grad_bias (device) float [N] or NULL, its sums in an
+ *   order that depends on the sizes and the device alone; amax (device) float [1] or NULL; workspace
+ *   (device), 16-byte aligned, of at least nvfp4_gemm_epilogue_backward_workspace bytes where
+ *   grad_bias is asked for. N % 8 == 0. At z = 0 the derivative of RELU is 0. */
+nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, const void* preact, int64_t M,
+                                          int64_t N, int32_t activation, void* grad_preact,
+                                          float* grad_bias, float* amax, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+nvfp4_status nvfp4_gemm_epilogue_backward_workspace(int64_t M, int64_t N, size_t* bytes);
+
+/* ---- AdamW over many tensors ------------------------------------------------------------------
+ * One step for every tensor of a list in one launch for every 64 tensors, with the weight that the
+ * quantizers take and its amax from the same pass. Per element, binary32 operations in this order:
+ *   g = grad * grad_scale;  m = m * beta1 + g * (1 - beta1);  v = v * beta2 + (g * g) * (1 - beta2)
+ *   p = p * (1 - lr * weight_decay) - (m * (lr / (1 - beta1^step))) /
+ *       (sqrt(v) * (1 - beta2^step)^-0.5 + eps)
+ *   weight = bf16(p), amax = max |weight|
+ * With 8-bit states, m and r = sqrt(v) are kept as E4M3 codes [n] and one E8M0 scale for each 32
+ * consecutive elements (the smallest 2^e, e >= -127, with the block's largest magnitude <= 448 * 2^e,
+ * as the checkpoints above); the step computes with the unrounded m and v and rounds them as it
+ * stores: m to nearest-even; r stochastically (a moving average of rate 1 - beta2 would not move
+ * otherwise: its steps are below half a code), t = r / 2^e as a multiple q of its code step becoming
+ * floor(q + u), at least one step where r > 0. u = 16 random bits / 65536 from one Philox4x32-10 draw
+ * for each 8 elements: key (lo32 seed, hi32 seed), counter (lo32 j, hi32 j, tensor, step) with j =
+ * element / 8 and tensor its index in the list, element i taking half i % 2 (low first) of word
+ * (i % 8) / 2. */
+typedef struct nvfp4_adamw_tensor {
+  int64_t n;              /* elements, >= 0; every buffer below (device), 16-byte aligned, scales any */
+  float* param;           /* [n], updated */
+  const void* grad;       /* [n], float or BF16 (grad_bytes) */
+  void* exp_avg;          /* [n] float, or uint8 E4M3 codes */
+  void* exp_avg_sq;       /* [n] float (v), or uint8 E4M3 codes of sqrt(v) */
+  uint8_t* exp_avg_scales, *exp_avg_sq_scales; /* [ceil(n / 32)] with 8-bit states */
+  void* weight;           /* BF16 [n] or NULL */
+  float weight_decay;
+} nvfp4_adamw_tensor;
+
+typedef struct nvfp4_adamw_config {
+  double lr, beta1, beta2; /* 0 <= beta < 1 */
+  double eps;              /* > 0 */
+  int64_t step;            /* 1 for the first; below 2^31 */
+  const int32_t* step_device; /* (device) int32 [1] or NULL: the step instead, read by the kernel, for
+                                 captured calls; a value below 1 counts as 1 */
+  const float* grad_scale; /* (device) float [1] or NULL (1): e.g. the clipping factor */
+  uint64_t seed;
+  int32_t state_bits;      /* 32 or 8 */
+  int32_t grad_bytes;      /* 4 or 2 */
+} nvfp4_adamw_config;
+
+/* tensors (host): read before the call returns. amax (device) float [count] or NULL: max |weight| of
+ * each tensor (of bf16(p) where weight is NULL). Buffers of different tensors must not overlap. */
+nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int32_t count,
+                              const nvfp4_adamw_config* cfg, float* amax, void* stream);
+
 /* The per-device workspace: the status word the kernels report to, and the counts, maxima and
  * claim bits of the single-launch amax. By default the library allocates it with cudaMalloc
  * (once per device, on the first call that needs it, zeroed) and never frees it. */

@@ -34,7 +34,10 @@ EXPORTED = ["nvfp4_status_string", "nvfp4_amax", "nvfp4_quantize", "nvfp4_quanti
             "nvfp4_moe_plan", "nvfp4_moe_dispatch", "nvfp4_moe_dispatch_backward",
             "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_swiglu_checkpoint",
             "nvfp4_swiglu_checkpoint_backward", "nvfp4_rmsnorm_checkpoint",
-            "nvfp4_rmsnorm_checkpoint_workspace", "nvfp4_rmsnorm_checkpoint_backward"]
+            "nvfp4_rmsnorm_checkpoint_workspace", "nvfp4_rmsnorm_checkpoint_backward",
+            "nvfp4_moe_router", "nvfp4_moe_router_backward", "nvfp4_gemm", "nvfp4_gemm_grouped",
+            "nvfp4_gemm_grouped_wgrad", "nvfp4_gemm_epilogue_backward",
+            "nvfp4_gemm_epilogue_backward_workspace", "nvfp4_adamw_step"]
 
 
 class Config(ctypes.Structure):
@@ -53,6 +56,36 @@ class Config(ctypes.Structure):
         ("fast_math", ctypes.c_int32),
         ("swizzle_scales", ctypes.c_int32),
     ]
+
+
+class Operand(ctypes.Structure):
+    """Mirror of ``struct nvfp4_operand``."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("gscale", ctypes.c_void_p),
+                ("code_pitch", ctypes.c_int64), ("scale_pitch", ctypes.c_int64),
+                ("code_batch", ctypes.c_int64), ("scale_batch", ctypes.c_int64)]
+
+
+class Epilogue(ctypes.Structure):
+    """Mirror of ``struct nvfp4_epilogue``."""
+    _fields_ = [("activation", ctypes.c_int32), ("out_bytes", ctypes.c_int32),
+                ("bias_bytes", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p), ("amax", ctypes.c_void_p)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """Mirror of ``struct nvfp4_adamw_tensor``."""
+    _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
+                ("exp_avg_scales", ctypes.c_void_p), ("exp_avg_sq_scales", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWConfig(ctypes.Structure):
+    """Mirror of ``struct nvfp4_adamw_config``."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_device", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint64),
+                ("state_bits", ctypes.c_int32), ("grad_bytes", ctypes.c_int32)]
 
 
 class NVFP4Error(RuntimeError):
@@ -154,7 +187,18 @@ def load(build_if_missing: bool = False):
              [vp, vp, i64, i64, f32, f32, vp, vp, vp, vp, vp, vp]),
             ("nvfp4_rmsnorm_checkpoint_workspace", [i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
             ("nvfp4_rmsnorm_checkpoint_backward",
-             [vp, vp, vp, vp, vp, i64, i64, f32, vp, vp, vp, vp, ctypes.c_size_t, vp])):
+             [vp, vp, vp, vp, vp, i64, i64, f32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            ("nvfp4_moe_router", [vp, i32, vp, i64, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
+            ("nvfp4_moe_router_backward",
+             [vp, vp, i32, vp, i64, i32, i32, i32, i32, f32, vp, vp]),
+            ("nvfp4_gemm", [vp, vp, i64, i64, i64, vp, vp, vp]),
+            ("nvfp4_gemm_grouped", [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp]),
+            ("nvfp4_gemm_grouped_wgrad", [vp, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp]),
+            ("nvfp4_gemm_epilogue_backward",
+             [vp, vp, i64, i64, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+            ("nvfp4_gemm_epilogue_backward_workspace",
+             [i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
+            ("nvfp4_adamw_step", [vp, i32, vp, vp, vp])):
         fn = getattr(L, name)
         fn.restype = ctypes.c_int
         fn.argtypes = args

@@ -579,6 +579,343 @@ def nvfp4_rmsnorm_checkpoint_backward(grad_y, codes, scales, rstd, weight, weigh
     return grad_x, grad_weight
 
 
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _check_logits(logits):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or \
+            logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be a 2-D float32 or bfloat16 tensor")
+    if not logits.is_cuda:
+        raise TypeError("logits must live on a CUDA device")
+    if not logits.is_contiguous():
+        raise ValueError("logits must be contiguous (row-major)")
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    return SCORES[score]
+
+
+def _small(v):
+    """An integer argument within a C int (the library refuses what is out of its range)."""
+    return max(-1, min(int(v), 1 << 20))
+
+
+def nvfp4_moe_router(logits, topk, score="softmax", bias=None, groups=1, top_groups=None,
+                     renormalize=True, scale=1.0, ids=None, weights=None):
+    """Choose `topk` experts a token from logits (float32 or BF16 [T, E]): those with the largest
+    score + bias (bias float32 [E], for the choice alone), best first, ties to the lower index, out of
+    the `top_groups` best of `groups` groups of neighbouring experts (a group counts the sum of its two
+    best). Returns (ids int32 [T, topk], weights float32 [T, topk]): scale * score of the chosen,
+    divided by their sum with `renormalize`. Experts with a logit or bias of -inf are not chosen; slots
+    that stay empty have id -1 (nvfp4_moe_plan drops them) and weight 0."""
+    _check_logits(logits)
+    L = _lib.load()
+    T, E = logits.shape
+    K, dev = _small(topk), logits.device
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (E,), dev)
+    ids = _out(ids, "ids", torch.int32, (T, max(K, 0)), dev)
+    weights = _out(weights, "weights", torch.float32, (T, max(K, 0)), dev)
+    status = L.nvfp4_moe_router(logits.data_ptr(), logits.element_size(), _ptr(bias), T, _small(E), K,
+                                _score(score), _small(groups),
+                                _small(groups if top_groups is None else top_groups),
+                                int(bool(renormalize)), scale, ids.data_ptr(), weights.data_ptr(),
+                                _stream(dev))
+    _raise_if(status, "nvfp4_moe_router")
+    return ids, weights
+
+
+def nvfp4_moe_router_backward(grad_weights, logits, ids, score="softmax", renormalize=True, scale=1.0,
+                              out=None):
+    """The gradient of the logits (their shape and type) from grad_weights (float32 [T, K], as
+    nvfp4_moe_combine_backward returns it) and the router's ids; the choice is constant."""
+    _check_logits(logits)
+    L = _lib.load()
+    T, E = logits.shape
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a 2-D int32 tensor")
+    K = ids.shape[1]
+    _check(ids, "ids", torch.int32, (T, K), dev)
+    _check(grad_weights, "grad_weights", torch.float32, (T, K), dev)
+    out = _out(out, "out", logits.dtype, (T, E), dev)
+    status = L.nvfp4_moe_router_backward(grad_weights.data_ptr(), logits.data_ptr(),
+                                         logits.element_size(), ids.data_ptr(), T, _small(E), _small(K),
+                                         _score(score), int(bool(renormalize)), scale, out.data_ptr(),
+                                         _stream(dev))
+    _raise_if(status, "nvfp4_moe_router_backward")
+    return out
+
+
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(
+            repr(k) for k in ACTIVATIONS if k is not None))
+    return ACTIVATIONS[name]
+
+
+def _check_rows(t, name, dim, device):
+    """Refuse what is not a uint8 tensor of `dim` dimensions on `device` with contiguous rows."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != dim:
+        raise TypeError("%s must be a %d-D uint8 tensor" % (name, dim))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s must have contiguous rows" % name)
+
+
+def _operand(name, codes, scales, gscale, device, experts=None, stacked=False):
+    """(Operand, rows, K) of codes [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with experts),
+    checked; stacked: codes and scales have a first dimension of experts."""
+    dim = 3 if stacked else 2
+    _check_rows(codes, name + "_codes", dim, device)
+    _check_rows(scales, name + "_scales", dim, device)
+    shape, K = codes.shape, 2 * codes.shape[-1]
+    if K % 32 != 0 or tuple(scales.shape) != tuple(shape[:-1]) + (K // 16,):
+        raise ValueError("%s_codes must be [.., K/2] with K a multiple of 32 and %s_scales [.., K/16]"
+                         % (name, name))
+    if stacked and shape[0] != experts:
+        raise ValueError("%s must have %d experts, not %d" % (name, experts, shape[0]))
+    _check(gscale, name + "_gscale", torch.float32, (2,) if experts is None else (experts, 2), device)
+    cs, ss = codes.stride(), scales.stride()
+    o = _lib.Operand(codes.data_ptr(), scales.data_ptr(), gscale.data_ptr(), cs[-2], ss[-2],
+                     cs[0] if stacked else 0, ss[0] if stacked else 0)
+    return o, shape[-2], K
+
+
+def _gemm_epilogue(bias, bias_shape, activation, residual, out, out_dtype, shape, keep_preact, preact,
+                   amax, with_amax, experts, dev):
+    """(Epilogue, result dict) of the products' shared options."""
+    if out is not None and out_dtype is None:
+        out_dtype = out.dtype
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    got = {"out": _out(out, "out", out_dtype, shape, dev)}
+    if bias is not None:
+        _check(bias, "bias", torch.float32 if bias.dtype is torch.float32 else torch.bfloat16,
+               bias_shape, dev)
+    if residual is not None:
+        _check(residual, "residual", out_dtype, shape, dev)
+    if keep_preact or preact is not None:
+        got["preact"] = _out(preact, "preact", torch.bfloat16, shape, dev)
+    if with_amax or amax is not None:
+        got["amax"] = _out(amax, "amax", torch.float32, (experts,), dev)
+    e = _lib.Epilogue(_activation(activation), 4 if out_dtype is torch.float32 else 2,
+                      0 if bias is None else bias.element_size(), _ptr(bias), _ptr(residual),
+                      _ptr(got.get("preact")), _ptr(got.get("amax")))
+    return e, got
+
+
+def _device_of(codes, name):
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+        raise TypeError("%s must live on a CUDA device" % name)
+    return codes.device
+
+
+def nvfp4_gemm(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, bias=None, activation=None,
+               residual=None, out_dtype=None, keep_preact=False, with_amax=False, out=None, preact=None,
+               amax=None):
+    """act(a b^T + bias) + residual of two NVFP4 operands: a [M, K] and b [N, K] as codes, row-major
+    scales and global scale of the quantize calls (rowwise outputs, or columnwise ones, whose K is the
+    tensor's rows); row strides may be larger than the rows. bias BF16 or float32 [N]; activation None,
+    'relu', 'relu2', 'gelu' (tanh form) or 'silu'; residual [M, N] in the output's type (BF16 or
+    float32), may be `out` itself. Returns a dict: out [M, N]; with keep_preact, preact BF16 [M, N],
+    the activation's input, which nvfp4_gemm_epilogue_backward takes; with with_amax, amax float32 [1]:
+    max |out|, the amax_row of the next quantization."""
+    dev = _device_of(a_codes, "a_codes")
+    L = _lib.load()
+    a, M, K = _operand("a", a_codes, a_scales, a_gscale, dev)
+    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev)
+    if K != Kb:
+        raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
+    e, got = _gemm_epilogue(bias, (N,), activation, residual, out, out_dtype, (M, N), keep_preact,
+                            preact, amax, with_amax, 1, dev)
+    status = L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, ctypes.byref(e),
+                          got["out"].data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_gemm")
+    return got
+
+
+def nvfp4_gemm_grouped(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, offsets, bias=None,
+                       activation=None, residual=None, out_dtype=None, keep_preact=False,
+                       with_amax=False, out=None, preact=None, amax=None):
+    """The experts' products of packed rows: out[rows of e] = act(a[rows of e] b[e]^T + bias[e]) +
+    residual. a [T, K] with a_gscale [E, 2] as nvfp4_quantize_grouped writes it, offsets int32 [E]
+    expert ends; b_codes [E, N, K/2], b_scales [E, N, K/16], b_gscale [E, 2] (strided views too: the
+    columnwise outputs of stacked weights [E * N', K'], as [K', E, N'/2] with the first two dimensions
+    exchanged, are the operand of the backward pass). bias [E, N], amax [E]; the rest as nvfp4_gemm.
+    Rows past the last end are not read and get zeros."""
+    dev = _device_of(a_codes, "a_codes")
+    L = _lib.load()
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1-D int32 CUDA tensor")
+    E = offsets.shape[0]
+    _check(offsets, "offsets", torch.int32, (E,), dev)
+    a, T, K = _operand("a", a_codes, a_scales, a_gscale, dev, E)
+    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev, E, stacked=True)
+    if K != Kb:
+        raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
+    e, got = _gemm_epilogue(bias, (E, N), activation, residual, out, out_dtype, (T, N), keep_preact,
+                            preact, amax, with_amax, E, dev)
+    status = L.nvfp4_gemm_grouped(ctypes.byref(a), ctypes.byref(b), offsets.data_ptr(), _small(E), T, N,
+                                  K, ctypes.byref(e), got["out"].data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_gemm_grouped")
+    return got
+
+
+def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, offsets,
+                             out_dtype=None, out=None, accumulate=False):
+    """The experts' weight gradients out[e] = a[:, tokens of e] b[:, tokens of e]^T (BF16 or float32
+    [E, M, N]) from the columnwise outputs of nvfp4_quantize_grouped for two packed tensors with these
+    offsets: codes [M or N, capacity / 2], scales [.., capacity / 16], gscale [E, 2] (both with the same
+    RHT signs, or neither). accumulate adds to `out`."""
+    dev = _device_of(a_codes, "a_codes")
+    L = _lib.load()
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
+        raise TypeError("offsets must be a 1-D int32 CUDA tensor")
+    E = offsets.shape[0]
+    _check(offsets, "offsets", torch.int32, (E,), dev)
+    a, M, K = _operand("a", a_codes, a_scales, a_gscale, dev, E)
+    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev, E)
+    if K != Kb:
+        raise ValueError("a and b must have the same capacity, not %d and %d" % (K, Kb))
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None and out_dtype is None:
+        out_dtype = out.dtype
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    out = _out(out, "out", out_dtype, (E, M, N), dev)
+    status = L.nvfp4_gemm_grouped_wgrad(ctypes.byref(a), ctypes.byref(b), offsets.data_ptr(), _small(E),
+                                        M, N, K, out.element_size(), int(bool(accumulate)),
+                                        out.data_ptr(), _stream(dev))
+    _raise_if(status, "nvfp4_gemm_grouped_wgrad")
+    return out
+
+
+def nvfp4_gemm_epilogue_backward_workspace(M, N):
+    """Bytes of workspace of nvfp4_gemm_epilogue_backward."""
+    n = ctypes.c_size_t(0)
+    _raise_if(_lib.load().nvfp4_gemm_epilogue_backward_workspace(M, N, ctypes.byref(n)),
+              "nvfp4_gemm_epilogue_backward_workspace")
+    return n.value
+
+
+def nvfp4_gemm_epilogue_backward(grad_out, preact, activation, grad_preact=None, grad_bias=None,
+                                 amax=None, workspace=None):
+    """The gradient through an epilogue: (grad_preact BF16 [M, N] = grad_out * act'(preact), grad_bias
+    float32 [N], amax float32 [1]) from grad_out and the kept preact, both BF16 [M, N]. grad_preact and
+    amax are what the quantization for the products of the backward pass takes; grad_preact may be
+    grad_out itself. workspace: a uint8 tensor of at least nvfp4_gemm_epilogue_backward_workspace(M, N)
+    bytes."""
+    _check_x(grad_out)
+    L = _lib.load()
+    M, N = grad_out.shape
+    dev = grad_out.device
+    if N % 8 != 0:
+        raise ValueError("grad_out must have a multiple of 8 columns")
+    _check(preact, "preact", torch.bfloat16, (M, N), dev)
+    grad_preact = _out(grad_preact, "grad_preact", torch.bfloat16, (M, N), dev)
+    grad_bias = _out(grad_bias, "grad_bias", torch.float32, (N,), dev)
+    amax = _out(amax, "amax", torch.float32, (1,), dev)
+    if workspace is None:
+        workspace = torch.empty(nvfp4_gemm_epilogue_backward_workspace(M, N), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    status = L.nvfp4_gemm_epilogue_backward(
+        grad_out.data_ptr(), preact.data_ptr(), M, N, _activation(activation), grad_preact.data_ptr(),
+        grad_bias.data_ptr(), amax.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dev))
+    _raise_if(status, "nvfp4_gemm_epilogue_backward")
+    return grad_preact, grad_bias, amax
+
+
+class AdamW:
+    """nvfp4_adamw_step over a fixed list of tensors: float32 parameters, gradients (float32 or BF16,
+    buffers that every step reads anew), BF16 weights (written by every step; optional) and states in
+    32 or 8 bits, all contiguous on one device, of any shape. weight_decay: a number, or one for each
+    tensor. `state`: a dict of lists as in `self.state` to go on from (a checkpoint); else zeros.
+
+    self.state: exp_avg, exp_avg_sq (float32, or uint8 E4M3 codes of the average and of the square
+    root), and with 8 bits exp_avg_scales, exp_avg_sq_scales (uint8 E8M0, one for 32 elements)."""
+
+    def __init__(self, params, grads, weights=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.01, state_bits=32, state=None):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        self.params, self.grads = list(params), list(grads)
+        n = len(self.params)
+        self.weights = [None] * n if weights is None else list(weights)
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else \
+            [float(v) for v in weight_decay]
+        if len(self.grads) != n or len(self.weights) != n or len(decay) != n:
+            raise ValueError("params, grads, weights and weight_decay must have the same length")
+        if n == 0:
+            raise ValueError("no parameters")
+        self.device = _device_of(self.params[0], "params")
+        grad_dtype = self.grads[0].dtype
+        if grad_dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError("grads must be float32 or bfloat16 tensors")
+        self.lr, self.betas, self.eps = lr, tuple(betas), eps
+        self.state_bits, self.grad_bytes = state_bits, self.grads[0].element_size()
+        kinds = {"exp_avg": torch.float32, "exp_avg_sq": torch.float32}
+        if state_bits == 8:
+            kinds = {"exp_avg": torch.uint8, "exp_avg_sq": torch.uint8,
+                     "exp_avg_scales": torch.uint8, "exp_avg_sq_scales": torch.uint8}
+        sizes = lambda k, p: (p.numel() + 31) // 32 if k.endswith("scales") else p.numel()  # noqa: E731
+        for p in self.params:
+            if not isinstance(p, torch.Tensor):
+                raise TypeError("params must be float32 tensors")
+        if state is None:
+            state = {k: [torch.zeros(sizes(k, p), dtype=t, device=self.device) for p in self.params]
+                     for k, t in kinds.items()}
+        if set(state) != set(kinds) or any(len(v) != n for v in state.values()):
+            raise ValueError("state must hold lists of %d tensors: %s" % (n, ", ".join(kinds)))
+        self.state = {k: list(v) for k, v in state.items()}
+        self._table = (_lib.AdamWTensor * n)()
+        for i, p in enumerate(self.params):
+            _check(p, "params[%d]" % i, torch.float32, p.shape, self.device)
+            _check(self.grads[i], "grads[%d]" % i, grad_dtype, p.shape, self.device)
+            if self.weights[i] is not None:
+                _check(self.weights[i], "weights[%d]" % i, torch.bfloat16, p.shape, self.device)
+            for k, t in kinds.items():
+                s = self.state[k][i]
+                shape = (sizes(k, p),) if k.endswith("scales") or s.dim() == 1 else p.shape
+                _check(s, "state[%r][%d]" % (k, i), t, shape, self.device)
+            at = {k: self.state[k][i].data_ptr() for k in kinds}
+            self._table[i] = _lib.AdamWTensor(
+                p.numel(), p.data_ptr(), self.grads[i].data_ptr(), at["exp_avg"], at["exp_avg_sq"],
+                at.get("exp_avg_scales"), at.get("exp_avg_sq_scales"), _ptr(self.weights[i]), decay[i])
+
+    def step(self, step, lr=None, grad_scale=None, seed=0, amax=None):
+        """One step (`step` = 1 for the first; an int, or an int32 [1] tensor that the kernel reads, for
+        captured calls). grad_scale: float32 [1], multiplies the gradients. seed: of the stochastic
+        rounding of 8-bit states. Returns amax float32 [tensors]: max |weight| of each."""
+        L = _lib.load()
+        dev = self.device
+        amax = _out(amax, "amax", torch.float32, (len(self.params),), dev)
+        on_device = isinstance(step, torch.Tensor)
+        if on_device:
+            _check(step, "step", torch.int32, (1,), dev)
+        if grad_scale is not None:
+            _check(grad_scale, "grad_scale", torch.float32, (1,), dev)
+        cfg = _lib.AdamWConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+                               0 if on_device else step, step.data_ptr() if on_device else None,
+                               _ptr(grad_scale), seed, self.state_bits, self.grad_bytes)
+        status = L.nvfp4_adamw_step(self._table, len(self.params), ctypes.byref(cfg), amax.data_ptr(),
+                                    _stream(dev))
+        _raise_if(status, "nvfp4_adamw_step")
+        return amax
+
+
 WORKSPACE_BYTES = 16384
 
 

@@ -18,9 +18,10 @@ SOURCES = ["quantize_row.cu", "quantize_col.cu", "quantize_rowcol.cu", "quantize
            "quantize_rowcol_rht_fast.cu",
            "quantize_2d.cu", "amax_dequant.cu", "nvfp4_api.cu", "quantize_noalloc.cu",
            "host_pipeline.cu", "amax_pass.cu", "mx_kernel.cu", "producer.cu",
-           "moe_route.cu", "checkpoint.cu", "moe_checkpoint_api.cu"]
+           "moe_route.cu", "checkpoint.cu", "moe_checkpoint_api.cu",
+           "router.cu", "gemm.cu", "gemm_epilogue.cu", "gemm_api.cu", "adamw.cu"]
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "aux_internal.h", "quantize_kernel.cuh",
-           "fused_amax.cuh", "tile_ring.h"]
+           "fused_amax.cuh", "tile_ring.h", "gemm_internal.h", "gemm_device.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -1,0 +1,332 @@
+// AdamW over many tensors at once, its states in 32 or in 8 bits (declared in include/nvfp4.h).
+//
+// A launch takes up to kTensors tensors, whose pointers travel in the kernel's parameters: nothing is
+// kept on the device between calls, and a captured call replays with what it was given. The tensors
+// are cut into chunks of kChunk elements; a CTA takes chunks of all tensors in turn. A thread has
+// eight consecutive elements, so that four lanes hold a block of 32 states.
+//
+// The order of the binary32 operations is fixed (no contraction), so that the states do not depend on
+// how the work is split.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "nvfp4.h"
+#include "nvfp4_device.cuh"
+#include "aux_internal.h"
+#include "nvfp4_internal.h"
+
+#define NVFP4_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kTensors = 128;
+constexpr int kThreads = 256;
+constexpr int kChunk = kThreads * 8;
+
+struct AdamwArgs {
+  int32_t count;                 // tensors of this launch
+  int32_t base;                  // index of the first one in the caller's list
+  float beta1, beta2, rest1, rest2, eps;
+  float lr, log_beta1, log_beta2;  // with step_device
+  float step_size, root_scale;     // lr / (1 - beta1^t), (1 - beta2^t)^-0.5
+  int32_t step;
+  const int32_t* step_device;
+  const float* grad_scale;
+  float* amax;
+  uint32_t key[2][10];
+  int64_t chunks;
+  int64_t first[kTensors];       // first chunk of each tensor
+  nvfp4_adamw_tensor t[kTensors];
+};
+static_assert(sizeof(AdamwArgs) < 32764, "kernel parameters");
+
+// The exponent e of the smallest 2^e, e >= -127, with top <= 448 * 2^e, plus 127.
+__device__ __forceinline__ uint32_t scale_of(float top) {
+  const uint32_t b = __float_as_uint(top);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(e, 0);
+}
+__device__ __forceinline__ float scale_value(uint32_t s) {  // 2^(s - 127)
+  return __uint_as_float(s == 0 ? 0x00400000u : s << 23);
+}
+__device__ __forceinline__ float scale_inverse(uint32_t s) {  // 2^(127 - s), s <= 247
+  return __uint_as_float((254u - s) << 23);
+}
+__device__ __forceinline__ void from_e4m3x2(uint32_t pair, float& lo, float& hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  lo = f.x;
+  hi = f.y;
+}
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Eight values of a buffer from element i, `have` of them inside (the rest zeros).
+template <typename T>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int have, float (&v)[8]) {
+  const T* const q = static_cast<const T*>(p) + i;
+  if constexpr (sizeof(T) == 4) {
+    if (have == 8) {
+      const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < have ? q[j] : 0.0f;
+  } else {
+    if (have == 8) {
+      const uint4 a = *reinterpret_cast<const uint4*>(q);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] = j < have ? __bfloat162float(q[j]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int64_t i, int have, const float (&v)[8]) {
+  if (have == 8) {
+    reinterpret_cast<float4*>(p + i)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p + i)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (j < have) p[i + j] = v[j];
+}
+__device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int have) {
+  const uint8_t* const q = static_cast<const uint8_t*>(p) + i;
+  if (have == 8) return *reinterpret_cast<const uint2*>(q);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (j < have) w[j / 4] |= (uint32_t)q[j] << (8 * (j % 4));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(void* p, int64_t i, int have, uint2 c) {
+  uint8_t* const q = static_cast<uint8_t*>(p) + i;
+  if (have == 8) {
+    *reinterpret_cast<uint2*>(q) = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (j < have) q[j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+}
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&v)[8]) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    from_e4m3x2((w[j / 2] >> (16 * (j % 2))) & 0xFFFFu, v[2 * j], v[2 * j + 1]);
+    v[2 * j] = __fmul_rn(v[2 * j], scale);
+    v[2 * j + 1] = __fmul_rn(v[2 * j + 1], scale);
+  }
+}
+__device__ __forceinline__ float block_max(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+}
+
+template <bool EIGHT, typename G>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs a) {
+  pdl_wait();
+  pdl_allow_next();
+  float step_size = a.step_size, root_scale = a.root_scale;
+  int32_t step = a.step;
+  if (a.step_device != nullptr) {
+    step = max(*a.step_device, 1);
+    step_size = __fdiv_rn(a.lr, -expm1f((float)step * a.log_beta1));
+    root_scale = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)step * a.log_beta2)));
+  }
+  const float grad_scale = a.grad_scale ? *a.grad_scale : 1.0f;
+  int at = 0;  // the chunk's tensor
+  uint32_t top = 0u;
+  auto report = [&]() {
+    if (a.amax == nullptr) return;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, top);
+    if ((threadIdx.x & 31) == 0 && m != 0u)
+      atomicMax(reinterpret_cast<uint32_t*>(a.amax) + a.base + at, m << 16);
+  };
+  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+    int now = at;
+    while (now + 1 < a.count && a.first[now + 1] <= chunk) now++;
+    if (now != at) {
+      report();
+      at = now;
+      top = 0u;
+    }
+    const nvfp4_adamw_tensor& t = a.t[at];
+    const int64_t i = (chunk - a.first[at]) * kChunk + threadIdx.x * 8;
+    const int have = (int)max((int64_t)0, min((int64_t)8, t.n - i));
+    float p[8], g[8], m[8], v[8], root[8];
+    load8<float>(t.param, i, have, p);
+    load8<G>(t.grad, i, have, g);
+    if constexpr (EIGHT) {
+      const int64_t b = i >> 5;
+      const uint32_t ms = have > 0 ? t.exp_avg_scales[b] : 0u, vs = have > 0 ? t.exp_avg_sq_scales[b] : 0u;
+      decode8(load_codes(t.exp_avg, i, have), scale_value(ms), m);
+      decode8(load_codes(t.exp_avg_sq, i, have), scale_value(vs), v);
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = __fmul_rn(v[j], v[j]);
+    } else {
+      load8<float>(t.exp_avg, i, have, m);
+      load8<float>(t.exp_avg_sq, i, have, v);
+    }
+    const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, t.weight_decay));
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const float x = __fmul_rn(g[j], grad_scale);
+      m[j] = __fadd_rn(__fmul_rn(m[j], a.beta1), __fmul_rn(x, a.rest1));
+      v[j] = __fadd_rn(__fmul_rn(v[j], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
+      root[j] = __fsqrt_rn(v[j]);
+      const float update = __fdiv_rn(__fmul_rn(m[j], step_size),
+                                     __fadd_rn(__fmul_rn(root[j], root_scale), a.eps));
+      p[j] = __fsub_rn(__fmul_rn(p[j], keep), update);
+      w[j] = __bfloat16_as_ushort(__float2bfloat16_rn(p[j]));
+      if (j < have) top = max(top, w[j] & 0x7FFFu);
+    }
+    store8(t.param, i, have, p);
+    if (t.weight != nullptr) {
+      if (have == 8) {
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.weight) + i)[0] =
+            make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+          if (j < have) static_cast<uint16_t*>(t.weight)[i + j] = (uint16_t)w[j];
+      }
+    }
+    if constexpr (EIGHT) {
+      const uint32_t ms = scale_of(block_max(m)), vs = scale_of(block_max(root));
+      const float mi = scale_inverse(ms), vi = scale_inverse(vs);
+      const uint64_t draw = (uint64_t)i >> 3;
+      const uint4 r = philox4x32_10_rk(make_uint4((uint32_t)draw, (uint32_t)(draw >> 32),
+                                                  (uint32_t)(a.base + at), (uint32_t)step), a.key);
+      const uint32_t words[4] = {r.x, r.y, r.z, r.w};
+      uint32_t mc[4], vc[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        mc[j] = to_e4m3x2(__fmul_rn(m[2 * j], mi), __fmul_rn(m[2 * j + 1], mi));
+        float q[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+          const float x = __fmul_rn(root[2 * j + k], vi);
+          const int e = max((int)(__float_as_uint(x) >> 23) - 127, -6) - 3;  // of the code step
+          const float u = __fmul_rn((float)(k ? words[j] >> 16 : words[j] & 0xFFFFu), 1.0f / 65536.0f);
+          float n = floorf(__fadd_rn(__fmul_rn(x, __uint_as_float((uint32_t)(127 - e) << 23)), u));
+          if (x > 0.0f) n = fmaxf(n, 1.0f);
+          q[k] = __fmul_rn(n, __uint_as_float((uint32_t)(127 + e) << 23));
+        }
+        vc[j] = to_e4m3x2(q[0], q[1]);
+      }
+      store_codes(t.exp_avg, i, have, make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16));
+      store_codes(t.exp_avg_sq, i, have, make_uint2(vc[0] | vc[1] << 16, vc[2] | vc[3] << 16));
+      if ((threadIdx.x & 3) == 0 && have > 0) {
+        t.exp_avg_scales[i >> 5] = (uint8_t)ms;
+        t.exp_avg_sq_scales[i >> 5] = (uint8_t)vs;
+      }
+    } else {
+      store8(static_cast<float*>(t.exp_avg), i, have, m);
+      store8(static_cast<float*>(t.exp_avg_sq), i, have, v);
+    }
+  }
+  report();
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+NVFP4_EXPORT nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int32_t count,
+                                           const nvfp4_adamw_config* cfg, float* amax, void* stream) {
+  if (count < 0 || cfg == nullptr || (count > 0 && tensors == nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if ((cfg->state_bits != 32 && cfg->state_bits != 8) || (cfg->grad_bytes != 4 && cfg->grad_bytes != 2) ||
+      !std::isfinite(cfg->lr) || !(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0) ||
+      !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0) || !std::isfinite(cfg->eps) ||
+      (cfg->step_device == nullptr && (cfg->step < 1 || cfg->step > INT32_MAX)))
+    return NVFP4_ERR_INVALID_ARG;
+  if ((float)cfg->eps == 0.0f) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(cfg->step_device, 4) || !aligned(cfg->grad_scale, 4) || !aligned(amax, 4))
+    return NVFP4_ERR_ALIGN;
+  const bool eight = cfg->state_bits == 8;
+  for (int32_t i = 0; i < count; i++) {
+    const nvfp4_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !std::isfinite(t.weight_decay)) return NVFP4_ERR_INVALID_ARG;
+    if (t.n > (int64_t(1) << 48)) return NVFP4_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr ||
+        (eight && (t.exp_avg_scales == nullptr || t.exp_avg_sq_scales == nullptr)))
+      return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(t.param, 16) || !aligned(t.grad, 16) || !aligned(t.exp_avg, 16) ||
+        !aligned(t.exp_avg_sq, 16) || !aligned(t.weight, 16))
+      return NVFP4_ERR_ALIGN;
+  }
+  if (count == 0) return NVFP4_OK;
+  int sms = 0;
+  uint32_t* status = nullptr;
+  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = zero_words(amax, count, s);
+  AdamwArgs a;
+  a.beta1 = (float)cfg->beta1;
+  a.beta2 = (float)cfg->beta2;
+  a.rest1 = (float)(1.0 - cfg->beta1);
+  a.rest2 = (float)(1.0 - cfg->beta2);
+  a.eps = (float)cfg->eps;
+  a.lr = (float)cfg->lr;
+  a.log_beta1 = (float)std::log(cfg->beta1);
+  a.log_beta2 = (float)std::log(cfg->beta2);
+  a.step = (int32_t)cfg->step;
+  a.step_size = a.root_scale = 0.0f;
+  if (cfg->step_device == nullptr) {
+    a.step_size = (float)(cfg->lr / (1.0 - std::pow(cfg->beta1, (double)cfg->step)));
+    a.root_scale = (float)std::pow(1.0 - std::pow(cfg->beta2, (double)cfg->step), -0.5);
+  }
+  a.step_device = cfg->step_device;
+  a.grad_scale = cfg->grad_scale;
+  a.amax = amax;
+  uint32_t k0 = (uint32_t)cfg->seed, k1 = (uint32_t)(cfg->seed >> 32);
+  for (int r = 0; r < 10; r++, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) a.key[0][r] = k0, a.key[1][r] = k1;
+  for (int32_t base = 0; base < count && e == cudaSuccess; base += kTensors) {
+    a.base = base;
+    a.count = count - base < kTensors ? count - base : kTensors;
+    a.chunks = 0;
+    for (int32_t i = 0; i < a.count; i++) {
+      a.first[i] = a.chunks;
+      a.t[i] = tensors[base + i];
+      a.chunks += (a.t[i].n + kChunk - 1) / kChunk;
+    }
+    if (a.chunks == 0) continue;
+    const dim3 grid((unsigned)(a.chunks < 8 * sms ? a.chunks : 8 * sms)), block(kThreads);
+    if (eight)
+      e = cfg->grad_bytes == 4 ? launch_pdl(adamw_kernel<true, float>, grid, block, 0, s, a)
+                               : launch_pdl(adamw_kernel<true, __nv_bfloat16>, grid, block, 0, s, a);
+    else
+      e = cfg->grad_bytes == 4 ? launch_pdl(adamw_kernel<false, float>, grid, block, 0, s, a)
+                               : launch_pdl(adamw_kernel<false, __nv_bfloat16>, grid, block, 0, s, a);
+  }
+  if (e == cudaSuccess) return NVFP4_OK;
+  (void)cudaGetLastError();
+  return NVFP4_ERR_CUDA;
+}

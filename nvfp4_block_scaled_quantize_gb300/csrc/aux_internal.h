@@ -98,6 +98,8 @@ cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, c
 // these two groups set up (nvfp4_api.cu); false when a CUDA call failed.
 bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas = nullptr);
 int setup_fault();  // nvfp4_debug_setup_fault
+// Clears n 32-bit words in stream order, by a kernel (moe_checkpoint_api.cu); p may be null.
+cudaError_t zero_words(void* p, int64_t n, cudaStream_t s);
 
 cudaError_t launch_amax_flat(const void* x, int64_t n_elems, float* out0, float* out1, int grid,
                              cudaStream_t s);

@@ -63,6 +63,8 @@ cudaError_t zero(void* p, int64_t n, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t nvfp4::zero_words(void* p, int64_t n, cudaStream_t s) { return zero(p, n, s); }
+
 NVFP4_EXPORT nvfp4_status nvfp4_moe_plan(const void* expert_ids, int32_t id_bytes, int64_t T,
                                          int32_t K, int32_t E, int32_t* row_of_slot,
                                          int32_t* slot_of_row, int32_t* offsets, void* stream) {

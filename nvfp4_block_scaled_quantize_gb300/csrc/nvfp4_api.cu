@@ -12,6 +12,7 @@
 #include "nvfp4.h"
 #include "nvfp4_device.cuh"
 #include "aux_internal.h"
+#include "gemm_internal.h"
 #include "nvfp4_internal.h"
 
 #define NVFP4_EXPORT extern "C" __attribute__((visibility("default")))
@@ -60,7 +61,8 @@ bool prepare_aux(DeviceState& st) {
   if (g_setup_fault.load() == 1) return false;
   if (st.aux_ready) return true;
   st.aux_ready = prepare_moe_kernels(&st.plan_ctas) == cudaSuccess &&
-                 prepare_checkpoint_kernels() == cudaSuccess;
+                 prepare_checkpoint_kernels() == cudaSuccess &&
+                 prepare_gemm_kernels() == cudaSuccess;
   if (!st.aux_ready) (void)cudaGetLastError();
   return st.aux_ready;
 }

@@ -1,0 +1,527 @@
+// The router: scores of T tokens, the choice of K experts each and their weights, and the gradient
+// of the logits (declared in include/nvfp4.h).
+//
+// A warp has a token, a lane up to SL of its logits. Experts are drawn one by one: a candidate is a
+// 32-bit key that ascends with p + bias (without a bias: with the logit), the warp's largest key and
+// its lowest index are one reduction instruction each (redux.sync). Binary32 scores are off by a few
+// units in the last place, which can exchange two candidates that are close: where two neighbours of
+// the drawn order (or the last kept and the first dropped group) are closer than that error allows,
+// the row is drawn again from binary64 scores. With normal logits that happens to one row in a few
+// hundred; ranking every row in binary64 would cost more than everything else here.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "nvfp4.h"
+#include "nvfp4_device.cuh"
+#include "aux_internal.h"
+#include "nvfp4_internal.h"
+
+#define NVFP4_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace nvfp4 {
+namespace {
+
+constexpr uint32_t kBadRoute = 0x4u;  // NVFP4_DEVICE_BAD_ROUTE
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr int kRouterWarps = 8;
+constexpr int kMaxE = 256;
+
+struct RouterArgs {
+  const void* logits;
+  const float* bias;
+  int64_t T;
+  int32_t E, K, groups, top_groups, size;  // size: experts of a group
+  float scale;
+  int32_t* ids;
+  float* weights;
+  uint32_t* status;
+};
+
+template <typename T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+// A key that ascends with v (-0 counts as 0); 0 is kept for what cannot be drawn.
+__device__ __forceinline__ uint32_t ascending(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (int32_t)b < 0 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ascending(uint32_t k) {
+  return __uint_as_float((int32_t)k < 0 ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = v + __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+
+// 1 / (1 + exp(-x)) over exp(c): c <= 0, and c = 0 where x > 0. Never 0 / 0, however low x is.
+__device__ __forceinline__ float sigmoid_over(float x, float c) {
+  if (x >= 0.0f) return __fdividef(1.0f, 1.0f + __expf(-x));
+  return __fdividef(__expf(x - c), 1.0f + __expf(x));
+}
+
+// One draw: the largest (value, lowest index) of the warp, in binary64.
+struct Best {
+  double v;
+  int i;
+};
+__device__ __forceinline__ Best warp_best(Best b) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const double v = __shfl_xor_sync(kAll, b.v, o);
+    const int i = __shfl_xor_sync(kAll, b.i, o);
+    if (i < kMaxE && (b.i >= kMaxE || v > b.v || (v == b.v && i < b.i))) b = {v, i};
+  }
+  return b;
+}
+
+// The row again with binary64 scores. `l`: this lane's logits. Lane k gets the k-th choice.
+template <int SL, int V, bool SOFTMAX>
+__device__ __noinline__ int draw_again(const RouterArgs& a, const float (&l)[SL], double* values) {
+  const int lane = threadIdx.x & 31;
+  double p[SL];
+  if (SOFTMAX) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < SL; j++) top = fmaxf(top, l[j]);
+    top = warp_max(top);
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < SL; j++) sum += p[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)top);
+    sum = warp_sum(sum);
+#pragma unroll
+    for (int j = 0; j < SL; j++) p[j] = p[j] / sum;
+  } else {
+#pragma unroll
+    for (int j = 0; j < SL; j++) p[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+  }
+  uint32_t held = 0;  // bit j: candidate j may be drawn
+#pragma unroll
+  for (int j = 0; j < SL; j++) {
+    const int e = ((j / V) * 32 + lane) * V + j % V;
+    if (e < a.E) {
+      const bool masked = l[j] == -INFINITY || (a.bias && __ldg(a.bias + e) == -INFINITY);
+      if (a.bias) p[j] += (double)__ldg(a.bias + e);
+      if (masked) p[j] = -INFINITY;
+      else held |= 1u << j;
+      values[e] = p[j];
+    }
+    if (!a.bias) p[j] = (double)l[j];
+  }
+  __syncwarp();
+  if (a.top_groups < a.groups) {
+    double rank[kMaxE / 32];
+    uint32_t kept = 0, open = 0;
+#pragma unroll
+    for (int j = 0; j < kMaxE / 32; j++) {
+      const int g = lane + 32 * j;
+      if (g >= a.groups) continue;
+      double v1 = -INFINITY, v2 = -INFINITY;
+      for (int i = 0; i < a.size; i++) {
+        const double v = values[g * a.size + i];
+        if (v > v1) v2 = v1, v1 = v;
+        else if (v > v2) v2 = v;
+      }
+      rank[j] = a.size > 1 ? v1 + v2 : v1;
+      open |= 1u << j;
+    }
+    for (int n = 0; n < a.top_groups; n++) {
+      Best b = {0.0, kMaxE};
+#pragma unroll
+      for (int j = 0; j < kMaxE / 32; j++)
+        if (((open >> j) & 1u) && (b.i >= kMaxE || rank[j] > b.v)) b = {rank[j], lane + 32 * j};
+      b = warp_best(b);
+      if ((b.i & 31) == lane) {
+        open &= ~(1u << (b.i >> 5));
+        kept |= 1u << (b.i >> 5);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const int e = ((j / V) * 32 + lane) * V + j % V, g = e < a.E ? e / a.size : 0;
+      const uint32_t k = __shfl_sync(kAll, kept, g & 31);
+      if (!((k >> (g >> 5)) & 1u)) held &= ~(1u << j);
+    }
+  }
+  int mine = -1;
+  for (int n = 0; n < a.K; n++) {
+    Best b = {0.0, kMaxE};
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const int e = ((j / V) * 32 + lane) * V + j % V;
+      if (((held >> j) & 1u) && (b.i >= kMaxE || p[j] > b.v)) b = {p[j], e};
+    }
+    b = warp_best(b);
+    if (b.i >= kMaxE) break;
+    if (lane == n) mine = b.i;
+    const int at = b.i / V;
+    if ((at & 31) == lane) held &= ~(1u << ((at >> 5) * V + b.i % V));
+  }
+  __syncwarp();
+  return mine;
+}
+
+template <int SL, int V, bool SOFTMAX, typename L>
+__global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterArgs a, bool renorm) {
+  __shared__ double values[kRouterWarps][kMaxE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_allow_next();
+  const int64_t step = (int64_t)gridDim.x * kRouterWarps;
+  const L* const logits = static_cast<const L*>(a.logits);
+  for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp; t < a.T; t += step) {
+    float l[SL];
+    uint32_t key[SL];
+    const L* const row = logits + t * a.E;
+    float top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const int e = ((j / V) * 32 + lane) * V + j % V;
+      l[j] = e < a.E ? widen<L>(row[e]) : -INFINITY;
+      bad |= !(l[j] < INFINITY);
+      top = fmaxf(top, l[j]);
+    }
+    top = warp_max(top);
+    // the error of p grows with the largest p of the row (tie)
+    float tie = 2e-6f, inv = 1.0f;
+    const bool scored = a.bias != nullptr || a.top_groups < a.groups || (SOFTMAX && !renorm);
+    if (SOFTMAX && scored) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
+      sum = warp_sum(sum);
+      inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+      tie *= inv;
+    }
+    float* const choice = reinterpret_cast<float*>(values[warp]);
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const int e = ((j / V) * 32 + lane) * V + j % V;
+      key[j] = 0u;
+      if (e >= a.E) continue;
+      float c = l[j];
+      if (scored) {
+        float p = SOFTMAX ? (l[j] == -INFINITY ? 0.0f : __expf(l[j] - top) * inv)
+                          : __fdividef(1.0f, 1.0f + __expf(-l[j]));
+        if (a.bias) {
+          const float b = __ldg(a.bias + e);
+          p += b;
+          bad |= !(p < INFINITY) || !(b < INFINITY);
+          c = l[j] == -INFINITY ? -INFINITY : p;
+        }
+        choice[e] = l[j] == -INFINITY ? -INFINITY : p;
+      }
+      if (c != -INFINITY) key[j] = ascending(c);
+    }
+    bad = __any_sync(kAll, bad);
+    bool close = false;
+    if (a.top_groups < a.groups && !bad) {
+      __syncwarp();
+      uint32_t rank[kMaxE / 32];
+      uint32_t kept = 0;
+#pragma unroll
+      for (int j = 0; j < kMaxE / 32; j++) {
+        const int g = lane + 32 * j;
+        rank[j] = 0u;
+        if (g >= a.groups) continue;
+        float v1 = -INFINITY, v2 = -INFINITY;
+        int at = lane % a.size;  // lanes start at different banks
+        for (int i = 0; i < a.size; i++) {
+          const float v = choice[g * a.size + at];
+          at = at + 1 == a.size ? 0 : at + 1;
+          v2 = fmaxf(v2, fminf(v1, v));
+          v1 = fmaxf(v1, v);
+        }
+        rank[j] = ascending(a.size > 1 ? v1 + v2 : v1);
+      }
+      __syncwarp();
+      uint32_t last = 0u;
+      for (int n = 0; n <= a.top_groups; n++) {  // the first that is dropped too
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < kMaxE / 32; j++) m = max(m, rank[j]);
+        const uint32_t best = __reduce_max_sync(kAll, m);
+        if (n == a.top_groups) {
+          const float x = from_ascending(last), y = from_ascending(best);
+          close = x - y < 2.0f * tie + 5e-7f * fmaxf(fabsf(x), fabsf(y));
+          break;
+        }
+        uint32_t g = kMaxE;
+#pragma unroll
+        for (int j = kMaxE / 32 - 1; j >= 0; j--)
+          if (rank[j] == best) g = lane + 32 * j;
+        g = __reduce_min_sync(kAll, g);
+#pragma unroll
+        for (int j = 0; j < kMaxE / 32; j++)
+          if (g == lane + 32 * j) {
+            rank[j] = 0u;
+            kept |= 1u << j;
+          }
+        last = best;
+      }
+#pragma unroll
+      for (int j = 0; j < SL; j++) {
+        const int e = ((j / V) * 32 + lane) * V + j % V, g = e < a.E ? e / a.size : 0;
+        const uint32_t k = __shfl_sync(kAll, kept, g & 31);
+        if (!((k >> (g >> 5)) & 1u)) key[j] = 0u;
+      }
+    }
+    int mine = -1;
+    if (!bad) {
+      uint32_t before = 0u;
+      int drawn = -1;
+      for (int n = 0; n <= a.K; n++) {  // one more than is taken, to see how close it is
+        if (n == a.K && !a.bias) break;
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < SL; j++) m = max(m, key[j]);
+        const uint32_t best = __reduce_max_sync(kAll, m);
+        if (best == 0u) break;
+        uint32_t e = kMaxE;
+#pragma unroll
+        for (int j = SL - 1; j >= 0; j--)
+          if (key[j] == best) e = ((j / V) * 32 + lane) * V + j % V;
+        e = __reduce_min_sync(kAll, e);
+        if (a.bias && n > 0) {
+          const float x = from_ascending(before), y = from_ascending(best);
+          if (x - y < tie + 2.5e-7f * fmaxf(fabsf(x), fabsf(y))) {
+            // the same logit and bias: equal in any precision
+            const bool same = widen<L>(row[e]) == widen<L>(row[drawn]) &&
+                              __ldg(a.bias + e) == __ldg(a.bias + drawn);
+            close |= !same;
+          }
+        }
+        if (n < a.K) {
+          if (lane == n) mine = (int)e;
+          drawn = (int)e;
+          before = best;
+#pragma unroll
+          for (int j = 0; j < SL; j++)
+            if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
+        }
+      }
+      if (close) mine = draw_again<SL, V, SOFTMAX>(a, l, values[warp]);
+    } else if (lane == 0) {
+      atomicOr(a.status, kBadRoute);
+    }
+    const float x = mine >= 0 ? widen<L>(row[mine]) : -INFINITY;
+    float w = 0.0f;
+    if (renorm) {
+      const float high = warp_max(x);
+      if (mine >= 0) w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
+      const float sum = warp_sum(w);
+      w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+    } else if (mine >= 0) {
+      w = SOFTMAX ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
+    }
+    if (lane < a.K) {
+      a.ids[t * a.K + lane] = mine;
+      a.weights[t * a.K + lane] = mine >= 0 ? w * a.scale : 0.0f;
+    }
+  }
+}
+
+struct RouterBackArgs {
+  const float* grad;
+  const void* logits;
+  const int32_t* ids;
+  int64_t T;
+  int32_t E, K;
+  float scale;
+  void* out;
+  uint32_t* status;
+};
+
+// d logit: with r = p / sum of the chosen p (renormalized) and g = scale * grad_weights,
+//   softmax:  r (g - sum r g)             sigmoid:  (1 - p) r (g - sum r g)
+// and without, p (g - sum p g) over all experts (g = 0 where not chosen) and p (1 - p) g. Only the
+// softmax without renormalization reads all logits; the rest gathers the chosen ones. Bound by the
+// write of the gradient.
+template <int SL, int V, bool SOFTMAX, typename L>
+__global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(const RouterBackArgs a,
+                                                                            bool renorm) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_allow_next();
+  const int64_t step = (int64_t)gridDim.x * kRouterWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp; t < a.T; t += step) {
+    const L* const row = static_cast<const L*>(a.logits) + t * a.E;
+    L* const out = static_cast<L*>(a.out) + t * a.E;
+    int id = -1;
+    float g = 0.0f, x = -INFINITY;
+    if (lane < a.K) {
+      id = a.ids[t * a.K + lane];
+      if (id >= a.E) {
+        atomicOr(a.status, kBadRoute);
+        id = -1;
+      }
+      if (id >= 0) {
+        g = a.grad[t * a.K + lane] * a.scale;
+        x = widen<L>(row[id]);
+      }
+    }
+    float d[SL];
+#pragma unroll
+    for (int j = 0; j < SL; j++) d[j] = 0.0f;
+    float mine = 0.0f;  // of this lane's slot
+    if (renorm) {
+      const float high = warp_max(x);
+      float w = 0.0f;
+      if (id >= 0 && high > -INFINITY)
+        w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
+      const float sum = warp_sum(w);
+      const float r = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+      const float mean = warp_sum(r * g);
+      mine = r * (g - mean);
+      if (!SOFTMAX) mine *= __fdividef(1.0f, 1.0f + __expf(x));  // 1 - p
+    } else if (!SOFTMAX) {
+      const float p = sigmoid_over(x, 0.0f);
+      if (id >= 0) mine = p * __fdividef(1.0f, 1.0f + __expf(x)) * g;
+    } else {
+      float l[SL], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < SL; j++) {
+        const int e = ((j / V) * 32 + lane) * V + j % V;
+        l[j] = e < a.E ? widen<L>(row[e]) : -INFINITY;
+        top = fmaxf(top, l[j]);
+      }
+      top = warp_max(top);
+#pragma unroll
+      for (int j = 0; j < SL; j++) sum += l[j] = l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
+      sum = warp_sum(sum);
+      const float inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+      const float p = id >= 0 && x > -INFINITY ? __expf(x - top) * inv : 0.0f;
+      mine = p * g;
+      const float mean = warp_sum(mine);
+      if (__any_sync(kAll, id >= 0)) {  // a dropped row has no gradient, NaN logits or not
+#pragma unroll
+        for (int j = 0; j < SL; j++) d[j] = -l[j] * inv * mean;
+      }
+    }
+    for (int k = 0; k < a.K; k++) {
+      const int e = __shfl_sync(kAll, id, k);
+      const float v = __shfl_sync(kAll, mine, k);
+#pragma unroll
+      for (int j = 0; j < SL; j++)
+        if (e == ((j / V) * 32 + lane) * V + j % V) d[j] += v;
+    }
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const int e = ((j / V) * 32 + lane) * V + j % V;
+      if (e < a.E) {
+        if constexpr (sizeof(L) == 4) out[e] = d[j];
+        else out[e] = __float2bfloat16_rn(d[j]);
+      }
+    }
+  }
+}
+
+int router_grid(int64_t T, int sms) {
+  const int64_t need = (T + kRouterWarps - 1) / kRouterWarps;
+  return (int)(need < 8 * sms ? need : 8 * sms);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+nvfp4_status check_router(int64_t T, int32_t E, int32_t K, int32_t bytes, int32_t score, int32_t renorm,
+                          float scale) {
+  if (T < 0 || E < 1 || E > kMaxE || K < 1 || K > E || (bytes != 2 && bytes != 4) ||
+      (score != NVFP4_SCORE_SOFTMAX && score != NVFP4_SCORE_SIGMOID) || (renorm != 0 && renorm != 1) ||
+      !std::isfinite(scale))
+    return NVFP4_ERR_INVALID_ARG;
+  if (K > kMaxTopk) return NVFP4_ERR_UNSUPPORTED;
+  if (T > (int64_t(1) << 40) / E) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+
+nvfp4_status cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return NVFP4_OK;
+  (void)cudaGetLastError();
+  return NVFP4_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+NVFP4_EXPORT nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_bytes, const float* bias,
+                                           int64_t T, int32_t E, int32_t K, int32_t score,
+                                           int32_t groups, int32_t top_groups, int32_t renormalize,
+                                           float scale, int32_t* expert_ids, float* weights,
+                                           void* stream) {
+  nvfp4_status st = check_router(T, E, K, logit_bytes, score, renormalize, scale);
+  if (st != NVFP4_OK) return st;
+  if (groups < 1 || groups > E || top_groups < 1 || top_groups > groups) return NVFP4_ERR_INVALID_ARG;
+  if (E % groups != 0 || K > top_groups * (E / groups)) return NVFP4_ERR_SHAPE;
+  if (T == 0) return NVFP4_OK;
+  if (logits == nullptr || expert_ids == nullptr || weights == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(logits, (uintptr_t)logit_bytes) || !aligned(bias, 4) || !aligned(expert_ids, 4) ||
+      !aligned(weights, 4))
+    return NVFP4_ERR_ALIGN;
+  int sms = 0;
+  uint32_t* status = nullptr;
+  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  RouterArgs a = {logits, bias, T, E, K, groups, top_groups, E / groups, scale, expert_ids, weights,
+                  status};
+  const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool soft = score == NVFP4_SCORE_SOFTMAX, renorm = renormalize != 0;
+  auto run = [&](auto soft_kernel, auto sig_kernel) {
+    return launch_pdl(soft ? soft_kernel : sig_kernel, grid, block, 0, s, a, renorm);
+  };
+  cudaError_t e;
+  if (logit_bytes == 4)
+    e = E <= 64 ? run(router_kernel<2, 1, true, float>, router_kernel<2, 1, false, float>)
+                : run(router_kernel<8, 1, true, float>, router_kernel<8, 1, false, float>);
+  else
+    e = E <= 64
+            ? run(router_kernel<2, 1, true, __nv_bfloat16>, router_kernel<2, 1, false, __nv_bfloat16>)
+            : run(router_kernel<8, 1, true, __nv_bfloat16>, router_kernel<8, 1, false, __nv_bfloat16>);
+  return cuda_status(e);
+}
+
+NVFP4_EXPORT nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, const void* logits,
+                                                    int32_t logit_bytes, const int32_t* expert_ids,
+                                                    int64_t T, int32_t E, int32_t K, int32_t score,
+                                                    int32_t renormalize, float scale,
+                                                    void* grad_logits, void* stream) {
+  nvfp4_status st = check_router(T, E, K, logit_bytes, score, renormalize, scale);
+  if (st != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  if (grad_weights == nullptr || logits == nullptr || expert_ids == nullptr || grad_logits == nullptr)
+    return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(logits, (uintptr_t)logit_bytes) || !aligned(grad_logits, (uintptr_t)logit_bytes) ||
+      !aligned(grad_weights, 4) || !aligned(expert_ids, 4))
+    return NVFP4_ERR_ALIGN;
+  int sms = 0;
+  uint32_t* status = nullptr;
+  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  RouterBackArgs a = {grad_weights, logits, expert_ids, T, E, K, scale, grad_logits, status};
+  const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool soft = score == NVFP4_SCORE_SOFTMAX, renorm = renormalize != 0;
+  auto run = [&](auto soft_kernel, auto sig_kernel) {
+    return launch_pdl(soft ? soft_kernel : sig_kernel, grid, block, 0, s, a, renorm);
+  };
+  return cuda_status(
+      logit_bytes == 4
+          ? run(router_backward_kernel<8, 1, true, float>, router_backward_kernel<8, 1, false, float>)
+          : run(router_backward_kernel<8, 1, true, __nv_bfloat16>,
+                router_backward_kernel<8, 1, false, __nv_bfloat16>));
+}
