@@ -21,7 +21,8 @@ SOURCES = ["quantize_row.cu", "quantize_col.cu", "quantize_rowcol.cu", "quantize
            "moe_route.cu", "checkpoint.cu", "moe_checkpoint_api.cu",
            "router.cu", "gemm.cu", "gemm_epilogue.cu", "gemm_api.cu", "adamw.cu"]
 HEADERS = ["nvfp4_device.cuh", "nvfp4_internal.h", "aux_internal.h", "quantize_kernel.cuh",
-           "fused_amax.cuh", "tile_ring.h", "gemm_internal.h", "gemm_device.cuh"]
+           "fused_amax.cuh", "tile_ring.h", "gemm_internal.h", "gemm_device.cuh",
+           "tcgen05.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

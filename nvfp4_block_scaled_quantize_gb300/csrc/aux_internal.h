@@ -98,6 +98,12 @@ cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, c
 // these two groups set up (nvfp4_api.cu); false when a CUDA call failed.
 bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas = nullptr);
 int setup_fault();  // nvfp4_debug_setup_fault
+// cuTensorMapEncodeTiled; set once a call above has succeeded (nvfp4_api.cu)
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
 // Clears n 32-bit words in stream order, by a kernel (moe_checkpoint_api.cu); p may be null.
 cudaError_t zero_words(void* p, int64_t n, cudaStream_t s);
 

@@ -1,9 +1,23 @@
-// Matrix products of NVFP4 operands (declared in include/nvfp4.h).
+// Matrix products of NVFP4 operands on the tensor cores (declared in include/nvfp4.h).
 //
-// First form: a CTA has a 64 x 64 tile of out, its operands' 16-element blocks decoded to binary32 in
-// shared memory, a thread 4 x 4 sums.
+// The instruction (tcgen05.mma kind::mxf4nvf4) multiplies packed E2M1 codes from shared memory and
+// reads one E4M3 scale for 16 elements from tensor memory, in a layout of its own: byte c of row r of
+// a 128 x 4 block at (r % 32) * 16 + (r / 32) * 4 + c. The operands here have the row-major scales that
+// the quantizers write, so that a row may start anywhere (an expert's rows, a slice): TMA brings a
+// block of 128 x 16 scale bytes as it is, and a warp turns it in place, four 16-byte loads and four
+// 16-byte stores a lane, while the codes of the same stage wait for their turn.
+//
+// Warps of a CTA: 0 loads (TMA), 1 issues the matrix instructions, 2 and 3 turn the scales, 4 to 7 are
+// the epilogue. `p` is the operand on the instruction's 128-row side, `q` the one on its N side:
+//   <2, 256, false>  a pair of CTAs has 256 x 256 of out; p is a, q is b
+//   <1, NT, true>    a CTA has 128 columns of out (p is b, the weights) and NT rows (q is a, tokens):
+//                    few tokens waste no tensor-core rows, and a warp's stores run along out's rows.
+//                    Where there are fewer tiles than SMs, the CTAs of a cluster share a tile's K and
+//                    add up their sums through distributed shared memory.
+// A stage is 256 elements of K. Everything waits with a limit; a wait that gives up sets
+// NVFP4_DEVICE_TIMEOUT and every warp leaves.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -14,145 +28,799 @@
 #include "gemm_device.cuh"
 #include "gemm_internal.h"
 #include "nvfp4_internal.h"
+#include "tcgen05.cuh"
 
 namespace nvfp4 {
 namespace {
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t e = (c >> 1) & 3u, f = c & 1u;
-  const float v = e == 0 ? 0.5f * f : (1.0f + 0.5f * f) * (float)(1 << (e - 1));
-  return (c & 8u) ? -v : v;
-}
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __half2float(__ushort_as_half((unsigned short)h));
-}
-__device__ __forceinline__ float act_any(int act, float z) {
-  switch (act) {
-    case NVFP4_ACT_RELU: return activate<NVFP4_ACT_RELU>(z);
-    case NVFP4_ACT_RELU2: return activate<NVFP4_ACT_RELU2>(z);
-    case NVFP4_ACT_GELU: return activate<NVFP4_ACT_GELU>(z);
-    case NVFP4_ACT_SILU: return activate<NVFP4_ACT_SILU>(z);
+constexpr uint32_t kBadOffsets = 0x1u, kTimeout = 0x2u;  // NVFP4_DEVICE_*
+constexpr int kThreads = 256;
+constexpr int kBlockK = 256;   // elements of a stage
+constexpr int kPBytes = 128 * kBlockK / 2;
+constexpr int kScaleBlock = 128 * kBlockK / 16;  // scales of 128 rows of a stage
+
+struct SideArgs {
+  CUtensorMap codes, scales;
+  const uint8_t* scale_ptr;
+  int64_t scale_pitch, scale_batch;
+  int32_t rows;      // of the operand (of one expert, where stacked)
+  int32_t tma;       // scales come by TMA; else by loads, of 4 bytes where words is set
+  int32_t words;
+  int32_t pad;
+};
+struct TcArgs {
+  SideArgs p, q;
+  const float *a_gscale, *b_gscale;
+  const int32_t* offsets;
+  int32_t mode, E;
+  int32_t M, N, K;   // of out, and the operands' columns
+  int32_t activation, out_bytes, bias_bytes;
+  int32_t wide;      // rows of out, residual and preact allow: 2 = 32-byte, 1 = 16-byte, 0 = single accesses
+  const void* bias;
+  const void* residual;
+  void* preact;
+  float* amax;
+  void* out;
+  uint32_t* status;
+};
+
+template <int CTAS, int NT>
+struct Shape {
+  static constexpr int kQRows = NT / CTAS;                       // rows of q that a CTA loads
+  static constexpr int kQBlocks = (NT + 127) / 128;              // blocks of 128 rows of scales
+  static constexpr int kQBytes = kQRows * kBlockK / 2;
+  static constexpr int kStage = kPBytes + kQBytes + (1 + kQBlocks) * kScaleBlock;
+  static constexpr int kStages = CTAS == 2 ? 5 : NT <= 32 ? 4 : NT <= 64 ? 3 : 6;
+  static constexpr int kPerSm = CTAS == 1 && NT <= 64 ? 2 : 1;
+  static constexpr int kColumns = kPerSm == 2 ? 256 : 512;       // of tensor memory
+  // Two accumulators. Of 256 columns they overlap by 64: those are read first, and the next tile's
+  // products start as soon as they are. `kLag`: the next tile but kLag - 1 waits.
+  static constexpr int kAccStride = NT == 256 ? 192 : NT;
+  static constexpr int kLag = NT == 256 ? 1 : 2;
+  static constexpr int kScaleColumn = NT == 256 ? 448 : 2 * NT;
+  static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
+  static constexpr int kSmem = kStages * kStage + 1024;
+  static_assert(kScaleColumn + 4 * kSlot <= kColumns, "tensor memory");
+  static_assert(kStage % 1024 == 0, "swizzle atoms");
+};
+
+// What a tile is: rows p0.. of p and q0.. of q (of which p_rows and q_rows count), experts of stacked
+// operands, columns [k_lo, k_hi) of K in stages [kb0, kb1).
+struct Tile {
+  int32_t p0, q0, p_rows, q_rows, pz, qz, k_lo, k_hi, kb0, kb1, e;
+};
+
+struct Table {
+  int32_t first[257];  // first tile of each expert
+  int32_t begin[257];  // its first row (grouped) or column of K (wgrad)
+  int32_t warp_sum[2][8];
+  int32_t bad;
+};
+
+// The experts' tiles, by all threads. Offsets out of order leave no tiles.
+template <int CTAS, int NT, bool SWAP>
+__device__ __forceinline__ void make_table(const TcArgs& a, Table& t) {
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  if (e == 0) t.bad = 0;
+  __syncthreads();
+  int32_t n = 0, tiles = 0;
+  bool bad = false;
+  if (e < a.E) {
+    const int32_t prev = e == 0 ? 0 : a.offsets[e - 1], end = a.offsets[e];
+    bad = prev < 0 || end < prev || end > (a.mode == kGemmGrouped ? a.M : a.K);
+    n = bad ? 0 : end - prev;
+    const int pt = 128 * CTAS;
+    if (a.mode == kGemmGrouped) {
+      const int tok = SWAP ? NT : pt, wt = SWAP ? pt : NT;
+      tiles = ((n + tok - 1) / tok) * ((a.N + wt - 1) / wt);
+    } else {
+      n = (n + 15) & ~15;
+      tiles = ((a.p.rows + pt - 1) / pt) * ((a.q.rows + NT - 1) / NT);
+    }
   }
-  return z;
+  if (bad) t.bad = 1;
+  int32_t sum_n = n, sum_t = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xFFFFFFFFu, sum_n, o), y = __shfl_up_sync(0xFFFFFFFFu, sum_t, o);
+    if (lane >= o) sum_n += x, sum_t += y;
+  }
+  if (lane == 31) t.warp_sum[0][warp] = sum_n, t.warp_sum[1][warp] = sum_t;
+  __syncthreads();
+  for (int w = 0; w < warp; w++) sum_n += t.warp_sum[0][w], sum_t += t.warp_sum[1][w];
+  t.begin[e + 1] = sum_n;
+  t.first[e + 1] = sum_t;
+  if (e == 0) t.begin[0] = t.first[0] = 0;
+  __syncthreads();
+  if (t.bad || (a.mode == kGemmWgrad && t.begin[a.E] > a.K)) {
+    if (e == 0) {
+      atomicOr(a.status, kBadOffsets);
+      t.bad = 1;
+    }
+    t.first[e + 1] = 0;
+  }
+  __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) gemm_simple_kernel(const GemmArgs g) {
-  __shared__ float sa[16][65], sb[16][65];
-  pdl_wait();
-  pdl_allow_next();
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  int e = blockIdx.z;
-  int64_t row0 = 0, rows = g.M, k0 = 0, k1 = g.K, batch = 0, out0 = 0;
-  if (g.mode == kGemmGrouped) {
-    row0 = e == 0 ? 0 : g.offsets[e - 1];
-    const int64_t end = g.offsets[e];
-    if (row0 < 0 || end < row0 || end > g.M) {
-      if (threadIdx.x == 0) atomicOr(g.status, 1u);
-      return;
+template <int CTAS, int NT, bool SWAP>
+__device__ __forceinline__ int tile_count(const TcArgs& a, const Table& t) {
+  if (a.mode != kGemmDense) return t.first[a.E];
+  return ((a.p.rows + 128 * CTAS - 1) / (128 * CTAS)) * ((a.q.rows + NT - 1) / NT);
+}
+
+// Tile number `i`; `e` is a cursor over the experts. Eight tiles of p share their tiles of q in turn.
+template <int CTAS, int NT, bool SWAP>
+__device__ __forceinline__ Tile get_tile(const TcArgs& a, const Table& t, int i, int& e, int split, int splits) {
+  Tile x;
+  constexpr int kPt = 128 * CTAS;
+  x.p0 = x.q0 = x.pz = x.qz = 0;
+  x.p_rows = a.p.rows;
+  x.q_rows = a.q.rows;
+  x.k_lo = 0;
+  x.k_hi = a.K;
+  if (a.mode != kGemmDense) {
+    while (i >= t.first[e + 1]) e++;
+    i -= t.first[e];
+    if (a.mode == kGemmGrouped) {
+      const int begin = t.begin[e], n = t.begin[e + 1] - begin;
+      if (SWAP) x.q0 = begin, x.q_rows = n, x.pz = e;
+      else x.p0 = begin, x.p_rows = n, x.qz = e;
+    } else {
+      x.k_lo = t.begin[e];
+      x.k_hi = t.begin[e + 1];
     }
-    rows = end - row0;
-    batch = e;
-  } else if (g.mode == kGemmWgrad) {
-    int64_t prev = 0, at = 0;
-    for (int i = 0; i <= e; i++) {
-      const int64_t end = g.offsets[i];
-      if (end < prev) {
-        if (threadIdx.x == 0) atomicOr(g.status, 1u);
+  }
+  x.e = e;
+  const int np = (x.p_rows + kPt - 1) / kPt, nq = (x.q_rows + NT - 1) / NT;
+  const int group = i / (8 * nq), first = group * 8, wide = min(8, np - first), rest = i - group * 8 * nq;
+  const int pi = first + rest % wide, qi = rest / wide;
+  x.p0 += pi * kPt;
+  x.q0 += qi * NT;
+  x.p_rows -= pi * kPt;
+  x.q_rows -= qi * NT;
+  x.kb0 = x.k_lo / kBlockK;
+  x.kb1 = x.k_hi > x.k_lo ? (x.k_hi + kBlockK - 1) / kBlockK : x.kb0;
+  if (splits > 1) {
+    const int n = x.kb1 - x.kb0, at = x.kb0;
+    x.kb0 = at + n * split / splits;
+    x.kb1 = at + n * (split + 1) / splits;
+  }
+  return x;
+}
+
+// ---- scales ---------------------------------------------------------------------------------------
+
+// 16 scale bytes of a row from byte `at`, zeros from byte `end` on, by loads.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int at, int end, bool words) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    w[j] = 0u;
+    const int c = at + 4 * j;
+    if (words && c + 4 <= end) {
+      w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + c));
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; b++)
+        if (c + b < end) w[j] |= (uint32_t)__ldg(row + c + b) << (8 * b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Bytes [lo, hi) of 16 stay.
+__device__ __forceinline__ uint32_t byte_mask(int lo, int hi, int word) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int b = 0; b < 4; b++)
+    if (4 * word + b >= lo && 4 * word + b < hi) m |= 0xFFu << (8 * b);
+  return m;
+}
+
+// Turns one block of 128 rows x 16 bytes at `addr` into four blocks of 512 bytes, one for each 64
+// elements of K. v[j] is row lane + 32 j.
+__device__ __forceinline__ void put_scales(uint32_t addr, const uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + k * 512 + lane * 16), "r"(x), "r"(y),
+                 "r"(z), "r"(w)
+                 : "memory");
+  };
+  put(0, v[0].x, v[1].x, v[2].x, v[3].x);
+  put(1, v[0].y, v[1].y, v[2].y, v[3].y);
+  put(2, v[0].z, v[1].z, v[2].z, v[3].z);
+  put(3, v[0].w, v[1].w, v[2].w, v[3].w);
+}
+
+// Warp 2 (the scales of p, one block) or 3 (of q): every stage's blocks turned, then the arrival on the
+// pair's `ready`.
+template <int CTAS, int NT, bool SWAP, int BLOCKS, int ROWS>
+__device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table, int tiles,
+                                            int cluster, int clusters, int split, int splits, bool is_q,
+                                            uint32_t stages, uint32_t offset, uint64_t* full, uint64_t* ready,
+                                            int row_shift) {
+  using S = Shape<CTAS, NT>;
+  const int lane = threadIdx.x & 31;
+  const int end = a.K / 16;
+  int e = 0, it = 0;
+  for (int i = cluster; i < tiles; i += clusters) {
+    const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+    const int row0 = (is_q ? x.q0 : x.p0) + row_shift, z = is_q ? x.qz : x.pz;
+    const uint8_t* const base = s.scale_ptr + (int64_t)z * s.scale_batch;
+    for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
+      const int stage = it % S::kStages;
+      const uint32_t at = stages + stage * S::kStage + offset;
+      const int lo = x.k_lo / 16 - kb * 16, hi = x.k_hi / 16 - kb * 16;
+      uint4 v[BLOCKS][4];
+      if (!s.tma) {
+#pragma unroll
+        for (int b = 0; b < BLOCKS; b++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int r = 128 * b + 32 * j + lane;
+            v[b][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < ROWS && row0 + r < s.rows)
+              v[b][j] = load_scales(base + (int64_t)(row0 + r) * s.scale_pitch, kb * 16, end, s.words);
+          }
+      }
+      if (!wait_phase(&full[stage], (uint32_t)(it / S::kStages) & 1u)) {
+        if (lane == 0) atomicOr(a.status, kTimeout);
         return;
       }
-      k0 = at;
-      at += (end - prev + 15) / 16 * 16;
-      prev = end;
+      if (s.tma) {
+#pragma unroll
+        for (int b = 0; b < BLOCKS; b++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int r = 128 * b + 32 * j + lane;
+            v[b][j] = r < ROWS ? lds128(at + r * 16) : make_uint4(0u, 0u, 0u, 0u);
+          }
+        __syncwarp();
+      }
+      if (lo > 0 || hi < 16) {  // another expert's columns share the stage
+#pragma unroll
+        for (int b = 0; b < BLOCKS; b++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            v[b][j].x &= byte_mask(lo, hi, 0);
+            v[b][j].y &= byte_mask(lo, hi, 1);
+            v[b][j].z &= byte_mask(lo, hi, 2);
+            v[b][j].w &= byte_mask(lo, hi, 3);
+          }
+      }
+#pragma unroll
+      for (int b = 0; b < BLOCKS; b++) put_scales(at + b * kScaleBlock, v[b]);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2) cluster_arrive(cluster_address(smem_u32(&ready[stage]), 0));
+        else mbar_arrive(&ready[stage]);
+      }
     }
-    k1 = at;
-    if (k1 > g.K) {
-      if (threadIdx.x == 0) atomicOr(g.status, 1u);
-      return;
-    }
-    out0 = (int64_t)e * g.M * g.N;
+  }
+}
+
+// ---- epilogue -------------------------------------------------------------------------------------
+
+template <int N>
+__device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
+  switch (act) {
+    case NVFP4_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_RELU>(z[i]);
+      break;
+    case NVFP4_ACT_RELU2:
+#pragma unroll
+      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_RELU2>(z[i]);
+      break;
+    case NVFP4_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_GELU>(z[i]);
+      break;
+    case NVFP4_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_SILU>(z[i]);
+      break;
+    default: break;
+  }
+}
+__device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ float bias_at(const TcArgs& a, int64_t i) {
+  return a.bias_bytes == 4 ? __ldg(static_cast<const float*>(a.bias) + i) : bf16_at(a.bias, i);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// 8 words to p, by one 32-byte or two 16-byte stores.
+__device__ __forceinline__ void store_words(void* p, int wide, const uint32_t* w) {
+  const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+  if (wide == 2) {
+    stg256(p, lo, hi);
   } else {
-    e = 0;
+    static_cast<uint4*>(p)[0] = lo;
+    static_cast<uint4*>(p)[1] = hi;
   }
-  const float alpha = g.a.gscale[2 * e + 1] * g.b.gscale[2 * e + 1];
-  float top = 0.0f;
-  const int64_t n0 = (int64_t)blockIdx.y * 64;
-  for (int64_t m0 = (int64_t)blockIdx.x * 64; m0 < rows; m0 += (int64_t)gridDim.x * 64) {
-    float acc[4][4] = {};
-    for (int64_t k = k0; k < k1; k += 16) {
-      for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int r = i / 8, c = i % 8;
-        const int64_t m = row0 + m0 + r, n = n0 + r;
-        float v = 0.0f, w = 0.0f, v2 = 0.0f, w2 = 0.0f;
-        if (m0 + r < rows) {
-          const uint32_t b = g.a.codes[m * g.a.code_pitch + k / 2 + c];
-          const float s = e4m3_value(g.a.scales[m * g.a.scale_pitch + k / 16]);
-          v = e2m1_value(b & 15) * s, v2 = e2m1_value(b >> 4) * s;
-        }
-        if (n < g.N) {
-          const uint32_t b = g.b.codes[batch * g.b.code_batch + n * g.b.code_pitch + k / 2 + c];
-          const float s = e4m3_value(g.b.scales[batch * g.b.scale_batch + n * g.b.scale_pitch + k / 16]);
-          w = e2m1_value(b & 15) * s, w2 = e2m1_value(b >> 4) * s;
-        }
-        sa[2 * c][r] = v, sa[2 * c + 1][r] = v2;
-        sb[2 * c][r] = w, sb[2 * c + 1][r] = w2;
+}
+
+// `C` consecutive elements of one row of out from element `at`, `have` of them inside the row. n: their
+// first column of the bias (already with the expert's part). Returns the largest bits of |out|.
+template <int C>
+__device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], float alpha, int64_t at, int64_t n,
+                                               int have) {
+  const bool whole = have >= C && a.wide != 0;
+#pragma unroll
+  for (int i = 0; i < C; i++) z[i] *= alpha;
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < C; i++)
+      if (i < have) z[i] += bias_at(a, n + i);
+  }
+  if (a.preact != nullptr) {
+    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.preact) + at;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < C; i += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = pack2(z[i + 2 * j], z[i + 2 * j + 1]);
+        store_words(to + i, a.wide, w);
       }
-      __syncthreads();
+    } else {
 #pragma unroll
-      for (int c = 0; c < 16; c++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            acc[i][j] = __fmaf_rn(sa[c][ty + 16 * i], sb[c][tx + 16 * j], acc[i][j]);
-      __syncthreads();
+      for (int i = 0; i < C; i++)
+        if (i < have) to[i] = __float2bfloat16_rn(z[i]);
     }
-    for (int i = 0; i < 4; i++)
-      for (int j = 0; j < 4; j++) {
-        const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (m >= rows || n >= g.N) continue;
-        float z = acc[i][j] * alpha;
-        const int64_t bn = (int64_t)e * g.N + n;
-        if (g.bias)
-          z += g.bias_bytes == 4 ? static_cast<const float*>(g.bias)[bn]
-                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(g.bias)[bn]);
-        const int64_t at = out0 + (row0 + m) * g.N + n;
-        if (g.preact) static_cast<__nv_bfloat16*>(g.preact)[at] = __float2bfloat16_rn(z);
-        float o = act_any(g.activation, z);
-        if (g.out_bytes == 4) {
-          if (g.residual) o += static_cast<const float*>(g.residual)[at];
-          static_cast<float*>(g.out)[at] = o;
-        } else {
-          if (g.residual) o += __bfloat162float(static_cast<const __nv_bfloat16*>(g.residual)[at]);
-          const __nv_bfloat16 b = __float2bfloat16_rn(o);
-          static_cast<__nv_bfloat16*>(g.out)[at] = b;
-          o = __bfloat162float(b);
+  }
+  activate_all<C>(a.activation, z);
+  uint32_t top = 0u;
+  if (a.out_bytes == 2) {
+    if (a.residual != nullptr) {
+      const __nv_bfloat16* const r = static_cast<const __nv_bfloat16*>(a.residual) + at;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < C; i += 8) {
+          const uint4 v = *reinterpret_cast<const uint4*>(r + i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            z[i + 2 * j] += __uint_as_float(w[j] << 16);
+            z[i + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+          }
         }
-        top = fmaxf(top, fabsf(o));
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; i++)
+          if (i < have) z[i] += __bfloat162float(r[i]);
       }
-  }
-  if (g.amax) atomicMax(reinterpret_cast<uint32_t*>(g.amax) + e, __float_as_uint(top));
-  if (g.mode == kGemmGrouped && e == g.E - 1) {
-    const int64_t end = g.offsets[e];
-    for (int64_t m = end + blockIdx.x; m < g.M; m += gridDim.x)
-      for (int64_t n = n0 + threadIdx.x; n < g.N && n < n0 + 64; n += 256) {
-        if (g.out_bytes == 4) static_cast<float*>(g.out)[m * g.N + n] = 0.0f;
-        else static_cast<uint16_t*>(g.out)[m * g.N + n] = 0;
-        if (g.preact) static_cast<uint16_t*>(g.preact)[m * g.N + n] = 0;
+    }
+    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + at;
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int j = 0; j < C / 2; j++) w[j] = pack2(z[2 * j], z[2 * j + 1]);
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < C / 2; j += 8) store_words(to + 2 * j, a.wide, w + j);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) to[i] = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i % 2))));
+    }
+    if (a.amax != nullptr) {
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) top = max(top, (w[i / 2] << (16 * (1 - i % 2))) & 0x7FFF0000u);
+    }
+  } else {
+    if (a.residual != nullptr) {
+      const float* const r = static_cast<const float*>(a.residual) + at;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < C; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(r + i);
+          z[i] += v.x, z[i + 1] += v.y, z[i + 2] += v.z, z[i + 3] += v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; i++)
+          if (i < have) z[i] += r[i];
       }
+    }
+    float* const to = static_cast<float*>(a.out) + at;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < C; i += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = __float_as_uint(z[i + j]);
+        store_words(to + i, a.wide, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) to[i] = z[i];
+    }
+    if (a.amax != nullptr) {
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) top = max(top, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+    }
   }
+  return top;
+}
+
+// One element of out (the swapped tiles: a warp has 32 neighbouring columns of a row).
+__device__ __forceinline__ uint32_t finish_one(const TcArgs& a, float v, float alpha, float bias, int64_t at) {
+  float z[1] = {v * alpha + bias};
+  if (a.preact != nullptr) static_cast<__nv_bfloat16*>(a.preact)[at] = __float2bfloat16_rn(z[0]);
+  activate_all<1>(a.activation, z);
+  if (a.out_bytes == 2) {
+    if (a.residual != nullptr) z[0] += bf16_at(a.residual, at);
+    const __nv_bfloat16 b = __float2bfloat16_rn(z[0]);
+    static_cast<__nv_bfloat16*>(a.out)[at] = b;
+    return ((uint32_t)__bfloat16_as_ushort(b) & 0x7FFFu) << 16;
+  }
+  if (a.residual != nullptr) z[0] += static_cast<const float*>(a.residual)[at];
+  static_cast<float*>(a.out)[at] = z[0];
+  return __float_as_uint(z[0]) & 0x7FFFFFFFu;
+}
+
+__device__ __forceinline__ void report_amax(const TcArgs& a, uint32_t top, int e) {
+  if (a.amax == nullptr) return;
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, top);
+  if ((threadIdx.x & 31) == 0 && m != 0u) atomicMax(reinterpret_cast<uint32_t*>(a.amax) + e, m);
+}
+
+// Zeros in bytes [lo, hi) of p, even numbers, by threads `at` of `count`.
+__device__ __forceinline__ void clear(void* p, int64_t lo, int64_t hi, int64_t at, int64_t count) {
+  uint8_t* const b = static_cast<uint8_t*>(p);
+  const int64_t head = min(hi, lo + (int64_t)((16 - (reinterpret_cast<uintptr_t>(b + lo) & 15)) & 15));
+  const int64_t body = head + (hi - head) / 16 * 16;
+  for (int64_t i = lo + 2 * at; i < head; i += 2 * count) *reinterpret_cast<uint16_t*>(b + i) = 0;
+  for (int64_t i = head + 16 * at; i < body; i += 16 * count)
+    *reinterpret_cast<uint4*>(b + i) = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t i = body + 2 * at; i < hi; i += 2 * count) *reinterpret_cast<uint16_t*>(b + i) = 0;
+}
+
+// ---- the kernel -----------------------------------------------------------------------------------
+
+template <int CTAS, int NT, bool SWAP>
+__global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
+    gemm_kernel(const __grid_constant__ TcArgs a, int splits) {
+  using S = Shape<CTAS, NT>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t full[S::kStages], ready[S::kStages], empty[S::kStages], acc_full[2], acc_free[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ Table table;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = CTAS == 2 || splits > 1 ? cluster_rank() : 0u;
+  const int half = CTAS == 2 ? (int)rank : 0;           // which half of the pair's tile
+  const int split = CTAS == 2 ? 0 : (int)rank;
+  const int per = CTAS == 2 ? 2 : splits;
+  const int cluster = blockIdx.x / per, clusters = gridDim.x / per;
+  const uint32_t stages = (smem_u32(raw) + 1023u) & ~1023u;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; i++) {
+      mbar_init(&full[i], 1);
+      mbar_init(&ready[i], 2 * CTAS);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full[0], 1);
+    mbar_init(&acc_full[1], 1);
+    mbar_init(&acc_free[0], 4 * CTAS);
+    mbar_init(&acc_free[1], 4 * CTAS);
+    fence_barrier_init();
+    prefetch_tensormap(&a.p.codes);
+    prefetch_tensormap(&a.q.codes);
+    if (a.p.tma) prefetch_tensormap(&a.p.scales);
+    if (a.q.tma) prefetch_tensormap(&a.q.scales);
+  }
+  if (warp == 1) tmem_alloc<CTAS>(&tmem_base, S::kColumns);
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (per > 1) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_allow_next();
+  if (a.mode != kGemmDense) make_table<CTAS, NT, SWAP>(a, table);
+  const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
+
+  if (warp == 0) {
+    const uint32_t bytes = kPBytes + S::kQBytes + (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
+    int e = 0, it = 0;
+    bool alive = true;
+    for (int i = cluster; i < tiles && alive; i += clusters) {
+      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+      for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
+        const int stage = it % S::kStages;
+        alive = wait_phase(&empty[stage], ((uint32_t)(it / S::kStages) & 1u) ^ 1u);
+        alive = __all_sync(0xFFFFFFFFu, alive);
+        if (!alive) {
+          if (lane == 0) atomicOr(a.status, kTimeout);
+          break;
+        }
+        const uint32_t to = stages + stage * S::kStage, sc = to + kPBytes + S::kQBytes;
+        if (elect_one()) {
+          mbar_expect_tx(&full[stage], bytes);
+          tma_load_3d(to, &a.p.codes, kb * (kBlockK / 2), x.p0 + 128 * half, x.pz, &full[stage]);
+          tma_load_3d(to + kPBytes, &a.q.codes, kb * (kBlockK / 2), x.q0 + S::kQRows * half, x.qz, &full[stage]);
+          if (a.p.tma) tma_load_3d(sc, &a.p.scales, kb * 16, x.p0 + 128 * half, x.pz, &full[stage]);
+          if (a.q.tma) tma_load_3d(sc + kScaleBlock, &a.q.scales, kb * 16, x.q0, x.qz, &full[stage]);
+        }
+        __syncwarp();
+      }
+    }
+    // every load has landed and every arrival of the products has come before anything here ends
+    for (int i = it > S::kStages ? it - S::kStages : 0; i < it; i++) {
+      const int stage = i % S::kStages;
+      wait_phase(&full[stage], (uint32_t)(i / S::kStages) & 1u);
+      if (alive) wait_phase(&empty[stage], (uint32_t)(i / S::kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (half == 0) {
+      constexpr uint32_t idesc = nvfp4_idesc(128 * CTAS, NT);
+      const uint32_t sf = tmem + S::kScaleColumn;
+      int e = 0, it = 0, count = 0;
+      bool alive = true;
+      for (int i = cluster; i < tiles; i += clusters, count++) {
+        const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+        const uint32_t acc = tmem + (count & 1) * S::kAccStride;
+        // an accumulator's barrier completes once for each of its tiles, and is never a phase ahead
+        if (count >= S::kLag)
+          alive = wait_phase(&acc_free[S::kLag == 1 ? 0 : count & 1],
+                               (uint32_t)(S::kLag == 1 ? count - 1 : (count >> 1) - 1) & 1u);
+        uint32_t accumulate = 0u;
+        for (int kb = x.kb0; kb < x.kb1 && alive; kb++, it++) {
+          const int stage = it % S::kStages;
+          alive = wait_phase(&ready[stage], (uint32_t)(it / S::kStages) & 1u);
+          alive = __all_sync(0xFFFFFFFFu, alive);
+          if (!alive) break;
+          tc_fence_after();
+          const uint32_t at = stages + stage * S::kStage;
+          const uint64_t pd = codes_descriptor(at), qd = codes_descriptor(at + kPBytes);
+          const uint64_t sd = scales_descriptor(at + kPBytes + S::kQBytes);
+          if (elect_one()) {
+            // columns of other experts in these 256 have zero scales: whole stages are multiplied
+#pragma unroll
+            for (int k = 0; k < kBlockK / 64; k++) {
+              tmem_copy_scales<CTAS>(sf + k * S::kSlot, sd + k * 32);
+#pragma unroll
+              for (int b = 0; b < S::kQBlocks; b++)
+                tmem_copy_scales<CTAS>(sf + k * S::kSlot + 4 + 4 * b, sd + (kScaleBlock / 16) * (1 + b) + k * 32);
+            }
+#pragma unroll
+            for (int k = 0; k < kBlockK / 64; k++) {
+              mma_nvfp4<CTAS>(acc, pd + k * 2, qd + k * 2, idesc, sf + k * S::kSlot, sf + k * S::kSlot + 4,
+                              accumulate);
+              accumulate = 1u;
+            }
+            mma_commit<CTAS>(&empty[stage]);
+          }
+          accumulate = 1u;
+          __syncwarp();
+        }
+        alive = __all_sync(0xFFFFFFFFu, alive);
+        if (!alive) {
+          if (lane == 0) atomicOr(a.status, kTimeout);
+          break;
+        }
+        if (elect_one()) mma_commit<CTAS>(&acc_full[count & 1]);
+        __syncwarp();
+      }
+    }
+  } else if (warp == 2) {
+    turn_scales<CTAS, NT, SWAP, 1, 128>(a, a.p, table, tiles, cluster, clusters, split, splits, false, stages,
+                                        kPBytes + S::kQBytes, full, ready, 128 * half);
+  } else if (warp == 3) {
+    turn_scales<CTAS, NT, SWAP, S::kQBlocks, NT>(a, a.q, table, tiles, cluster, clusters, split, splits, true,
+                                                 stages, kPBytes + S::kQBytes + kScaleBlock, full, ready, 0);
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    int e = 0, count = 0;
+    for (int i = cluster; i < tiles; i += clusters, count++) {
+      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+      const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
+      if (!wait_phase(&acc_full[count & 1], (uint32_t)(count >> 1) & 1u)) {
+        if (lane == 0) atomicOr(a.status, kTimeout);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + lanes + (count & 1) * S::kAccStride;
+      const int r = 128 * half + 32 * quarter + lane;  // row of the tile
+      uint32_t top = 0u;
+      const int64_t base = a.mode == kGemmWgrad ? (int64_t)x.e * a.M * a.N : 0;
+      constexpr int kChunks = NT / 32;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; c++) {
+        // the columns that the other accumulator shares come first
+        const int chunk = S::kAccStride < NT && (count & 1) == 0 ? (c + S::kAccStride / 32) % kChunks : c;
+        uint32_t v[32];
+        tmem_load32(acc + 32 * chunk, v);
+        tmem_wait_load();
+        if (c == (S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks) - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            uint64_t* const bar = &acc_free[S::kLag == 1 ? 0 : count & 1];
+            if (CTAS == 2) cluster_arrive(cluster_address(smem_u32(bar), 0));
+            else mbar_arrive(bar);
+          }
+        }
+        if (x.kb0 == x.kb1) {
+#pragma unroll
+          for (int j = 0; j < 32; j++) v[j] = 0u;
+        }
+        const int left = x.q_rows - 32 * chunk;  // columns (rows of q) that count
+        if constexpr (!SWAP) {
+          if (r < x.p_rows && left > 0) {
+            float z[32];
+#pragma unroll
+            for (int j = 0; j < 32; j++) z[j] = __uint_as_float(v[j]);
+            const int64_t n = x.q0 + 32 * chunk;
+            top = max(top, finish_row<32>(a, z, alpha, base + (int64_t)(x.p0 + r) * a.N + n,
+                                          (int64_t)x.e * a.N + n, left));
+          }
+        } else if (splits > 1) {
+          // the sums of this share of K, for the cluster
+          const uint32_t to = stages + ((32 * chunk) * 128 + r) * 4;
+#pragma unroll
+          for (int j = 0; j < 32; j++)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 512), "r"(v[j]) : "memory");
+        } else if (r < x.p_rows) {
+          const float bias = a.bias ? bias_at(a, (int64_t)x.e * a.N + x.p0 + r) : 0.0f;
+          const int64_t at = base + (int64_t)(x.q0 + 32 * chunk) * a.N + x.p0 + r;
+#pragma unroll
+          for (int j = 0; j < 32; j++)
+            if (j < left) top = max(top, finish_one(a, __uint_as_float(v[j]), alpha, bias, at + (int64_t)j * a.N));
+        }
+      }
+      if (splits == 1) report_amax(a, top, x.e);
+    }
+    if (a.mode == kGemmGrouped && !table.bad) {
+      const int64_t live = (int64_t)table.begin[a.E] * a.N, all = (int64_t)a.M * a.N;
+      const int64_t me = (int64_t)blockIdx.x * 128 + (threadIdx.x & 127), count = (int64_t)gridDim.x * 128;
+      clear(a.out, live * a.out_bytes, all * a.out_bytes, me, count);
+      if (a.preact) clear(a.preact, live * 2, all * 2, me, count);
+    }
+  }
+  if (CTAS == 1 && splits > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 4 && cluster < tiles) {  // the host launches one tile a cluster: every CTA takes some rows of q
+      int e = 0;
+      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, cluster, e, split, splits);
+      const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
+      const int r = 32 * (warp & 3) + lane;
+      uint32_t top = 0u;
+      if (r < x.p_rows) {
+        const float bias = a.bias ? bias_at(a, (int64_t)x.e * a.N + x.p0 + r) : 0.0f;
+        for (int c = split; c < min(NT, x.q_rows); c += splits) {
+          float v = 0.0f;
+          for (int s = 0; s < splits; s++) v += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
+          top = max(top, finish_one(a, v, alpha, bias, (int64_t)(x.q0 + c) * a.N + x.p0 + r));
+        }
+      }
+      report_amax(a, top, x.e);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (per > 1) cluster_sync();
+  if (warp == 1) tmem_free<CTAS>(tmem, S::kColumns);
+}
+
+template <int CTAS, int NT, bool SWAP>
+cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<CTAS, NT>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS == 2 ? 2 : splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CTAS, NT, SWAP>, a, splits);
+}
+template <int CTAS, int NT, bool SWAP>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(gemm_kernel<CTAS, NT, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<CTAS, NT>::kSmem);
+}
+
+// The maps of an operand for boxes of `box_rows` rows of codes and `scale_rows` of scales.
+bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int32_t experts, int box_rows,
+               int scale_rows) {
+  s.scale_ptr = o.scales;
+  s.scale_pitch = o.scale_pitch;
+  s.scale_batch = experts > 1 ? o.scale_batch : 0;
+  s.rows = (int32_t)rows;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(o.scales) | (uintptr_t)(rows > 1 ? s.scale_pitch : 0) |
+                        (uintptr_t)s.scale_batch;
+  s.tma = all % 16 == 0;
+  s.words = all % 4 == 0;
+  if (K == 0) {  // nothing is loaded
+    s.tma = 0;
+    return true;
+  }
+  auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
+  auto encode = [&](CUtensorMap* map, const uint8_t* p, int64_t width, int64_t pitch, int64_t batch, int box_x,
+                    int box_y, CUtensorMapSwizzle swizzle) {
+    // a single row has any pitch, a single expert any distance
+    const cuuint64_t row = (cuuint64_t)(rows > 1 ? pitch : up16(width));
+    const cuuint64_t next = experts > 1 ? (cuuint64_t)batch : row * (cuuint64_t)rows;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)experts};
+    const cuuint64_t strides[2] = {row, next};
+    const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1}, one[3] = {1, 1, 1};
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p), dims, strides, box,
+                          one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (!encode(&s.codes, o.codes, K / 2, o.code_pitch, o.code_batch, kBlockK / 2, box_rows,
+              CU_TENSOR_MAP_SWIZZLE_128B))
+    return false;
+  return !s.tma || encode(&s.scales, o.scales, K / 16, s.scale_pitch, s.scale_batch, 16, scale_rows,
+                          CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 }  // namespace
 
-cudaError_t prepare_gemm_kernels() { return cudaSuccess; }
+cudaError_t prepare_gemm_kernels() {
+  cudaError_t e = prepare_one<2, 256, false>(), r;
+  if ((r = prepare_one<1, 32, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<1, 128, true>()) != cudaSuccess) e = r;
+  return e;
+}
 
 cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
-  const int64_t mt = (g.M + 63) / 64;
-  const dim3 grid((unsigned)(g.mode == kGemmGrouped ? (mt < 64 ? mt : 64) : mt),
-                  (unsigned)((g.N + 63) / 64), g.mode == kGemmDense ? 1 : g.E);
-  return launch_pdl(gemm_simple_kernel, grid, dim3(256), 0, s, g);
+  TcArgs t = {};
+  t.a_gscale = g.a.gscale, t.b_gscale = g.b.gscale;
+  t.offsets = g.offsets, t.mode = g.mode, t.E = g.E;
+  t.M = (int32_t)g.M, t.N = (int32_t)g.N, t.K = (int32_t)g.K;
+  t.activation = g.activation, t.out_bytes = g.out_bytes, t.bias_bytes = g.bias_bytes;
+  t.bias = g.bias, t.residual = g.residual, t.preact = g.preact, t.amax = g.amax, t.out = g.out;
+  t.status = g.status;
+  // a row's first element and every 16th after it lie on `wide` boundaries
+  const uintptr_t rows = (uintptr_t)(g.N * g.out_bytes) | reinterpret_cast<uintptr_t>(g.out) |
+                         reinterpret_cast<uintptr_t>(g.residual) |
+                         (g.preact ? (uintptr_t)(g.N * 2) | reinterpret_cast<uintptr_t>(g.preact) : 0);
+  t.wide = rows % 32 == 0 ? 2 : rows % 16 == 0 ? 1 : 0;
+  const int32_t b_experts = g.mode == kGemmGrouped ? g.E : 1;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  // rows of a that a tile is likely to find: all of them, or an expert's mean share
+  const int64_t rows_a = g.mode == kGemmGrouped ? up(g.M, g.E) : g.M;
+  const int64_t many = g.mode == kGemmDense ? 1 : g.E;
+  const int64_t big = up(rows_a, 256) * up(g.N, 256) * many;
+  if (rows_a > 128 && 2 * big >= sm_count / 2) {
+    if (!make_side(t.p, g.a, g.M, g.K, 1, 128, 128) || !make_side(t.q, g.b, g.N, g.K, b_experts, 128, 256))
+      return cudaErrorInvalidValue;
+    const int64_t most = g.mode == kGemmDense ? big : sm_count / 2;
+    return launch_one<2, 256, false>(t, (int)(2 * (most < sm_count / 2 ? most : sm_count / 2)), 1, s);
+  }
+  const int nt = rows_a <= 32 ? 32 : 128;
+  if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, nt, nt))
+    return cudaErrorInvalidValue;
+  const int per_sm = nt == 32 ? 2 : 1;
+  int splits = 1;
+  int64_t grid = (int64_t)sm_count * per_sm;
+  if (g.mode == kGemmDense) {
+    const int64_t tiles = up(g.N, 128) * up(g.M, nt);
+    while (splits < 8 && 2 * splits * tiles <= sm_count * per_sm && up(g.K, kBlockK) >= 4 * splits) splits *= 2;
+    if (splits > 1 || tiles < grid) grid = tiles * splits;
+  }
+  return nt == 32 ? launch_one<1, 32, true>(t, (int)grid, splits, s)
+                  : launch_one<1, 128, true>(t, (int)grid, splits, s);
 }
 
 }  // namespace nvfp4

@@ -48,10 +48,6 @@ std::atomic<int32_t> g_setup_fault{0};
 std::atomic<int32_t> g_fail_next{0};
 int launch_grid(int grid) { return g_fail_next.exchange(0) ? 0 : grid; }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
 // Sets up the routing and checkpoint kernels (under g_mutex): with the quantizer's, so that a capture
@@ -183,6 +179,8 @@ void take_fuse_debug(QuantArgs& q) {
   q.fuse_extra = g_fuse_extra.exchange(0);
   q.fuse_late = g_fuse_late.exchange(0);
 }
+
+EncodeTiledFn encode_tiled() { return g_encode; }
 
 cudaError_t launch_quantize(const QuantMode& m, const QuantArgs& args, int grid, cudaStream_t s) {
   if (m.two_d) return launch_quantize_2d(m, args, grid, s);

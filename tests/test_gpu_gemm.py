@@ -90,6 +90,23 @@ def test_gemm(M, N, K, dtype):
     assert api.nvfp4_get_status() == (0, 0)
 
 
+@pytest.mark.parametrize("M,N,K", [(2049, 1300, 288), (1290, 2048, 544), (2304, 2816, 32),
+                                   (4000, 1016, 1312), (130, 9984, 320), (2560, 2560, 2560)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gemm_of_many_tiles(M, N, K, dtype):
+    """Out of more 256 x 256 tiles than half the SMs, partial ones among them, several to a pair of SMs."""
+    dev = cuda()
+    a, b = operand(M, K, 1 + M, dev), operand(N, K, 2 + N, dev)
+    g = torch.Generator().manual_seed(5)
+    bias = torch.randn(N, generator=g).to(dev)
+    residual = torch.randn(M, N, generator=g).to(dtype).to(dev)
+    got = api.nvfp4_gemm(*a, *b, bias=bias, activation="gelu", residual=residual, out_dtype=dtype,
+                         keep_preact=True, with_amax=True)
+    check_product(got["out"], values(*a), values(*b), bias, "gelu", residual, preact=got["preact"])
+    assert got["amax"].item() == got["out"].abs().max().item()
+    assert api.nvfp4_get_status() == (0, 0)
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "relu2", "gelu", "silu"])
 @pytest.mark.parametrize("M,N,K", [(1, 160, 256), (45, 72, 96), (140, 261, 512), (700, 1028, 640)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -215,6 +232,71 @@ def test_grouped(counts, N, K, rest):
         assert got["amax"][e].item() == (got["out"][rows].abs().max().item() if n else 0.0)
         check_product(full["out"][rows], x, w, bias[e], "silu", preact=full["preact"][rows])
     assert not got["out"][live:].any() and not full["out"][live:].any() and not full["preact"][live:].any()
+    assert api.nvfp4_get_status() == (0, 0)
+
+
+@pytest.mark.parametrize("counts,rest", [([700, 900, 0, 400], 21), ([1500, 3, 260, 257, 511], 0)])
+@pytest.mark.parametrize("N,K", [(2056, 288), (1300, 1056)])
+def test_grouped_of_many_rows(counts, rest, N, K):
+    dev = cuda()
+    E, live = len(counts), sum(counts)
+    T = live + rest
+    ends = torch.tensor(np.cumsum(counts), dtype=torch.int32, device=dev)
+    a, b = list(operand(T, K, 70, dev)), operand(N, K, 71, dev, lead=(E,))
+    a[2] = torch.rand(E, 2, generator=torch.Generator().manual_seed(72)).to(dev) + 0.5
+    a[1][live:] = 0x7F
+    got = api.nvfp4_gemm_grouped(*a, *b, ends, activation="silu", with_amax=True, keep_preact=True)
+    begin = 0
+    for e, n in enumerate(counts):
+        rows = slice(begin, begin + n)
+        begin += n
+        x, w = values(a[0][rows], a[1][rows], a[2][e]), values(b[0][e], b[1][e], b[2][e])
+        check_product(got["out"][rows], x, w, None, "silu", preact=got["preact"][rows])
+        assert got["amax"][e].item() == (got["out"][rows].abs().max().item() if n else 0.0)
+    assert not got["out"][live:].any() and not got["preact"][live:].any()
+
+
+@pytest.mark.parametrize("counts", [[300, 2, 0, 41], [0, 0, 520, 1, 255, 16]])
+@pytest.mark.parametrize("M,N", [(1032, 776), (520, 2056)])
+def test_grouped_wgrad_of_many_tiles(counts, M, N):
+    dev = cuda()
+    E, pads = len(counts), [(n + 15) // 16 * 16 for n in counts]
+    cap = (sum(pads) + 31) // 32 * 32 + 32
+    ends = torch.tensor(np.cumsum(counts), dtype=torch.int32, device=dev)
+    a, b = list(operand(M, cap, 73, dev)), list(operand(N, cap, 74, dev))
+    a[2], b[2] = torch.rand(E, 2).to(dev) + 0.5, torch.rand(E, 2).to(dev) + 0.5
+    for x in (a, b):
+        x[1][:, sum(pads) // 16:] = 0x7F
+    before = torch.randn(E, M, N, generator=torch.Generator().manual_seed(75)).to(dev)
+    got = api.nvfp4_gemm_grouped_wgrad(*a, *b, ends)
+    added = api.nvfp4_gemm_grouped_wgrad(*a, *b, ends, out=before.clone(), accumulate=True)
+    at = 0
+    for e, n in enumerate(pads):
+        c, s = slice(at // 2, (at + n) // 2), slice(at // 16, (at + n) // 16)
+        at += n
+        x, y = (values(o[0][:, c].contiguous(), o[1][:, s].contiguous(), o[2][e]) for o in (a, b))
+        check_product(got[e], x, y)
+        check_product(added[e], x, y, residual=before[e])
+
+
+@pytest.mark.parametrize("E,most", [(24, 5), (9, 100)])
+def test_grouped_of_many_small_experts(E, most):
+    """More tiles of the small kernels than the GPU holds at once: several to a CTA."""
+    dev = cuda()
+    N, K = 128 * 80 - 8, 1312
+    counts = [int(n) for n in torch.randint(0, most, (E,), generator=torch.Generator().manual_seed(76))]
+    T = sum(counts)
+    ends = torch.tensor(np.cumsum(counts), dtype=torch.int32, device=dev)
+    a, b = list(operand(T, K, 77, dev)), operand(N, K, 78, dev, lead=(E,))
+    a[2] = torch.rand(E, 2, generator=torch.Generator().manual_seed(79)).to(dev) + 0.5
+    got = api.nvfp4_gemm_grouped(*a, *b, ends, with_amax=True)
+    begin = 0
+    for e, n in enumerate(counts):
+        rows = slice(begin, begin + n)
+        begin += n
+        check_product(got["out"][rows], values(a[0][rows], a[1][rows], a[2][e]),
+                      values(b[0][e], b[1][e], b[2][e]))
+        assert got["amax"][e].item() == (got["out"][rows].abs().max().item() if n else 0.0)
     assert api.nvfp4_get_status() == (0, 0)
 
 
