@@ -344,24 +344,37 @@ __device__ __forceinline__ void store_words(void* p, int wide, const uint32_t* w
   }
 }
 
-// `C` consecutive elements of one row of out from element `at`, `have` of them inside the row. n: their
-// first column of the bias (already with the expert's part). Returns the largest bits of |out|.
-template <int C>
-__device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], float alpha, int64_t at, int64_t n,
-                                               int have) {
-  const bool whole = have >= C && a.wide != 0;
+// C elements of out from element `at`, `stride` apart, of which the first `have` count. SWAP false: they
+// are neighbours in a row (stride 1), n is their first column of the bias (with the expert's part); true:
+// a column, with one value of the bias. Returns the largest bits of |out|.
+template <int C, bool SWAP>
+__device__ __forceinline__ uint32_t finish(const TcArgs& a, float (&z)[C], float alpha, int64_t at, int64_t stride,
+                                           int64_t n, int have) {
+  const bool whole = !SWAP && have >= C && a.wide != 0;
 #pragma unroll
   for (int i = 0; i < C; i++) z[i] *= alpha;
   if (a.bias != nullptr) {
+    if constexpr (SWAP) {
+      const float b = bias_at(a, n);
 #pragma unroll
-    for (int i = 0; i < C; i++)
-      if (i < have) z[i] += bias_at(a, n + i);
+      for (int i = 0; i < C; i++) z[i] += b;
+    } else if (a.bias_bytes == 4) {
+      const float* const b = static_cast<const float*>(a.bias) + n;
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) z[i] += __ldg(b + i);
+    } else {
+      const __nv_bfloat16* const b = static_cast<const __nv_bfloat16*>(a.bias) + n;
+#pragma unroll
+      for (int i = 0; i < C; i++)
+        if (i < have) z[i] += __bfloat162float(b[i]);
+    }
   }
   if (a.preact != nullptr) {
-    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.preact) + at;
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.preact) + at;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < C; i += 16) {
+      for (int i = 0; i + 16 <= C; i += 16) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) w[j] = pack2(z[i + 2 * j], z[i + 2 * j + 1]);
@@ -369,18 +382,18 @@ __device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], f
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) to[i] = __float2bfloat16_rn(z[i]);
+      for (int i = 0; i < C; i++, to += stride)
+        if (i < have) *to = __float2bfloat16_rn(z[i]);
     }
   }
   activate_all<C>(a.activation, z);
   uint32_t top = 0u;
   if (a.out_bytes == 2) {
     if (a.residual != nullptr) {
-      const __nv_bfloat16* const r = static_cast<const __nv_bfloat16*>(a.residual) + at;
+      const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + at;
       if (whole) {
 #pragma unroll
-        for (int i = 0; i < C; i += 8) {
+        for (int i = 0; i + 8 <= C; i += 8) {
           const uint4 v = *reinterpret_cast<const uint4*>(r + i);
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -391,21 +404,21 @@ __device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], f
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < C; i++)
-          if (i < have) z[i] += __bfloat162float(r[i]);
+        for (int i = 0; i < C; i++, r += stride)
+          if (i < have) z[i] += __bfloat162float(*r);
       }
     }
-    __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(a.out) + at;
-    uint32_t w[C / 2];
+    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
+    uint32_t w[(C + 1) / 2];
 #pragma unroll
-    for (int j = 0; j < C / 2; j++) w[j] = pack2(z[2 * j], z[2 * j + 1]);
+    for (int j = 0; j < (C + 1) / 2; j++) w[j] = pack2(z[2 * j], 2 * j + 1 < C ? z[(2 * j + 1) % C] : 0.0f);
     if (whole) {
 #pragma unroll
-      for (int j = 0; j < C / 2; j += 8) store_words(to + 2 * j, a.wide, w + j);
+      for (int j = 0; j + 8 <= C / 2; j += 8) store_words(to + 2 * j, a.wide, w + j);
     } else {
 #pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) to[i] = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i % 2))));
+      for (int i = 0; i < C; i++, to += stride)
+        if (i < have) *to = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i % 2))));
     }
     if (a.amax != nullptr) {
 #pragma unroll
@@ -414,23 +427,23 @@ __device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], f
     }
   } else {
     if (a.residual != nullptr) {
-      const float* const r = static_cast<const float*>(a.residual) + at;
+      const float* r = static_cast<const float*>(a.residual) + at;
       if (whole) {
 #pragma unroll
-        for (int i = 0; i < C; i += 4) {
+        for (int i = 0; i + 4 <= C; i += 4) {
           const float4 v = *reinterpret_cast<const float4*>(r + i);
           z[i] += v.x, z[i + 1] += v.y, z[i + 2] += v.z, z[i + 3] += v.w;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < C; i++)
-          if (i < have) z[i] += r[i];
+        for (int i = 0; i < C; i++, r += stride)
+          if (i < have) z[i] += *r;
       }
     }
-    float* const to = static_cast<float*>(a.out) + at;
+    float* to = static_cast<float*>(a.out) + at;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i < C; i += 8) {
+      for (int i = 0; i + 8 <= C; i += 8) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) w[j] = __float_as_uint(z[i + j]);
@@ -438,8 +451,8 @@ __device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], f
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) to[i] = z[i];
+      for (int i = 0; i < C; i++, to += stride)
+        if (i < have) *to = z[i];
     }
     if (a.amax != nullptr) {
 #pragma unroll
@@ -448,22 +461,6 @@ __device__ __forceinline__ uint32_t finish_row(const TcArgs& a, float (&z)[C], f
     }
   }
   return top;
-}
-
-// One element of out (the swapped tiles: a warp has 32 neighbouring columns of a row).
-__device__ __forceinline__ uint32_t finish_one(const TcArgs& a, float v, float alpha, float bias, int64_t at) {
-  float z[1] = {v * alpha + bias};
-  if (a.preact != nullptr) static_cast<__nv_bfloat16*>(a.preact)[at] = __float2bfloat16_rn(z[0]);
-  activate_all<1>(a.activation, z);
-  if (a.out_bytes == 2) {
-    if (a.residual != nullptr) z[0] += bf16_at(a.residual, at);
-    const __nv_bfloat16 b = __float2bfloat16_rn(z[0]);
-    static_cast<__nv_bfloat16*>(a.out)[at] = b;
-    return ((uint32_t)__bfloat16_as_ushort(b) & 0x7FFFu) << 16;
-  }
-  if (a.residual != nullptr) z[0] += static_cast<const float*>(a.residual)[at];
-  static_cast<float*>(a.out)[at] = z[0];
-  return __float_as_uint(z[0]) & 0x7FFFFFFFu;
 }
 
 __device__ __forceinline__ void report_amax(const TcArgs& a, uint32_t top, int e) {
@@ -656,27 +653,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
           for (int j = 0; j < 32; j++) v[j] = 0u;
         }
         const int left = x.q_rows - 32 * chunk;  // columns (rows of q) that count
-        if constexpr (!SWAP) {
-          if (r < x.p_rows && left > 0) {
-            float z[32];
-#pragma unroll
-            for (int j = 0; j < 32; j++) z[j] = __uint_as_float(v[j]);
-            const int64_t n = x.q0 + 32 * chunk;
-            top = max(top, finish_row<32>(a, z, alpha, base + (int64_t)(x.p0 + r) * a.N + n,
-                                          (int64_t)x.e * a.N + n, left));
-          }
-        } else if (splits > 1) {
+        if (SWAP && splits > 1) {
           // the sums of this share of K, for the cluster
           const uint32_t to = stages + ((32 * chunk) * 128 + r) * 4;
 #pragma unroll
           for (int j = 0; j < 32; j++)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 512), "r"(v[j]) : "memory");
-        } else if (r < x.p_rows) {
-          const float bias = a.bias ? bias_at(a, (int64_t)x.e * a.N + x.p0 + r) : 0.0f;
-          const int64_t at = base + (int64_t)(x.q0 + 32 * chunk) * a.N + x.p0 + r;
+        } else if (r < x.p_rows && left > 0) {
+          float z[32];
 #pragma unroll
-          for (int j = 0; j < 32; j++)
-            if (j < left) top = max(top, finish_one(a, __uint_as_float(v[j]), alpha, bias, at + (int64_t)j * a.N));
+          for (int j = 0; j < 32; j++) z[j] = __uint_as_float(v[j]);
+          const int row = SWAP ? x.q0 + 32 * chunk : x.p0 + r, col = SWAP ? x.p0 + r : x.q0 + 32 * chunk;
+          top = max(top, finish<32, SWAP>(a, z, alpha, base + (int64_t)row * a.N + col, SWAP ? a.N : 1,
+                                          (int64_t)x.e * a.N + col, left));
         }
       }
       if (splits == 1) report_amax(a, top, x.e);
@@ -698,11 +687,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
       const int r = 32 * (warp & 3) + lane;
       uint32_t top = 0u;
       if (r < x.p_rows) {
-        const float bias = a.bias ? bias_at(a, (int64_t)x.e * a.N + x.p0 + r) : 0.0f;
         for (int c = split; c < min(NT, x.q_rows); c += splits) {
-          float v = 0.0f;
-          for (int s = 0; s < splits; s++) v += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
-          top = max(top, finish_one(a, v, alpha, bias, (int64_t)(x.q0 + c) * a.N + x.p0 + r));
+          float v[1] = {0.0f};
+          for (int s = 0; s < splits; s++) v[0] += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
+          top = max(top, finish<1, true>(a, v, alpha, (int64_t)(x.q0 + c) * a.N + x.p0 + r, a.N, x.p0 + r, 1));
         }
       }
       report_amax(a, top, x.e);
