@@ -7,8 +7,8 @@
 // block of 128 x 16 scale bytes as it is, and a warp turns it in place, four 16-byte loads and four
 // 16-byte stores a lane, while the codes of the same stage wait for their turn.
 //
-// Warps of a CTA: 0 loads (TMA), 1 issues the matrix instructions, 2 and 3 turn the scales, 4 to 7 are
-// the epilogue. `p` is the operand on the instruction's 128-row side, `q` the one on its N side:
+// A warp loads (TMA), one issues the matrix instructions, two or three turn the scales, the others are the
+// epilogue. `p` is the operand on the instruction's 128-row side, `q` the one on its N side:
 //   <2, 256, false>  a pair of CTAs has 256 x 256 of out; p is a, q is b
 //   <1, NT, true>    a CTA has 128 columns of out (p is b, the weights) and NT rows (q is a, tokens):
 //                    few tokens waste no tensor-core rows, and a warp's stores run along out's rows.
@@ -34,7 +34,6 @@ namespace nvfp4 {
 namespace {
 
 constexpr uint32_t kBadOffsets = 0x1u, kTimeout = 0x2u;  // NVFP4_DEVICE_*
-constexpr int kThreads = 256;
 constexpr int kBlockK = 256;   // elements of a stage
 constexpr int kPBytes = 128 * kBlockK / 2;
 constexpr int kScaleBlock = 128 * kBlockK / 16;  // scales of 128 rows of a stage
@@ -44,9 +43,7 @@ struct SideArgs {
   const uint8_t* scale_ptr;
   int64_t scale_pitch, scale_batch;
   int32_t rows;      // of the operand (of one expert, where stacked)
-  int32_t tma;       // scales come by TMA; else by loads, of 4 bytes where words is set
-  int32_t words;
-  int32_t pad;
+  int32_t tma;       // every row of scales starts on a 16-byte boundary: they come by TMA, else by loads
 };
 struct TcArgs {
   SideArgs p, q;
@@ -80,6 +77,10 @@ struct Shape {
   static constexpr int kScaleColumn = NT == 256 ? 448 : 2 * NT;
   static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
   static constexpr int kSmem = kStages * kStage + 1024;
+  // warps: the epilogue (a multiple of four: a warp reads the lane quarter of its number), loads, matrix
+  // instructions, scales of p, a block of 128 scales of q each
+  static constexpr int kEpi = CTAS == 2 ? 8 : 4;
+  static constexpr int kThreads = 32 * (kEpi + 3 + kQBlocks);
   static_assert(kScaleColumn + 4 * kSlot <= kColumns, "tensor memory");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
@@ -125,11 +126,13 @@ __device__ __forceinline__ void make_table(const TcArgs& a, Table& t) {
     const int32_t x = __shfl_up_sync(0xFFFFFFFFu, sum_n, o), y = __shfl_up_sync(0xFFFFFFFFu, sum_t, o);
     if (lane >= o) sum_n += x, sum_t += y;
   }
-  if (lane == 31) t.warp_sum[0][warp] = sum_n, t.warp_sum[1][warp] = sum_t;
+  if (lane == 31 && warp < 8) t.warp_sum[0][warp] = sum_n, t.warp_sum[1][warp] = sum_t;
   __syncthreads();
-  for (int w = 0; w < warp; w++) sum_n += t.warp_sum[0][w], sum_t += t.warp_sum[1][w];
-  t.begin[e + 1] = sum_n;
-  t.first[e + 1] = sum_t;
+  for (int w = 0; w < min(warp, 8); w++) sum_n += t.warp_sum[0][w], sum_t += t.warp_sum[1][w];
+  if (e < 256) {
+    t.begin[e + 1] = sum_n;
+    t.first[e + 1] = sum_t;
+  }
   if (e == 0) t.begin[0] = t.first[0] = 0;
   __syncthreads();
   if (t.bad || (a.mode == kGemmWgrad && t.begin[a.E] > a.K)) {
@@ -137,7 +140,7 @@ __device__ __forceinline__ void make_table(const TcArgs& a, Table& t) {
       atomicOr(a.status, kBadOffsets);
       t.bad = 1;
     }
-    t.first[e + 1] = 0;
+    if (e < 256) t.first[e + 1] = 0;
   }
   __syncthreads();
 }
@@ -190,22 +193,26 @@ __device__ __forceinline__ Tile get_tile(const TcArgs& a, const Table& t, int i,
 
 // ---- scales ---------------------------------------------------------------------------------------
 
-// 16 scale bytes of a row from byte `at`, zeros from byte `end` on, by loads.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int at, int end, bool words) {
-  uint32_t w[4];
+// The aligned 16 bytes at `p`, zeros where no byte of the row (which ends at `end`) is among them. The
+// bytes around a row that a load brings along lie in the row's own allocation, whose ends are aligned,
+// and are masked or belong to rows that do not count.
+__device__ __forceinline__ uint4 load_chunk(const uint8_t* p, const uint8_t* end) {
+  return p < end ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+// 16 bytes from byte `shift` (0 to 15) of the 32 bytes lo, hi.
+__device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint32_t shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8u) {
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    w[j] = 0u;
-    const int c = at + 4 * j;
-    if (words && c + 4 <= end) {
-      w[j] = __ldg(reinterpret_cast<const uint32_t*>(row + c));
-    } else {
-#pragma unroll
-      for (int b = 0; b < 4; b++)
-        if (c + b < end) w[j] |= (uint32_t)__ldg(row + c + b) << (8 * b);
-    }
+    for (int i = 0; i < 6; i++) w[i] = w[i + 2];
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  if (shift & 4u) {
+#pragma unroll
+    for (int i = 0; i < 5; i++) w[i] = w[i + 1];
+  }
+  const uint32_t bits = (shift & 3u) * 8u;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 // Bytes [lo, hi) of 16 stay.
 __device__ __forceinline__ uint32_t byte_mask(int lo, int hi, int word) {
@@ -231,36 +238,52 @@ __device__ __forceinline__ void put_scales(uint32_t addr, const uint4 (&v)[4]) {
   put(3, v[0].w, v[1].w, v[2].w, v[3].w);
 }
 
-// Warp 2 (the scales of p, one block) or 3 (of q): every stage's blocks turned, then the arrival on the
-// pair's `ready`.
-template <int CTAS, int NT, bool SWAP, int BLOCKS, int ROWS>
+// A warp turns one block of scales of every stage: rows `row_shift`.. of the tile's rows of p or q, of
+// which ROWS exist. Then it arrives on the pair's `ready`.
+template <int CTAS, int NT, bool SWAP, int ROWS>
 __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table, int tiles,
                                             int cluster, int clusters, int split, int splits, bool is_q,
-                                            uint32_t stages, uint32_t offset, uint64_t* full, uint64_t* ready,
-                                            int row_shift) {
+                                            uint32_t blocks, uint64_t* full, uint64_t* ready, int row_shift) {
   using S = Shape<CTAS, NT>;
   const int lane = threadIdx.x & 31;
-  const int end = a.K / 16;
   int e = 0, it = 0;
   for (int i = cluster; i < tiles; i += clusters) {
     const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
-    const int row0 = (is_q ? x.q0 : x.p0) + row_shift, z = is_q ? x.qz : x.pz;
-    const uint8_t* const base = s.scale_ptr + (int64_t)z * s.scale_batch;
+    // Where rows start anywhere: aligned loads, two stages ahead. A stage is 16 bytes of a row, so that
+    // its upper part is the next stage's lower one.
+    uint4 lo[4], hi[4], next[4];
+    const uint8_t *at[4], *end[4];
+    uint32_t shift[4];
+    if (!s.tma) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int r = 32 * j + lane, row = (is_q ? x.q0 : x.p0) + row_shift + r;
+        const uint8_t* const p = s.scale_ptr + (int64_t)(is_q ? x.qz : x.pz) * s.scale_batch +
+                                 (int64_t)row * s.scale_pitch;
+        shift[j] = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+        at[j] = p - shift[j] + 16 * x.kb0;
+        // (without columns of K a row has no bytes, and its address may be none)
+        end[j] = r < ROWS && row < s.rows && x.kb1 > x.kb0 ? p + a.K / 16 : nullptr;
+        lo[j] = load_chunk(at[j], end[j]);
+        hi[j] = load_chunk(at[j] + 16, end[j]);
+        next[j] = load_chunk(at[j] + 32, end[j]);
+        at[j] += 48;
+      }
+    }
     for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
       const int stage = it % S::kStages;
-      const uint32_t at = stages + stage * S::kStage + offset;
-      const int lo = x.k_lo / 16 - kb * 16, hi = x.k_hi / 16 - kb * 16;
-      uint4 v[BLOCKS][4];
+      const uint32_t to = blocks + stage * S::kStage;
+      const int first = x.k_lo / 16 - kb * 16, last = x.k_hi / 16 - kb * 16;
+      uint4 v[4];
       if (!s.tma) {
 #pragma unroll
-        for (int b = 0; b < BLOCKS; b++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const int r = 128 * b + 32 * j + lane;
-            v[b][j] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < ROWS && row0 + r < s.rows)
-              v[b][j] = load_scales(base + (int64_t)(row0 + r) * s.scale_pitch, kb * 16, end, s.words);
-          }
+        for (int j = 0; j < 4; j++) {
+          v[j] = shifted(lo[j], hi[j], shift[j]);
+          lo[j] = hi[j];
+          hi[j] = next[j];
+          next[j] = load_chunk(at[j], end[j]);
+          at[j] += 16;
+        }
       }
       if (!wait_phase(&full[stage], (uint32_t)(it / S::kStages) & 1u)) {
         if (lane == 0) atomicOr(a.status, kTimeout);
@@ -268,27 +291,22 @@ __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, 
       }
       if (s.tma) {
 #pragma unroll
-        for (int b = 0; b < BLOCKS; b++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const int r = 128 * b + 32 * j + lane;
-            v[b][j] = r < ROWS ? lds128(at + r * 16) : make_uint4(0u, 0u, 0u, 0u);
-          }
+        for (int j = 0; j < 4; j++) {
+          const int r = 32 * j + lane;
+          v[j] = r < ROWS ? lds128(to + r * 16) : make_uint4(0u, 0u, 0u, 0u);
+        }
         __syncwarp();
       }
-      if (lo > 0 || hi < 16) {  // another expert's columns share the stage
+      if (first > 0 || last < 16) {  // other experts' columns, or what follows the row
 #pragma unroll
-        for (int b = 0; b < BLOCKS; b++)
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            v[b][j].x &= byte_mask(lo, hi, 0);
-            v[b][j].y &= byte_mask(lo, hi, 1);
-            v[b][j].z &= byte_mask(lo, hi, 2);
-            v[b][j].w &= byte_mask(lo, hi, 3);
-          }
+        for (int j = 0; j < 4; j++) {
+          v[j].x &= byte_mask(first, last, 0);
+          v[j].y &= byte_mask(first, last, 1);
+          v[j].z &= byte_mask(first, last, 2);
+          v[j].w &= byte_mask(first, last, 3);
+        }
       }
-#pragma unroll
-      for (int b = 0; b < BLOCKS; b++) put_scales(at + b * kScaleBlock, v[b]);
+      put_scales(to, v);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
@@ -301,28 +319,6 @@ __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, 
 
 // ---- epilogue -------------------------------------------------------------------------------------
 
-template <int N>
-__device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
-  switch (act) {
-    case NVFP4_ACT_RELU:
-#pragma unroll
-      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_RELU>(z[i]);
-      break;
-    case NVFP4_ACT_RELU2:
-#pragma unroll
-      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_RELU2>(z[i]);
-      break;
-    case NVFP4_ACT_GELU:
-#pragma unroll
-      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_GELU>(z[i]);
-      break;
-    case NVFP4_ACT_SILU:
-#pragma unroll
-      for (int i = 0; i < N; i++) z[i] = activate<NVFP4_ACT_SILU>(z[i]);
-      break;
-    default: break;
-  }
-}
 __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
@@ -344,123 +340,157 @@ __device__ __forceinline__ void store_words(void* p, int wide, const uint32_t* w
   }
 }
 
-// C elements of out from element `at`, `stride` apart, of which the first `have` count. SWAP false: they
-// are neighbours in a row (stride 1), n is their first column of the bias (with the expert's part); true:
-// a column, with one value of the bias. Returns the largest bits of |out|.
-template <int C, bool SWAP>
-__device__ __forceinline__ uint32_t finish(const TcArgs& a, float (&z)[C], float alpha, int64_t at, int64_t stride,
-                                           int64_t n, int have) {
-  const bool whole = !SWAP && have >= C && a.wide != 0;
+// 32 elements as 16 packed pairs.
+using Pairs = uint64_t[16];
+
+template <int ACT>
+__device__ __forceinline__ void activate_pairs(Pairs& z) {
 #pragma unroll
-  for (int i = 0; i < C; i++) z[i] *= alpha;
-  if (a.bias != nullptr) {
-    if constexpr (SWAP) {
-      const float b = bias_at(a, n);
-#pragma unroll
-      for (int i = 0; i < C; i++) z[i] += b;
-    } else if (a.bias_bytes == 4) {
-      const float* const b = static_cast<const float*>(a.bias) + n;
-#pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) z[i] += __ldg(b + i);
-    } else {
-      const __nv_bfloat16* const b = static_cast<const __nv_bfloat16*>(a.bias) + n;
-#pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) z[i] += __bfloat162float(b[i]);
-    }
+  for (int i = 0; i < 16; i++) z[i] = activate2<ACT>(z[i]);
+}
+__device__ __forceinline__ void activate_pairs(int act, Pairs& z) {
+  switch (act) {
+    case NVFP4_ACT_RELU: activate_pairs<NVFP4_ACT_RELU>(z); break;
+    case NVFP4_ACT_RELU2: activate_pairs<NVFP4_ACT_RELU2>(z); break;
+    case NVFP4_ACT_GELU: activate_pairs<NVFP4_ACT_GELU>(z); break;
+    case NVFP4_ACT_SILU: activate_pairs<NVFP4_ACT_SILU>(z); break;
+    default: break;
   }
-  if (a.preact != nullptr) {
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.preact) + at;
+}
+__device__ __forceinline__ void pack_pairs(const Pairs& z, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const float2 f = f2_unpack(z[i]);
+    w[i] = pack2(f.x, f.y);
+  }
+}
+
+// The residual's 32 elements, loaded ahead of the sums: `whole` by 16-byte loads, else the first `have`,
+// `stride` apart. Words of BF16 pairs or of binary32.
+__device__ __forceinline__ void load_residual(const TcArgs& a, uint32_t (&w)[32], int64_t at, int64_t stride,
+                                              int have, bool whole) {
+  if (a.out_bytes == 2) {
+    const uint16_t* r = static_cast<const uint16_t*>(a.residual) + at;
     if (whole) {
 #pragma unroll
-      for (int i = 0; i + 16 <= C; i += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = pack2(z[i + 2 * j], z[i + 2 * j + 1]);
-        store_words(to + i, a.wide, w);
+      for (int i = 0; i < 4; i++) {
+        const uint4 v = reinterpret_cast<const uint4*>(r)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; i++, to += stride)
-        if (i < have) *to = __float2bfloat16_rn(z[i]);
+      return;
     }
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const uint32_t lo = 2 * i < have ? r[0] : 0u, hi = 2 * i + 1 < have ? r[stride] : 0u;
+      w[i] = lo | hi << 16;
+      r += 2 * stride;
+    }
+    return;
   }
-  activate_all<C>(a.activation, z);
-  uint32_t top = 0u;
+  const uint32_t* r = static_cast<const uint32_t*>(a.residual) + at;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint4 v = reinterpret_cast<const uint4*>(r)[i];
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i++, r += stride) w[i] = i < have ? *r : 0u;
+}
+// 32 elements (`whole`) or the first `have` of them, `stride` apart, of 2 bytes.
+__device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint32_t (&w)[16], int64_t at,
+                                            int64_t stride, int have, bool whole) {
+  uint16_t* to = static_cast<uint16_t*>(p) + at;
+  if (whole) {
+    store_words(to, a.wide, w);
+    store_words(to + 16, a.wide, w + 8);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; i++, to += stride)
+    if (i < have) *to = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+}
+
+// z = alpha * sums + bias through the activation and the residual into out: 32 elements from element
+// `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
+// aligned. Returns the largest |out| as binary32 bits.
+__device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint32_t (&residual)[32], int64_t at,
+                                           int64_t stride, int have, bool whole) {
+  uint32_t w[16];
+  if (a.preact != nullptr) {
+    pack_pairs(z, w);
+    store_pairs(a, a.preact, w, at, stride, have, whole);
+  }
+  activate_pairs(a.activation, z);
   if (a.out_bytes == 2) {
     if (a.residual != nullptr) {
-      const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual) + at;
-      if (whole) {
 #pragma unroll
-        for (int i = 0; i + 8 <= C; i += 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(r + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            z[i + 2 * j] += __uint_as_float(w[j] << 16);
-            z[i + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < C; i++, r += stride)
-          if (i < have) z[i] += __bfloat162float(*r);
-      }
+      for (int i = 0; i < 16; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
     }
-    __nv_bfloat16* to = static_cast<__nv_bfloat16*>(a.out) + at;
-    uint32_t w[(C + 1) / 2];
+    pack_pairs(z, w);
+    store_pairs(a, a.out, w, at, stride, have, whole);
+    if (a.amax == nullptr) return 0u;
+    uint32_t top = 0u;
 #pragma unroll
-    for (int j = 0; j < (C + 1) / 2; j++) w[j] = pack2(z[2 * j], 2 * j + 1 < C ? z[(2 * j + 1) % C] : 0.0f);
-    if (whole) {
-#pragma unroll
-      for (int j = 0; j + 8 <= C / 2; j += 8) store_words(to + 2 * j, a.wide, w + j);
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; i++, to += stride)
-        if (i < have) *to = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i % 2))));
+    for (int i = 0; i < 16; i++) {
+      if (2 * i >= have) w[i] = 0u;
+      else if (2 * i + 1 >= have) w[i] &= 0xFFFFu;
+      top = hmax_abs2(top, w[i]);
     }
-    if (a.amax != nullptr) {
+    top &= 0x7FFF7FFFu;
+    return max(top << 16, top & 0xFFFF0000u);
+  }
+  if (a.residual != nullptr) {
 #pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) top = max(top, (w[i / 2] << (16 * (1 - i % 2))) & 0x7FFF0000u);
-    }
+    for (int i = 0; i < 16; i++)
+      z[i] = f2_add(z[i], f2_pack(__uint_as_float(residual[2 * i]), __uint_as_float(residual[2 * i + 1])));
+  }
+  uint32_t o[32], top = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const float2 f = f2_unpack(z[i]);
+    o[2 * i] = __float_as_uint(f.x);
+    o[2 * i + 1] = __float_as_uint(f.y);
+  }
+  uint32_t* to = static_cast<uint32_t*>(a.out) + at;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) store_words(to + i, a.wide, o + i);
   } else {
-    if (a.residual != nullptr) {
-      const float* r = static_cast<const float*>(a.residual) + at;
-      if (whole) {
 #pragma unroll
-        for (int i = 0; i + 4 <= C; i += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(r + i);
-          z[i] += v.x, z[i + 1] += v.y, z[i + 2] += v.z, z[i + 3] += v.w;
-        }
-      } else {
+    for (int i = 0; i < 32; i++, to += stride)
+      if (i < have) *to = o[i];
+  }
+  if (a.amax != nullptr) {
 #pragma unroll
-        for (int i = 0; i < C; i++, r += stride)
-          if (i < have) z[i] += *r;
-      }
-    }
-    float* to = static_cast<float*>(a.out) + at;
-    if (whole) {
-#pragma unroll
-      for (int i = 0; i + 8 <= C; i += 8) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = __float_as_uint(z[i + j]);
-        store_words(to + i, a.wide, w);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < C; i++, to += stride)
-        if (i < have) *to = z[i];
-    }
-    if (a.amax != nullptr) {
-#pragma unroll
-      for (int i = 0; i < C; i++)
-        if (i < have) top = max(top, __float_as_uint(z[i]) & 0x7FFFFFFFu);
-    }
+    for (int i = 0; i < 32; i++)
+      if (i < have) top = max(top, o[i] & 0x7FFFFFFFu);
   }
   return top;
+}
+
+// One element (the tiles whose sums a cluster adds up).
+__device__ __forceinline__ uint32_t finish_one(const TcArgs& a, float sum, float alpha, float bias, int64_t at) {
+  float z = sum * alpha + bias;
+  if (a.preact != nullptr) static_cast<__nv_bfloat16*>(a.preact)[at] = __float2bfloat16_rn(z);
+  switch (a.activation) {
+    case NVFP4_ACT_RELU: z = activate<NVFP4_ACT_RELU>(z); break;
+    case NVFP4_ACT_RELU2: z = activate<NVFP4_ACT_RELU2>(z); break;
+    case NVFP4_ACT_GELU: z = activate<NVFP4_ACT_GELU>(z); break;
+    case NVFP4_ACT_SILU: z = activate<NVFP4_ACT_SILU>(z); break;
+    default: break;
+  }
+  if (a.out_bytes == 2) {
+    if (a.residual != nullptr) z += bf16_at(a.residual, at);
+    const __nv_bfloat16 b = __float2bfloat16_rn(z);
+    static_cast<__nv_bfloat16*>(a.out)[at] = b;
+    return ((uint32_t)__bfloat16_as_ushort(b) & 0x7FFFu) << 16;
+  }
+  if (a.residual != nullptr) z += static_cast<const float*>(a.residual)[at];
+  static_cast<float*>(a.out)[at] = z;
+  return __float_as_uint(z) & 0x7FFFFFFFu;
 }
 
 __device__ __forceinline__ void report_amax(const TcArgs& a, uint32_t top, int e) {
@@ -483,12 +513,13 @@ __device__ __forceinline__ void clear(void* p, int64_t lo, int64_t hi, int64_t a
 // ---- the kernel -----------------------------------------------------------------------------------
 
 template <int CTAS, int NT, bool SWAP>
-__global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
+__global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>::kPerSm))
     gemm_kernel(const __grid_constant__ TcArgs a, int splits) {
   using S = Shape<CTAS, NT>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[S::kStages], ready[S::kStages], empty[S::kStages], acc_full[2], acc_free[2];
   __shared__ uint32_t tmem_base;
+  __shared__ __align__(16) float bias_stage[S::kEpi][32];
   __shared__ Table table;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CTAS == 2 || splits > 1 ? cluster_rank() : 0u;
@@ -501,20 +532,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; i++) {
       mbar_init(&full[i], 1);
-      mbar_init(&ready[i], 2 * CTAS);
+      mbar_init(&ready[i], (1 + S::kQBlocks) * CTAS);
       mbar_init(&empty[i], 1);
     }
     mbar_init(&acc_full[0], 1);
     mbar_init(&acc_full[1], 1);
-    mbar_init(&acc_free[0], 4 * CTAS);
-    mbar_init(&acc_free[1], 4 * CTAS);
+    mbar_init(&acc_free[0], S::kEpi * CTAS);
+    mbar_init(&acc_free[1], S::kEpi * CTAS);
     fence_barrier_init();
     prefetch_tensormap(&a.p.codes);
     prefetch_tensormap(&a.q.codes);
     if (a.p.tma) prefetch_tensormap(&a.p.scales);
     if (a.q.tma) prefetch_tensormap(&a.q.scales);
   }
-  if (warp == 1) tmem_alloc<CTAS>(&tmem_base, S::kColumns);
+  if (warp == S::kEpi + 1) tmem_alloc<CTAS>(&tmem_base, S::kColumns);
   tc_fence_before();
   __syncthreads();
   __syncwarp();
@@ -526,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
   if (a.mode != kGemmDense) make_table<CTAS, NT, SWAP>(a, table);
   const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
 
-  if (warp == 0) {
+  if (warp == S::kEpi) {
     const uint32_t bytes = kPBytes + S::kQBytes + (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
     int e = 0, it = 0;
     bool alive = true;
@@ -557,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
       wait_phase(&full[stage], (uint32_t)(i / S::kStages) & 1u);
       if (alive) wait_phase(&empty[stage], (uint32_t)(i / S::kStages) & 1u);
     }
-  } else if (warp == 1) {
+  } else if (warp == S::kEpi + 1) {
     if (half == 0) {
       constexpr uint32_t idesc = nvfp4_idesc(128 * CTAS, NT);
       const uint32_t sf = tmem + S::kScaleColumn;
@@ -609,37 +640,59 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
         __syncwarp();
       }
     }
-  } else if (warp == 2) {
-    turn_scales<CTAS, NT, SWAP, 1, 128>(a, a.p, table, tiles, cluster, clusters, split, splits, false, stages,
-                                        kPBytes + S::kQBytes, full, ready, 128 * half);
-  } else if (warp == 3) {
-    turn_scales<CTAS, NT, SWAP, S::kQBlocks, NT>(a, a.q, table, tiles, cluster, clusters, split, splits, true,
-                                                 stages, kPBytes + S::kQBytes + kScaleBlock, full, ready, 0);
+  } else if (warp == S::kEpi + 2) {
+    turn_scales<CTAS, NT, SWAP, 128>(a, a.p, table, tiles, cluster, clusters, split, splits, false,
+                                     stages + kPBytes + S::kQBytes, full, ready, 128 * half);
+  } else if (warp > S::kEpi + 2) {
+    const int block = warp - S::kEpi - 3;
+    turn_scales<CTAS, NT, SWAP, (NT < 128 ? NT : 128)>(a, a.q, table, tiles, cluster, clusters, split, splits, true,
+                                                       stages + kPBytes + S::kQBytes + kScaleBlock * (1 + block),
+                                                       full, ready, 128 * block);
   } else {
     const int quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    constexpr int kChunks = NT / 32, kStep = S::kEpi / 4;  // kStep warps share a quarter's chunks in turn
+    constexpr int kFreed = S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks;
+    float* const mine = bias_stage[warp];
     int e = 0, count = 0;
     for (int i = cluster; i < tiles; i += clusters, count++) {
       const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
       const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
+      const int r = 128 * half + 32 * quarter + lane;  // row of the tile
+      const bool live = r < x.p_rows;
+      const int64_t base = a.mode == kGemmWgrad ? (int64_t)x.e * a.M * a.N : 0;
+      const uint64_t alpha2 = f2_pack(alpha, alpha);
+      uint64_t bias2 = 0;
+      if (SWAP && a.bias != nullptr && live) {
+        const float b = bias_at(a, (int64_t)x.e * a.N + x.p0 + r);
+        bias2 = f2_pack(b, b);
+      }
       if (!wait_phase(&acc_full[count & 1], (uint32_t)(count >> 1) & 1u)) {
         if (lane == 0) atomicOr(a.status, kTimeout);
         break;
       }
       tc_fence_after();
       const uint32_t acc = tmem + lanes + (count & 1) * S::kAccStride;
-      const int r = 128 * half + 32 * quarter + lane;  // row of the tile
       uint32_t top = 0u;
-      const int64_t base = a.mode == kGemmWgrad ? (int64_t)x.e * a.M * a.N : 0;
-      constexpr int kChunks = NT / 32;
 #pragma unroll 1
-      for (int c = 0; c < kChunks; c++) {
+      for (int c = warp >> 2; c < kChunks; c += kStep) {
         // the columns that the other accumulator shares come first
         const int chunk = S::kAccStride < NT && (count & 1) == 0 ? (c + S::kAccStride / 32) % kChunks : c;
-        uint32_t v[32];
+        const int left = x.q_rows - 32 * chunk;  // columns (rows of q) that count
+        const int row = SWAP ? x.q0 + 32 * chunk : x.p0 + r, col = SWAP ? x.p0 + r : x.q0 + 32 * chunk;
+        const int64_t at = base + (int64_t)row * a.N + col, stride = SWAP ? a.N : 1;
+        const bool whole = !SWAP && a.wide != 0 && left >= 32;
+        const bool counts = live && left > 0 && !(SWAP && splits > 1);
+        uint32_t v[32], residual[32];
+        if (a.residual != nullptr && counts) load_residual(a, residual, at, stride, left, whole);
+        if (!SWAP && a.bias != nullptr) {
+          __syncwarp();
+          mine[lane] = lane < left ? bias_at(a, (int64_t)x.e * a.N + col + lane) : 0.0f;
+          __syncwarp();
+        }
         tmem_load32(acc + 32 * chunk, v);
         tmem_wait_load();
-        if (c == (S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks) - 1) {
+        if (c + kStep >= kFreed && c < kFreed) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -652,27 +705,39 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
 #pragma unroll
           for (int j = 0; j < 32; j++) v[j] = 0u;
         }
-        const int left = x.q_rows - 32 * chunk;  // columns (rows of q) that count
         if (SWAP && splits > 1) {
           // the sums of this share of K, for the cluster
           const uint32_t to = stages + ((32 * chunk) * 128 + r) * 4;
 #pragma unroll
           for (int j = 0; j < 32; j++)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 512), "r"(v[j]) : "memory");
-        } else if (r < x.p_rows && left > 0) {
-          float z[32];
-#pragma unroll
-          for (int j = 0; j < 32; j++) z[j] = __uint_as_float(v[j]);
-          const int row = SWAP ? x.q0 + 32 * chunk : x.p0 + r, col = SWAP ? x.p0 + r : x.q0 + 32 * chunk;
-          top = max(top, finish<32, SWAP>(a, z, alpha, base + (int64_t)row * a.N + col, SWAP ? a.N : 1,
-                                          (int64_t)x.e * a.N + col, left));
+          continue;
         }
+        Pairs z;
+#pragma unroll
+        for (int j = 0; j < 16; j++)
+          z[j] = f2_mul(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), alpha2);
+        if (a.bias != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            if (SWAP) {
+              z[j] = f2_add(z[j], bias2);
+              z[j + 1] = f2_add(z[j + 1], bias2);
+            } else {
+              const float4 b = reinterpret_cast<const float4*>(mine)[j / 2];
+              z[j] = f2_add(z[j], f2_pack(b.x, b.y));
+              z[j + 1] = f2_add(z[j + 1], f2_pack(b.z, b.w));
+            }
+          }
+        }
+        if (counts) top = max(top, finish(a, z, residual, at, stride, left, whole));
       }
       if (splits == 1) report_amax(a, top, x.e);
     }
     if (a.mode == kGemmGrouped && !table.bad) {
       const int64_t live = (int64_t)table.begin[a.E] * a.N, all = (int64_t)a.M * a.N;
-      const int64_t me = (int64_t)blockIdx.x * 128 + (threadIdx.x & 127), count = (int64_t)gridDim.x * 128;
+      const int64_t me = (int64_t)blockIdx.x * (32 * S::kEpi) + threadIdx.x;
+      const int64_t count = (int64_t)gridDim.x * (32 * S::kEpi);
       clear(a.out, live * a.out_bytes, all * a.out_bytes, me, count);
       if (a.preact) clear(a.preact, live * 2, all * 2, me, count);
     }
@@ -680,17 +745,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
   if (CTAS == 1 && splits > 1) {
     __syncwarp();
     cluster_sync();
-    if (warp >= 4 && cluster < tiles) {  // the host launches one tile a cluster: every CTA takes some rows of q
+    if (warp < S::kEpi && cluster < tiles) {  // the host launches one tile a cluster: every CTA takes some rows of q
       int e = 0;
       const Tile x = get_tile<CTAS, NT, SWAP>(a, table, cluster, e, split, splits);
       const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
       const int r = 32 * (warp & 3) + lane;
       uint32_t top = 0u;
       if (r < x.p_rows) {
+        const float bias = a.bias ? bias_at(a, x.p0 + r) : 0.0f;
         for (int c = split; c < min(NT, x.q_rows); c += splits) {
-          float v[1] = {0.0f};
-          for (int s = 0; s < splits; s++) v[0] += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
-          top = max(top, finish<1, true>(a, v, alpha, (int64_t)(x.q0 + c) * a.N + x.p0 + r, a.N, x.p0 + r, 1));
+          float v = 0.0f;
+          for (int s = 0; s < splits; s++) v += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
+          top = max(top, finish_one(a, v, alpha, bias, (int64_t)(x.q0 + c) * a.N + x.p0 + r));
         }
       }
       report_amax(a, top, x.e);
@@ -701,14 +767,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<CTAS, NT>::kPerSm))
   __syncthreads();
   __syncwarp();
   if (per > 1) cluster_sync();
-  if (warp == 1) tmem_free<CTAS>(tmem, S::kColumns);
+  if (warp == S::kEpi + 1) tmem_free<CTAS>(tmem, S::kColumns);
 }
 
 template <int CTAS, int NT, bool SWAP>
 cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Shape<CTAS, NT>::kThreads);
   cfg.dynamicSmemBytes = Shape<CTAS, NT>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -737,7 +803,6 @@ bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int
   const uintptr_t all = reinterpret_cast<uintptr_t>(o.scales) | (uintptr_t)(rows > 1 ? s.scale_pitch : 0) |
                         (uintptr_t)s.scale_batch;
   s.tma = all % 16 == 0;
-  s.words = all % 4 == 0;
   if (K == 0) {  // nothing is loaded
     s.tma = 0;
     return true;
