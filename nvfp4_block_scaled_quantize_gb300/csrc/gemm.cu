@@ -47,11 +47,13 @@ struct SideArgs {
 };
 struct TcArgs {
   SideArgs p, q;
+  CUtensorMap out_map, preact_map;  // boxes of 32 rows x 64 bytes; where `boxes` is set
   const float *a_gscale, *b_gscale;
   const int32_t* offsets;
   int32_t mode, E;
   int32_t M, N, K;   // of out, and the operands' columns
   int32_t activation, out_bytes, bias_bytes;
+  int32_t boxes;     // rows of out and preact start on 16-byte boundaries: they leave by TMA
   int32_t wide;      // rows of out, residual and preact allow: 2 = 32-byte, 1 = 16-byte, 0 = single accesses
   const void* bias;
   const void* residual;
@@ -61,7 +63,7 @@ struct TcArgs {
   uint32_t* status;
 };
 
-template <int CTAS, int NT>
+template <int CTAS, int NT, bool SWAP = CTAS == 1>
 struct Shape {
   static constexpr int kQRows = NT / CTAS;                       // rows of q that a CTA loads
   static constexpr int kQBlocks = (NT + 127) / 128;              // blocks of 128 rows of scales
@@ -76,7 +78,8 @@ struct Shape {
   static constexpr int kLag = NT == 256 ? 1 : 2;
   static constexpr int kScaleColumn = NT == 256 ? 448 : 2 * NT;
   static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
-  static constexpr int kSmem = kStages * kStage + 1024;
+  static constexpr int kOutBox = SWAP ? 0 : 32 * 64;  // a warp's staging of out
+  static constexpr int kSmem = kStages * kStage + 1024 + kOutBox * (CTAS == 2 ? 8 : 4);
   // warps: the epilogue (a multiple of four: a warp reads the lane quarter of its number), loads, matrix
   // instructions, scales of p, a block of 128 scales of q each
   static constexpr int kEpi = CTAS == 2 ? 8 : 4;
@@ -413,15 +416,46 @@ __device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint
     if (i < have) *to = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
 }
 
+// A warp's 32 rows x 64 bytes to a box of a map, a lane's row in w, through its staging buffer (rows of
+// 64 bytes in the 64-byte swizzle: the 16-byte stores of eight lanes meet eight different bank groups).
+// Stores straight from the lanes would touch 32 lines each, and the warps that turn scales would wait
+// behind them for their shared memory (2000 cycles a stage in place of 300).
+__device__ __forceinline__ void store_box(uint32_t buffer, const CUtensorMap* map, const uint32_t (&w)[16],
+                                          int32_t x, int32_t y, int32_t z) {
+  const uint32_t lane = threadIdx.x & 31;
+  if (elect_one()) bulk_wait_read();
+  __syncwarp();
+  const uint32_t row = buffer + lane * 64, turn = (lane >> 1) & 3u;
+#pragma unroll
+  for (uint32_t c = 0; c < 4; c++)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ turn) << 4)), "r"(w[4 * c]),
+                 "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+  fence_proxy_async();
+  __syncwarp();
+  if (elect_one()) {
+    tma_store_box(map, buffer, x, y, z);
+    bulk_commit();
+  }
+  __syncwarp();
+}
+// Where a warp's rows leave in boxes.
+struct BoxAt {
+  uint32_t buffer;  // 0: they do not
+  int32_t x, y, z;
+};
+
 // z = alpha * sums + bias through the activation and the residual into out: 32 elements from element
 // `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
 // aligned. Returns the largest |out| as binary32 bits.
+template <bool BOXES>
 __device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint32_t (&residual)[32], int64_t at,
-                                           int64_t stride, int have, bool whole) {
+                                           int64_t stride, int have, bool whole, bool live, const BoxAt& box) {
   uint32_t w[16];
   if (a.preact != nullptr) {
     pack_pairs(z, w);
-    store_pairs(a, a.preact, w, at, stride, have, whole);
+    if (BOXES && box.buffer) store_box(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
+    else if (live) store_pairs(a, a.preact, w, at, stride, have, whole);
   }
   activate_pairs(a.activation, z);
   if (a.out_bytes == 2) {
@@ -430,8 +464,9 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint
       for (int i = 0; i < 16; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
     }
     pack_pairs(z, w);
-    store_pairs(a, a.out, w, at, stride, have, whole);
-    if (a.amax == nullptr) return 0u;
+    if (BOXES && box.buffer) store_box(box.buffer, &a.out_map, w, box.x, box.y, box.z);
+    else if (live) store_pairs(a, a.out, w, at, stride, have, whole);
+    if (a.amax == nullptr || !live) return 0u;
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < 16; i++) {
@@ -455,7 +490,16 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint
     o[2 * i + 1] = __float_as_uint(f.y);
   }
   uint32_t* to = static_cast<uint32_t*>(a.out) + at;
-  if (whole) {
+  if (BOXES && box.buffer) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int i = 0; i < 16; i++) w[i] = o[16 * h + i];
+      store_box(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
+    }
+  } else if (!live) {
+    return 0u;
+  } else if (whole) {
 #pragma unroll
     for (int i = 0; i < 32; i += 8) store_words(to + i, a.wide, o + i);
   } else {
@@ -463,7 +507,7 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint
     for (int i = 0; i < 32; i++, to += stride)
       if (i < have) *to = o[i];
   }
-  if (a.amax != nullptr) {
+  if (a.amax != nullptr && live) {
 #pragma unroll
     for (int i = 0; i < 32; i++)
       if (i < have) top = max(top, o[i] & 0x7FFFFFFFu);
@@ -552,10 +596,18 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   if (per > 1) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  if (a.mode != kGemmDense) {
+    pdl_wait();
+    make_table<CTAS, NT, SWAP>(a, table);
+  }
+  const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
+  if (cluster < tiles) {  // brings the parameters that it reads into the constant cache before the wait
+    int e = 0;
+    const Tile x = get_tile<CTAS, NT, SWAP>(a, table, cluster, e, split, splits);
+    asm volatile("" ::"r"(x.p0), "r"(x.q0), "r"(x.kb0), "r"(x.kb1), "r"(a.p.tma), "r"(a.q.tma));
+  }
   pdl_wait();
   pdl_allow_next();
-  if (a.mode != kGemmDense) make_table<CTAS, NT, SWAP>(a, table);
-  const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
 
   if (warp == S::kEpi) {
     const uint32_t bytes = kPBytes + S::kQBytes + (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
@@ -654,6 +706,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     constexpr int kChunks = NT / 32, kStep = S::kEpi / 4;  // kStep warps share a quarter's chunks in turn
     constexpr int kFreed = S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks;
     float* const mine = bias_stage[warp];
+    const uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
     int e = 0, count = 0;
     for (int i = cluster; i < tiles; i += clusters, count++) {
       const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
@@ -683,6 +736,11 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
         const int64_t at = base + (int64_t)row * a.N + col, stride = SWAP ? a.N : 1;
         const bool whole = !SWAP && a.wide != 0 && left >= 32;
         const bool counts = live && left > 0 && !(SWAP && splits > 1);
+        // an expert's last rows are not stored in boxes, which end with the tensor alone
+        const int rows_left = x.p_rows - 128 * half - 32 * quarter;
+        const bool boxes = !SWAP && a.boxes != 0 && rows_left > 0 && left > 0 &&
+                           (a.mode != kGemmGrouped || rows_left >= 32);
+        const BoxAt box = {boxes ? staging : 0u, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
         uint32_t v[32], residual[32];
         if (a.residual != nullptr && counts) load_residual(a, residual, at, stride, left, whole);
         if (!SWAP && a.bias != nullptr) {
@@ -730,10 +788,12 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
             }
           }
         }
-        if (counts) top = max(top, finish(a, z, residual, at, stride, left, whole));
+        if (counts || boxes) top = max(top, finish<!SWAP>(a, z, residual, at, stride, left, whole, counts, box));
       }
       if (splits == 1) report_amax(a, top, x.e);
     }
+    if (!SWAP && elect_one()) bulk_wait_all();
+    __syncwarp();
     if (a.mode == kGemmGrouped && !table.bad) {
       const int64_t live = (int64_t)table.begin[a.E] * a.N, all = (int64_t)a.M * a.N;
       const int64_t me = (int64_t)blockIdx.x * (32 * S::kEpi) + threadIdx.x;
@@ -753,10 +813,18 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
       uint32_t top = 0u;
       if (r < x.p_rows) {
         const float bias = a.bias ? bias_at(a, x.p0 + r) : 0.0f;
-        for (int c = split; c < min(NT, x.q_rows); c += splits) {
-          float v = 0.0f;
-          for (int s = 0; s < splits; s++) v += cluster_load(cluster_address(stages + (c * 128 + r) * 4, s));
-          top = max(top, finish_one(a, v, alpha, bias, (int64_t)(x.q0 + c) * a.N + x.p0 + r));
+        constexpr int kTurn = 8;  // rows of q whose loads are under way together
+        for (int c = kTurn * split; c < min(NT, x.q_rows); c += kTurn * splits) {
+          float v[kTurn];
+#pragma unroll
+          for (int j = 0; j < kTurn; j++) v[j] = 0.0f;
+          for (int s = 0; s < splits; s++) {
+            const uint32_t from = cluster_address(stages + (c * 128 + r) * 4, s);
+#pragma unroll
+            for (int j = 0; j < kTurn; j++) v[j] += cluster_load(from + j * 512);
+          }
+          for (int j = 0; j < kTurn && c + j < x.q_rows; j++)
+            top = max(top, finish_one(a, v[j], alpha, bias, (int64_t)(x.q0 + c + j) * a.N + x.p0 + r));
         }
       }
       report_amax(a, top, x.e);
@@ -827,6 +895,20 @@ bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int
                           CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+bool make_out_maps(TcArgs& t, const GemmArgs& g) {
+  auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, void* p, int bytes) {
+    const cuuint64_t dims[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)(g.mode == kGemmWgrad ? g.E : 1)};
+    const cuuint64_t strides[2] = {(cuuint64_t)(g.N * bytes), (cuuint64_t)(g.M * g.N * bytes)};
+    const cuuint32_t box[3] = {(cuuint32_t)(64 / bytes), 32, 1}, one[3] = {1, 1, 1};
+    return encode_tiled()(map, type, 3, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  return encode(&t.out_map, g.out_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                g.out, g.out_bytes) &&
+         (g.preact == nullptr || encode(&t.preact_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g.preact, 2));
+}
+
 }  // namespace
 
 cudaError_t prepare_gemm_kernels() {
@@ -849,6 +931,7 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
                          reinterpret_cast<uintptr_t>(g.residual) |
                          (g.preact ? (uintptr_t)(g.N * 2) | reinterpret_cast<uintptr_t>(g.preact) : 0);
   t.wide = rows % 32 == 0 ? 2 : rows % 16 == 0 ? 1 : 0;
+  t.boxes = t.wide != 0;
   const int32_t b_experts = g.mode == kGemmGrouped ? g.E : 1;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   // rows of a that a tile is likely to find: all of them, or an expert's mean share
@@ -858,6 +941,7 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   if (rows_a > 128 && 2 * big >= sm_count / 2) {
     if (!make_side(t.p, g.a, g.M, g.K, 1, 128, 128) || !make_side(t.q, g.b, g.N, g.K, b_experts, 128, 256))
       return cudaErrorInvalidValue;
+    if (t.boxes && !make_out_maps(t, g)) return cudaErrorInvalidValue;
     const int64_t most = g.mode == kGemmDense ? big : sm_count / 2;
     return launch_one<2, 256, false>(t, (int)(2 * (most < sm_count / 2 ? most : sm_count / 2)), 1, s);
   }

@@ -41,7 +41,7 @@ __device__ __forceinline__ void cluster_arrive(uint32_t cluster_addr) {
 }
 __device__ __forceinline__ float cluster_load(uint32_t cluster_addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
   return v;
 }
 // Waits for phase `parity`, giving up after kWaitCycles of the SM's clock (about 2 s). The global timer,
@@ -61,6 +61,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tensor_map
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(tensor_map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Box at (x, y, z) from shared memory (a bulk group); what lies outside the tensor is not written.
+__device__ __forceinline__ void tma_store_box(const void* tensor_map, uint32_t from, int32_t x, int32_t y,
+                                              int32_t z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tensor_map),
+               "r"(from), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() {
