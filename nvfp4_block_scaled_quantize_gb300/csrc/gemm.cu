@@ -78,13 +78,14 @@ struct Shape {
   static constexpr int kLag = NT == 256 ? 1 : 2;
   static constexpr int kScaleColumn = NT == 256 ? 448 : 2 * NT;
   static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
+  static constexpr int kStageSlots = kBlockK / 64 * kSlot;
   static constexpr int kOutBox = SWAP ? 0 : 32 * 64;  // a warp's staging of out
   static constexpr int kSmem = kStages * kStage + 1024 + kOutBox * (CTAS == 2 ? 8 : 4);
   // warps: the epilogue (a multiple of four: a warp reads the lane quarter of its number), loads, matrix
   // instructions, scales of p, a block of 128 scales of q each
   static constexpr int kEpi = CTAS == 2 ? 8 : 4;
   static constexpr int kThreads = 32 * (kEpi + 3 + kQBlocks);
-  static_assert(kScaleColumn + 4 * kSlot <= kColumns, "tensor memory");
+  static_assert(kScaleColumn + kStageSlots <= kColumns, "tensor memory");
   static_assert(kStage % 1024 == 0, "swizzle atoms");
 };
 
@@ -227,18 +228,19 @@ __device__ __forceinline__ uint32_t byte_mask(int lo, int hi, int word) {
 }
 
 // Turns one block of 128 rows x 16 bytes at `addr` into four blocks of 512 bytes, one for each 64
-// elements of K. v[j] is row lane + 32 j.
-__device__ __forceinline__ void put_scales(uint32_t addr, const uint4 (&v)[4]) {
+// elements of K. vj is row lane + 32 j.
+__device__ __forceinline__ void put_scales(uint32_t addr, const uint4& v0, const uint4& v1, const uint4& v2,
+                                           const uint4& v3) {
   const int lane = threadIdx.x & 31;
   auto put = [&](int k, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr + k * 512 + lane * 16), "r"(x), "r"(y),
                  "r"(z), "r"(w)
                  : "memory");
   };
-  put(0, v[0].x, v[1].x, v[2].x, v[3].x);
-  put(1, v[0].y, v[1].y, v[2].y, v[3].y);
-  put(2, v[0].z, v[1].z, v[2].z, v[3].z);
-  put(3, v[0].w, v[1].w, v[2].w, v[3].w);
+  put(0, v0.x, v1.x, v2.x, v3.x);
+  put(1, v0.y, v1.y, v2.y, v3.y);
+  put(2, v0.z, v1.z, v2.z, v3.z);
+  put(3, v0.w, v1.w, v2.w, v3.w);
 }
 
 // A warp turns one block of scales of every stage: rows `row_shift`.. of the tile's rows of p or q, of
@@ -246,7 +248,7 @@ __device__ __forceinline__ void put_scales(uint32_t addr, const uint4 (&v)[4]) {
 template <int CTAS, int NT, bool SWAP, int ROWS>
 __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table, int tiles,
                                             int cluster, int clusters, int split, int splits, bool is_q,
-                                            uint32_t blocks, uint64_t* full, uint64_t* ready, int row_shift) {
+                                            uint32_t blocks, uint64_t* landed, uint64_t* ready, int row_shift) {
   using S = Shape<CTAS, NT>;
   const int lane = threadIdx.x & 31;
   int e = 0, it = 0;
@@ -275,7 +277,7 @@ __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, 
     }
     for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
       const int stage = it % S::kStages;
-      const uint32_t to = blocks + stage * S::kStage;
+      const uint32_t phase = (uint32_t)(it / S::kStages) & 1u, to = blocks + stage * S::kStage;
       const int first = x.k_lo / 16 - kb * 16, last = x.k_hi / 16 - kb * 16;
       uint4 v[4];
       if (!s.tma) {
@@ -288,10 +290,7 @@ __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, 
           at[j] += 16;
         }
       }
-      if (!wait_phase(&full[stage], (uint32_t)(it / S::kStages) & 1u)) {
-        if (lane == 0) atomicOr(a.status, kTimeout);
-        return;
-      }
+      bool there = wait_phase(&landed[stage], phase);
       if (s.tma) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -309,9 +308,13 @@ __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, 
           v[j].w &= byte_mask(first, last, 3);
         }
       }
-      put_scales(to, v);
+      put_scales(to, v[0], v[1], v[2], v[3]);
       fence_proxy_async();
-      __syncwarp();
+      there = __all_sync(0xFFFFFFFFu, there);
+      if (!there) {
+        if (lane == 0) atomicOr(a.status, kTimeout);
+        return;
+      }
       if (lane == 0) {
         if (CTAS == 2) cluster_arrive(cluster_address(smem_u32(&ready[stage]), 0));
         else mbar_arrive(&ready[stage]);
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     gemm_kernel(const __grid_constant__ TcArgs a, int splits) {
   using S = Shape<CTAS, NT>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t full[S::kStages], ready[S::kStages], empty[S::kStages], acc_full[2], acc_free[2];
+  __shared__ __align__(8) uint64_t full[S::kStages], landed[S::kStages], ready[S::kStages], empty[S::kStages], acc_full[2], acc_free[2];
   __shared__ uint32_t tmem_base;
   __shared__ __align__(16) float bias_stage[S::kEpi][32];
   __shared__ Table table;
@@ -576,6 +579,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; i++) {
       mbar_init(&full[i], 1);
+      mbar_init(&landed[i], 1);
       mbar_init(&ready[i], (1 + S::kQBlocks) * CTAS);
       mbar_init(&empty[i], 1);
     }
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   pdl_allow_next();
 
   if (warp == S::kEpi) {
-    const uint32_t bytes = kPBytes + S::kQBytes + (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
+    const uint32_t bytes = (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
     int e = 0, it = 0;
     bool alive = true;
     for (int i = cluster; i < tiles && alive; i += clusters) {
@@ -625,11 +629,15 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
         }
         const uint32_t to = stages + stage * S::kStage, sc = to + kPBytes + S::kQBytes;
         if (elect_one()) {
-          mbar_expect_tx(&full[stage], bytes);
-          tma_load_3d(to, &a.p.codes, kb * (kBlockK / 2), x.p0 + 128 * half, x.pz, &full[stage]);
-          tma_load_3d(to + kPBytes, &a.q.codes, kb * (kBlockK / 2), x.q0 + S::kQRows * half, x.qz, &full[stage]);
-          if (a.p.tma) tma_load_3d(sc, &a.p.scales, kb * 16, x.p0 + 128 * half, x.pz, &full[stage]);
-          if (a.q.tma) tma_load_3d(sc + kScaleBlock, &a.q.scales, kb * 16, x.q0, x.qz, &full[stage]);
+          // the scales first, so that they are turned while the codes are on their way
+          mbar_expect_tx(&landed[stage], bytes);
+          if (a.p.tma) tma_load_3d(sc, &a.p.scales, kb * 16, x.p0 + 128 * half, x.pz, &landed[stage]);
+          if (a.q.tma) tma_load_3d(sc + kScaleBlock, &a.q.scales, kb * 16, x.q0, x.qz, &landed[stage]);
+          // the codes of both CTAs of a pair complete the barrier of the one that multiplies them
+          if (half == 0) mbar_expect_tx(&full[stage], CTAS * (kPBytes + S::kQBytes));
+          const uint32_t bar = CTAS == 2 ? cluster_address(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
+          tma_load_3d_pair<CTAS>(to, &a.p.codes, kb * (kBlockK / 2), x.p0 + 128 * half, x.pz, bar);
+          tma_load_3d_pair<CTAS>(to + kPBytes, &a.q.codes, kb * (kBlockK / 2), x.q0 + S::kQRows * half, x.qz, bar);
         }
         __syncwarp();
       }
@@ -637,13 +645,13 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     // every load has landed and every arrival of the products has come before anything here ends
     for (int i = it > S::kStages ? it - S::kStages : 0; i < it; i++) {
       const int stage = i % S::kStages;
-      wait_phase(&full[stage], (uint32_t)(i / S::kStages) & 1u);
+      wait_phase(&landed[stage], (uint32_t)(i / S::kStages) & 1u);
+      if (half == 0) wait_phase(&full[stage], (uint32_t)(i / S::kStages) & 1u);
       if (alive) wait_phase(&empty[stage], (uint32_t)(i / S::kStages) & 1u);
     }
   } else if (warp == S::kEpi + 1) {
     if (half == 0) {
       constexpr uint32_t idesc = nvfp4_idesc(128 * CTAS, NT);
-      const uint32_t sf = tmem + S::kScaleColumn;
       int e = 0, it = 0, count = 0;
       bool alive = true;
       for (int i = cluster; i < tiles; i += clusters, count++) {
@@ -656,12 +664,14 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
         uint32_t accumulate = 0u;
         for (int kb = x.kb0; kb < x.kb1 && alive; kb++, it++) {
           const int stage = it % S::kStages;
-          alive = wait_phase(&ready[stage], (uint32_t)(it / S::kStages) & 1u);
+          alive = wait_phase(&ready[stage], (uint32_t)(it / S::kStages) & 1u) &&
+                  wait_phase(&full[stage], (uint32_t)(it / S::kStages) & 1u);
           alive = __all_sync(0xFFFFFFFFu, alive);
           if (!alive) break;
           tc_fence_after();
           const uint32_t at = stages + stage * S::kStage;
           const uint64_t pd = codes_descriptor(at), qd = codes_descriptor(at + kPBytes);
+          const uint32_t sf = tmem + S::kScaleColumn;
           const uint64_t sd = scales_descriptor(at + kPBytes + S::kQBytes);
           if (elect_one()) {
             // columns of other experts in these 256 have zero scales: whole stages are multiplied
@@ -694,12 +704,12 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     }
   } else if (warp == S::kEpi + 2) {
     turn_scales<CTAS, NT, SWAP, 128>(a, a.p, table, tiles, cluster, clusters, split, splits, false,
-                                     stages + kPBytes + S::kQBytes, full, ready, 128 * half);
+                                     stages + kPBytes + S::kQBytes, landed, ready, 128 * half);
   } else if (warp > S::kEpi + 2) {
     const int block = warp - S::kEpi - 3;
     turn_scales<CTAS, NT, SWAP, (NT < 128 ? NT : 128)>(a, a.q, table, tiles, cluster, clusters, split, splits, true,
                                                        stages + kPBytes + S::kQBytes + kScaleBlock * (1 + block),
-                                                       full, ready, 128 * block);
+                                                       landed, ready, 128 * block);
   } else {
     const int quarter = warp & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -953,7 +963,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   int64_t grid = (int64_t)sm_count * per_sm;
   if (g.mode == kGemmDense) {
     const int64_t tiles = up(g.N, 128) * up(g.M, nt);
-    while (splits < 8 && 2 * splits * tiles <= sm_count * per_sm && up(g.K, kBlockK) >= 4 * splits) splits *= 2;
+    while (splits < 8 && 2 * splits * tiles <= sm_count * per_sm && up(g.K, kBlockK) >= (nt == 32 ? 4 : 16) * splits)
+      splits *= 2;
     if (splits > 1 || tiles < grid) grid = tiles * splits;
   }
   return nt == 32 ? launch_one<1, 32, true>(t, (int)grid, splits, s)

@@ -63,6 +63,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tensor_map
       : "memory");
 }
 
+// The same completing on a barrier of either CTA of a pair (an address in the cluster).
+template <int CTAS>
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tensor_map, int32_t x, int32_t y,
+                                                 int32_t z, uint32_t bar) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tensor_map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tensor_map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 // Box at (x, y, z) from shared memory (a bulk group); what lies outside the tensor is not written.
 __device__ __forceinline__ void tma_store_box(const void* tensor_map, uint32_t from, int32_t x, int32_t y,
                                               int32_t z) {
