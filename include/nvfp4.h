@@ -568,8 +568,9 @@ nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, const void* prea
 nvfp4_status nvfp4_gemm_epilogue_backward_workspace(int64_t M, int64_t N, size_t* bytes);
 
 /* ---- AdamW over many tensors ------------------------------------------------------------------
- * One step for every tensor of a list in one launch for every 64 tensors, with the weight that the
- * quantizers take and its amax from the same pass. Per element, binary32 operations in this order:
+ * One step for every tensor of a list, in one launch for every 128 tensors, with the weight that the
+ * quantizers take and its amax from the same pass. Per element, binary32 operations in this order (the
+ * quotient is off by at most 2 units in the last place):
  *   g = grad * grad_scale;  m = m * beta1 + g * (1 - beta1);  v = v * beta2 + (g * g) * (1 - beta2)
  *   p = p * (1 - lr * weight_decay) - (m * (lr / (1 - beta1^step))) /
  *       (sqrt(v) * (1 - beta2^step)^-0.5 + eps)
@@ -596,7 +597,7 @@ typedef struct nvfp4_adamw_tensor {
 
 typedef struct nvfp4_adamw_config {
   double lr, beta1, beta2; /* 0 <= beta < 1 */
-  double eps;              /* > 0 */
+  double eps;              /* >= 2^-126 */
   int64_t step;            /* 1 for the first; below 2^31 */
   const int32_t* step_device; /* (device) int32 [1] or NULL: the step instead, read by the kernel, for
                                  captured calls; a value below 1 counts as 1 */

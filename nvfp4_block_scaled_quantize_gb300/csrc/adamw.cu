@@ -70,6 +70,18 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return d;
 }
 
+// The E4M3 code of t >= 0 (at most 448) rounded up with probability of the part above the code below, u =
+// random / 65536. For normal codes the sum of t's bits and the random bits, cut behind three bits of the
+// mantissa, is that code but for the exponent's bias: u is added in units of the code step, and a carry
+// moves to the next binade by itself.
+__device__ __forceinline__ uint32_t random_code(float t, uint32_t random) {
+  const uint32_t bits = __float_as_uint(t);
+  if (t >= 0x1p-6f) return min(((bits + (random << 4)) >> 20) - ((127 - 7) << 3), 0x7Fu);  // inf: NaN
+  if (!(t > 0.0f)) return t == 0.0f ? 0u : 0x7Fu;  // NaN stays
+  const float q = floorf(__fadd_rn(__fmul_rn(t, 512.0f), __fmul_rn((float)random, 1.0f / 65536.0f)));
+  return (uint32_t)fmaxf(q, 1.0f);  // subnormal codes, and 8, the first normal one
+}
+
 // Eight values of a buffer from element i, `have` of them inside (the rest zeros).
 template <typename T>
 __device__ __forceinline__ void load8(const void* p, int64_t i, int have, float (&v)[8]) {
@@ -160,13 +172,17 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   uint32_t top = 0u;
   auto report = [&]() {
     if (a.amax == nullptr) return;
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, top);
-    if ((threadIdx.x & 31) == 0 && m != 0u)
-      atomicMax(reinterpret_cast<uint32_t*>(a.amax) + a.base + at, m << 16);
+    const uint32_t abs = top & 0x7FFF7FFFu;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(abs << 16, abs & 0xFFFF0000u));
+    if ((threadIdx.x & 31) == 0 && m != 0u) atomicMax(reinterpret_cast<uint32_t*>(a.amax) + a.base + at, m);
   };
   for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    int now = at;
-    while (now + 1 < a.count && a.first[now + 1] <= chunk) now++;
+    int now = at, above = a.count;  // the last tensor whose first chunk is not above this one
+    while (now + 1 < above) {
+      const int mid = (now + above) / 2;
+      if (a.first[mid] <= chunk) now = mid;
+      else above = mid;
+    }
     if (now != at) {
       report();
       at = now;
@@ -190,28 +206,38 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       load8<float>(t.exp_avg_sq, i, have, v);
     }
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, t.weight_decay));
-    uint32_t w[8];
+    uint32_t w[4];
+    auto both = [](float v) { return f2_pack(v, v); };
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const float x = __fmul_rn(g[j], grad_scale);
-      m[j] = __fadd_rn(__fmul_rn(m[j], a.beta1), __fmul_rn(x, a.rest1));
-      v[j] = __fadd_rn(__fmul_rn(v[j], a.beta2), __fmul_rn(__fmul_rn(x, x), a.rest2));
-      root[j] = __fsqrt_rn(v[j]);
-      const float update = __fdiv_rn(__fmul_rn(m[j], step_size),
-                                     __fadd_rn(__fmul_rn(root[j], root_scale), a.eps));
-      p[j] = __fsub_rn(__fmul_rn(p[j], keep), update);
-      w[j] = __bfloat16_as_ushort(__float2bfloat16_rn(p[j]));
-      if (j < have) top = max(top, w[j] & 0x7FFFu);
+    for (int j = 0; j < 8; j += 2) {
+      // packed pairs: each operation rounds its halves as the scalar one does
+      const uint64_t x = f2_mul(f2_pack(g[j], g[j + 1]), both(grad_scale));
+      const uint64_t m2 = f2_add(f2_mul(f2_pack(m[j], m[j + 1]), both(a.beta1)), f2_mul(x, both(a.rest1)));
+      const uint64_t v2 = f2_add(f2_mul(f2_pack(v[j], v[j + 1]), both(a.beta2)),
+                                 f2_mul(f2_mul(x, x), both(a.rest2)));
+      const float2 mf = f2_unpack(m2), vf = f2_unpack(v2);
+      m[j] = mf.x, m[j + 1] = mf.y, v[j] = vf.x, v[j + 1] = vf.y;
+      root[j] = __fsqrt_rn(vf.x);
+      root[j + 1] = __fsqrt_rn(vf.y);
+      const float2 num = f2_unpack(f2_mul(m2, both(step_size)));
+      const float2 den = f2_unpack(f2_add(f2_mul(f2_pack(root[j], root[j + 1]), both(root_scale)), both(a.eps)));
+      const uint64_t update = f2_pack(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
+      const float2 pf = f2_unpack(f2_sub(f2_mul(f2_pack(p[j], p[j + 1]), both(keep)), update));
+      p[j] = pf.x, p[j + 1] = pf.y;
+      const __nv_bfloat162 b = __floats2bfloat162_rn(pf.x, pf.y);
+      w[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
+      // beyond the tensor's end everything is 0
+      top = hmax_abs2(top, w[j / 2]);
     }
     store8(t.param, i, have, p);
     if (t.weight != nullptr) {
       if (have == 8) {
         reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.weight) + i)[0] =
-            make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+            make_uint4(w[0], w[1], w[2], w[3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
-          if (j < have) static_cast<uint16_t*>(t.weight)[i + j] = (uint16_t)w[j];
+          if (j < have) static_cast<uint16_t*>(t.weight)[i + j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
       }
     }
     if constexpr (EIGHT) {
@@ -225,17 +251,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         mc[j] = to_e4m3x2(__fmul_rn(m[2 * j], mi), __fmul_rn(m[2 * j + 1], mi));
-        float q[2];
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-          const float x = __fmul_rn(root[2 * j + k], vi);
-          const int e = max((int)(__float_as_uint(x) >> 23) - 127, -6) - 3;  // of the code step
-          const float u = __fmul_rn((float)(k ? words[j] >> 16 : words[j] & 0xFFFFu), 1.0f / 65536.0f);
-          float n = floorf(__fadd_rn(__fmul_rn(x, __uint_as_float((uint32_t)(127 - e) << 23)), u));
-          if (x > 0.0f) n = fmaxf(n, 1.0f);
-          q[k] = __fmul_rn(n, __uint_as_float((uint32_t)(127 + e) << 23));
-        }
-        vc[j] = to_e4m3x2(q[0], q[1]);
+        vc[j] = random_code(__fmul_rn(root[2 * j], vi), words[j] & 0xFFFFu) |
+                random_code(__fmul_rn(root[2 * j + 1], vi), words[j] >> 16) << 8;
       }
       store_codes(t.exp_avg, i, have, make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16));
       store_codes(t.exp_avg_sq, i, have, make_uint2(vc[0] | vc[1] << 16, vc[2] | vc[3] << 16));
@@ -266,7 +283,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, in
       !(cfg->beta2 >= 0.0 && cfg->beta2 < 1.0) || !(cfg->eps > 0.0) || !std::isfinite(cfg->eps) ||
       (cfg->step_device == nullptr && (cfg->step < 1 || cfg->step > INT32_MAX)))
     return NVFP4_ERR_INVALID_ARG;
-  if ((float)cfg->eps == 0.0f) return NVFP4_ERR_INVALID_ARG;
+  if (!((float)cfg->eps >= 1.17549435e-38f)) return NVFP4_ERR_INVALID_ARG;  // a normal divisor
   if (!aligned(cfg->step_device, 4) || !aligned(cfg->grad_scale, 4) || !aligned(amax, 4))
     return NVFP4_ERR_ALIGN;
   const bool eight = cfg->state_bits == 8;

@@ -59,22 +59,30 @@ __device__ __forceinline__ uint64_t activate2(uint64_t z) {
   if constexpr (ACT == NVFP4_ACT_SILU) return f2_mul(z, logistic2(f2_mul(z, f2_pack(-kLog2e, -kLog2e))));
   return z;
 }
+// The derivative, of a packed pair. With p = 1 / (1 + exp(-x)) both GELU (x = 2 u) and SILU (x = z) are
+// z p, and theirs is p (1 + z (1 - p) x').
 template <int ACT>
-__device__ __forceinline__ float activation_slope(float z) {
-  if constexpr (ACT == NVFP4_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-  if constexpr (ACT == NVFP4_ACT_RELU2) return z < 0.0f ? 0.0f : 2.0f * z;
+__device__ __forceinline__ uint64_t activation_slope2(uint64_t z) {
+  constexpr float kLog2e = 1.4426950408889634f, k = -2.0f * kGeluC * kLog2e;
+  if constexpr (ACT == NVFP4_ACT_RELU || ACT == NVFP4_ACT_RELU2) {
+    const float2 f = f2_unpack(z);
+    if constexpr (ACT == NVFP4_ACT_RELU)
+      return f2_pack(f.x > 0.0f ? 1.0f : (f.x <= 0.0f ? 0.0f : f.x), f.y > 0.0f ? 1.0f : (f.y <= 0.0f ? 0.0f : f.y));
+    return f2_pack(f.x < 0.0f ? 0.0f : 2.0f * f.x, f.y < 0.0f ? 0.0f : 2.0f * f.y);
+  }
+  const uint64_t one = f2_pack(1.0f, 1.0f);
   if constexpr (ACT == NVFP4_ACT_GELU) {
-    // p = sigmoid(2u): p + z p (1 - p) 2 u'
-    const float q = kGeluA * z * z;
-    const float p = sigmoid(2.0f * kGeluC * z * (1.0f + q));
-    const float du = 2.0f * kGeluC * (1.0f + 3.0f * q);
-    return p * (1.0f + z * (1.0f - p) * du);
+    const uint64_t z2 = f2_mul(z, z);
+    const uint64_t p = logistic2(f2_mul(z, f2_fma(z2, f2_pack(k * kGeluA, k * kGeluA), f2_pack(k, k))));
+    const uint64_t x1 = f2_fma(z2, f2_pack(6.0f * kGeluC * kGeluA, 6.0f * kGeluC * kGeluA),
+                               f2_pack(2.0f * kGeluC, 2.0f * kGeluC));
+    return f2_fma(p, f2_mul(f2_mul(z, x1), f2_sub(one, p)), p);
   }
   if constexpr (ACT == NVFP4_ACT_SILU) {
-    const float p = sigmoid(z);
-    return p * (1.0f + z * (1.0f - p));
+    const uint64_t p = logistic2(f2_mul(z, f2_pack(-kLog2e, -kLog2e)));
+    return f2_fma(p, f2_mul(z, f2_sub(one, p)), p);
   }
-  return 1.0f;
+  return one;
 }
 
 }  // namespace nvfp4

@@ -74,7 +74,7 @@ __device__ __forceinline__ float sigmoid_over(float x, float c) {
   return __fdividef(__expf(x - c), 1.0f + __expf(x));
 }
 
-// One draw: the largest (value, lowest index) of the warp, in binary64.
+// The largest (value, lowest index) of the warp, in binary64; index kMaxE: none.
 struct Best {
   double v;
   int i;
@@ -88,96 +88,242 @@ __device__ __forceinline__ Best warp_best(Best b) {
   }
   return b;
 }
-
-// The row again with binary64 scores. `l`: this lane's logits. Lane k gets the k-th choice.
-template <int SL, int V, bool SOFTMAX>
-__device__ __noinline__ int draw_again(const RouterArgs& a, const float (&l)[SL], double* values) {
+// The largest of n values that is above -inf, taken out.
+__device__ __forceinline__ int draw(double* values, int n) {
   const int lane = threadIdx.x & 31;
-  double p[SL];
-  if (SOFTMAX) {
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < SL; j++) top = fmaxf(top, l[j]);
-    top = warp_max(top);
-    double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < SL; j++) sum += p[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)top);
-    sum = warp_sum(sum);
-#pragma unroll
-    for (int j = 0; j < SL; j++) p[j] = p[j] / sum;
-  } else {
-#pragma unroll
-    for (int j = 0; j < SL; j++) p[j] = 1.0 / (1.0 + exp(-(double)l[j]));
+  Best b = {-INFINITY, kMaxE};
+  for (int e = lane; e < n; e += 32)
+    if (values[e] > b.v) b = {values[e], e};
+  b = warp_best(b);
+  __syncwarp();
+  if (b.i < kMaxE && lane == 0) values[b.i] = -INFINITY;
+  __syncwarp();
+  return b.i;
+}
+
+// The row again with binary64 scores, in the warp's shared memory. Lane k gets the k-th choice.
+template <bool SOFTMAX, typename L>
+__device__ __noinline__ int draw_again(const RouterArgs& a, const L* row, double* values, double* ranks) {
+  const int lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int e = lane; e < a.E; e += 32) top = fmaxf(top, widen<L>(row[e]));
+  top = warp_max(top);
+  double sum = 0.0;
+  for (int e = lane; e < a.E; e += 32) {
+    const double l = (double)widen<L>(row[e]);
+    values[e] = SOFTMAX ? exp(l - (double)top) : 1.0 / (1.0 + exp(-l));
+    sum += values[e];
   }
-  uint32_t held = 0;  // bit j: candidate j may be drawn
-#pragma unroll
-  for (int j = 0; j < SL; j++) {
-    const int e = ((j / V) * 32 + lane) * V + j % V;
-    if (e < a.E) {
-      const bool masked = l[j] == -INFINITY || (a.bias && __ldg(a.bias + e) == -INFINITY);
-      if (a.bias) p[j] += (double)__ldg(a.bias + e);
-      if (masked) p[j] = -INFINITY;
-      else held |= 1u << j;
-      values[e] = p[j];
-    }
-    if (!a.bias) p[j] = (double)l[j];
+  if (SOFTMAX) sum = warp_sum(sum);
+  for (int e = lane; e < a.E; e += 32) {
+    if (SOFTMAX) values[e] /= sum;
+    if (a.bias) values[e] += (double)__ldg(a.bias + e);
+    if (widen<L>(row[e]) == -INFINITY) values[e] = -INFINITY;
   }
   __syncwarp();
+  uint32_t kept = 0;  // of groups lane, lane + 32, ...
   if (a.top_groups < a.groups) {
-    double rank[kMaxE / 32];
-    uint32_t kept = 0, open = 0;
-#pragma unroll
-    for (int j = 0; j < kMaxE / 32; j++) {
-      const int g = lane + 32 * j;
-      if (g >= a.groups) continue;
+    for (int g = lane; g < a.groups; g += 32) {
       double v1 = -INFINITY, v2 = -INFINITY;
-      for (int i = 0; i < a.size; i++) {
-        const double v = values[g * a.size + i];
+      for (int i = g * a.size; i < (g + 1) * a.size; i++) {
+        const double v = values[i];
         if (v > v1) v2 = v1, v1 = v;
         else if (v > v2) v2 = v;
       }
-      rank[j] = a.size > 1 ? v1 + v2 : v1;
-      open |= 1u << j;
+      // one that is masked counts below all others, and is kept where nothing else is left
+      ranks[g] = fmax(a.size > 1 ? v1 + v2 : v1, -1e300);
     }
+    __syncwarp();
     for (int n = 0; n < a.top_groups; n++) {
-      Best b = {0.0, kMaxE};
-#pragma unroll
-      for (int j = 0; j < kMaxE / 32; j++)
-        if (((open >> j) & 1u) && (b.i >= kMaxE || rank[j] > b.v)) b = {rank[j], lane + 32 * j};
-      b = warp_best(b);
-      if ((b.i & 31) == lane) {
-        open &= ~(1u << (b.i >> 5));
-        kept |= 1u << (b.i >> 5);
-      }
+      const int g = draw(ranks, a.groups);
+      if ((g & 31) == lane) kept |= 1u << (g >> 5);
     }
-#pragma unroll
-    for (int j = 0; j < SL; j++) {
-      const int e = ((j / V) * 32 + lane) * V + j % V, g = e < a.E ? e / a.size : 0;
-      const uint32_t k = __shfl_sync(kAll, kept, g & 31);
-      if (!((k >> (g >> 5)) & 1u)) held &= ~(1u << j);
-    }
+  } else {
+    kept = 0xFFu;
   }
-  int mine = -1;
-  for (int n = 0; n < a.K; n++) {
-    Best b = {0.0, kMaxE};
-#pragma unroll
-    for (int j = 0; j < SL; j++) {
-      const int e = ((j / V) * 32 + lane) * V + j % V;
-      if (((held >> j) & 1u) && (b.i >= kMaxE || p[j] > b.v)) b = {p[j], e};
+  for (int base = 0; base < a.E; base += 32) {
+    const int e = base + lane, g = e < a.E ? e / a.size : 0;
+    const uint32_t k = __shfl_sync(kAll, kept, g & 31);
+    if (e < a.E) {
+      if (!((k >> (g >> 5)) & 1u)) values[e] = -INFINITY;
+      else if (!a.bias) values[e] = (double)widen<L>(row[e]);
     }
-    b = warp_best(b);
-    if (b.i >= kMaxE) break;
-    if (lane == n) mine = b.i;
-    const int at = b.i / V;
-    if ((at & 31) == lane) held &= ~(1u << ((at >> 5) * V + b.i % V));
   }
   __syncwarp();
+  int mine = -1;
+  for (int n = 0; n < a.K; n++) {
+    const int e = draw(values, a.E);
+    if (e >= kMaxE) break;
+    if (lane == n) mine = e;
+  }
   return mine;
 }
 
+// The weights of the drawn experts: lane k has the k-th (mine >= 0) and its logit x.
+template <bool SOFTMAX>
+__device__ __forceinline__ void put_weights(const RouterArgs& a, bool renorm, int64_t t, int mine, float x,
+                                            float top, float inv) {
+  const int lane = threadIdx.x & 31;
+  float w = 0.0f;
+  if (renorm) {
+    const float high = warp_max(mine >= 0 ? x : -INFINITY);
+    if (mine >= 0) w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
+    const float sum = warp_sum(w);
+    w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
+  } else if (mine >= 0) {
+    w = SOFTMAX ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
+  }
+  if (lane < a.K) {
+    a.ids[t * a.K + lane] = mine;
+    a.weights[t * a.K + lane] = mine >= 0 ? w * a.scale : 0.0f;
+  }
+}
+
+// This lane's logits: V neighbours by one load, -inf beyond the row.
+template <int SL, int V, typename L>
+__device__ __forceinline__ void load_row(const L* row, int E, float (&l)[SL]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < SL; j += V) {
+    const int e = ((j / V) * 32 + lane) * V;
+    if constexpr (V == 1) {
+      l[j] = e < E ? widen<L>(row[e]) : -INFINITY;
+    } else {  // E is a multiple of V
+      constexpr int W = V * sizeof(L) / 4;
+      uint32_t w[W];
+      if (e < E) {
+        if constexpr (W == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + e);
+          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (W == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + e);
+          w[0] = v.x, w[1] = v.y;
+        } else {
+          w[0] = *reinterpret_cast<const uint32_t*>(row + e);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < W; i++) w[i] = sizeof(L) == 4 ? 0xFF800000u : 0xFF80FF80u;
+      }
+#pragma unroll
+      for (int i = 0; i < V; i++)
+        l[j + i] = sizeof(L) == 4 ? __uint_as_float(w[i % W])
+                                  : __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+  }
+}
+
+template <int SL, int V, typename L>
+__device__ __forceinline__ void store_row(L* row, int E, const float (&d)[SL]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < SL; j += V) {
+    const int e = ((j / V) * 32 + lane) * V;
+    if (e >= E) continue;
+    if constexpr (V == 1) {
+      if constexpr (sizeof(L) == 4) row[e] = d[j];
+      else row[e] = __float2bfloat16_rn(d[j]);
+    } else {
+      constexpr int W = V * sizeof(L) / 4;
+      uint32_t w[W];
+#pragma unroll
+      for (int i = 0; i < W; i++) {
+        if constexpr (sizeof(L) == 4) {
+          w[i] = __float_as_uint(d[j + i]);
+        } else {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(d[j + (2 * i) % V], d[j + (2 * i + 1) % V]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+      }
+      if constexpr (W == 4) *reinterpret_cast<uint4*>(row + e) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (W == 2) *reinterpret_cast<uint2*>(row + e) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(row + e) = w[0];
+    }
+  }
+}
+
+// Without bias and groups the order is that of the logits. BF16 logits leave room for the index in the
+// key: one reduction a draw.
 template <int SL, int V, bool SOFTMAX, typename L>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterArgs a, bool renorm) {
-  __shared__ double values[kRouterWarps][kMaxE];
+__global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const RouterArgs a, bool renorm) {
+  constexpr bool kShort = sizeof(L) == 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_allow_next();
+  const int64_t step = (int64_t)gridDim.x * kRouterWarps;
+  const L* const logits = static_cast<const L*>(a.logits);
+  int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp;
+  float next[SL];
+  if (t < a.T) load_row<SL, V, L>(logits + t * a.E, a.E, next);
+  for (; t < a.T; t += step) {
+    float l[SL];
+    uint32_t key[SL];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      l[j] = next[j];
+      bad |= !(l[j] < INFINITY);
+      const uint32_t e = ((j / V) * 32 + lane) * V + j % V;
+      key[j] = kShort ? (ascending(l[j]) & 0xFFFF0000u) | (0xFFFFu - e) : ascending(l[j]);
+      if (l[j] == -INFINITY) key[j] = 0u;
+    }
+    if (t + step < a.T) load_row<SL, V, L>(logits + (t + step) * a.E, a.E, next);
+    bad = __any_sync(kAll, bad);
+    float top = 0.0f, inv = 0.0f;
+    if (SOFTMAX && !renorm) {
+      top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < SL; j++) top = fmaxf(top, l[j]);
+      top = warp_max(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
+      sum = warp_sum(sum);
+      inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+    }
+    int mine = -1;
+    uint32_t kept = 0u;  // the key of this lane's choice
+    if (!bad) {
+      for (int n = 0; n < a.K; n++) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < SL; j++) m = max(m, key[j]);
+        const uint32_t best = __reduce_max_sync(kAll, m);
+        if (best == 0u) break;
+        if (kShort) {
+          if (lane == n) kept = best;
+#pragma unroll
+          for (int j = 0; j < SL; j++)
+            if (key[j] == best) key[j] = 0u;
+        } else {
+          uint32_t e = kMaxE;
+#pragma unroll
+          for (int j = SL - 1; j >= 0; j--)
+            if (key[j] == best) e = ((j / V) * 32 + lane) * V + j % V;
+          e = __reduce_min_sync(kAll, e);
+          if (lane == n) kept = best, mine = (int)e;
+#pragma unroll
+          for (int j = 0; j < SL; j++)
+            if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
+        }
+      }
+    } else if (lane == 0) {
+      atomicOr(a.status, kBadRoute);
+    }
+    float x = 0.0f;
+    if (kept != 0u) {
+      if (kShort) mine = 0xFFFF - (int)(kept & 0xFFFFu);
+      // (of a negative number the cut-off half of an ascending key is all ones)
+      x = from_ascending(kShort ? ((int32_t)kept < 0 ? kept & 0xFFFF0000u : kept | 0xFFFFu) : kept);
+    }
+    put_weights<SOFTMAX>(a, renorm, t, mine, x, top, inv);
+  }
+}
+
+// With a bias or groups.
+template <int SL, int V, bool SOFTMAX, typename L>
+__global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const RouterArgs a, bool renorm) {
+  __shared__ double values[kRouterWarps][kMaxE], ranks[kRouterWarps][kMaxE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_allow_next();
@@ -187,20 +333,18 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
     float l[SL];
     uint32_t key[SL];
     const L* const row = logits + t * a.E;
-    float top = -INFINITY;
+    load_row<SL, V, L>(row, a.E, l);
     bool bad = false;
+    float top = -INFINITY, inv = 1.0f;
 #pragma unroll
     for (int j = 0; j < SL; j++) {
-      const int e = ((j / V) * 32 + lane) * V + j % V;
-      l[j] = e < a.E ? widen<L>(row[e]) : -INFINITY;
       bad |= !(l[j] < INFINITY);
       top = fmaxf(top, l[j]);
     }
     top = warp_max(top);
-    // the error of p grows with the largest p of the row (tie)
-    float tie = 2e-6f, inv = 1.0f;
-    const bool scored = a.bias != nullptr || a.top_groups < a.groups || (SOFTMAX && !renorm);
-    if (SOFTMAX && scored) {
+    // the error of p grows with the largest p of the row
+    float tie = 2e-6f;
+    if (SOFTMAX) {
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
@@ -214,18 +358,16 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
       const int e = ((j / V) * 32 + lane) * V + j % V;
       key[j] = 0u;
       if (e >= a.E) continue;
-      float c = l[j];
-      if (scored) {
-        float p = SOFTMAX ? (l[j] == -INFINITY ? 0.0f : __expf(l[j] - top) * inv)
-                          : __fdividef(1.0f, 1.0f + __expf(-l[j]));
-        if (a.bias) {
-          const float b = __ldg(a.bias + e);
-          p += b;
-          bad |= !(p < INFINITY) || !(b < INFINITY);
-          c = l[j] == -INFINITY ? -INFINITY : p;
-        }
-        choice[e] = l[j] == -INFINITY ? -INFINITY : p;
+      float p = 0.0f;  // masked (top may be -inf, too)
+      if (l[j] != -INFINITY) p = SOFTMAX ? __expf(l[j] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-l[j]));
+      if (a.bias) {
+        const float b = __ldg(a.bias + e);
+        p += b;
+        bad |= !(p < INFINITY) || !(b < INFINITY);
       }
+      if (l[j] == -INFINITY) p = -INFINITY;
+      const float c = a.bias ? p : l[j];
+      choice[e] = p;
       if (c != -INFINITY) key[j] = ascending(c);
     }
     bad = __any_sync(kAll, bad);
@@ -249,7 +391,6 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
         }
         rank[j] = ascending(a.size > 1 ? v1 + v2 : v1);
       }
-      __syncwarp();
       uint32_t last = 0u;
       for (int n = 0; n <= a.top_groups; n++) {  // the first that is dropped too
         uint32_t m = 0u;
@@ -315,24 +456,14 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const RouterA
             if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
         }
       }
-      if (close) mine = draw_again<SL, V, SOFTMAX>(a, l, values[warp]);
+      __syncwarp();
+      if (close) mine = draw_again<SOFTMAX, L>(a, row, values[warp], ranks[warp]);
     } else if (lane == 0) {
       atomicOr(a.status, kBadRoute);
     }
-    const float x = mine >= 0 ? widen<L>(row[mine]) : -INFINITY;
-    float w = 0.0f;
-    if (renorm) {
-      const float high = warp_max(x);
-      if (mine >= 0) w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
-      const float sum = warp_sum(w);
-      w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
-    } else if (mine >= 0) {
-      w = SOFTMAX ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
-    }
-    if (lane < a.K) {
-      a.ids[t * a.K + lane] = mine;
-      a.weights[t * a.K + lane] = mine >= 0 ? w * a.scale : 0.0f;
-    }
+    const float x = mine >= 0 ? widen<L>(row[mine]) : 0.0f;
+    put_weights<SOFTMAX>(a, renorm, t, mine, x, top, inv);
+    __syncwarp();
   }
 }
 
@@ -394,12 +525,9 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
       if (id >= 0) mine = p * __fdividef(1.0f, 1.0f + __expf(x)) * g;
     } else {
       float l[SL], top = -INFINITY, sum = 0.0f;
+      load_row<SL, V, L>(row, a.E, l);
 #pragma unroll
-      for (int j = 0; j < SL; j++) {
-        const int e = ((j / V) * 32 + lane) * V + j % V;
-        l[j] = e < a.E ? widen<L>(row[e]) : -INFINITY;
-        top = fmaxf(top, l[j]);
-      }
+      for (int j = 0; j < SL; j++) top = fmaxf(top, l[j]);
       top = warp_max(top);
 #pragma unroll
       for (int j = 0; j < SL; j++) sum += l[j] = l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
@@ -420,20 +548,34 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
       for (int j = 0; j < SL; j++)
         if (e == ((j / V) * 32 + lane) * V + j % V) d[j] += v;
     }
-#pragma unroll
-    for (int j = 0; j < SL; j++) {
-      const int e = ((j / V) * 32 + lane) * V + j % V;
-      if (e < a.E) {
-        if constexpr (sizeof(L) == 4) out[e] = d[j];
-        else out[e] = __float2bfloat16_rn(d[j]);
-      }
-    }
+    store_row<SL, V, L>(out, a.E, d);
   }
 }
 
 int router_grid(int64_t T, int sms) {
   const int64_t need = (T + kRouterWarps - 1) / kRouterWarps;
   return (int)(need < 8 * sms ? need : 8 * sms);
+}
+
+// Calls run(SL, V) as compile-time numbers: a lane has up to SL logits, V neighbours by one access where
+// rows allow it (8 bytes of them at least).
+template <int N>
+struct Number {
+  static constexpr int value = N;
+};
+template <typename L, typename F>
+cudaError_t by_width(int32_t E, uintptr_t at, F run) {
+  constexpr int kWide = 16 / sizeof(L);  // 4 or 8
+  if (E <= 64) {
+    if ((at | (uintptr_t)E * sizeof(L)) % (2 * sizeof(L)) == 0) return run(Number<2>(), Number<2>());
+    return run(Number<2>(), Number<1>());
+  }
+  if (E <= 128) {
+    if ((at | (uintptr_t)E * sizeof(L)) % (4 * sizeof(L)) == 0) return run(Number<4>(), Number<4>());
+    return run(Number<4>(), Number<1>());
+  }
+  if ((at | (uintptr_t)E * sizeof(L)) % (kWide * sizeof(L)) == 0) return run(Number<8>(), Number<kWide>());
+  return run(Number<8>(), Number<1>());
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -482,18 +624,19 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_byt
   const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool soft = score == NVFP4_SCORE_SOFTMAX, renorm = renormalize != 0;
-  auto run = [&](auto soft_kernel, auto sig_kernel) {
-    return launch_pdl(soft ? soft_kernel : sig_kernel, grid, block, 0, s, a, renorm);
+  const bool plain = bias == nullptr && top_groups == groups;
+  auto launch = [&](auto type) {
+    using L = decltype(type);
+    return by_width<L>(E, reinterpret_cast<uintptr_t>(logits), [&](auto sl, auto v) {
+      constexpr int SL = decltype(sl)::value, V = decltype(v)::value;
+      if (plain)
+        return launch_pdl(soft ? router_plain_kernel<SL, V, true, L> : router_plain_kernel<SL, V, false, L>, grid,
+                          block, 0, s, a, renorm);
+      return launch_pdl(soft ? router_kernel<SL, V, true, L> : router_kernel<SL, V, false, L>, grid, block, 0, s,
+                        a, renorm);
+    });
   };
-  cudaError_t e;
-  if (logit_bytes == 4)
-    e = E <= 64 ? run(router_kernel<2, 1, true, float>, router_kernel<2, 1, false, float>)
-                : run(router_kernel<8, 1, true, float>, router_kernel<8, 1, false, float>);
-  else
-    e = E <= 64
-            ? run(router_kernel<2, 1, true, __nv_bfloat16>, router_kernel<2, 1, false, __nv_bfloat16>)
-            : run(router_kernel<8, 1, true, __nv_bfloat16>, router_kernel<8, 1, false, __nv_bfloat16>);
-  return cuda_status(e);
+  return cuda_status(logit_bytes == 4 ? launch(float()) : launch(__nv_bfloat16()));
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, const void* logits,
@@ -516,12 +659,15 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, c
   const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool soft = score == NVFP4_SCORE_SOFTMAX, renorm = renormalize != 0;
-  auto run = [&](auto soft_kernel, auto sig_kernel) {
-    return launch_pdl(soft ? soft_kernel : sig_kernel, grid, block, 0, s, a, renorm);
+  auto launch = [&](auto type) {
+    using L = decltype(type);
+    return by_width<L>(E, reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(grad_logits),
+                       [&](auto sl, auto v) {
+                         constexpr int SL = decltype(sl)::value, V = decltype(v)::value;
+                         return launch_pdl(soft ? router_backward_kernel<SL, V, true, L>
+                                                : router_backward_kernel<SL, V, false, L>,
+                                           grid, block, 0, s, a, renorm);
+                       });
   };
-  return cuda_status(
-      logit_bytes == 4
-          ? run(router_backward_kernel<8, 1, true, float>, router_backward_kernel<8, 1, false, float>)
-          : run(router_backward_kernel<8, 1, true, __nv_bfloat16>,
-                router_backward_kernel<8, 1, false, __nv_bfloat16>));
+  return cuda_status(logit_bytes == 4 ? launch(float()) : launch(__nv_bfloat16()));
 }
