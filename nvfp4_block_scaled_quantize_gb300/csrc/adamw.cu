@@ -57,12 +57,11 @@ __device__ __forceinline__ float scale_value(uint32_t s) {  // 2^(s - 127)
 __device__ __forceinline__ float scale_inverse(uint32_t s) {  // 2^(127 - s), s <= 247
   return __uint_as_float((254u - s) << 23);
 }
-__device__ __forceinline__ void from_e4m3x2(uint32_t pair, float& lo, float& hi) {
+__device__ __forceinline__ uint64_t from_e4m3x2(uint32_t pair) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  lo = f.x;
-  hi = f.y;
+  return f2_pack(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t d;
@@ -82,33 +81,7 @@ __device__ __forceinline__ uint32_t random_code(float t, uint32_t random) {
   return (uint32_t)fmaxf(q, 1.0f);  // subnormal codes, and 8, the first normal one
 }
 
-// Eight values of a buffer from element i, `have` of them inside (the rest zeros).
-template <typename T>
-__device__ __forceinline__ void load8(const void* p, int64_t i, int have, float (&v)[8]) {
-  const T* const q = static_cast<const T*>(p) + i;
-  if constexpr (sizeof(T) == 4) {
-    if (have == 8) {
-      const float4 a = reinterpret_cast<const float4*>(q)[0], b = reinterpret_cast<const float4*>(q)[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = j < have ? q[j] : 0.0f;
-  } else {
-    if (have == 8) {
-      const uint4 a = *reinterpret_cast<const uint4*>(q);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = j < have ? __bfloat162float(q[j]) : 0.0f;
-  }
-}
+// Eight values, `have` of them inside the buffer.
 __device__ __forceinline__ void store8(float* p, int64_t i, int have, const float (&v)[8]) {
   if (have == 8) {
     reinterpret_cast<float4*>(p + i)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -118,15 +91,6 @@ __device__ __forceinline__ void store8(float* p, int64_t i, int have, const floa
 #pragma unroll
   for (int j = 0; j < 8; j++)
     if (j < have) p[i + j] = v[j];
-}
-__device__ __forceinline__ uint2 load_codes(const void* p, int64_t i, int have) {
-  const uint8_t* const q = static_cast<const uint8_t*>(p) + i;
-  if (have == 8) return *reinterpret_cast<const uint2*>(q);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 8; j++)
-    if (j < have) w[j / 4] |= (uint32_t)q[j] << (8 * (j % 4));
-  return make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ void store_codes(void* p, int64_t i, int have, uint2 c) {
   uint8_t* const q = static_cast<uint8_t*>(p) + i;
@@ -139,15 +103,6 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int have, uint2 
   for (int j = 0; j < 8; j++)
     if (j < have) q[j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
 }
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&v)[8]) {
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    from_e4m3x2((w[j / 2] >> (16 * (j % 2))) & 0xFFFFu, v[2 * j], v[2 * j + 1]);
-    v[2 * j] = __fmul_rn(v[2 * j], scale);
-    v[2 * j + 1] = __fmul_rn(v[2 * j + 1], scale);
-  }
-}
 __device__ __forceinline__ float block_max(const float (&v)[8]) {
   float m = 0.0f;
 #pragma unroll
@@ -156,8 +111,74 @@ __device__ __forceinline__ float block_max(const float (&v)[8]) {
   return fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
 }
 
+// What a thread reads of its eight elements, as it is stored.
 template <bool EIGHT, typename G>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamwArgs a) {
+struct Raw {
+  float p[8];
+  uint32_t g[sizeof(G) * 2];
+  uint32_t m[EIGHT ? 2 : 8], v[EIGHT ? 2 : 8];
+  uint32_t ms, vs;
+};
+template <int W>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[W]) {
+  if constexpr (W == 2) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = static_cast<const uint4*>(p)[i / 4];
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  }
+}
+// The first `have` of eight elements of W / 2 bytes, zeros behind them.
+template <int W>
+__device__ __forceinline__ void load_some(const void* p, int have, uint32_t (&w)[W]) {
+  constexpr int kBytes = W / 2;
+#pragma unroll
+  for (int i = 0; i < W; i++) w[i] = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    if (j >= have) break;
+    if constexpr (kBytes == 4) w[j] = static_cast<const uint32_t*>(p)[j];
+    else if constexpr (kBytes == 2) w[j / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[j] << (16 * (j % 2));
+    else w[j / 4] |= (uint32_t)static_cast<const uint8_t*>(p)[j] << (8 * (j % 4));
+  }
+}
+template <bool EIGHT, typename G>
+__device__ __forceinline__ Raw<EIGHT, G> load_raw(const nvfp4_adamw_tensor& t, int64_t i, int have) {
+  Raw<EIGHT, G> r;
+  const void* const g = static_cast<const G*>(t.grad) + i;
+  const int64_t at = EIGHT ? i : 4 * i;
+  const void* const m = static_cast<const uint8_t*>(t.exp_avg) + at;
+  const void* const v = static_cast<const uint8_t*>(t.exp_avg_sq) + at;
+  uint32_t p[8];
+  if (have == 8) {
+    load_words(t.param + i, p);
+    load_words(g, r.g);
+    load_words(m, r.m);
+    load_words(v, r.v);
+  } else {
+    load_some(t.param + i, have, p);
+    load_some(g, have, r.g);
+    load_some(m, have, r.m);
+    load_some(v, have, r.v);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j++) r.p[j] = __uint_as_float(p[j]);
+  r.ms = r.vs = 0u;
+  if (EIGHT && have > 0) {
+    r.ms = t.exp_avg_scales[i >> 5];
+    r.vs = t.exp_avg_sq_scales[i >> 5];
+  }
+  return r;
+}
+
+// The next chunk's reads are under way while a chunk is computed: without that the kernel alternates
+// between waiting and computing (8 bits, 203 M elements: 702 us).
+template <bool EIGHT, typename G>
+__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamwArgs a) {
   pdl_wait();
   pdl_allow_next();
   float step_size = a.step_size, root_scale = a.root_scale;
@@ -168,85 +189,96 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     root_scale = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)step * a.log_beta2)));
   }
   const float grad_scale = a.grad_scale ? *a.grad_scale : 1.0f;
-  int at = 0;  // the chunk's tensor
+  auto both = [](float v) { return f2_pack(v, v); };
+  // the chunk's tensor: `at` or one behind it
+  auto find = [&](int at, int64_t chunk) {
+    if (at + 1 >= a.count || chunk < a.first[at + 1]) return at;
+    int above = a.count;
+    while (at + 1 < above) {
+      const int mid = (at + above) / 2;
+      if (a.first[mid] <= chunk) at = mid;
+      else above = mid;
+    }
+    return at;
+  };
+  auto place = [&](int at, int64_t chunk) { return (chunk - a.first[at]) * kChunk + threadIdx.x * 8; };
+  auto inside = [&](int at, int64_t i) { return (int)max((int64_t)0, min((int64_t)8, a.t[at].n - i)); };
   uint32_t top = 0u;
-  auto report = [&]() {
+  auto report = [&](int at) {
     if (a.amax == nullptr) return;
     const uint32_t abs = top & 0x7FFF7FFFu;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(abs << 16, abs & 0xFFFF0000u));
     if ((threadIdx.x & 31) == 0 && m != 0u) atomicMax(reinterpret_cast<uint32_t*>(a.amax) + a.base + at, m);
+    top = 0u;
   };
-  for (int64_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
-    int now = at, above = a.count;  // the last tensor whose first chunk is not above this one
-    while (now + 1 < above) {
-      const int mid = (now + above) / 2;
-      if (a.first[mid] <= chunk) now = mid;
-      else above = mid;
-    }
-    if (now != at) {
-      report();
-      at = now;
-      top = 0u;
-    }
+  int64_t chunk = blockIdx.x;
+  int at = find(0, chunk);
+  int64_t i = place(at, chunk);
+  int have = inside(at, i);
+  Raw<EIGHT, G> r = load_raw<EIGHT, G>(a.t[at], i, have);
+  while (true) {
     const nvfp4_adamw_tensor& t = a.t[at];
-    const int64_t i = (chunk - a.first[at]) * kChunk + threadIdx.x * 8;
-    const int have = (int)max((int64_t)0, min((int64_t)8, t.n - i));
-    float p[8], g[8], m[8], v[8], root[8];
-    load8<float>(t.param, i, have, p);
-    load8<G>(t.grad, i, have, g);
-    if constexpr (EIGHT) {
-      const int64_t b = i >> 5;
-      const uint32_t ms = have > 0 ? t.exp_avg_scales[b] : 0u, vs = have > 0 ? t.exp_avg_sq_scales[b] : 0u;
-      decode8(load_codes(t.exp_avg, i, have), scale_value(ms), m);
-      decode8(load_codes(t.exp_avg_sq, i, have), scale_value(vs), v);
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[j] = __fmul_rn(v[j], v[j]);
-    } else {
-      load8<float>(t.exp_avg, i, have, m);
-      load8<float>(t.exp_avg_sq, i, have, v);
-    }
-    const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, t.weight_decay));
+    const int64_t next = chunk + gridDim.x;
+    const bool more = next < a.chunks;
+    const int next_at = more ? find(at, next) : at;
+    const int64_t next_i = more ? place(next_at, next) : 0;
+    const int next_have = more ? inside(next_at, next_i) : 0;
+    Raw<EIGHT, G> ahead;
+    if (more) ahead = load_raw<EIGHT, G>(a.t[next_at], next_i, next_have);
+
+    const uint64_t keep = both(__fsub_rn(1.0f, __fmul_rn(a.lr, t.weight_decay)));
     uint32_t w[4];
-    auto both = [](float v) { return f2_pack(v, v); };
+    float m[8], root[8];
+    const float m_scale = scale_value(r.ms), v_scale = scale_value(r.vs);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
+    for (int j = 0; j < 4; j++) {
       // packed pairs: each operation rounds its halves as the scalar one does
-      const uint64_t x = f2_mul(f2_pack(g[j], g[j + 1]), both(grad_scale));
-      const uint64_t m2 = f2_add(f2_mul(f2_pack(m[j], m[j + 1]), both(a.beta1)), f2_mul(x, both(a.rest1)));
-      const uint64_t v2 = f2_add(f2_mul(f2_pack(v[j], v[j + 1]), both(a.beta2)),
-                                 f2_mul(f2_mul(x, x), both(a.rest2)));
+      uint64_t g, m2, v2;
+      if constexpr (sizeof(G) == 4) g = f2_pack(__uint_as_float(r.g[2 * j]), __uint_as_float(r.g[2 * j + 1]));
+      else g = f2_from_bf16x2(r.g[j]);
+      if constexpr (EIGHT) {
+        m2 = f2_mul(from_e4m3x2((r.m[j / 2] >> (16 * (j % 2))) & 0xFFFFu), both(m_scale));
+        v2 = f2_mul(from_e4m3x2((r.v[j / 2] >> (16 * (j % 2))) & 0xFFFFu), both(v_scale));
+        v2 = f2_mul(v2, v2);
+      } else {
+        m2 = f2_pack(__uint_as_float(r.m[2 * j]), __uint_as_float(r.m[2 * j + 1]));
+        v2 = f2_pack(__uint_as_float(r.v[2 * j]), __uint_as_float(r.v[2 * j + 1]));
+      }
+      const uint64_t x = f2_mul(g, both(grad_scale));
+      m2 = f2_add(f2_mul(m2, both(a.beta1)), f2_mul(x, both(a.rest1)));
+      v2 = f2_add(f2_mul(v2, both(a.beta2)), f2_mul(f2_mul(x, x), both(a.rest2)));
       const float2 mf = f2_unpack(m2), vf = f2_unpack(v2);
-      m[j] = mf.x, m[j + 1] = mf.y, v[j] = vf.x, v[j + 1] = vf.y;
-      root[j] = __fsqrt_rn(vf.x);
-      root[j + 1] = __fsqrt_rn(vf.y);
+      m[2 * j] = mf.x, m[2 * j + 1] = mf.y;
+      root[2 * j] = __fsqrt_rn(vf.x);
+      root[2 * j + 1] = __fsqrt_rn(vf.y);
       const float2 num = f2_unpack(f2_mul(m2, both(step_size)));
-      const float2 den = f2_unpack(f2_add(f2_mul(f2_pack(root[j], root[j + 1]), both(root_scale)), both(a.eps)));
+      const float2 den = f2_unpack(f2_add(f2_mul(f2_pack(root[2 * j], root[2 * j + 1]), both(root_scale)), both(a.eps)));
       const uint64_t update = f2_pack(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
-      const float2 pf = f2_unpack(f2_sub(f2_mul(f2_pack(p[j], p[j + 1]), both(keep)), update));
-      p[j] = pf.x, p[j + 1] = pf.y;
+      const float2 pf = f2_unpack(f2_sub(f2_mul(f2_pack(r.p[2 * j], r.p[2 * j + 1]), keep), update));
+      r.p[2 * j] = pf.x, r.p[2 * j + 1] = pf.y;
+      if constexpr (!EIGHT) r.v[2 * j] = __float_as_uint(vf.x), r.v[2 * j + 1] = __float_as_uint(vf.y);
       const __nv_bfloat162 b = __floats2bfloat162_rn(pf.x, pf.y);
-      w[j / 2] = *reinterpret_cast<const uint32_t*>(&b);
-      // beyond the tensor's end everything is 0
-      top = hmax_abs2(top, w[j / 2]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      top = hmax_abs2(top, w[j]);  // behind the tensor's end everything is 0
     }
-    store8(t.param, i, have, p);
+    store8(t.param, i, have, r.p);
     if (t.weight != nullptr) {
+      uint16_t* const to = static_cast<uint16_t*>(t.weight) + i;
       if (have == 8) {
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(t.weight) + i)[0] =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
-          if (j < have) static_cast<uint16_t*>(t.weight)[i + j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
+          if (j < have) to[j] = (uint16_t)(w[j / 2] >> (16 * (j % 2)));
       }
     }
     if constexpr (EIGHT) {
       const uint32_t ms = scale_of(block_max(m)), vs = scale_of(block_max(root));
       const float mi = scale_inverse(ms), vi = scale_inverse(vs);
       const uint64_t draw = (uint64_t)i >> 3;
-      const uint4 r = philox4x32_10_rk(make_uint4((uint32_t)draw, (uint32_t)(draw >> 32),
-                                                  (uint32_t)(a.base + at), (uint32_t)step), a.key);
-      const uint32_t words[4] = {r.x, r.y, r.z, r.w};
+      const uint4 rnd = philox4x32_10_rk(make_uint4((uint32_t)draw, (uint32_t)(draw >> 32),
+                                                    (uint32_t)(a.base + at), (uint32_t)step), a.key);
+      const uint32_t words[4] = {rnd.x, rnd.y, rnd.z, rnd.w};
       uint32_t mc[4], vc[4];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
@@ -261,11 +293,20 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
         t.exp_avg_sq_scales[i >> 5] = (uint8_t)vs;
       }
     } else {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = __uint_as_float(r.v[j]);
       store8(static_cast<float*>(t.exp_avg), i, have, m);
       store8(static_cast<float*>(t.exp_avg_sq), i, have, v);
     }
+    if (!more || next_at != at) report(at);
+    if (!more) break;
+    chunk = next;
+    at = next_at;
+    i = next_i;
+    have = next_have;
+    r = ahead;
   }
-  report();
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -335,7 +376,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, in
       a.chunks += (a.t[i].n + kChunk - 1) / kChunk;
     }
     if (a.chunks == 0) continue;
-    const dim3 grid((unsigned)(a.chunks < 8 * sms ? a.chunks : 8 * sms)), block(kThreads);
+    const dim3 grid((unsigned)(a.chunks < 3 * sms ? a.chunks : 3 * sms)), block(kThreads);
     if (eight)
       e = cfg->grad_bytes == 4 ? launch_pdl(adamw_kernel<true, float>, grid, block, 0, s, a)
                                : launch_pdl(adamw_kernel<true, __nv_bfloat16>, grid, block, 0, s, a);
