@@ -10,6 +10,7 @@ torch.empty on the input's device and returned in a dict:
 (gscale = [amax, S_dec]; grouped: [E, 2]).
 """
 import ctypes
+import struct
 
 import torch
 
@@ -600,7 +601,7 @@ def _score(score):
 
 def _small(v):
     """An integer argument within a C int (the library refuses what is out of its range)."""
-    return max(-1, min(int(v), 1 << 20))
+    return v if type(v) is int and 0 <= v <= 256 else max(-1, min(int(v), 1 << 20))
 
 
 def nvfp4_moe_router(logits, topk, score="softmax", bias=None, groups=1, top_groups=None,
@@ -616,15 +617,17 @@ def nvfp4_moe_router(logits, topk, score="softmax", bias=None, groups=1, top_gro
     T, E = logits.shape
     K, dev = _small(topk), logits.device
     if bias is not None:
-        _check(bias, "bias", torch.float32, (E,), dev)
-    ids = _out(ids, "ids", torch.int32, (T, max(K, 0)), dev)
-    weights = _out(weights, "weights", torch.float32, (T, max(K, 0)), dev)
-    status = L.nvfp4_moe_router(logits.data_ptr(), logits.element_size(), _ptr(bias), T, _small(E), K,
-                                _score(score), _small(groups),
-                                _small(groups if top_groups is None else top_groups),
-                                int(bool(renormalize)), scale, ids.data_ptr(), weights.data_ptr(),
+        bias = _check(bias, "bias", torch.float32, (E,), dev).data_ptr()
+    shape = (T, K if K > 0 else 0)
+    ids = _out(ids, "ids", torch.int32, shape, dev)
+    weights = _out(weights, "weights", torch.float32, shape, dev)
+    groups = _small(groups)
+    status = L.nvfp4_moe_router(logits.data_ptr(), logits.element_size(), bias, T, E, K, _score(score),
+                                groups, groups if top_groups is None else _small(top_groups),
+                                1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(),
                                 _stream(dev))
-    _raise_if(status, "nvfp4_moe_router")
+    if status:
+        _raise_if(status, "nvfp4_moe_router")
     return ids, weights
 
 
@@ -643,8 +646,8 @@ def nvfp4_moe_router_backward(grad_weights, logits, ids, score="softmax", renorm
     _check(grad_weights, "grad_weights", torch.float32, (T, K), dev)
     out = _out(out, "out", logits.dtype, (T, E), dev)
     status = L.nvfp4_moe_router_backward(grad_weights.data_ptr(), logits.data_ptr(),
-                                         logits.element_size(), ids.data_ptr(), T, _small(E), _small(K),
-                                         _score(score), int(bool(renormalize)), scale, out.data_ptr(),
+                                         logits.element_size(), ids.data_ptr(), T, E, K, _score(score),
+                                         1 if renormalize else 0, scale, out.data_ptr(),
                                          _stream(dev))
     _raise_if(status, "nvfp4_moe_router_backward")
     return out
@@ -660,6 +663,12 @@ def _activation(name):
     return ACTIVATIONS[name]
 
 
+# The structures of the C ABI as packed bytes: a ctypes.Structure costs a microsecond more to make.
+_OPERAND = struct.Struct("@PPPqqqq")        # _lib.Operand
+_EPILOGUE = struct.Struct("@iii4xPPPP")     # _lib.Epilogue
+_ADAMW_CONFIG = struct.Struct("@ddddqPPQii")  # _lib.AdamWConfig
+
+
 def _check_rows(t, name, dim, device):
     """Refuse what is not a uint8 tensor of `dim` dimensions on `device` with contiguous rows."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.dim() != dim:
@@ -671,45 +680,48 @@ def _check_rows(t, name, dim, device):
 
 
 def _operand(name, codes, scales, gscale, device, experts=None, stacked=False):
-    """(Operand, rows, K) of codes [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with experts),
-    checked; stacked: codes and scales have a first dimension of experts."""
+    """(packed nvfp4_operand, rows, K) of codes [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with
+    experts), checked; stacked: codes and scales have a first dimension of experts."""
     dim = 3 if stacked else 2
     _check_rows(codes, name + "_codes", dim, device)
     _check_rows(scales, name + "_scales", dim, device)
-    shape, K = codes.shape, 2 * codes.shape[-1]
-    if K % 32 != 0 or tuple(scales.shape) != tuple(shape[:-1]) + (K // 16,):
+    shape, sshape = codes.shape, scales.shape
+    K = 2 * shape[-1]
+    if K % 32 != 0 or sshape[-1] * 16 != K or sshape[:-1] != shape[:-1]:
         raise ValueError("%s_codes must be [.., K/2] with K a multiple of 32 and %s_scales [.., K/16]"
                          % (name, name))
     if stacked and shape[0] != experts:
         raise ValueError("%s must have %d experts, not %d" % (name, experts, shape[0]))
     _check(gscale, name + "_gscale", torch.float32, (2,) if experts is None else (experts, 2), device)
     cs, ss = codes.stride(), scales.stride()
-    o = _lib.Operand(codes.data_ptr(), scales.data_ptr(), gscale.data_ptr(), cs[-2], ss[-2],
-                     cs[0] if stacked else 0, ss[0] if stacked else 0)
+    o = _OPERAND.pack(codes.data_ptr(), scales.data_ptr(), gscale.data_ptr(), cs[-2], ss[-2],
+                      cs[0] if stacked else 0, ss[0] if stacked else 0)
     return o, shape[-2], K
 
 
 def _gemm_epilogue(bias, bias_shape, activation, residual, out, out_dtype, shape, keep_preact, preact,
                    amax, with_amax, experts, dev):
-    """(Epilogue, result dict) of the products' shared options."""
-    if out is not None and out_dtype is None:
-        out_dtype = out.dtype
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    """(packed nvfp4_epilogue, result dict) of the products' shared options."""
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     got = {"out": _out(out, "out", out_dtype, shape, dev)}
+    at = bias_bytes = at_residual = at_preact = at_amax = 0
     if bias is not None:
         _check(bias, "bias", torch.float32 if bias.dtype is torch.float32 else torch.bfloat16,
                bias_shape, dev)
+        at, bias_bytes = bias.data_ptr(), bias.element_size()
     if residual is not None:
-        _check(residual, "residual", out_dtype, shape, dev)
+        at_residual = _check(residual, "residual", out_dtype, shape, dev).data_ptr()
     if keep_preact or preact is not None:
         got["preact"] = _out(preact, "preact", torch.bfloat16, shape, dev)
+        at_preact = got["preact"].data_ptr()
     if with_amax or amax is not None:
         got["amax"] = _out(amax, "amax", torch.float32, (experts,), dev)
-    e = _lib.Epilogue(_activation(activation), 4 if out_dtype is torch.float32 else 2,
-                      0 if bias is None else bias.element_size(), _ptr(bias), _ptr(residual),
-                      _ptr(got.get("preact")), _ptr(got.get("amax")))
+        at_amax = got["amax"].data_ptr()
+    e = _EPILOGUE.pack(_activation(activation), 4 if out_dtype is torch.float32 else 2, bias_bytes, at,
+                       at_residual, at_preact, at_amax)
     return e, got
 
 
@@ -737,7 +749,7 @@ def nvfp4_gemm(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, bias=No
         raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
     e, got = _gemm_epilogue(bias, (N,), activation, residual, out, out_dtype, (M, N), keep_preact,
                             preact, amax, with_amax, 1, dev)
-    status = L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, ctypes.byref(e),
+    status = L.nvfp4_gemm(a, b, M, N, K, e,
                           got["out"].data_ptr(), _stream(dev))
     _raise_if(status, "nvfp4_gemm")
     return got
@@ -764,8 +776,8 @@ def nvfp4_gemm_grouped(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale,
         raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
     e, got = _gemm_epilogue(bias, (E, N), activation, residual, out, out_dtype, (T, N), keep_preact,
                             preact, amax, with_amax, E, dev)
-    status = L.nvfp4_gemm_grouped(ctypes.byref(a), ctypes.byref(b), offsets.data_ptr(), _small(E), T, N,
-                                  K, ctypes.byref(e), got["out"].data_ptr(), _stream(dev))
+    status = L.nvfp4_gemm_grouped(a, b, offsets.data_ptr(), _small(E), T, N, K, e,
+                                  got["out"].data_ptr(), _stream(dev))
     _raise_if(status, "nvfp4_gemm_grouped")
     return got
 
@@ -794,8 +806,8 @@ def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_g
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     out = _out(out, "out", out_dtype, (E, M, N), dev)
-    status = L.nvfp4_gemm_grouped_wgrad(ctypes.byref(a), ctypes.byref(b), offsets.data_ptr(), _small(E),
-                                        M, N, K, out.element_size(), int(bool(accumulate)),
+    status = L.nvfp4_gemm_grouped_wgrad(a, b, offsets.data_ptr(), _small(E), M, N, K,
+                                        out.element_size(), int(bool(accumulate)),
                                         out.data_ptr(), _stream(dev))
     _raise_if(status, "nvfp4_gemm_grouped_wgrad")
     return out
@@ -907,11 +919,12 @@ class AdamW:
             _check(step, "step", torch.int32, (1,), dev)
         if grad_scale is not None:
             _check(grad_scale, "grad_scale", torch.float32, (1,), dev)
-        cfg = _lib.AdamWConfig(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
-                               0 if on_device else step, step.data_ptr() if on_device else None,
-                               _ptr(grad_scale), seed, self.state_bits, self.grad_bytes)
-        status = L.nvfp4_adamw_step(self._table, len(self.params), ctypes.byref(cfg), amax.data_ptr(),
-                                    _stream(dev))
+        cfg = _ADAMW_CONFIG.pack(self.lr if lr is None else lr, self.betas[0], self.betas[1], self.eps,
+                                 0 if on_device else min(max(int(step), -1), 1 << 40),
+                                 step.data_ptr() if on_device else 0,
+                                 0 if grad_scale is None else grad_scale.data_ptr(),
+                                 seed & 0xFFFFFFFFFFFFFFFF, self.state_bits, self.grad_bytes)
+        status = L.nvfp4_adamw_step(self._table, len(self.params), cfg, amax.data_ptr(), _stream(dev))
         _raise_if(status, "nvfp4_adamw_step")
         return amax
 
