@@ -69,8 +69,8 @@ struct Shape {
   static constexpr int kQBlocks = (NT + 127) / 128;              // blocks of 128 rows of scales
   static constexpr int kQBytes = kQRows * kBlockK / 2;
   static constexpr int kStage = kPBytes + kQBytes + (1 + kQBlocks) * kScaleBlock;
-  static constexpr int kStages = CTAS == 2 ? 5 : NT <= 32 ? 4 : NT <= 64 ? 3 : 6;
-  static constexpr int kPerSm = CTAS == 1 && NT <= 64 ? 2 : 1;
+  static constexpr int kStages = CTAS == 2 ? 5 : NT == 32 ? 4 : NT == 64 ? 7 : 6;
+  static constexpr int kPerSm = CTAS == 1 && NT == 32 ? 2 : 1;
   static constexpr int kColumns = kPerSm == 2 ? 256 : 512;       // of tensor memory
   // Two accumulators. Of 256 columns they overlap by 64: those are read first, and the next tile's
   // products start as soon as they are. `kLag`: the next tile but kLag - 1 waits.
@@ -155,9 +155,9 @@ __device__ __forceinline__ int tile_count(const TcArgs& a, const Table& t) {
   return ((a.p.rows + 128 * CTAS - 1) / (128 * CTAS)) * ((a.q.rows + NT - 1) / NT);
 }
 
-// Tile number `i`; `e` is a cursor over the experts. Eight tiles of p share their tiles of q in turn.
+// Tile number `i`, of expert `e` or one behind it. Eight tiles of p share their tiles of q in turn.
 template <int CTAS, int NT, bool SWAP>
-__device__ __forceinline__ Tile get_tile(const TcArgs& a, const Table& t, int i, int& e, int split, int splits) {
+__device__ __forceinline__ Tile get_tile(const TcArgs& a, const Table& t, int i, int e, int split, int splits) {
   Tile x;
   constexpr int kPt = 128 * CTAS;
   x.p0 = x.q0 = x.pz = x.qz = 0;
@@ -246,14 +246,16 @@ __device__ __forceinline__ void put_scales(uint32_t addr, const uint4& v0, const
 // A warp turns one block of scales of every stage: rows `row_shift`.. of the tile's rows of p or q, of
 // which ROWS exist. Then it arrives on the pair's `ready`.
 template <int CTAS, int NT, bool SWAP, int ROWS>
-__device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table, int tiles,
+__device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table,
+                                            const Tile& first_tile, int tiles,
                                             int cluster, int clusters, int split, int splits, bool is_q,
                                             uint32_t blocks, uint64_t* landed, uint64_t* ready, int row_shift) {
   using S = Shape<CTAS, NT>;
   const int lane = threadIdx.x & 31;
-  int e = 0, it = 0;
+  int it = 0;
+  Tile x = first_tile;
   for (int i = cluster; i < tiles; i += clusters) {
-    const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+    if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
     // Where rows start anywhere: aligned loads, two stages ahead. A stage is 16 bytes of a row, so that
     // its upper part is the next stage's lower one.
     uint4 lo[4], hi[4], next[4];
@@ -346,15 +348,14 @@ __device__ __forceinline__ void store_words(void* p, int wide, const uint32_t* w
   }
 }
 
-// 32 elements as 16 packed pairs.
-using Pairs = uint64_t[16];
-
-template <int ACT>
-__device__ __forceinline__ void activate_pairs(Pairs& z) {
+// Elements as P packed pairs (16: a chunk of 32 columns).
+template <int ACT, int P>
+__device__ __forceinline__ void activate_pairs(uint64_t (&z)[P]) {
 #pragma unroll
-  for (int i = 0; i < 16; i++) z[i] = activate2<ACT>(z[i]);
+  for (int i = 0; i < P; i++) z[i] = activate2<ACT>(z[i]);
 }
-__device__ __forceinline__ void activate_pairs(int act, Pairs& z) {
+template <int P>
+__device__ __forceinline__ void activate_pairs(int act, uint64_t (&z)[P]) {
   switch (act) {
     case NVFP4_ACT_RELU: activate_pairs<NVFP4_ACT_RELU>(z); break;
     case NVFP4_ACT_RELU2: activate_pairs<NVFP4_ACT_RELU2>(z); break;
@@ -363,66 +364,70 @@ __device__ __forceinline__ void activate_pairs(int act, Pairs& z) {
     default: break;
   }
 }
-__device__ __forceinline__ void pack_pairs(const Pairs& z, uint32_t (&w)[16]) {
+template <int P>
+__device__ __forceinline__ void pack_pairs(const uint64_t (&z)[P], uint32_t (&w)[P]) {
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
+  for (int i = 0; i < P; i++) {
     const float2 f = f2_unpack(z[i]);
     w[i] = pack2(f.x, f.y);
   }
 }
 
-// The residual's 32 elements, loaded ahead of the sums: `whole` by 16-byte loads, else the first `have`,
-// `stride` apart. Words of BF16 pairs or of binary32.
-__device__ __forceinline__ void load_residual(const TcArgs& a, uint32_t (&w)[32], int64_t at, int64_t stride,
+// The residual's elements, loaded ahead of the sums: `whole` (P = 16) by 16-byte loads, else the first
+// `have`, `stride` apart. Words of BF16 pairs or of binary32.
+template <int P>
+__device__ __forceinline__ void load_residual(const TcArgs& a, uint32_t (&w)[2 * P], int64_t at, int64_t stride,
                                               int have, bool whole) {
   if (a.out_bytes == 2) {
-    const uint16_t* r = static_cast<const uint16_t*>(a.residual) + at;
-    if (whole) {
+    const uint16_t* const r = static_cast<const uint16_t*>(a.residual) + at;
+    if (P == 16 && whole) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
+      for (int i = 0; i < P / 4; i++) {
         const uint4 v = reinterpret_cast<const uint4*>(r)[i];
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
       return;
     }
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-      const uint32_t lo = 2 * i < have ? r[0] : 0u, hi = 2 * i + 1 < have ? r[stride] : 0u;
+    for (int i = 0; i < P; i++) {
+      const uint32_t lo = 2 * i < have ? r[2 * i * stride] : 0u, hi = 2 * i + 1 < have ? r[(2 * i + 1) * stride] : 0u;
       w[i] = lo | hi << 16;
-      r += 2 * stride;
     }
     return;
   }
-  const uint32_t* r = static_cast<const uint32_t*>(a.residual) + at;
-  if (whole) {
+  const uint32_t* const r = static_cast<const uint32_t*>(a.residual) + at;
+  if (P == 16 && whole) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < P / 2; i++) {
       const uint4 v = reinterpret_cast<const uint4*>(r)[i];
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 32; i++, r += stride) w[i] = i < have ? *r : 0u;
+  for (int i = 0; i < 2 * P; i++) w[i] = i < have ? r[i * stride] : 0u;
 }
-// 32 elements (`whole`) or the first `have` of them, `stride` apart, of 2 bytes.
-__device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint32_t (&w)[16], int64_t at,
+// Elements of 2 bytes: `whole`, or the first `have`, `stride` apart.
+template <int P>
+__device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint32_t (&w)[P], int64_t at,
                                             int64_t stride, int have, bool whole) {
-  uint16_t* to = static_cast<uint16_t*>(p) + at;
-  if (whole) {
-    store_words(to, a.wide, w);
-    store_words(to + 16, a.wide, w + 8);
-    return;
+  uint16_t* const to = static_cast<uint16_t*>(p) + at;
+  if constexpr (P == 16) {
+    if (whole) {
+      store_words(to, a.wide, w);
+      store_words(to + 16, a.wide, w + 8);
+      return;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 32; i++, to += stride)
-    if (i < have) *to = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+  for (int i = 0; i < 2 * P; i++)
+    if (i < have) to[i * stride] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
 }
 
 // A warp's 32 rows x 64 bytes to a box of a map, a lane's row in w, through its staging buffer (rows of
 // 64 bytes in the 64-byte swizzle: the 16-byte stores of eight lanes meet eight different bank groups).
-// Stores straight from the lanes would touch 32 lines each, and the warps that turn scales would wait
-// behind them for their shared memory (2000 cycles a stage in place of 300).
+// Stores straight from the lanes touch 32 lines each: the weight gradient of 32768 rows took 733 us with
+// them, 612 in boxes.
 __device__ __forceinline__ void store_box(uint32_t buffer, const CUtensorMap* map, const uint32_t (&w)[16],
                                           int32_t x, int32_t y, int32_t z) {
   const uint32_t lane = threadIdx.x & 31;
@@ -448,31 +453,37 @@ struct BoxAt {
   int32_t x, y, z;
 };
 
-// z = alpha * sums + bias through the activation and the residual into out: 32 elements from element
+// z = alpha * sums + bias through the activation and the residual into out: 2 P elements from element
 // `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
-// aligned. Returns the largest |out| as binary32 bits.
-template <bool BOXES>
-__device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint32_t (&residual)[32], int64_t at,
-                                           int64_t stride, int have, bool whole, bool live, const BoxAt& box) {
-  uint32_t w[16];
+// aligned. With BOXES a warp's rows may leave together, `live` or not. Returns the largest |out| as
+// binary32 bits.
+template <bool BOXES, int P>
+__device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], const uint32_t (&residual)[2 * P],
+                                           int64_t at, int64_t stride, int have, bool whole, bool live,
+                                           const BoxAt& box) {
+  uint32_t w[P];
   if (a.preact != nullptr) {
     pack_pairs(z, w);
-    if (BOXES && box.buffer) store_box(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
-    else if (live) store_pairs(a, a.preact, w, at, stride, have, whole);
+    if constexpr (BOXES) {
+      if (box.buffer) store_box(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
+    }
+    if ((!BOXES || !box.buffer) && live) store_pairs(a, a.preact, w, at, stride, have, whole);
   }
   activate_pairs(a.activation, z);
   if (a.out_bytes == 2) {
     if (a.residual != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 16; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
+      for (int i = 0; i < P; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
     }
     pack_pairs(z, w);
-    if (BOXES && box.buffer) store_box(box.buffer, &a.out_map, w, box.x, box.y, box.z);
-    else if (live) store_pairs(a, a.out, w, at, stride, have, whole);
+    if constexpr (BOXES) {
+      if (box.buffer) store_box(box.buffer, &a.out_map, w, box.x, box.y, box.z);
+    }
+    if ((!BOXES || !box.buffer) && live) store_pairs(a, a.out, w, at, stride, have, whole);
     if (a.amax == nullptr || !live) return 0u;
     uint32_t top = 0u;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
+    for (int i = 0; i < P; i++) {
       if (2 * i >= have) w[i] = 0u;
       else if (2 * i + 1 >= have) w[i] &= 0xFFFFu;
       top = hmax_abs2(top, w[i]);
@@ -482,62 +493,44 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, Pairs& z, const uint
   }
   if (a.residual != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 16; i++)
+    for (int i = 0; i < P; i++)
       z[i] = f2_add(z[i], f2_pack(__uint_as_float(residual[2 * i]), __uint_as_float(residual[2 * i + 1])));
   }
-  uint32_t o[32], top = 0u;
+  uint32_t o[2 * P], top = 0u;
 #pragma unroll
-  for (int i = 0; i < 16; i++) {
+  for (int i = 0; i < P; i++) {
     const float2 f = f2_unpack(z[i]);
     o[2 * i] = __float_as_uint(f.x);
     o[2 * i + 1] = __float_as_uint(f.y);
   }
-  uint32_t* to = static_cast<uint32_t*>(a.out) + at;
-  if (BOXES && box.buffer) {
+  uint32_t* const to = static_cast<uint32_t*>(a.out) + at;
+  if constexpr (BOXES) {
+    if (box.buffer) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
+      for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int i = 0; i < 16; i++) w[i] = o[16 * h + i];
-      store_box(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
+        for (int i = 0; i < 16; i++) w[i] = o[16 * h + i];
+        store_box(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
+      }
     }
-  } else if (!live) {
-    return 0u;
-  } else if (whole) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 8) store_words(to + i, a.wide, o + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; i++, to += stride)
-      if (i < have) *to = o[i];
   }
-  if (a.amax != nullptr && live) {
+  if (!live) return 0u;
+  if (!BOXES || !box.buffer) {
+    if (P == 16 && whole) {
 #pragma unroll
-    for (int i = 0; i < 32; i++)
+      for (int i = 0; i < 2 * P; i += 8) store_words(to + i, a.wide, o + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * P; i++)
+        if (i < have) to[i * stride] = o[i];
+    }
+  }
+  if (a.amax != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 2 * P; i++)
       if (i < have) top = max(top, o[i] & 0x7FFFFFFFu);
   }
   return top;
-}
-
-// One element (the tiles whose sums a cluster adds up).
-__device__ __forceinline__ uint32_t finish_one(const TcArgs& a, float sum, float alpha, float bias, int64_t at) {
-  float z = sum * alpha + bias;
-  if (a.preact != nullptr) static_cast<__nv_bfloat16*>(a.preact)[at] = __float2bfloat16_rn(z);
-  switch (a.activation) {
-    case NVFP4_ACT_RELU: z = activate<NVFP4_ACT_RELU>(z); break;
-    case NVFP4_ACT_RELU2: z = activate<NVFP4_ACT_RELU2>(z); break;
-    case NVFP4_ACT_GELU: z = activate<NVFP4_ACT_GELU>(z); break;
-    case NVFP4_ACT_SILU: z = activate<NVFP4_ACT_SILU>(z); break;
-    default: break;
-  }
-  if (a.out_bytes == 2) {
-    if (a.residual != nullptr) z += bf16_at(a.residual, at);
-    const __nv_bfloat16 b = __float2bfloat16_rn(z);
-    static_cast<__nv_bfloat16*>(a.out)[at] = b;
-    return ((uint32_t)__bfloat16_as_ushort(b) & 0x7FFFu) << 16;
-  }
-  if (a.residual != nullptr) z += static_cast<const float*>(a.residual)[at];
-  static_cast<float*>(a.out)[at] = z;
-  return __float_as_uint(z) & 0x7FFFFFFFu;
 }
 
 __device__ __forceinline__ void report_amax(const TcArgs& a, uint32_t top, int e) {
@@ -605,20 +598,19 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     make_table<CTAS, NT, SWAP>(a, table);
   }
   const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
-  if (cluster < tiles) {  // brings the parameters that it reads into the constant cache before the wait
-    int e = 0;
-    const Tile x = get_tile<CTAS, NT, SWAP>(a, table, cluster, e, split, splits);
-    asm volatile("" ::"r"(x.p0), "r"(x.q0), "r"(x.kb0), "r"(x.kb1), "r"(a.p.tma), "r"(a.q.tma));
-  }
+  // (in a dense product before the previous kernel has ended: it takes five divisions)
+  Tile first = {};
+  if (cluster < tiles) first = get_tile<CTAS, NT, SWAP>(a, table, cluster, 0, split, splits);
   pdl_wait();
   pdl_allow_next();
 
   if (warp == S::kEpi) {
     const uint32_t bytes = (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
-    int e = 0, it = 0;
+    int it = 0;
     bool alive = true;
+    Tile x = first;
     for (int i = cluster; i < tiles && alive; i += clusters) {
-      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+      if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
       for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
         const int stage = it % S::kStages;
         alive = wait_phase(&empty[stage], ((uint32_t)(it / S::kStages) & 1u) ^ 1u);
@@ -652,10 +644,11 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   } else if (warp == S::kEpi + 1) {
     if (half == 0) {
       constexpr uint32_t idesc = nvfp4_idesc(128 * CTAS, NT);
-      int e = 0, it = 0, count = 0;
+      int it = 0, count = 0;
       bool alive = true;
+      Tile x = first;
       for (int i = cluster; i < tiles; i += clusters, count++) {
-        const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+        if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
         const uint32_t acc = tmem + (count & 1) * S::kAccStride;
         // an accumulator's barrier completes once for each of its tiles, and is never a phase ahead
         if (count >= S::kLag)
@@ -703,11 +696,11 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
       }
     }
   } else if (warp == S::kEpi + 2) {
-    turn_scales<CTAS, NT, SWAP, 128>(a, a.p, table, tiles, cluster, clusters, split, splits, false,
+    turn_scales<CTAS, NT, SWAP, 128>(a, a.p, table, first, tiles, cluster, clusters, split, splits, false,
                                      stages + kPBytes + S::kQBytes, landed, ready, 128 * half);
   } else if (warp > S::kEpi + 2) {
     const int block = warp - S::kEpi - 3;
-    turn_scales<CTAS, NT, SWAP, (NT < 128 ? NT : 128)>(a, a.q, table, tiles, cluster, clusters, split, splits, true,
+    turn_scales<CTAS, NT, SWAP, (NT < 128 ? NT : 128)>(a, a.q, table, first, tiles, cluster, clusters, split, splits, true,
                                                        stages + kPBytes + S::kQBytes + kScaleBlock * (1 + block),
                                                        landed, ready, 128 * block);
   } else {
@@ -717,9 +710,10 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     constexpr int kFreed = S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks;
     float* const mine = bias_stage[warp];
     const uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
-    int e = 0, count = 0;
+    int count = 0;
+    Tile x = first;
     for (int i = cluster; i < tiles; i += clusters, count++) {
-      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, i, e, split, splits);
+      if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
       const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
       const int r = 128 * half + 32 * quarter + lane;  // row of the tile
       const bool live = r < x.p_rows;
@@ -752,7 +746,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
                            (a.mode != kGemmGrouped || rows_left >= 32);
         const BoxAt box = {boxes ? staging : 0u, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
         uint32_t v[32], residual[32];
-        if (a.residual != nullptr && counts) load_residual(a, residual, at, stride, left, whole);
+        if (a.residual != nullptr && counts) load_residual<16>(a, residual, at, stride, left, whole);
         if (!SWAP && a.bias != nullptr) {
           __syncwarp();
           mine[lane] = lane < left ? bias_at(a, (int64_t)x.e * a.N + col + lane) : 0.0f;
@@ -781,7 +775,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 512), "r"(v[j]) : "memory");
           continue;
         }
-        Pairs z;
+        uint64_t z[16];
 #pragma unroll
         for (int j = 0; j < 16; j++)
           z[j] = f2_mul(f2_pack(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), alpha2);
@@ -798,7 +792,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
             }
           }
         }
-        if (counts || boxes) top = max(top, finish<!SWAP>(a, z, residual, at, stride, left, whole, counts, box));
+        if (counts || boxes) top = max(top, finish<!SWAP, 16>(a, z, residual, at, stride, left, whole, counts, box));
       }
       if (splits == 1) report_amax(a, top, x.e);
     }
@@ -816,25 +810,33 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     __syncwarp();
     cluster_sync();
     if (warp < S::kEpi && cluster < tiles) {  // the host launches one tile a cluster: every CTA takes some rows of q
-      int e = 0;
-      const Tile x = get_tile<CTAS, NT, SWAP>(a, table, cluster, e, split, splits);
+      const Tile& x = first;
       const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
       const int r = 32 * (warp & 3) + lane;
       uint32_t top = 0u;
       if (r < x.p_rows) {
         const float bias = a.bias ? bias_at(a, x.p0 + r) : 0.0f;
+        const uint64_t alpha2 = f2_pack(alpha, alpha), bias2 = f2_pack(bias, bias);
         constexpr int kTurn = 8;  // rows of q whose loads are under way together
         for (int c = kTurn * split; c < min(NT, x.q_rows); c += kTurn * splits) {
-          float v[kTurn];
+          const int64_t at = (int64_t)(x.q0 + c) * a.N + x.p0 + r;
+          uint32_t residual[kTurn];
+          if (a.residual != nullptr) load_residual<kTurn / 2>(a, residual, at, a.N, x.q_rows - c, false);
+          uint64_t z[kTurn / 2];
 #pragma unroll
-          for (int j = 0; j < kTurn; j++) v[j] = 0.0f;
+          for (int j = 0; j < kTurn / 2; j++) z[j] = 0ull;
           for (int s = 0; s < splits; s++) {
             const uint32_t from = cluster_address(stages + (c * 128 + r) * 4, s);
 #pragma unroll
-            for (int j = 0; j < kTurn; j++) v[j] += cluster_load(from + j * 512);
+            for (int j = 0; j < kTurn / 2; j++)
+              z[j] = f2_add(z[j], f2_pack(cluster_load(from + 2 * j * 512), cluster_load(from + (2 * j + 1) * 512)));
           }
-          for (int j = 0; j < kTurn && c + j < x.q_rows; j++)
-            top = max(top, finish_one(a, v[j], alpha, bias, (int64_t)(x.q0 + c + j) * a.N + x.p0 + r));
+#pragma unroll
+          for (int j = 0; j < kTurn / 2; j++) {
+            z[j] = f2_mul(z[j], alpha2);
+            if (a.bias != nullptr) z[j] = f2_add(z[j], bias2);
+          }
+          top = max(top, finish<false, kTurn / 2>(a, z, residual, at, a.N, x.q_rows - c, false, true, BoxAt()));
         }
       }
       report_amax(a, top, x.e);
@@ -924,6 +926,7 @@ bool make_out_maps(TcArgs& t, const GemmArgs& g) {
 cudaError_t prepare_gemm_kernels() {
   cudaError_t e = prepare_one<2, 256, false>(), r;
   if ((r = prepare_one<1, 32, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<1, 64, true>()) != cudaSuccess) e = r;
   if ((r = prepare_one<1, 128, true>()) != cudaSuccess) e = r;
   return e;
 }
@@ -944,31 +947,51 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   t.boxes = t.wide != 0;
   const int32_t b_experts = g.mode == kGemmGrouped ? g.E : 1;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  // rows of a that a tile is likely to find: all of them, or an expert's mean share
-  const int64_t rows_a = g.mode == kGemmGrouped ? up(g.M, g.E) : g.M;
-  const int64_t many = g.mode == kGemmDense ? 1 : g.E;
-  const int64_t big = up(rows_a, 256) * up(g.N, 256) * many;
-  if (rows_a > 128 && 2 * big >= sm_count / 2) {
+  // Which tiles: the least estimated time. Rows of a that an expert is likely to have: the mean.
+  const int64_t rows_a = g.mode == kGemmGrouped ? up(g.M, g.E) : g.M, many = g.mode == kGemmDense ? 1 : g.E;
+  const int64_t kb = up(g.mode == kGemmWgrad ? up(g.K, g.E) : g.K, kBlockK);
+  // Cycles of a stage (what its loads take an SM, at 64 bytes a cycle), of a tile's epilogue where
+  // nothing hides it, of the whole call; measured with one tile a CTA. With several, the epilogue runs
+  // beside the next tile's products.
+  struct Choice {
+    int rows, cols, per_sm, stage, tail;  // of out a tile; CTAs (pairs: halves of one) an SM
+  };
+  constexpr Choice choices[4] = {{32, 128, 2, 400, 1500}, {64, 128, 1, 450, 2200}, {128, 128, 1, 580, 4000},
+                                 {256, 256, 0, 690, 5500}};
+  int best = 0, splits = 1;
+  double least = 0.0;
+  for (int c = 0; c < 4; c++) {
+    const Choice& x = choices[c];
+    const int64_t tiles = up(rows_a, x.rows) * up(g.N, x.cols) * many;
+    const int64_t slots = x.per_sm ? (int64_t)sm_count * x.per_sm : sm_count / 2;
+    int sp = 1;  // few rows: the weights' bytes should come through all SMs
+    if (c == 0 && g.mode == kGemmDense)
+      while (sp < 8 && 2 * sp * tiles <= slots && kb >= 8 * sp) sp *= 2;
+    const int64_t rounds = up(tiles * sp, slots);
+    const double busy = x.per_sm == 2 && tiles * sp > sm_count ? 2.0 : 1.0;  // CTAs that share an SM's port
+    const double stages = (double)up(kb, sp) * x.stage * busy;
+    const double time = (double)rounds * (stages > x.tail || rounds == 1 ? stages : x.tail) + x.tail +
+                        (sp > 1 ? 2500.0 : 0.0);
+    if (c == 0 || time < least) best = c, least = time, splits = c == 0 ? sp : 1;
+  }
+  const Choice& x = choices[best];
+  const int64_t tiles = up(rows_a, x.rows) * up(g.N, x.cols);
+  if (best == 3) {
     if (!make_side(t.p, g.a, g.M, g.K, 1, 128, 128) || !make_side(t.q, g.b, g.N, g.K, b_experts, 128, 256))
       return cudaErrorInvalidValue;
     if (t.boxes && !make_out_maps(t, g)) return cudaErrorInvalidValue;
-    const int64_t most = g.mode == kGemmDense ? big : sm_count / 2;
+    const int64_t most = g.mode == kGemmDense ? tiles : sm_count / 2;
     return launch_one<2, 256, false>(t, (int)(2 * (most < sm_count / 2 ? most : sm_count / 2)), 1, s);
   }
-  const int nt = rows_a <= 32 ? 32 : 128;
-  if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, nt, nt))
+  if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, x.rows, x.rows))
     return cudaErrorInvalidValue;
-  const int per_sm = nt == 32 ? 2 : 1;
-  int splits = 1;
-  int64_t grid = (int64_t)sm_count * per_sm;
-  if (g.mode == kGemmDense) {
-    const int64_t tiles = up(g.N, 128) * up(g.M, nt);
-    while (splits < 8 && 2 * splits * tiles <= sm_count * per_sm && up(g.K, kBlockK) >= (nt == 32 ? 4 : 16) * splits)
-      splits *= 2;
-    if (splits > 1 || tiles < grid) grid = tiles * splits;
+  int64_t grid = (int64_t)sm_count * x.per_sm;
+  if (g.mode == kGemmDense && (splits > 1 || tiles < grid)) grid = tiles * splits;
+  switch (best) {
+    case 0: return launch_one<1, 32, true>(t, (int)grid, splits, s);
+    case 1: return launch_one<1, 64, true>(t, (int)grid, 1, s);
+    default: return launch_one<1, 128, true>(t, (int)grid, 1, s);
   }
-  return nt == 32 ? launch_one<1, 32, true>(t, (int)grid, splits, s)
-                  : launch_one<1, 128, true>(t, (int)grid, splits, s);
 }
 
 }  // namespace nvfp4
