@@ -53,6 +53,7 @@ struct TcArgs {
   int32_t mode, E;
   int32_t M, N, K;   // of out, and the operands' columns
   int32_t activation, out_bytes, bias_bytes;
+  int32_t q_rows;    // rows of q that a CTA loads: fewer than its tile's where q has fewer
   int32_t boxes;     // rows of out and preact start on 16-byte boundaries: they leave by TMA
   int32_t wide;      // rows of out, residual and preact allow: 2 = 32-byte, 1 = 16-byte, 0 = single accesses
   const void* bias;
@@ -69,8 +70,8 @@ struct Shape {
   static constexpr int kQBlocks = (NT + 127) / 128;              // blocks of 128 rows of scales
   static constexpr int kQBytes = kQRows * kBlockK / 2;
   static constexpr int kStage = kPBytes + kQBytes + (1 + kQBlocks) * kScaleBlock;
-  static constexpr int kStages = CTAS == 2 ? 5 : NT == 32 ? 4 : NT == 64 ? 7 : 6;
-  static constexpr int kPerSm = CTAS == 1 && NT == 32 ? 2 : 1;
+  static constexpr int kStages = CTAS == 2 ? 5 : NT == 32 ? 8 : NT == 64 ? 7 : 6;
+  static constexpr int kPerSm = 1;
   static constexpr int kColumns = kPerSm == 2 ? 256 : 512;       // of tensor memory
   // Two accumulators. Of 256 columns they overlap by 64: those are read first, and the next tile's
   // products start as soon as they are. `kLag`: the next tile but kLag - 1 waits.
@@ -605,7 +606,9 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   pdl_allow_next();
 
   if (warp == S::kEpi) {
-    const uint32_t bytes = (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? NT * 16 : 0);
+    // (what lies behind q's last row keeps what it had: it reaches columns that do not count)
+    const uint32_t bytes = (a.p.tma ? kScaleBlock : 0) + (a.q.tma ? min(NT, CTAS * a.q_rows) * 16 : 0);
+    const uint32_t code_bytes = CTAS * (kPBytes + a.q_rows * (kBlockK / 2));
     int it = 0;
     bool alive = true;
     Tile x = first;
@@ -626,7 +629,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
           if (a.p.tma) tma_load_3d(sc, &a.p.scales, kb * 16, x.p0 + 128 * half, x.pz, &landed[stage]);
           if (a.q.tma) tma_load_3d(sc + kScaleBlock, &a.q.scales, kb * 16, x.q0, x.qz, &landed[stage]);
           // the codes of both CTAs of a pair complete the barrier of the one that multiplies them
-          if (half == 0) mbar_expect_tx(&full[stage], CTAS * (kPBytes + S::kQBytes));
+          if (half == 0) mbar_expect_tx(&full[stage], code_bytes);
           const uint32_t bar = CTAS == 2 ? cluster_address(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
           tma_load_3d_pair<CTAS>(to, &a.p.codes, kb * (kBlockK / 2), x.p0 + 128 * half, x.pz, bar);
           tma_load_3d_pair<CTAS>(to + kPBytes, &a.q.codes, kb * (kBlockK / 2), x.q0 + S::kQRows * half, x.qz, bar);
@@ -956,7 +959,7 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   struct Choice {
     int rows, cols, per_sm, stage, tail;  // of out a tile; CTAs (pairs: halves of one) an SM
   };
-  constexpr Choice choices[4] = {{32, 128, 2, 400, 1500}, {64, 128, 1, 450, 2200}, {128, 128, 1, 580, 4000},
+  constexpr Choice choices[4] = {{32, 128, 1, 400, 1500}, {64, 128, 1, 450, 2200}, {128, 128, 1, 580, 4000},
                                  {256, 256, 0, 690, 5500}};
   int best = 0, splits = 1;
   double least = 0.0;
@@ -977,13 +980,15 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   const Choice& x = choices[best];
   const int64_t tiles = up(rows_a, x.rows) * up(g.N, x.cols);
   if (best == 3) {
+    t.q_rows = 128;
     if (!make_side(t.p, g.a, g.M, g.K, 1, 128, 128) || !make_side(t.q, g.b, g.N, g.K, b_experts, 128, 256))
       return cudaErrorInvalidValue;
     if (t.boxes && !make_out_maps(t, g)) return cudaErrorInvalidValue;
     const int64_t most = g.mode == kGemmDense ? tiles : sm_count / 2;
     return launch_one<2, 256, false>(t, (int)(2 * (most < sm_count / 2 ? most : sm_count / 2)), 1, s);
   }
-  if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, x.rows, x.rows))
+  t.q_rows = (int32_t)(g.M < x.rows ? g.M : x.rows);  // out-of-range rows of a box take as long as others
+  if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, t.q_rows, t.q_rows))
     return cudaErrorInvalidValue;
   int64_t grid = (int64_t)sm_count * x.per_sm;
   if (g.mode == kGemmDense && (splits > 1 || tiles < grid)) grid = tiles * splits;
