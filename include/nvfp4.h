@@ -527,7 +527,15 @@ typedef struct nvfp4_epilogue {
  * gradient and the columnwise weights, the weights' gradient from two columnwise operands (both
  * transformed with the same signs, or neither). K == 0: the sum is 0. */
 nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t M, int64_t N,
-                        int64_t K, const nvfp4_epilogue* epilogue, void* out, void* stream);
+                        int64_t K, const nvfp4_epilogue* epilogue, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that make large products of these operands faster: 0 where the rows of both
+ * scales start on 16-byte boundaries, else room for a copy that does. E experts of a stacked b (1: none;
+ * nvfp4_gemm_grouped_wgrad: K = capacity, E = 1). The products take any workspace (device, 16-byte
+ * aligned, NULL with 0 bytes for none; free for other use afterwards in stream order). */
+nvfp4_status nvfp4_gemm_workspace(const nvfp4_operand* a, const nvfp4_operand* b, int64_t M, int64_t N,
+                                  int64_t K, int32_t E, size_t* bytes);
 
 /* The experts' products of packed rows: for every expert e, out[rows of e] = a[rows of e] b[e]^T
  * through the epilogue.
@@ -539,7 +547,8 @@ nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t 
  * non-decreasing within [0, T] set NVFP4_DEVICE_BAD_OFFSETS; out is undefined then. */
 nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4_operand* b,
                                 const int32_t* offsets, int32_t E, int64_t T, int64_t N, int64_t K,
-                                const nvfp4_epilogue* epilogue, void* out, void* stream);
+                                const nvfp4_epilogue* epilogue, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* The experts' weight gradients: out[e] = a[:, tokens of e] b[:, tokens of e]^T, out [E][M][N].
  *   a [M][capacity], b [N][capacity]: the columnwise outputs that nvfp4_quantize_grouped writes for
@@ -551,7 +560,7 @@ nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4_operand* b,
 nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const nvfp4_operand* b,
                                       const int32_t* offsets, int32_t E, int64_t M, int64_t N,
                                       int64_t capacity, int32_t out_bytes, int32_t accumulate,
-                                      void* out, void* stream);
+                                      void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The gradient through an epilogue: grad_preact = grad_out * act'(preact) in BF16 (rounded once), the
  * column sums of its binary32 values, and its amax: what the quantizations and products of the

@@ -35,7 +35,7 @@ EXPORTED = ["nvfp4_status_string", "nvfp4_amax", "nvfp4_quantize", "nvfp4_quanti
             "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_swiglu_checkpoint",
             "nvfp4_swiglu_checkpoint_backward", "nvfp4_rmsnorm_checkpoint",
             "nvfp4_rmsnorm_checkpoint_workspace", "nvfp4_rmsnorm_checkpoint_backward",
-            "nvfp4_moe_router", "nvfp4_moe_router_backward", "nvfp4_gemm", "nvfp4_gemm_grouped",
+            "nvfp4_moe_router", "nvfp4_moe_router_backward", "nvfp4_gemm", "nvfp4_gemm_workspace", "nvfp4_gemm_grouped",
             "nvfp4_gemm_grouped_wgrad", "nvfp4_gemm_epilogue_backward",
             "nvfp4_gemm_epilogue_backward_workspace", "nvfp4_adamw_step"]
 
@@ -191,9 +191,12 @@ def load(build_if_missing: bool = False):
             ("nvfp4_moe_router", [vp, i32, vp, i64, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
             ("nvfp4_moe_router_backward",
              [vp, vp, i32, vp, i64, i32, i32, i32, i32, f32, vp, vp]),
-            ("nvfp4_gemm", [vp, vp, i64, i64, i64, vp, vp, vp]),
-            ("nvfp4_gemm_grouped", [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp]),
-            ("nvfp4_gemm_grouped_wgrad", [vp, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp]),
+            ("nvfp4_gemm", [vp, vp, i64, i64, i64, vp, vp, vp, ctypes.c_size_t, vp]),
+            ("nvfp4_gemm_workspace",
+             [vp, vp, i64, i64, i64, i32, ctypes.POINTER(ctypes.c_size_t)]),
+            ("nvfp4_gemm_grouped", [vp, vp, vp, i32, i64, i64, i64, vp, vp, vp, ctypes.c_size_t, vp]),
+            ("nvfp4_gemm_grouped_wgrad",
+             [vp, vp, vp, i32, i64, i64, i64, i32, i32, vp, vp, ctypes.c_size_t, vp]),
             ("nvfp4_gemm_epilogue_backward",
              [vp, vp, i64, i64, i32, vp, vp, vp, vp, ctypes.c_size_t, vp]),
             ("nvfp4_gemm_epilogue_backward_workspace",

@@ -680,8 +680,9 @@ def _check_rows(t, name, dim, device):
 
 
 def _operand(name, codes, scales, gscale, device, experts=None, stacked=False):
-    """(packed nvfp4_operand, rows, K) of codes [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with
-    experts), checked; stacked: codes and scales have a first dimension of experts."""
+    """(packed nvfp4_operand, rows, K, whether rows of scales start off 16-byte boundaries) of codes
+    [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with experts), checked; stacked: codes and scales
+    have a first dimension of experts."""
     dim = 3 if stacked else 2
     _check_rows(codes, name + "_codes", dim, device)
     _check_rows(scales, name + "_scales", dim, device)
@@ -694,9 +695,30 @@ def _operand(name, codes, scales, gscale, device, experts=None, stacked=False):
         raise ValueError("%s must have %d experts, not %d" % (name, experts, shape[0]))
     _check(gscale, name + "_gscale", torch.float32, (2,) if experts is None else (experts, 2), device)
     cs, ss = codes.stride(), scales.stride()
-    o = _OPERAND.pack(codes.data_ptr(), scales.data_ptr(), gscale.data_ptr(), cs[-2], ss[-2],
-                      cs[0] if stacked else 0, ss[0] if stacked else 0)
-    return o, shape[-2], K
+    at = scales.data_ptr()
+    o = _OPERAND.pack(codes.data_ptr(), at, gscale.data_ptr(), cs[-2], ss[-2], cs[0] if stacked else 0,
+                      ss[0] if stacked else 0)
+    return o, shape[-2], K, (at | ss[-2] | (ss[0] if stacked else 0)) % 16
+
+
+def _gemm_workspace(workspace, a, b, M, N, K, E, loose, dev):
+    """(pointer, bytes) of the products' optional workspace: the caller's, or a new one where scales are
+    `loose` (their rows do not start on 16-byte boundaries) and the product is large enough to gain."""
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        return workspace.data_ptr(), workspace.numel(), workspace
+    if not loose or M <= 128 or M * N * E < 1 << 21:
+        return None, 0, None
+    n = nvfp4_gemm_workspace(a, b, M, N, K, E)
+    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    return workspace.data_ptr(), n, workspace
+
+
+def nvfp4_gemm_workspace(a, b, M, N, K, E=1):
+    """Bytes of workspace that make large products of these operands (packed nvfp4_operand) faster."""
+    n = ctypes.c_size_t(0)
+    _raise_if(_lib.load().nvfp4_gemm_workspace(a, b, M, N, K, E, ctypes.byref(n)), "nvfp4_gemm_workspace")
+    return n.value
 
 
 def _gemm_epilogue(bias, bias_shape, activation, residual, out, out_dtype, shape, keep_preact, preact,
@@ -733,31 +755,32 @@ def _device_of(codes, name):
 
 def nvfp4_gemm(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, bias=None, activation=None,
                residual=None, out_dtype=None, keep_preact=False, with_amax=False, out=None, preact=None,
-               amax=None):
+               amax=None, workspace=None):
     """act(a b^T + bias) + residual of two NVFP4 operands: a [M, K] and b [N, K] as codes, row-major
     scales and global scale of the quantize calls (rowwise outputs, or columnwise ones, whose K is the
     tensor's rows); row strides may be larger than the rows. bias BF16 or float32 [N]; activation None,
     'relu', 'relu2', 'gelu' (tanh form) or 'silu'; residual [M, N] in the output's type (BF16 or
     float32), may be `out` itself. Returns a dict: out [M, N]; with keep_preact, preact BF16 [M, N],
     the activation's input, which nvfp4_gemm_epilogue_backward takes; with with_amax, amax float32 [1]:
-    max |out|, the amax_row of the next quantization."""
+    max |out|, the amax_row of the next quantization. workspace: a uint8 tensor, used (and made here where
+    none is given) by large products whose scales' rows do not start on 16-byte boundaries."""
     dev = _device_of(a_codes, "a_codes")
     L = _lib.load()
-    a, M, K = _operand("a", a_codes, a_scales, a_gscale, dev)
-    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev)
+    a, M, K, loose_a = _operand("a", a_codes, a_scales, a_gscale, dev)
+    b, N, Kb, loose_b = _operand("b", b_codes, b_scales, b_gscale, dev)
     if K != Kb:
         raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
     e, got = _gemm_epilogue(bias, (N,), activation, residual, out, out_dtype, (M, N), keep_preact,
                             preact, amax, with_amax, 1, dev)
-    status = L.nvfp4_gemm(a, b, M, N, K, e,
-                          got["out"].data_ptr(), _stream(dev))
+    at, room, workspace = _gemm_workspace(workspace, a, b, M, N, K, 1, loose_a or loose_b, dev)
+    status = L.nvfp4_gemm(a, b, M, N, K, e, got["out"].data_ptr(), at, room, _stream(dev))
     _raise_if(status, "nvfp4_gemm")
     return got
 
 
 def nvfp4_gemm_grouped(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, offsets, bias=None,
                        activation=None, residual=None, out_dtype=None, keep_preact=False,
-                       with_amax=False, out=None, preact=None, amax=None):
+                       with_amax=False, out=None, preact=None, amax=None, workspace=None):
     """The experts' products of packed rows: out[rows of e] = act(a[rows of e] b[e]^T + bias[e]) +
     residual. a [T, K] with a_gscale [E, 2] as nvfp4_quantize_grouped writes it, offsets int32 [E]
     expert ends; b_codes [E, N, K/2], b_scales [E, N, K/16], b_gscale [E, 2] (strided views too: the
@@ -768,22 +791,23 @@ def nvfp4_gemm_grouped(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale,
     L = _lib.load()
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         raise TypeError("offsets must be a 1-D int32 CUDA tensor")
-    E = offsets.shape[0]
+    E = _small(offsets.shape[0])
     _check(offsets, "offsets", torch.int32, (E,), dev)
-    a, T, K = _operand("a", a_codes, a_scales, a_gscale, dev, E)
-    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev, E, stacked=True)
+    a, T, K, loose_a = _operand("a", a_codes, a_scales, a_gscale, dev, E)
+    b, N, Kb, loose_b = _operand("b", b_codes, b_scales, b_gscale, dev, E, stacked=True)
     if K != Kb:
         raise ValueError("a and b must have the same K, not %d and %d" % (K, Kb))
     e, got = _gemm_epilogue(bias, (E, N), activation, residual, out, out_dtype, (T, N), keep_preact,
                             preact, amax, with_amax, E, dev)
-    status = L.nvfp4_gemm_grouped(a, b, offsets.data_ptr(), _small(E), T, N, K, e,
-                                  got["out"].data_ptr(), _stream(dev))
+    at, room, workspace = _gemm_workspace(workspace, a, b, T, N, K, E, loose_a or loose_b, dev)
+    status = L.nvfp4_gemm_grouped(a, b, offsets.data_ptr(), E, T, N, K, e, got["out"].data_ptr(), at, room,
+                                  _stream(dev))
     _raise_if(status, "nvfp4_gemm_grouped")
     return got
 
 
 def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, offsets,
-                             out_dtype=None, out=None, accumulate=False):
+                             out_dtype=None, out=None, accumulate=False, workspace=None):
     """The experts' weight gradients out[e] = a[:, tokens of e] b[:, tokens of e]^T (BF16 or float32
     [E, M, N]) from the columnwise outputs of nvfp4_quantize_grouped for two packed tensors with these
     offsets: codes [M or N, capacity / 2], scales [.., capacity / 16], gscale [E, 2] (both with the same
@@ -792,10 +816,10 @@ def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_g
     L = _lib.load()
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         raise TypeError("offsets must be a 1-D int32 CUDA tensor")
-    E = offsets.shape[0]
+    E = _small(offsets.shape[0])
     _check(offsets, "offsets", torch.int32, (E,), dev)
-    a, M, K = _operand("a", a_codes, a_scales, a_gscale, dev, E)
-    b, N, Kb = _operand("b", b_codes, b_scales, b_gscale, dev, E)
+    a, M, K, loose_a = _operand("a", a_codes, a_scales, a_gscale, dev, E)
+    b, N, Kb, loose_b = _operand("b", b_codes, b_scales, b_gscale, dev, E)
     if K != Kb:
         raise ValueError("a and b must have the same capacity, not %d and %d" % (K, Kb))
     if accumulate and out is None:
@@ -806,9 +830,9 @@ def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_g
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
     out = _out(out, "out", out_dtype, (E, M, N), dev)
-    status = L.nvfp4_gemm_grouped_wgrad(a, b, offsets.data_ptr(), _small(E), M, N, K,
-                                        out.element_size(), int(bool(accumulate)),
-                                        out.data_ptr(), _stream(dev))
+    at, room, workspace = _gemm_workspace(workspace, a, b, M, N, K, 1, loose_a or loose_b, dev)
+    status = L.nvfp4_gemm_grouped_wgrad(a, b, offsets.data_ptr(), E, M, N, K, out.element_size(),
+                                        int(bool(accumulate)), out.data_ptr(), at, room, _stream(dev))
     _raise_if(status, "nvfp4_gemm_grouped_wgrad")
     return out
 

@@ -9,8 +9,8 @@
 //
 // A warp loads (TMA), one issues the matrix instructions, two or three turn the scales, the others are the
 // epilogue. `p` is the operand on the instruction's 128-row side, `q` the one on its N side:
-//   <2, 256, false>  a pair of CTAs has 256 x 256 of out; p is a, q is b
-//   <1, NT, true>    a CTA has 128 columns of out (p is b, the weights) and NT rows (q is a, tokens):
+//   <2, 256, .>      a pair of CTAs has 256 x 256 of out; p is a, q is b
+//   <1, NT, false>   a CTA has 128 columns of out (p is b, the weights) and NT rows (q is a, tokens):
 //                    few tokens waste no tensor-core rows, and a warp's stores run along out's rows.
 //                    Where there are fewer tiles than SMs, the CTAs of a cluster share a tile's K and
 //                    add up their sums through distributed shared memory.
@@ -64,13 +64,15 @@ struct TcArgs {
   uint32_t* status;
 };
 
-template <int CTAS, int NT, bool SWAP = CTAS == 1>
+// LONG: outputs of 4 bytes, whose epilogue is twice as long, get two staging boxes a warp for one stage
+// less (weight gradient of 32768 rows 618 -> 540 us; BF16 8192 x 14336 x 4096 172 -> 180).
+template <int CTAS, int NT, bool LONG>
 struct Shape {
   static constexpr int kQRows = NT / CTAS;                       // rows of q that a CTA loads
   static constexpr int kQBlocks = (NT + 127) / 128;              // blocks of 128 rows of scales
   static constexpr int kQBytes = kQRows * kBlockK / 2;
   static constexpr int kStage = kPBytes + kQBytes + (1 + kQBlocks) * kScaleBlock;
-  static constexpr int kStages = CTAS == 2 ? 5 : NT == 32 ? 8 : NT == 64 ? 7 : 6;
+  static constexpr int kStages = CTAS == 2 ? (LONG ? 4 : 5) : NT == 32 ? 8 : NT == 64 ? 7 : 6;
   static constexpr int kPerSm = 1;
   static constexpr int kColumns = kPerSm == 2 ? 256 : 512;       // of tensor memory
   // Two accumulators. Of 256 columns they overlap by 64: those are read first, and the next tile's
@@ -80,7 +82,8 @@ struct Shape {
   static constexpr int kScaleColumn = NT == 256 ? 448 : 2 * NT;
   static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
   static constexpr int kStageSlots = kBlockK / 64 * kSlot;
-  static constexpr int kOutBox = SWAP ? 0 : 32 * 64;  // a warp's staging of out
+  static constexpr int kBoxes = CTAS == 1 ? 0 : LONG ? 2 : 1;  // a warp's staging of out
+  static constexpr int kOutBox = kBoxes * 32 * 64;
   static constexpr int kSmem = kStages * kStage + 1024 + kOutBox * (CTAS == 2 ? 8 : 4);
   // warps: the epilogue (a multiple of four: a warp reads the lane quarter of its number), loads, matrix
   // instructions, scales of p, a block of 128 scales of q each
@@ -104,8 +107,9 @@ struct Table {
 };
 
 // The experts' tiles, by all threads. Offsets out of order leave no tiles.
-template <int CTAS, int NT, bool SWAP>
+template <int CTAS, int NT, bool LONG>
 __device__ __forceinline__ void make_table(const TcArgs& a, Table& t) {
+  constexpr bool SWAP = CTAS == 1;
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   if (e == 0) t.bad = 0;
   __syncthreads();
@@ -150,16 +154,17 @@ __device__ __forceinline__ void make_table(const TcArgs& a, Table& t) {
   __syncthreads();
 }
 
-template <int CTAS, int NT, bool SWAP>
+template <int CTAS, int NT, bool LONG>
 __device__ __forceinline__ int tile_count(const TcArgs& a, const Table& t) {
   if (a.mode != kGemmDense) return t.first[a.E];
   return ((a.p.rows + 128 * CTAS - 1) / (128 * CTAS)) * ((a.q.rows + NT - 1) / NT);
 }
 
 // Tile number `i`, of expert `e` or one behind it. Eight tiles of p share their tiles of q in turn.
-template <int CTAS, int NT, bool SWAP>
+template <int CTAS, int NT, bool LONG>
 __device__ __forceinline__ Tile get_tile(const TcArgs& a, const Table& t, int i, int e, int split, int splits) {
   Tile x;
+  constexpr bool SWAP = CTAS == 1;
   constexpr int kPt = 128 * CTAS;
   x.p0 = x.q0 = x.pz = x.qz = 0;
   x.p_rows = a.p.rows;
@@ -219,6 +224,28 @@ __device__ __forceinline__ uint4 shifted(const uint4& lo, const uint4& hi, uint3
   return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
+// Rows of scales that start anywhere, copied to rows that start on 16-byte boundaries: a warp a row. The
+// pair's kernel takes a quarter longer with the loads that it would need for the former (weight gradient
+// of 32768 rows, 7168 + 2048 columns: 540 us, with this copy 470).
+constexpr int kAlignWarps = 8;
+__global__ void __launch_bounds__(32 * kAlignWarps) align_rows_kernel(const uint8_t* from, int64_t pitch,
+                                                                      int64_t batch, int32_t rows, int32_t all,
+                                                                      int32_t width, uint8_t* to,
+                                                                      int64_t to_pitch) {
+  pdl_wait();
+  pdl_allow_next();
+  const int lane = threadIdx.x & 31;
+  for (int32_t r = blockIdx.x * kAlignWarps + (threadIdx.x >> 5); r < all; r += gridDim.x * kAlignWarps) {
+    const uint8_t* const p = from + (int64_t)(r / rows) * batch + (int64_t)(r % rows) * pitch;
+    const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+    for (int c = 16 * lane; c < width; c += 512) {
+      const uint8_t* const at = p - shift + c;
+      const uint4 lo = load_chunk(at, p + width), hi = load_chunk(at + 16, p + width);
+      *reinterpret_cast<uint4*>(to + r * to_pitch + c) = shifted(lo, hi, shift);
+    }
+  }
+}
+
 // Bytes [lo, hi) of 16 stay.
 __device__ __forceinline__ uint32_t byte_mask(int lo, int hi, int word) {
   uint32_t m = 0u;
@@ -246,17 +273,17 @@ __device__ __forceinline__ void put_scales(uint32_t addr, const uint4& v0, const
 
 // A warp turns one block of scales of every stage: rows `row_shift`.. of the tile's rows of p or q, of
 // which ROWS exist. Then it arrives on the pair's `ready`.
-template <int CTAS, int NT, bool SWAP, int ROWS>
+template <int CTAS, int NT, bool LONG, int ROWS>
 __device__ __forceinline__ void turn_scales(const TcArgs& a, const SideArgs& s, const Table& table,
                                             const Tile& first_tile, int tiles,
                                             int cluster, int clusters, int split, int splits, bool is_q,
                                             uint32_t blocks, uint64_t* landed, uint64_t* ready, int row_shift) {
-  using S = Shape<CTAS, NT>;
+  using S = Shape<CTAS, NT, LONG>;
   const int lane = threadIdx.x & 31;
   int it = 0;
   Tile x = first_tile;
   for (int i = cluster; i < tiles; i += clusters) {
-    if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
+    if (i != cluster) x = get_tile<CTAS, NT, LONG>(a, table, i, x.e, split, splits);
     // Where rows start anywhere: aligned loads, two stages ahead. A stage is 16 bytes of a row, so that
     // its upper part is the next stage's lower one.
     uint4 lo[4], hi[4], next[4];
@@ -425,14 +452,19 @@ __device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint
     if (i < have) to[i * stride] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
 }
 
-// A warp's 32 rows x 64 bytes to a box of a map, a lane's row in w, through its staging buffer (rows of
-// 64 bytes in the 64-byte swizzle: the 16-byte stores of eight lanes meet eight different bank groups).
+// A warp's 32 rows x 64 bytes to a box of a map, a lane's row in w, through a staging buffer of the warp's
+// (rows of 64 bytes in the 64-byte swizzle: the 16-byte stores of eight lanes meet eight different bank
+// groups), of which it has BOXES, used in turn.
 // Stores straight from the lanes touch 32 lines each: the weight gradient of 32768 rows took 733 us with
 // them, 612 in boxes.
-__device__ __forceinline__ void store_box(uint32_t buffer, const CUtensorMap* map, const uint32_t (&w)[16],
+template <int BOXES>
+__device__ __forceinline__ void store_box(uint32_t& buffer, const CUtensorMap* map, const uint32_t (&w)[16],
                                           int32_t x, int32_t y, int32_t z) {
   const uint32_t lane = threadIdx.x & 31;
-  if (elect_one()) bulk_wait_read();
+  if (elect_one()) {
+    if (BOXES == 2) bulk_wait_read_but_one();
+    else bulk_wait_read();
+  }
   __syncwarp();
   const uint32_t row = buffer + lane * 64, turn = (lane >> 1) & 3u;
 #pragma unroll
@@ -446,6 +478,7 @@ __device__ __forceinline__ void store_box(uint32_t buffer, const CUtensorMap* ma
     tma_store_box(map, buffer, x, y, z);
     bulk_commit();
   }
+  if (BOXES == 2) buffer ^= 32 * 64;
   __syncwarp();
 }
 // Where a warp's rows leave in boxes.
@@ -458,15 +491,15 @@ struct BoxAt {
 // `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
 // aligned. With BOXES a warp's rows may leave together, `live` or not. Returns the largest |out| as
 // binary32 bits.
-template <bool BOXES, int P>
+template <int BOXES, int P>
 __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], const uint32_t (&residual)[2 * P],
                                            int64_t at, int64_t stride, int have, bool whole, bool live,
-                                           const BoxAt& box) {
+                                           BoxAt& box) {
   uint32_t w[P];
   if (a.preact != nullptr) {
     pack_pairs(z, w);
-    if constexpr (BOXES) {
-      if (box.buffer) store_box(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
+    if constexpr (BOXES > 0) {
+      if (box.buffer) store_box<BOXES>(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
     }
     if ((!BOXES || !box.buffer) && live) store_pairs(a, a.preact, w, at, stride, have, whole);
   }
@@ -477,8 +510,8 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
       for (int i = 0; i < P; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
     }
     pack_pairs(z, w);
-    if constexpr (BOXES) {
-      if (box.buffer) store_box(box.buffer, &a.out_map, w, box.x, box.y, box.z);
+    if constexpr (BOXES > 0) {
+      if (box.buffer) store_box<BOXES>(box.buffer, &a.out_map, w, box.x, box.y, box.z);
     }
     if ((!BOXES || !box.buffer) && live) store_pairs(a, a.out, w, at, stride, have, whole);
     if (a.amax == nullptr || !live) return 0u;
@@ -505,13 +538,13 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
     o[2 * i + 1] = __float_as_uint(f.y);
   }
   uint32_t* const to = static_cast<uint32_t*>(a.out) + at;
-  if constexpr (BOXES) {
+  if constexpr (BOXES > 0) {
     if (box.buffer) {
 #pragma unroll
       for (int h = 0; h < 2; h++) {
 #pragma unroll
         for (int i = 0; i < 16; i++) w[i] = o[16 * h + i];
-        store_box(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
+        store_box<BOXES>(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
       }
     }
   }
@@ -553,10 +586,11 @@ __device__ __forceinline__ void clear(void* p, int64_t lo, int64_t hi, int64_t a
 
 // ---- the kernel -----------------------------------------------------------------------------------
 
-template <int CTAS, int NT, bool SWAP>
-__global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>::kPerSm))
+template <int CTAS, int NT, bool LONG>
+__global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS, NT, LONG>::kPerSm))
     gemm_kernel(const __grid_constant__ TcArgs a, int splits) {
-  using S = Shape<CTAS, NT>;
+  using S = Shape<CTAS, NT, LONG>;
+  constexpr bool SWAP = CTAS == 1;  // out's rows are q's
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[S::kStages], landed[S::kStages], ready[S::kStages], empty[S::kStages], acc_full[2], acc_free[2];
   __shared__ uint32_t tmem_base;
@@ -596,12 +630,12 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   const uint32_t tmem = tmem_base;
   if (a.mode != kGemmDense) {
     pdl_wait();
-    make_table<CTAS, NT, SWAP>(a, table);
+    make_table<CTAS, NT, LONG>(a, table);
   }
-  const int tiles = tile_count<CTAS, NT, SWAP>(a, table);
+  const int tiles = tile_count<CTAS, NT, LONG>(a, table);
   // (in a dense product before the previous kernel has ended: it takes five divisions)
   Tile first = {};
-  if (cluster < tiles) first = get_tile<CTAS, NT, SWAP>(a, table, cluster, 0, split, splits);
+  if (cluster < tiles) first = get_tile<CTAS, NT, LONG>(a, table, cluster, 0, split, splits);
   pdl_wait();
   pdl_allow_next();
 
@@ -613,7 +647,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     bool alive = true;
     Tile x = first;
     for (int i = cluster; i < tiles && alive; i += clusters) {
-      if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
+      if (i != cluster) x = get_tile<CTAS, NT, LONG>(a, table, i, x.e, split, splits);
       for (int kb = x.kb0; kb < x.kb1; kb++, it++) {
         const int stage = it % S::kStages;
         alive = wait_phase(&empty[stage], ((uint32_t)(it / S::kStages) & 1u) ^ 1u);
@@ -651,7 +685,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
       bool alive = true;
       Tile x = first;
       for (int i = cluster; i < tiles; i += clusters, count++) {
-        if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
+        if (i != cluster) x = get_tile<CTAS, NT, LONG>(a, table, i, x.e, split, splits);
         const uint32_t acc = tmem + (count & 1) * S::kAccStride;
         // an accumulator's barrier completes once for each of its tiles, and is never a phase ahead
         if (count >= S::kLag)
@@ -699,11 +733,11 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
       }
     }
   } else if (warp == S::kEpi + 2) {
-    turn_scales<CTAS, NT, SWAP, 128>(a, a.p, table, first, tiles, cluster, clusters, split, splits, false,
+    turn_scales<CTAS, NT, LONG, 128>(a, a.p, table, first, tiles, cluster, clusters, split, splits, false,
                                      stages + kPBytes + S::kQBytes, landed, ready, 128 * half);
   } else if (warp > S::kEpi + 2) {
     const int block = warp - S::kEpi - 3;
-    turn_scales<CTAS, NT, SWAP, (NT < 128 ? NT : 128)>(a, a.q, table, first, tiles, cluster, clusters, split, splits, true,
+    turn_scales<CTAS, NT, LONG, (NT < 128 ? NT : 128)>(a, a.q, table, first, tiles, cluster, clusters, split, splits, true,
                                                        stages + kPBytes + S::kQBytes + kScaleBlock * (1 + block),
                                                        landed, ready, 128 * block);
   } else {
@@ -712,11 +746,11 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
     constexpr int kChunks = NT / 32, kStep = S::kEpi / 4;  // kStep warps share a quarter's chunks in turn
     constexpr int kFreed = S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks;
     float* const mine = bias_stage[warp];
-    const uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
+    uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
     int count = 0;
     Tile x = first;
     for (int i = cluster; i < tiles; i += clusters, count++) {
-      if (i != cluster) x = get_tile<CTAS, NT, SWAP>(a, table, i, x.e, split, splits);
+      if (i != cluster) x = get_tile<CTAS, NT, LONG>(a, table, i, x.e, split, splits);
       const float alpha = a.a_gscale[2 * x.e + 1] * a.b_gscale[2 * x.e + 1];
       const int r = 128 * half + 32 * quarter + lane;  // row of the tile
       const bool live = r < x.p_rows;
@@ -747,7 +781,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
         const int rows_left = x.p_rows - 128 * half - 32 * quarter;
         const bool boxes = !SWAP && a.boxes != 0 && rows_left > 0 && left > 0 &&
                            (a.mode != kGemmGrouped || rows_left >= 32);
-        const BoxAt box = {boxes ? staging : 0u, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
+        BoxAt box = {boxes ? staging : 0u, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
         uint32_t v[32], residual[32];
         if (a.residual != nullptr && counts) load_residual<16>(a, residual, at, stride, left, whole);
         if (!SWAP && a.bias != nullptr) {
@@ -795,7 +829,8 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
             }
           }
         }
-        if (counts || boxes) top = max(top, finish<!SWAP, 16>(a, z, residual, at, stride, left, whole, counts, box));
+        if (counts || boxes) top = max(top, finish<S::kBoxes, 16>(a, z, residual, at, stride, left, whole, counts, box));
+        if (boxes) staging = box.buffer;
       }
       if (splits == 1) report_amax(a, top, x.e);
     }
@@ -820,6 +855,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
       if (r < x.p_rows) {
         const float bias = a.bias ? bias_at(a, x.p0 + r) : 0.0f;
         const uint64_t alpha2 = f2_pack(alpha, alpha), bias2 = f2_pack(bias, bias);
+        BoxAt none = {};
         constexpr int kTurn = 8;  // rows of q whose loads are under way together
         for (int c = kTurn * split; c < min(NT, x.q_rows); c += kTurn * splits) {
           const int64_t at = (int64_t)(x.q0 + c) * a.N + x.p0 + r;
@@ -839,7 +875,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
             z[j] = f2_mul(z[j], alpha2);
             if (a.bias != nullptr) z[j] = f2_add(z[j], bias2);
           }
-          top = max(top, finish<false, kTurn / 2>(a, z, residual, at, a.N, x.q_rows - c, false, true, BoxAt()));
+          top = max(top, finish<0, kTurn / 2>(a, z, residual, at, a.N, x.q_rows - c, false, true, none));
         }
       }
       report_amax(a, top, x.e);
@@ -853,12 +889,12 @@ __global__ void __launch_bounds__((Shape<CTAS, NT>::kThreads), (Shape<CTAS, NT>:
   if (warp == S::kEpi + 1) tmem_free<CTAS>(tmem, S::kColumns);
 }
 
-template <int CTAS, int NT, bool SWAP>
+template <int CTAS, int NT, bool LONG>
 cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(Shape<CTAS, NT>::kThreads);
-  cfg.dynamicSmemBytes = Shape<CTAS, NT>::kSmem;
+  cfg.blockDim = dim3(Shape<CTAS, NT, LONG>::kThreads);
+  cfg.dynamicSmemBytes = Shape<CTAS, NT, LONG>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -868,14 +904,19 @@ cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CTAS, NT, SWAP>, a, splits);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CTAS, NT, LONG>, a, splits);
 }
-template <int CTAS, int NT, bool SWAP>
+template <int CTAS, int NT, bool LONG>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(gemm_kernel<CTAS, NT, SWAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Shape<CTAS, NT>::kSmem);
+  return cudaFuncSetAttribute(gemm_kernel<CTAS, NT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<CTAS, NT, LONG>::kSmem);
 }
 
+int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+bool scales_aligned(const nvfp4_operand& o, int64_t rows, int32_t experts) {
+  return ((reinterpret_cast<uintptr_t>(o.scales) | (uintptr_t)(rows > 1 ? o.scale_pitch : 0) |
+           (uintptr_t)(experts > 1 ? o.scale_batch : 0)) & 15u) == 0;
+}
 // The maps of an operand for boxes of `box_rows` rows of codes and `scale_rows` of scales.
 bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int32_t experts, int box_rows,
                int scale_rows) {
@@ -883,14 +924,11 @@ bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int
   s.scale_pitch = o.scale_pitch;
   s.scale_batch = experts > 1 ? o.scale_batch : 0;
   s.rows = (int32_t)rows;
-  const uintptr_t all = reinterpret_cast<uintptr_t>(o.scales) | (uintptr_t)(rows > 1 ? s.scale_pitch : 0) |
-                        (uintptr_t)s.scale_batch;
-  s.tma = all % 16 == 0;
+  s.tma = scales_aligned(o, rows, experts);
   if (K == 0) {  // nothing is loaded
     s.tma = 0;
     return true;
   }
-  auto up16 = [](int64_t v) { return (v + 15) / 16 * 16; };
   auto encode = [&](CUtensorMap* map, const uint8_t* p, int64_t width, int64_t pitch, int64_t batch, int box_x,
                     int box_y, CUtensorMapSwizzle swizzle) {
     // a single row has any pitch, a single expert any distance
@@ -908,6 +946,25 @@ bool make_side(SideArgs& s, const nvfp4_operand& o, int64_t rows, int64_t K, int
     return false;
   return !s.tma || encode(&s.scales, o.scales, K / 16, s.scale_pitch, s.scale_batch, 16, scale_rows,
                           CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// The operand with its scales copied to `workspace` where their rows are not aligned and it has room.
+cudaError_t align_scales(nvfp4_operand& o, int64_t rows, int64_t K, int32_t experts, uint8_t*& workspace,
+                         int64_t& bytes, int sm_count, cudaStream_t s) {
+  const int64_t pitch = up16(K / 16), need = pitch * rows * experts;
+  if (K == 0 || scales_aligned(o, rows, experts) || bytes < need || rows * experts > INT32_MAX - (1 << 20))
+    return cudaSuccess;
+  const int64_t all = rows * experts, ctas = (all + kAlignWarps - 1) / kAlignWarps;
+  const cudaError_t e = launch_pdl(align_rows_kernel, dim3((unsigned)(ctas < 8 * sm_count ? ctas : 8 * sm_count)),
+                                   dim3(32 * kAlignWarps), 0, s, o.scales, o.scale_pitch,
+                                   experts > 1 ? o.scale_batch : (int64_t)0, (int32_t)rows, (int32_t)all,
+                                   (int32_t)(K / 16), workspace, pitch);
+  o.scales = workspace;
+  o.scale_pitch = pitch;
+  o.scale_batch = pitch * rows;
+  workspace += need;
+  bytes -= need;
+  return e;
 }
 
 bool make_out_maps(TcArgs& t, const GemmArgs& g) {
@@ -928,10 +985,18 @@ bool make_out_maps(TcArgs& t, const GemmArgs& g) {
 
 cudaError_t prepare_gemm_kernels() {
   cudaError_t e = prepare_one<2, 256, false>(), r;
-  if ((r = prepare_one<1, 32, true>()) != cudaSuccess) e = r;
-  if ((r = prepare_one<1, 64, true>()) != cudaSuccess) e = r;
-  if ((r = prepare_one<1, 128, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<2, 256, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<1, 32, false>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<1, 64, false>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<1, 128, false>()) != cudaSuccess) e = r;
   return e;
+}
+
+int64_t gemm_workspace(const GemmArgs& g) {
+  const int32_t b_experts = g.mode == kGemmGrouped ? g.E : 1;
+  const int64_t pitch = up16(g.K / 16);
+  return (scales_aligned(g.a, g.M, 1) ? 0 : pitch * g.M) +
+         (scales_aligned(g.b, g.N, b_experts) ? 0 : pitch * g.N * b_experts);
 }
 
 cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
@@ -981,11 +1046,18 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   const int64_t tiles = up(rows_a, x.rows) * up(g.N, x.cols);
   if (best == 3) {
     t.q_rows = 128;
-    if (!make_side(t.p, g.a, g.M, g.K, 1, 128, 128) || !make_side(t.q, g.b, g.N, g.K, b_experts, 128, 256))
+    nvfp4_operand oa = g.a, ob = g.b;
+    uint8_t* work = static_cast<uint8_t*>(g.workspace);
+    int64_t room = work != nullptr ? (int64_t)g.workspace_bytes : 0;
+    cudaError_t e = align_scales(oa, g.M, g.K, 1, work, room, sm_count, s);
+    if (e == cudaSuccess) e = align_scales(ob, g.N, g.K, b_experts, work, room, sm_count, s);
+    if (e != cudaSuccess) return e;
+    if (!make_side(t.p, oa, g.M, g.K, 1, 128, 128) || !make_side(t.q, ob, g.N, g.K, b_experts, 128, 256))
       return cudaErrorInvalidValue;
     if (t.boxes && !make_out_maps(t, g)) return cudaErrorInvalidValue;
     const int64_t most = g.mode == kGemmDense ? tiles : sm_count / 2;
-    return launch_one<2, 256, false>(t, (int)(2 * (most < sm_count / 2 ? most : sm_count / 2)), 1, s);
+    const int grid = (int)(2 * (most < sm_count / 2 ? most : sm_count / 2));
+    return g.out_bytes == 4 ? launch_one<2, 256, true>(t, grid, 1, s) : launch_one<2, 256, false>(t, grid, 1, s);
   }
   t.q_rows = (int32_t)(g.M < x.rows ? g.M : x.rows);  // out-of-range rows of a box take as long as others
   if (!make_side(t.p, g.b, g.N, g.K, b_experts, 128, 128) || !make_side(t.q, g.a, g.M, g.K, 1, t.q_rows, t.q_rows))
@@ -993,9 +1065,9 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
   int64_t grid = (int64_t)sm_count * x.per_sm;
   if (g.mode == kGemmDense && (splits > 1 || tiles < grid)) grid = tiles * splits;
   switch (best) {
-    case 0: return launch_one<1, 32, true>(t, (int)grid, splits, s);
-    case 1: return launch_one<1, 64, true>(t, (int)grid, 1, s);
-    default: return launch_one<1, 128, true>(t, (int)grid, 1, s);
+    case 0: return launch_one<1, 32, false>(t, (int)grid, splits, s);
+    case 1: return launch_one<1, 64, false>(t, (int)grid, 1, s);
+    default: return launch_one<1, 128, false>(t, (int)grid, 1, s);
   }
 }
 

@@ -54,6 +54,11 @@ nvfp4_status check_operand(const nvfp4_operand* o, int64_t rows, int64_t K, int3
   return NVFP4_OK;
 }
 
+nvfp4_status check_workspace(const void* workspace, size_t bytes) {
+  if (workspace == nullptr && bytes != 0) return NVFP4_ERR_INVALID_ARG;
+  return aligned(workspace, 16) ? NVFP4_OK : NVFP4_ERR_ALIGN;
+}
+
 nvfp4_status check_epilogue(const nvfp4_epilogue* e, const void* out, bool empty) {
   if (e == nullptr || (e->out_bytes != 2 && e->out_bytes != 4) || e->activation < NVFP4_ACT_NONE ||
       e->activation > NVFP4_ACT_SILU || (e->bias && e->bias_bytes != 2 && e->bias_bytes != 4))
@@ -78,14 +83,29 @@ void take_epilogue(GemmArgs& g, const nvfp4_epilogue& e) {
 
 }  // namespace
 
+NVFP4_EXPORT nvfp4_status nvfp4_gemm_workspace(const nvfp4_operand* a, const nvfp4_operand* b, int64_t M,
+                                               int64_t N, int64_t K, int32_t E, size_t* bytes) {
+  if (bytes == nullptr || E < 1 || E > kMaxSegments) return NVFP4_ERR_INVALID_ARG;
+  nvfp4_status st = check_sizes(M, N, K);
+  if (st != NVFP4_OK || (st = check_operand(a, M, K, 1)) != NVFP4_OK ||
+      (st = check_operand(b, N, K, E)) != NVFP4_OK)
+    return st;
+  GemmArgs g = {};
+  g.a = *a, g.b = *b;
+  g.M = M, g.N = N, g.K = K, g.mode = kGemmGrouped, g.E = E;
+  *bytes = (size_t)gemm_workspace(g);
+  return NVFP4_OK;
+}
+
 NVFP4_EXPORT nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t M,
                                      int64_t N, int64_t K, const nvfp4_epilogue* epilogue, void* out,
-                                     void* stream) {
+                                     void* workspace, size_t workspace_bytes, void* stream) {
   nvfp4_status st = check_sizes(M, N, K);
   const bool empty = M == 0 || N == 0;
   if (st != NVFP4_OK || (st = check_operand(a, M, K, 1)) != NVFP4_OK ||
       (st = check_operand(b, N, K, 1)) != NVFP4_OK ||
-      (st = check_epilogue(epilogue, out, empty)) != NVFP4_OK)
+      (st = check_epilogue(epilogue, out, empty)) != NVFP4_OK ||
+      (st = check_workspace(workspace, workspace_bytes)) != NVFP4_OK)
     return st;
   int sms = 0;
   uint32_t* status = nullptr;
@@ -97,21 +117,22 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand
   g.a = *a, g.b = *b;
   g.M = M, g.N = N, g.K = K, g.mode = kGemmDense, g.E = 1;
   take_epilogue(g, *epilogue);
-  g.out = out, g.status = status;
+  g.out = out, g.workspace = workspace, g.workspace_bytes = workspace_bytes, g.status = status;
   return cuda_status(launch_gemm(g, sms, s));
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4_operand* b,
                                              const int32_t* offsets, int32_t E, int64_t T, int64_t N,
                                              int64_t K, const nvfp4_epilogue* epilogue, void* out,
-                                             void* stream) {
+                                             void* workspace, size_t workspace_bytes, void* stream) {
   nvfp4_status st = check_sizes(T, N, K);
   const bool empty = T == 0 || N == 0;
   if (st != NVFP4_OK) return st;
   if (E < 1 || E > kMaxSegments || offsets == nullptr) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(offsets, 4)) return NVFP4_ERR_ALIGN;
   if ((st = check_operand(a, T, K, 1)) != NVFP4_OK || (st = check_operand(b, N, K, E)) != NVFP4_OK ||
-      (st = check_epilogue(epilogue, out, empty)) != NVFP4_OK)
+      (st = check_epilogue(epilogue, out, empty)) != NVFP4_OK ||
+      (st = check_workspace(workspace, workspace_bytes)) != NVFP4_OK)
     return st;
   int sms = 0;
   uint32_t* status = nullptr;
@@ -123,14 +144,15 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4
   g.a = *a, g.b = *b;
   g.M = T, g.N = N, g.K = K, g.mode = kGemmGrouped, g.E = E, g.offsets = offsets;
   take_epilogue(g, *epilogue);
-  g.out = out, g.status = status;
+  g.out = out, g.workspace = workspace, g.workspace_bytes = workspace_bytes, g.status = status;
   return cuda_status(launch_gemm(g, sms, s));
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const nvfp4_operand* b,
                                                    const int32_t* offsets, int32_t E, int64_t M,
                                                    int64_t N, int64_t capacity, int32_t out_bytes,
-                                                   int32_t accumulate, void* out, void* stream) {
+                                                   int32_t accumulate, void* out, void* workspace,
+                                                   size_t workspace_bytes, void* stream) {
   nvfp4_status st = check_sizes(M, N, capacity);
   const bool empty = M == 0 || N == 0;
   if (st != NVFP4_OK) return st;
@@ -141,7 +163,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const
   ep.out_bytes = out_bytes;
   if ((st = check_operand(a, M, capacity, 1)) != NVFP4_OK ||
       (st = check_operand(b, N, capacity, 1)) != NVFP4_OK ||
-      (st = check_epilogue(&ep, out, empty)) != NVFP4_OK)
+      (st = check_epilogue(&ep, out, empty)) != NVFP4_OK ||
+      (st = check_workspace(workspace, workspace_bytes)) != NVFP4_OK)
     return st;
   if (accumulate) ep.residual = out;
   if (empty) return NVFP4_OK;
@@ -152,7 +175,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const
   g.a = *a, g.b = *b;
   g.M = M, g.N = N, g.K = capacity, g.mode = kGemmWgrad, g.E = E, g.offsets = offsets;
   take_epilogue(g, ep);
-  g.out = out, g.status = status;
+  g.out = out, g.workspace = workspace, g.workspace_bytes = workspace_bytes, g.status = status;
   return cuda_status(launch_gemm(g, sms, static_cast<cudaStream_t>(stream)));
 }
 

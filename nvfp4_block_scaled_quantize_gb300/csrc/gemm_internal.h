@@ -26,10 +26,14 @@ struct GemmArgs {
   void* preact;
   float* amax;
   void* out;
+  void* workspace;        // 16-byte aligned, or null
+  size_t workspace_bytes;
   uint32_t* status;
 };
 cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s);
 cudaError_t prepare_gemm_kernels();
+// bytes of workspace that spare the large tiles' kernel scales at any address
+int64_t gemm_workspace(const GemmArgs& g);
 
 constexpr int64_t kEpilogueMaxPartials = 512;  // rows of the bias gradient's partial sums
 cudaError_t launch_epilogue_backward(const void* grad, const void* preact, int64_t M, int64_t N,

@@ -88,6 +88,11 @@ __device__ __forceinline__ void tma_store_box(const void* tensor_map, uint32_t f
                : "memory");
 }
 
+// Wait until all but the last of the bulk stores committed by this thread have read their shared memory.
+__device__ __forceinline__ void bulk_wait_read_but_one() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }

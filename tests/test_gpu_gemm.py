@@ -107,6 +107,26 @@ def test_gemm_of_many_tiles(M, N, K, dtype):
     assert api.nvfp4_get_status() == (0, 0)
 
 
+@pytest.mark.parametrize("K,offset", [(288, 0), (512, 3), (2080, 5)])
+def test_large_products_without_a_workspace(K, offset):
+    """Scales whose rows start anywhere are copied to a workspace or, without one, read as they are."""
+    dev = cuda()
+    M, N = 1300, 2056
+    a, b = list(operand(M, K, 81, dev)), list(operand(N, K, 82, dev))
+    for x in (a, b):
+        wide = torch.full((x[1].shape[0], K // 16 + 7), 0x7F, dtype=torch.uint8, device=dev)
+        wide[:, offset:offset + K // 16] = x[1]
+        x[1] = wide[:, offset:offset + K // 16]
+    none = torch.empty(0, dtype=torch.uint8, device=dev)
+    some = torch.empty((M * K // 16 + 16 * M) // 16 * 16, dtype=torch.uint8, device=dev)  # for a alone
+    want = api.nvfp4_gemm(*a, *b)["out"]
+    for workspace in (none, some):
+        for dtype in (torch.bfloat16, torch.float32):
+            got = api.nvfp4_gemm(*a, *b, out_dtype=dtype, workspace=workspace)["out"]
+            check_product(got, values(*a), values(*b))
+        assert torch.equal(api.nvfp4_gemm(*a, *b, workspace=workspace)["out"], want)
+
+
 @pytest.mark.parametrize("activation", ["none", "relu", "relu2", "gelu", "silu"])
 @pytest.mark.parametrize("M,N,K", [(1, 160, 256), (45, 72, 96), (140, 261, 512), (700, 1028, 640)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

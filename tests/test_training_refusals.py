@@ -62,11 +62,11 @@ def epilogue(**kw):
 
 
 def test_gemm(L):
-    def gemm(M=8, N=16, K=64, a=None, b=None, e=None, out=FAKE):
+    def gemm(M=8, N=16, K=64, a=None, b=None, e=None, out=FAKE, ws=0, size=0):
         a = operand(K=K) if a is None else a
         b = operand(K=K) if b is None else b
         e = epilogue() if e is None else e
-        return L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, ctypes.byref(e), p(out), None)
+        return L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, ctypes.byref(e), p(out), p(ws), size, None)
     assert gemm(M=-1) == INVALID and gemm(K=48) == SHAPE and gemm(M=2 ** 31) == SHAPE
     assert gemm(out=0) == INVALID and gemm(out=FAKE + 1) == ALIGN
     for bad in (operand(codes=0), operand(scales=0), operand(gs=0)):
@@ -82,27 +82,38 @@ def test_gemm(L):
                     (epilogue(amax=FAKE + 2), ALIGN)):
         assert gemm(e=e) == want
     assert gemm(out=FAKE + 2, e=epilogue(out_bytes=4)) == ALIGN
+    assert gemm(size=16) == INVALID and gemm(ws=FAKE + 8, size=64) == ALIGN
+    n, loose = ctypes.c_size_t(), operand(scales=FAKE + 1)
+    ask = lambda a, b, E=1: L.nvfp4_gemm_workspace(ctypes.byref(a), ctypes.byref(b), 8, 16, 64, E,  # noqa: E731
+                                                   ctypes.byref(n))
+    wide = operand(spitch=16)
+    assert ask(wide, wide) == OK and n.value == 0
+    assert ask(loose, wide) == OK and n.value == 8 * 16
+    assert ask(operand(), operand()) == OK and n.value == (8 + 16) * 16
+    assert ask(wide, operand(batch=512, sbatch=64), 3) == OK and n.value == 16 * 16 * 3
+    assert ask(wide, wide, 0) == INVALID and ask(wide, operand(pitch=16)) == SHAPE
     a, e = operand(), epilogue()
-    assert L.nvfp4_gemm(None, ctypes.byref(a), 8, 16, 64, ctypes.byref(e), p(FAKE), None) == INVALID
-    assert L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(a), 8, 16, 64, None, p(FAKE), None) == INVALID
+    assert L.nvfp4_gemm(None, ctypes.byref(a), 8, 16, 64, ctypes.byref(e), p(FAKE), None, 0, None) == INVALID
+    assert L.nvfp4_gemm(ctypes.byref(a), ctypes.byref(a), 8, 16, 64, None, p(FAKE), None, 0, None) == INVALID
 
 
 def test_grouped(L):
-    def grouped(T=8, N=16, K=64, E=2, a=None, b=None, offsets=FAKE, out=FAKE):
+    def grouped(T=8, N=16, K=64, E=2, a=None, b=None, offsets=FAKE, out=FAKE, ws=0, size=0):
         a = operand(K=K) if a is None else a
         b = operand(K=K, batch=16 * 32, sbatch=64) if b is None else b
         e = epilogue()
         return L.nvfp4_gemm_grouped(ctypes.byref(a), ctypes.byref(b), p(offsets), E, T, N, K,
-                                    ctypes.byref(e), p(out), None)
+                                    ctypes.byref(e), p(out), p(ws), size, None)
     assert grouped(E=0) == INVALID and grouped(E=257) == INVALID and grouped(offsets=0) == INVALID
     assert grouped(offsets=FAKE + 2) == ALIGN and grouped(K=16) == SHAPE and grouped(out=0) == INVALID
     assert grouped(b=operand()) == SHAPE and grouped(b=operand(batch=520, sbatch=64)) == ALIGN
 
-    def wgrad(M=8, N=16, cap=64, E=2, width=4, acc=0, offsets=FAKE, out=FAKE):
+    def wgrad(M=8, N=16, cap=64, E=2, width=4, acc=0, offsets=FAKE, out=FAKE, ws=0, size=0):
         a = operand(K=cap)
         return L.nvfp4_gemm_grouped_wgrad(ctypes.byref(a), ctypes.byref(a), p(offsets), E, M, N, cap,
-                                          width, acc, p(out), None)
+                                          width, acc, p(out), p(ws), size, None)
     assert wgrad(cap=80) == SHAPE and wgrad(width=1) == INVALID and wgrad(acc=2) == INVALID
+    assert grouped(ws=FAKE + 4, size=64) == ALIGN and wgrad(ws=FAKE + 4, size=64) == ALIGN
     assert wgrad(offsets=0) == INVALID and wgrad(out=0) == INVALID and wgrad(out=FAKE + 2) == ALIGN
     assert wgrad(E=300) == INVALID and wgrad(M=0, out=0) == OK
 
