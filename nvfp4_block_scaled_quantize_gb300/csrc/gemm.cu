@@ -47,7 +47,7 @@ struct SideArgs {
 };
 struct TcArgs {
   SideArgs p, q;
-  CUtensorMap out_map, preact_map;  // boxes of 32 rows x 64 bytes; where `boxes` is set
+  CUtensorMap out_map, preact_map;  // boxes of 32 rows x 32 columns; where `boxes` is set
   const float *a_gscale, *b_gscale;
   const int32_t* offsets;
   int32_t mode, E;
@@ -83,7 +83,7 @@ struct Shape {
   static constexpr int kSlot = 4 + 4 * kQBlocks;                 // columns of the scales of 64 elements of K
   static constexpr int kStageSlots = kBlockK / 64 * kSlot;
   static constexpr int kBoxes = CTAS == 1 ? 0 : LONG ? 2 : 1;  // a warp's staging of out
-  static constexpr int kOutBox = kBoxes * 32 * 64;
+  static constexpr int kOutBox = LONG ? kBoxes * 32 * 128 : kBoxes * 32 * 64;
   static constexpr int kSmem = kStages * kStage + 1024 + kOutBox * (CTAS == 2 ? 8 : 4);
   // warps: the epilogue (a multiple of four: a warp reads the lane quarter of its number), loads, matrix
   // instructions, scales of p, a block of 128 scales of q each
@@ -452,41 +452,43 @@ __device__ __forceinline__ void store_pairs(const TcArgs& a, void* p, const uint
     if (i < have) to[i * stride] = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
 }
 
-// A warp's 32 rows x 64 bytes to a box of a map, a lane's row in w, through a staging buffer of the warp's
-// (rows of 64 bytes in the 64-byte swizzle: the 16-byte stores of eight lanes meet eight different bank
-// groups), of which it has BOXES, used in turn.
+// Where a warp's rows leave in boxes.
+struct BoxAt {
+  uint32_t buffer;  // the warp's staging; 0: they do not
+  uint32_t at;      // of its next buffer
+  int32_t x, y, z;
+};
+
+// A warp's 32 rows of 64 bytes (128 where it has two BOXES, used in turn, and out is binary32) to a box of
+// a map, a lane's row in w, through a staging buffer of the warp's (in the swizzle of that width: the
+// 16-byte stores of eight lanes meet eight different bank groups).
 // Stores straight from the lanes touch 32 lines each: the weight gradient of 32768 rows took 733 us with
 // them, 612 in boxes.
-template <int BOXES>
-__device__ __forceinline__ void store_box(uint32_t& buffer, const CUtensorMap* map, const uint32_t (&w)[16],
-                                          int32_t x, int32_t y, int32_t z) {
+template <int BOXES, int W>
+__device__ __forceinline__ void store_box(BoxAt& box, const CUtensorMap* map, const uint32_t (&w)[W]) {
+  static_assert(W == 16 || W == 32, "rows of 64 or 128 bytes");
   const uint32_t lane = threadIdx.x & 31;
   if (elect_one()) {
     if (BOXES == 2) bulk_wait_read_but_one();
     else bulk_wait_read();
   }
   __syncwarp();
-  const uint32_t row = buffer + lane * 64, turn = (lane >> 1) & 3u;
+  const uint32_t buffer = box.buffer + box.at;
+  const uint32_t row = buffer + lane * (W * 4), turn = W == 16 ? (lane >> 1) & 3u : lane & 7u;
 #pragma unroll
-  for (uint32_t c = 0; c < 4; c++)
+  for (uint32_t c = 0; c < W / 4; c++)
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ turn) << 4)), "r"(w[4 * c]),
                  "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                  : "memory");
   fence_proxy_async();
   __syncwarp();
   if (elect_one()) {
-    tma_store_box(map, buffer, x, y, z);
+    tma_store_box(map, buffer, box.x, box.y, box.z);
     bulk_commit();
   }
-  if (BOXES == 2) buffer ^= 32 * 64;
+  if (BOXES == 2) box.at ^= 32 * 128;
   __syncwarp();
 }
-// Where a warp's rows leave in boxes.
-struct BoxAt {
-  uint32_t buffer;  // 0: they do not
-  int32_t x, y, z;
-};
-
 // z = alpha * sums + bias through the activation and the residual into out: 2 P elements from element
 // `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
 // aligned. With BOXES a warp's rows may leave together, `live` or not. Returns the largest |out| as
@@ -499,7 +501,7 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
   if (a.preact != nullptr) {
     pack_pairs(z, w);
     if constexpr (BOXES > 0) {
-      if (box.buffer) store_box<BOXES>(box.buffer, &a.preact_map, w, box.x, box.y, box.z);
+      if (box.buffer) store_box<BOXES>(box, &a.preact_map, w);
     }
     if ((!BOXES || !box.buffer) && live) store_pairs(a, a.preact, w, at, stride, have, whole);
   }
@@ -511,7 +513,7 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
     }
     pack_pairs(z, w);
     if constexpr (BOXES > 0) {
-      if (box.buffer) store_box<BOXES>(box.buffer, &a.out_map, w, box.x, box.y, box.z);
+      if (box.buffer) store_box<BOXES>(box, &a.out_map, w);
     }
     if ((!BOXES || !box.buffer) && live) store_pairs(a, a.out, w, at, stride, have, whole);
     if (a.amax == nullptr || !live) return 0u;
@@ -539,17 +541,10 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
   }
   uint32_t* const to = static_cast<uint32_t*>(a.out) + at;
   if constexpr (BOXES > 0) {
-    if (box.buffer) {
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-#pragma unroll
-        for (int i = 0; i < 16; i++) w[i] = o[16 * h + i];
-        store_box<BOXES>(box.buffer, &a.out_map, w, box.x + 16 * h, box.y, box.z);
-      }
-    }
+    if (BOXES == 2 && box.buffer) store_box<BOXES>(box, &a.out_map, o);
   }
   if (!live) return 0u;
-  if (!BOXES || !box.buffer) {
+  if (BOXES != 2 || !box.buffer) {
     if (P == 16 && whole) {
 #pragma unroll
       for (int i = 0; i < 2 * P; i += 8) store_words(to + i, a.wide, o + i);
@@ -746,7 +741,8 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
     constexpr int kChunks = NT / 32, kStep = S::kEpi / 4;  // kStep warps share a quarter's chunks in turn
     constexpr int kFreed = S::kLag == 1 ? (NT - S::kAccStride) / 32 : kChunks;
     float* const mine = bias_stage[warp];
-    uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
+    uint32_t staging_at = 0;
+    const uint32_t staging = stages + S::kStages * S::kStage + warp * S::kOutBox;
     int count = 0;
     Tile x = first;
     for (int i = cluster; i < tiles; i += clusters, count++) {
@@ -781,7 +777,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
         const int rows_left = x.p_rows - 128 * half - 32 * quarter;
         const bool boxes = !SWAP && a.boxes != 0 && rows_left > 0 && left > 0 &&
                            (a.mode != kGemmGrouped || rows_left >= 32);
-        BoxAt box = {boxes ? staging : 0u, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
+        BoxAt box = {boxes ? staging : 0u, staging_at, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
         uint32_t v[32], residual[32];
         if (a.residual != nullptr && counts) load_residual<16>(a, residual, at, stride, left, whole);
         if (!SWAP && a.bias != nullptr) {
@@ -830,7 +826,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
           }
         }
         if (counts || boxes) top = max(top, finish<S::kBoxes, 16>(a, z, residual, at, stride, left, whole, counts, box));
-        if (boxes) staging = box.buffer;
+        staging_at = box.at;
       }
       if (splits == 1) report_amax(a, top, x.e);
     }
@@ -971,9 +967,10 @@ bool make_out_maps(TcArgs& t, const GemmArgs& g) {
   auto encode = [&](CUtensorMap* map, CUtensorMapDataType type, void* p, int bytes) {
     const cuuint64_t dims[3] = {(cuuint64_t)g.N, (cuuint64_t)g.M, (cuuint64_t)(g.mode == kGemmWgrad ? g.E : 1)};
     const cuuint64_t strides[2] = {(cuuint64_t)(g.N * bytes), (cuuint64_t)(g.M * g.N * bytes)};
-    const cuuint32_t box[3] = {(cuuint32_t)(64 / bytes), 32, 1}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {32, 32, 1}, one[3] = {1, 1, 1};
     return encode_tiled()(map, type, 3, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          bytes == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   return encode(&t.out_map, g.out_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
