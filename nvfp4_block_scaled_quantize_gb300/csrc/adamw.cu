@@ -63,6 +63,12 @@ __device__ __forceinline__ uint64_t from_e4m3x2(uint32_t pair) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
   return f2_pack(f.x, f.y);
 }
+// A sum of products whose rounding counts: packed additions are merged with packed multiplications into
+// multiply-adds (a moment that lies halfway between two codes then goes the other way), these are not.
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  const float2 x = f2_unpack(a), y = f2_unpack(b);
+  return f2_pack(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t d;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
@@ -245,16 +251,16 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
         v2 = f2_pack(__uint_as_float(r.v[2 * j]), __uint_as_float(r.v[2 * j + 1]));
       }
       const uint64_t x = f2_mul(g, both(grad_scale));
-      m2 = f2_add(f2_mul(m2, both(a.beta1)), f2_mul(x, both(a.rest1)));
-      v2 = f2_add(f2_mul(v2, both(a.beta2)), f2_mul(f2_mul(x, x), both(a.rest2)));
+      m2 = add2(f2_mul(m2, both(a.beta1)), f2_mul(x, both(a.rest1)));
+      v2 = add2(f2_mul(v2, both(a.beta2)), f2_mul(f2_mul(x, x), both(a.rest2)));
       const float2 mf = f2_unpack(m2), vf = f2_unpack(v2);
       m[2 * j] = mf.x, m[2 * j + 1] = mf.y;
       root[2 * j] = __fsqrt_rn(vf.x);
       root[2 * j + 1] = __fsqrt_rn(vf.y);
       const float2 num = f2_unpack(f2_mul(m2, both(step_size)));
-      const float2 den = f2_unpack(f2_add(f2_mul(f2_pack(root[2 * j], root[2 * j + 1]), both(root_scale)), both(a.eps)));
-      const uint64_t update = f2_pack(__fdividef(num.x, den.x), __fdividef(num.y, den.y));
-      const float2 pf = f2_unpack(f2_sub(f2_mul(f2_pack(r.p[2 * j], r.p[2 * j + 1]), keep), update));
+      const float2 den = f2_unpack(add2(f2_mul(f2_pack(root[2 * j], root[2 * j + 1]), both(root_scale)), both(a.eps)));
+      const uint64_t update = f2_pack(-__fdividef(num.x, den.x), -__fdividef(num.y, den.y));
+      const float2 pf = f2_unpack(add2(f2_mul(f2_pack(r.p[2 * j], r.p[2 * j + 1]), keep), update));
       r.p[2 * j] = pf.x, r.p[2 * j + 1] = pf.y;
       if constexpr (!EIGHT) r.v[2 * j] = __float_as_uint(vf.x), r.v[2 * j + 1] = __float_as_uint(vf.y);
       const __nv_bfloat162 b = __floats2bfloat162_rn(pf.x, pf.y);

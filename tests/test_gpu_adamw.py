@@ -156,6 +156,32 @@ def test_steps_with_8_bit_states(grad_dtype, count):
             assert amax[i].item() == w[i].abs().max().item() and torch.equal(w[i], p[i].to(torch.bfloat16))
 
 
+def test_averages_halfway_between_two_codes():
+    """Gradients of a few bits: with a clipping factor of 3/4, 0.9 m + 0.1 g falls halfway between two
+    codes in one element of two hundred, and the rounding of each operation decides."""
+    dev = cuda()
+    n = 32 * 4000
+    g = torch.Generator().manual_seed(9)
+    spread = torch.randn(n // 32, 1, generator=g).exp().expand(-1, 32).reshape(-1) * 1e-3
+    grad = (torch.randn(n, generator=g) * spread).to(torch.bfloat16).to(dev)
+    p = torch.randn(n, generator=g).to(dev)
+    opt = api.AdamW([p], [grad], betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, lr=3e-4, state_bits=8)
+    clip = torch.tensor([0.75], device=dev)
+    keys = ("exp_avg", "exp_avg_scales", "exp_avg_sq", "exp_avg_sq_scales")
+    for step in (40, 41, 42):
+        before = [opt.state[k][0].cpu().numpy().copy() for k in keys]
+        x = p.cpu().numpy().copy()
+        opt.step(step, grad_scale=clip, seed=77)
+        want = step8(x, grad.float().cpu().numpy(), *before, lr=3e-4, b1=0.9, b2=0.95, eps=1e-8, decay=0.1,
+                     step=step, clip=0.75, seed=77, index=0)
+        for k, y in zip(keys, want[1:]):
+            got = opt.state[k][0].cpu().numpy()
+            if k == "exp_avg":  # either zero
+                got, y = np.where(got == 0x80, 0, got), np.where(y == 0x80, 0, y)
+            assert np.array_equal(got, y), (step, k, int((got != y).sum()))
+        grad.mul_(-1.5)
+
+
 def test_the_average_of_squares_moves():
     """Constant gradients after larger ones: the kept root follows its average down, which rounding to
     nearest would not (a step is 0.05% of it, half a code 3% to 6%); and the roots are unbiased."""
