@@ -569,7 +569,7 @@ nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const nvfp4_operan
  *   [M][N], 16-byte aligned, may be grad_out; grad_bias (device) float [N] or NULL, its sums in an
  *   order that depends on the sizes and the device alone; amax (device) float [1] or NULL; workspace
  *   (device), 16-byte aligned, of at least nvfp4_gemm_epilogue_backward_workspace bytes where
- *   grad_bias is asked for. N % 8 == 0. At z = 0 the derivative of RELU is 0. */
+ *   grad_bias is asked for. Any N (a multiple of 16 is fastest). At z = 0 the derivative of RELU is 0. */
 nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, const void* preact, int64_t M,
                                           int64_t N, int32_t activation, void* grad_preact,
                                           float* grad_bias, float* amax, void* workspace,

@@ -856,8 +856,6 @@ def nvfp4_gemm_epilogue_backward(grad_out, preact, activation, grad_preact=None,
     L = _lib.load()
     M, N = grad_out.shape
     dev = grad_out.device
-    if N % 8 != 0:
-        raise ValueError("grad_out must have a multiple of 8 columns")
     _check(preact, "preact", torch.bfloat16, (M, N), dev)
     grad_preact = _out(grad_preact, "grad_preact", torch.bfloat16, (M, N), dev)
     grad_bias = _out(grad_bias, "grad_bias", torch.float32, (N,), dev)

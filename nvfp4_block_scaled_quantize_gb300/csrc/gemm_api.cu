@@ -181,7 +181,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const
 
 NVFP4_EXPORT nvfp4_status nvfp4_gemm_epilogue_backward_workspace(int64_t M, int64_t N, size_t* bytes) {
   if (bytes == nullptr || M < 0 || N < 0) return NVFP4_ERR_INVALID_ARG;
-  if (N % 8 != 0 || M > kMaxDim || N > kMaxDim) return NVFP4_ERR_SHAPE;
+  if (M > kMaxDim || N > kMaxDim) return NVFP4_ERR_SHAPE;
   *bytes = (size_t)(M < kEpilogueMaxPartials ? M : kEpilogueMaxPartials) * (size_t)N * 4;
   return NVFP4_OK;
 }

@@ -453,12 +453,13 @@ def test_two_streams_at_once():
 
 
 @pytest.mark.parametrize("activation", ["none", "relu", "relu2", "gelu", "silu"])
-@pytest.mark.parametrize("M,N", [(1, 8), (3, 2048), (700, 72), (129, 4104), (1030, 1024)])
+@pytest.mark.parametrize("M,N", [(1, 8), (3, 2048), (700, 72), (129, 4104), (1030, 1024), (1, 1), (517, 7),
+                                 (90, 1001), (3, 4098), (1003, 999), (4097, 33)])
 def test_epilogue_backward(activation, M, N):
     dev = cuda()
     g = torch.Generator().manual_seed(M + N)
     z = (2 * torch.randn(M, N, generator=g)).to(torch.bfloat16)
-    z[0, :4] = torch.tensor([0.0, -0.0, 60.0, -60.0])
+    z[0, :4] = torch.tensor([0.0, -0.0, 60.0, -60.0])[:N]
     dy = torch.randn(M, N, generator=g).to(torch.bfloat16)
     z, dy = z.to(dev), dy.to(dev)
     d, db, amax = api.nvfp4_gemm_epilogue_backward(dy, z, activation)
