@@ -664,6 +664,7 @@ def _activation(name):
 
 
 # The structures of the C ABI as packed bytes: a ctypes.Structure costs a microsecond more to make.
+_U8 = torch.uint8
 _OPERAND = struct.Struct("@PPPqqqq")        # _lib.Operand
 _EPILOGUE = struct.Struct("@iii4xPPPP")     # _lib.Epilogue
 _ADAMW_CONFIG = struct.Struct("@ddddqPPQii")  # _lib.AdamWConfig
@@ -683,22 +684,28 @@ def _operand(name, codes, scales, gscale, device, experts=None, stacked=False):
     """(packed nvfp4_operand, rows, K, whether rows of scales start off 16-byte boundaries) of codes
     [.., K/2], scales [.., K/16] and gscale [2] ([E, 2] with experts), checked; stacked: codes and scales
     have a first dimension of experts."""
+    shape, sshape, cs, ss = codes.shape, scales.shape, codes.stride(), scales.stride()
     dim = 3 if stacked else 2
-    _check_rows(codes, name + "_codes", dim, device)
-    _check_rows(scales, name + "_scales", dim, device)
-    shape, sshape = codes.shape, scales.shape
+    if not (codes.dtype is _U8 and scales.dtype is _U8 and len(shape) == dim == len(sshape) and
+            cs[-1] == 1 == ss[-1] and codes.device == device == scales.device):
+        _check_rows(codes, name + "_codes", dim, device)
+        _check_rows(scales, name + "_scales", dim, device)
     K = 2 * shape[-1]
-    if K % 32 != 0 or sshape[-1] * 16 != K or sshape[:-1] != shape[:-1]:
+    rows = shape[-2]
+    if K % 32 != 0 or sshape[-1] * 16 != K or sshape[-2] != rows or (stacked and sshape[0] != shape[0]):
         raise ValueError("%s_codes must be [.., K/2] with K a multiple of 32 and %s_scales [.., K/16]"
                          % (name, name))
-    if stacked and shape[0] != experts:
-        raise ValueError("%s must have %d experts, not %d" % (name, experts, shape[0]))
-    _check(gscale, name + "_gscale", torch.float32, (2,) if experts is None else (experts, 2), device)
-    cs, ss = codes.stride(), scales.stride()
-    at = scales.data_ptr()
-    o = _OPERAND.pack(codes.data_ptr(), at, gscale.data_ptr(), cs[-2], ss[-2], cs[0] if stacked else 0,
-                      ss[0] if stacked else 0)
-    return o, shape[-2], K, (at | ss[-2] | (ss[0] if stacked else 0)) % 16
+    if experts is None:
+        _check(gscale, name + "_gscale", torch.float32, (2,), device)
+    else:
+        if stacked and shape[0] != experts:
+            raise ValueError("%s must have %d experts, not %d" % (name, experts, shape[0]))
+        _check(gscale, name + "_gscale", torch.float32, (experts, 2), device)
+    at, pitch = scales.data_ptr(), ss[-2]
+    if stacked:
+        return (_OPERAND.pack(codes.data_ptr(), at, gscale.data_ptr(), cs[1], pitch, cs[0], ss[0]), rows, K,
+                (at | pitch | ss[0]) & 15)
+    return _OPERAND.pack(codes.data_ptr(), at, gscale.data_ptr(), cs[0], pitch, 0, 0), rows, K, (at | pitch) & 15
 
 
 def _gemm_workspace(workspace, a, b, M, N, K, E, loose, dev):
@@ -747,8 +754,11 @@ def _gemm_epilogue(bias, bias_shape, activation, residual, out, out_dtype, shape
     return e, got
 
 
-def _device_of(codes, name):
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda:
+def _device_of(codes, name, *others):
+    for t in (codes,) + others:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("operands must be tensors")
+    if not codes.is_cuda:
         raise TypeError("%s must live on a CUDA device" % name)
     return codes.device
 
@@ -764,7 +774,7 @@ def nvfp4_gemm(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale, bias=No
     the activation's input, which nvfp4_gemm_epilogue_backward takes; with with_amax, amax float32 [1]:
     max |out|, the amax_row of the next quantization. workspace: a uint8 tensor, used (and made here where
     none is given) by large products whose scales' rows do not start on 16-byte boundaries."""
-    dev = _device_of(a_codes, "a_codes")
+    dev = _device_of(a_codes, "a_codes", a_scales, b_codes, b_scales)
     L = _lib.load()
     a, M, K, loose_a = _operand("a", a_codes, a_scales, a_gscale, dev)
     b, N, Kb, loose_b = _operand("b", b_codes, b_scales, b_gscale, dev)
@@ -787,7 +797,7 @@ def nvfp4_gemm_grouped(a_codes, a_scales, a_gscale, b_codes, b_scales, b_gscale,
     columnwise outputs of stacked weights [E * N', K'], as [K', E, N'/2] with the first two dimensions
     exchanged, are the operand of the backward pass). bias [E, N], amax [E]; the rest as nvfp4_gemm.
     Rows past the last end are not read and get zeros."""
-    dev = _device_of(a_codes, "a_codes")
+    dev = _device_of(a_codes, "a_codes", a_scales, b_codes, b_scales)
     L = _lib.load()
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         raise TypeError("offsets must be a 1-D int32 CUDA tensor")
@@ -812,7 +822,7 @@ def nvfp4_gemm_grouped_wgrad(a_codes, a_scales, a_gscale, b_codes, b_scales, b_g
     [E, M, N]) from the columnwise outputs of nvfp4_quantize_grouped for two packed tensors with these
     offsets: codes [M or N, capacity / 2], scales [.., capacity / 16], gscale [E, 2] (both with the same
     RHT signs, or neither). accumulate adds to `out`."""
-    dev = _device_of(a_codes, "a_codes")
+    dev = _device_of(a_codes, "a_codes", a_scales, b_codes, b_scales)
     L = _lib.load()
     if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1:
         raise TypeError("offsets must be a 1-D int32 CUDA tensor")
