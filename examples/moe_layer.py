@@ -5,8 +5,8 @@
 The norm and the SwiGLU keep their inputs in 8 bits for the backward pass; tokens are packed by
 expert and summed back with the router's weights. The rows that enter each of the experts' products
 are quantized to NVFP4 with the amax that the dispatch and the SwiGLU already found: the operands of
-block-scaled GEMMs. This library has no GEMM: the experts' products below are plain torch products
-over each expert's BF16 rows, and main() shows how far the operands are from those.
+block-scaled GEMMs. The experts' products below are plain torch products over each expert's BF16 rows,
+and main() shows how far the operands are from those; moe_nvfp4_step.py multiplies the operands.
 
     python examples/moe_layer.py [--tokens 512 --hidden 1024 --width 512 --experts 8 --topk 2]
 """
@@ -63,8 +63,8 @@ class MoELayer:
 
     def forward(self, x):
         n = api.nvfp4_rmsnorm_checkpoint(x, self.norm)
-        logits, ids = (n["y"].float() @ self.router).topk(self.topk, dim=1)
-        weights = torch.softmax(logits, dim=1)
+        logits = n["y"].float() @ self.router
+        ids, weights = api.nvfp4_moe_router(logits, self.topk)
         plan = api.nvfp4_moe_plan(ids, self.experts)
         packed, amax = api.nvfp4_moe_dispatch(n["y"], plan)
         operands = api.nvfp4_quantize_grouped(packed, plan["offsets"], columnwise=False,
@@ -77,8 +77,8 @@ class MoELayer:
         y = expert_products(act["y"], self.w2, ends)
         out = x + api.nvfp4_moe_combine(y, weights, plan)
         # what the backward pass needs; the norm's and the SwiGLU's inputs in 8 bits
-        self.saved = dict(norm={k: n[k] for k in ("codes", "scales", "rstd")}, n=n["y"], ids=ids,
-                          weights=weights, plan=plan, ends=ends, packed=packed, y=y,
+        self.saved = dict(norm={k: n[k] for k in ("codes", "scales", "rstd")}, n=n["y"],
+                          logits=logits, ids=ids.long(), weights=weights, plan=plan, ends=ends, packed=packed, y=y,
                           glu={k: act[k] for k in ("codes", "scales")}, act=act["y"],
                           operands={"packed": operands, "act": act_operands})
         return out, operands
@@ -94,10 +94,7 @@ class MoELayer:
         grads["w1"] = expert_weight_gradients(s["packed"], grad_h, ends)
         grad_packed = expert_products(grad_h, self.w1.transpose(1, 2), ends)
         grad_n = api.nvfp4_moe_dispatch_backward(grad_packed, plan)
-        # the router: softmax over the chosen logits
-        grad_top = s["weights"] * (grad_w - (grad_w * s["weights"]).sum(1, keepdim=True))
-        grad_logits = torch.zeros(grad_top.shape[0], self.experts, device=grad_top.device)
-        grad_logits.scatter_(1, s["ids"], grad_top)
+        grad_logits = api.nvfp4_moe_router_backward(grad_w, s["logits"], s["ids"].int())
         grads["router"] = s["n"].float().t() @ grad_logits
         grad_n = (grad_n.float() + grad_logits @ self.router.t()).to(torch.bfloat16)
         grads["x"], grads["norm"] = api.nvfp4_rmsnorm_checkpoint_backward(

@@ -349,7 +349,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, in
   if (count == 0) return NVFP4_OK;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = zero_words(amax, count, s);
   AdamwArgs a;

@@ -97,6 +97,8 @@ cudaError_t launch_rmsnorm_checkpoint_backward(const RmsArgs& a, int sm_count, c
 // The current device's SM count, status word and largest cluster of the plan, with the kernels of
 // these two groups set up (nvfp4_api.cu); false when a CUDA call failed.
 bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas = nullptr);
+// The same without those kernels' set-up, with the matrix products' where `gemm` is set.
+bool device_basics(int* sm_count, uint32_t** status, bool gemm = false);
 int setup_fault();  // nvfp4_debug_setup_fault
 // cuTensorMapEncodeTiled; set once a call above has succeeded (nvfp4_api.cu)
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

@@ -109,7 +109,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand
     return st;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status, true)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = zero_words(epilogue->amax, 1, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
@@ -136,7 +136,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped(const nvfp4_operand* a, const nvfp4
     return st;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status, true)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = zero_words(epilogue->amax, E, s);
   if (e != cudaSuccess || empty) return cuda_status(e);
@@ -170,7 +170,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const
   if (empty) return NVFP4_OK;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status, true)) return NVFP4_ERR_CUDA;
   GemmArgs g = {};
   g.a = *a, g.b = *b;
   g.M = M, g.N = N, g.K = capacity, g.mode = kGemmWgrad, g.E = E, g.offsets = offsets;
@@ -203,7 +203,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, con
     return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status)) return NVFP4_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = zero_words(amax, 1, s);
   if (e == cudaSuccess && empty) e = zero_words(grad_bias, N, s);

@@ -28,6 +28,7 @@ static_assert((kFuseWsOffset + kFuseWsWords) * 4 <= (int)kWorkspaceBytes, "works
 struct DeviceState {
   bool ready = false;
   bool aux_ready = false;         // the routing and checkpoint kernels' attributes are set
+  bool gemm_ready = false;        // the matrix products' are
   int sm_count = 0;
   int plan_ctas = 0;              // the largest cluster of the routing plan
   uint32_t* workspace = nullptr;  // [0] status word; the library's own or the caller's
@@ -57,10 +58,17 @@ bool prepare_aux(DeviceState& st) {
   if (g_setup_fault.load() == 1) return false;
   if (st.aux_ready) return true;
   st.aux_ready = prepare_moe_kernels(&st.plan_ctas) == cudaSuccess &&
-                 prepare_checkpoint_kernels() == cudaSuccess &&
-                 prepare_gemm_kernels() == cudaSuccess;
+                 prepare_checkpoint_kernels() == cudaSuccess;
   if (!st.aux_ready) (void)cudaGetLastError();
   return st.aux_ready;
+}
+
+// The same for the matrix products, which depend on none of those and none of those on them.
+bool prepare_gemm(DeviceState& st) {
+  if (st.gemm_ready) return true;
+  st.gemm_ready = prepare_gemm_kernels() == cudaSuccess;
+  if (!st.gemm_ready) (void)cudaGetLastError();
+  return st.gemm_ready;
 }
 
 // Everything of a device's state but its workspace (under g_mutex).
@@ -79,6 +87,7 @@ nvfp4_status init_device(DeviceState& st, int dev) {
     g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   }
   (void)prepare_aux(st);
+  (void)prepare_gemm(st);
   st.ready = true;
   return NVFP4_OK;
 }
@@ -172,6 +181,18 @@ bool device_resources(int* sm_count, uint32_t** status, int* plan_ctas) {
   *sm_count = ds->sm_count;
   *status = ds->workspace;
   if (plan_ctas) *plan_ctas = ds->plan_ctas;
+  return true;
+}
+
+bool device_basics(int* sm_count, uint32_t** status, bool gemm) {
+  DeviceState* ds = nullptr;
+  if (device_state(&ds) != NVFP4_OK) return false;
+  if (gemm) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!prepare_gemm(*ds)) return false;
+  }
+  *sm_count = ds->sm_count;
+  *status = ds->workspace;
   return true;
 }
 

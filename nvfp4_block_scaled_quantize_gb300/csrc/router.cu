@@ -618,7 +618,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_byt
     return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status)) return NVFP4_ERR_CUDA;
   RouterArgs a = {logits, bias, T, E, K, groups, top_groups, E / groups, scale, expert_ids, weights,
                   status};
   const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
@@ -654,7 +654,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, c
     return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;
-  if (!device_resources(&sms, &status)) return NVFP4_ERR_CUDA;
+  if (!device_basics(&sms, &status)) return NVFP4_ERR_CUDA;
   RouterBackArgs a = {grad_weights, logits, expert_ids, T, E, K, scale, grad_logits, status};
   const dim3 grid(router_grid(T, sms)), block(32 * kRouterWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
