@@ -102,8 +102,8 @@ __device__ __forceinline__ int draw(double* values, int n) {
 }
 
 // The row again with binary64 scores, in the warp's shared memory. Lane k gets the k-th choice.
-template <bool SOFTMAX, typename L>
-__device__ __noinline__ int draw_again(const RouterArgs& a, const L* row, double* values, double* ranks) {
+template <typename L>
+__device__ __noinline__ int draw_again(const RouterArgs& a, bool softmax, const L* row, double* values, double* ranks) {
   const int lane = threadIdx.x & 31;
   float top = -INFINITY;
   for (int e = lane; e < a.E; e += 32) top = fmaxf(top, widen<L>(row[e]));
@@ -111,12 +111,12 @@ __device__ __noinline__ int draw_again(const RouterArgs& a, const L* row, double
   double sum = 0.0;
   for (int e = lane; e < a.E; e += 32) {
     const double l = (double)widen<L>(row[e]);
-    values[e] = SOFTMAX ? exp(l - (double)top) : 1.0 / (1.0 + exp(-l));
+    values[e] = softmax ? exp(l - (double)top) : 1.0 / (1.0 + exp(-l));
     sum += values[e];
   }
-  if (SOFTMAX) sum = warp_sum(sum);
+  if (softmax) sum = warp_sum(sum);
   for (int e = lane; e < a.E; e += 32) {
-    if (SOFTMAX) values[e] /= sum;
+    if (softmax) values[e] /= sum;
     if (a.bias) values[e] += (double)__ldg(a.bias + e);
     if (widen<L>(row[e]) == -INFINITY) values[e] = -INFINITY;
   }
@@ -160,18 +160,17 @@ __device__ __noinline__ int draw_again(const RouterArgs& a, const L* row, double
 }
 
 // The weights of the drawn experts: lane k has the k-th (mine >= 0) and its logit x.
-template <bool SOFTMAX>
-__device__ __forceinline__ void put_weights(const RouterArgs& a, bool renorm, int64_t t, int mine, float x,
+__device__ __forceinline__ void put_weights(const RouterArgs& a, bool softmax, bool renorm, int64_t t, int mine, float x,
                                             float top, float inv) {
   const int lane = threadIdx.x & 31;
   float w = 0.0f;
   if (renorm) {
     const float high = warp_max(mine >= 0 ? x : -INFINITY);
-    if (mine >= 0) w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
+    if (mine >= 0) w = softmax ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
     const float sum = warp_sum(w);
     w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
   } else if (mine >= 0) {
-    w = SOFTMAX ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
+    w = softmax ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
   }
   if (lane < a.K) {
     a.ids[t * a.K + lane] = mine;
@@ -244,8 +243,8 @@ __device__ __forceinline__ void store_row(L* row, int E, const float (&d)[SL]) {
 
 // Without bias and groups the order is that of the logits. BF16 logits leave room for the index in the
 // key: one reduction a draw.
-template <int SL, int V, bool SOFTMAX, typename L>
-__global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const RouterArgs a, bool renorm) {
+template <int SL, int V, typename L>
+__global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const RouterArgs a, bool softmax, bool renorm) {
   constexpr bool kShort = sizeof(L) == 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const R
     if (t + step < a.T) load_row<SL, V, L>(logits + (t + step) * a.E, a.E, next);
     bad = __any_sync(kAll, bad);
     float top = 0.0f, inv = 0.0f;
-    if (SOFTMAX && !renorm) {
+    if (softmax && !renorm) {
       top = -INFINITY;
 #pragma unroll
       for (int j = 0; j < SL; j++) top = fmaxf(top, l[j]);
@@ -316,13 +315,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const R
       // (of a negative number the cut-off half of an ascending key is all ones)
       x = from_ascending(kShort ? ((int32_t)kept < 0 ? kept & 0xFFFF0000u : kept | 0xFFFFu) : kept);
     }
-    put_weights<SOFTMAX>(a, renorm, t, mine, x, top, inv);
+    put_weights(a, softmax, renorm, t, mine, x, top, inv);
   }
 }
 
 // With a bias or groups.
-template <int SL, int V, bool SOFTMAX, typename L>
-__global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const RouterArgs a, bool renorm) {
+template <int SL, int V, typename L>
+__global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const RouterArgs a, bool softmax, bool renorm) {
   __shared__ double values[kRouterWarps][kMaxE], ranks[kRouterWarps][kMaxE];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
@@ -344,7 +343,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
     top = warp_max(top);
     // the error of p grows with the largest p of the row
     float tie = 2e-6f;
-    if (SOFTMAX) {
+    if (softmax) {
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
       key[j] = 0u;
       if (e >= a.E) continue;
       float p = 0.0f;  // masked (top may be -inf, too)
-      if (l[j] != -INFINITY) p = SOFTMAX ? __expf(l[j] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-l[j]));
+      if (l[j] != -INFINITY) p = softmax ? __expf(l[j] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-l[j]));
       if (a.bias) {
         const float b = __ldg(a.bias + e);
         p += b;
@@ -457,12 +456,12 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
         }
       }
       __syncwarp();
-      if (close) mine = draw_again<SOFTMAX, L>(a, row, values[warp], ranks[warp]);
+      if (close) mine = draw_again<L>(a, softmax, row, values[warp], ranks[warp]);
     } else if (lane == 0) {
       atomicOr(a.status, kBadRoute);
     }
     const float x = mine >= 0 ? widen<L>(row[mine]) : 0.0f;
-    put_weights<SOFTMAX>(a, renorm, t, mine, x, top, inv);
+    put_weights(a, softmax, renorm, t, mine, x, top, inv);
     __syncwarp();
   }
 }
@@ -483,9 +482,9 @@ struct RouterBackArgs {
 // and without, p (g - sum p g) over all experts (g = 0 where not chosen) and p (1 - p) g. Only the
 // softmax without renormalization reads all logits; the rest gathers the chosen ones. Bound by the
 // write of the gradient.
-template <int SL, int V, bool SOFTMAX, typename L>
+template <int SL, int V, typename L>
 __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(const RouterBackArgs a,
-                                                                            bool renorm) {
+                                                                            bool softmax, bool renorm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_allow_next();
@@ -514,13 +513,13 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
       const float high = warp_max(x);
       float w = 0.0f;
       if (id >= 0 && high > -INFINITY)
-        w = SOFTMAX ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
+        w = softmax ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
       const float sum = warp_sum(w);
       const float r = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
       const float mean = warp_sum(r * g);
       mine = r * (g - mean);
-      if (!SOFTMAX) mine *= __fdividef(1.0f, 1.0f + __expf(x));  // 1 - p
-    } else if (!SOFTMAX) {
+      if (!softmax) mine *= __fdividef(1.0f, 1.0f + __expf(x));  // 1 - p
+    } else if (!softmax) {
       const float p = sigmoid_over(x, 0.0f);
       if (id >= 0) mine = p * __fdividef(1.0f, 1.0f + __expf(x)) * g;
     } else {
@@ -630,10 +629,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_byt
     return by_width<L>(E, reinterpret_cast<uintptr_t>(logits), [&](auto sl, auto v) {
       constexpr int SL = decltype(sl)::value, V = decltype(v)::value;
       if (plain)
-        return launch_pdl(soft ? router_plain_kernel<SL, V, true, L> : router_plain_kernel<SL, V, false, L>, grid,
-                          block, 0, s, a, renorm);
-      return launch_pdl(soft ? router_kernel<SL, V, true, L> : router_kernel<SL, V, false, L>, grid, block, 0, s,
-                        a, renorm);
+        return launch_pdl(router_plain_kernel<SL, V, L>, grid, block, 0, s, a, soft, renorm);
+      return launch_pdl(router_kernel<SL, V, L>, grid, block, 0, s, a, soft, renorm);
     });
   };
   return cuda_status(logit_bytes == 4 ? launch(float()) : launch(__nv_bfloat16()));
@@ -664,9 +661,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, c
     return by_width<L>(E, reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(grad_logits),
                        [&](auto sl, auto v) {
                          constexpr int SL = decltype(sl)::value, V = decltype(v)::value;
-                         return launch_pdl(soft ? router_backward_kernel<SL, V, true, L>
-                                                : router_backward_kernel<SL, V, false, L>,
-                                           grid, block, 0, s, a, renorm);
+                         return launch_pdl(router_backward_kernel<SL, V, L>, grid, block, 0, s, a, soft, renorm);
                        });
   };
   return cuda_status(logit_bytes == 4 ? launch(float()) : launch(__nv_bfloat16()));
