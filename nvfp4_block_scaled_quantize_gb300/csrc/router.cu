@@ -2,8 +2,8 @@
 // of the logits (declared in include/nvfp4.h).
 //
 // A warp has a token, a lane up to SL of its logits. Experts are drawn one by one: a candidate is a
-// 32-bit key that ascends with p + bias (without a bias: with the logit), the warp's largest key and
-// its lowest index are one reduction instruction each (redux.sync). Binary32 scores are off by a few
+// 32-bit key that ascends with p + bias (without a bias: with the logit), the warp's largest key is one
+// reduction instruction (redux.sync). Binary32 scores are off by a few
 // units in the last place, which can exchange two candidates that are close: where two neighbours of
 // the drawn order (or the last kept and the first dropped group) are closer than that error allows,
 // the row is drawn again from binary64 scores. With normal logits that happens to one row in a few
@@ -319,7 +319,95 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_plain_kernel(const R
   }
 }
 
-// With a bias or groups.
+// Descending order of a lane's keys (Batcher's odd-even merge sort of 2, 4 or 8).
+template <int SL>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[SL]) {
+#pragma unroll
+  for (int p = 1; p < SL; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < SL; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; i++)
+          if (i + j + q < SL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t x = k[i + j], y = k[i + j + q];
+            k[i + j] = max(x, y);
+            k[i + j + q] = min(x, y);
+          }
+}
+
+// Keeps the best groups' experts: `choice` (shared, of all experts) ranks the groups, keys of the others
+// become 0. True where binary32 cannot tell the last kept from the first dropped group.
+template <int SL, int V>
+__device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* choice, uint32_t* ranks,
+                                            uint32_t (&key)[SL], float tie) {
+  const int lane = threadIdx.x & 31;
+  if (a.groups <= 32) {  // `lanes` lanes a group, each from an element of its own (other banks)
+    const int lanes = 32 >> (32 - __clz(a.groups - 1)), g = lane / lanes, sub = lane % lanes;
+    float v1 = -INFINITY, v2 = -INFINITY;
+    if (g < a.groups) {
+      const int count = (a.size - sub + lanes - 1) / lanes;  // elements sub, sub + lanes, ...
+      int at = count > 0 ? g % count : 0;
+      for (int i = 0; i < count; i++) {
+        const float v = choice[g * a.size + sub + at * lanes];
+        at = at + 1 == count ? 0 : at + 1;
+        v2 = fmaxf(v2, fminf(v1, v));
+        v1 = fmaxf(v1, v);
+      }
+    }
+    for (int o = 1; o < lanes; o *= 2) {
+      const float w1 = __shfl_xor_sync(kAll, v1, o), w2 = __shfl_xor_sync(kAll, v2, o);
+      v2 = fmaxf(fminf(v1, w1), fmaxf(v2, w2));
+      v1 = fmaxf(v1, w1);
+    }
+    if (g < a.groups && sub == 0) ranks[g] = ascending(a.size > 1 ? v1 + v2 : v1);
+  } else {
+    for (int g = lane; g < a.groups; g += 32) {
+      float v1 = -INFINITY, v2 = -INFINITY;
+      for (int i = 0; i < a.size; i++) {
+        const float v = choice[g * a.size + i];
+        v2 = fmaxf(v2, fminf(v1, v));
+        v1 = fmaxf(v1, v);
+      }
+      ranks[g] = ascending(a.size > 1 ? v1 + v2 : v1);
+    }
+  }
+  __syncwarp();
+  uint32_t kept = 0, last = 0u;
+  bool close = false;
+  for (int n = 0; n <= a.top_groups; n++) {  // the first that is dropped too
+    uint32_t m = 0u, at = kMaxE;
+    for (int g = lane; g < a.groups; g += 32)
+      if (ranks[g] > m) m = ranks[g], at = g;
+    const uint32_t best = __reduce_max_sync(kAll, m);
+    if (n == a.top_groups) {
+      const float x = from_ascending(last), y = from_ascending(best);
+      close = x - y < 2.0f * tie + 5e-7f * fmaxf(fabsf(x), fabsf(y));
+      break;
+    }
+    const uint32_t g = __reduce_min_sync(kAll, m == best ? at : (uint32_t)kMaxE);
+    if ((g & 31) == (uint32_t)lane) {
+      ranks[g] = 0u;  // (read by this lane alone)
+      kept |= 1u << (g >> 5);
+    }
+    last = best;
+  }
+  const uint32_t by_size = (65535u + a.size) / a.size;  // e / size = e * by_size >> 16 for e < 256
+#pragma unroll
+  for (int j = 0; j < SL; j++) {
+    const uint32_t g = ((uint32_t)(((j / V) * 32 + lane) * V + j % V) * by_size) >> 16;
+    const uint32_t k = __shfl_sync(kAll, kept, g & 31);
+    if (!((k >> (g >> 5)) & 1u)) key[j] = 0u;
+  }
+  __syncwarp();
+  return close;
+}
+
+// With a bias or groups. Three ways to the same order, each where the one before cannot tell neighbours
+// apart: keys cut to 24 bits beside the expert's number, sorted in each lane, one reduction a draw; whole
+// keys (32768 x 256 with a bias 70 us with these alone, 59 with both; 8 groups too 126 and 103); binary64.
+// Bound by instructions, 1100 a row of 256: its loads and stores would take 5 us.
 template <int SL, int V, typename L>
 __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const RouterArgs a, bool softmax, bool renorm) {
   __shared__ double values[kRouterWarps][kMaxE], ranks[kRouterWarps][kMaxE];
@@ -328,6 +416,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
   pdl_allow_next();
   const int64_t step = (int64_t)gridDim.x * kRouterWarps;
   const L* const logits = static_cast<const L*>(a.logits);
+  const bool grouped = a.top_groups < a.groups;
   for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp; t < a.T; t += step) {
     float l[SL];
     uint32_t key[SL];
@@ -340,10 +429,10 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
       bad |= !(l[j] < INFINITY);
       top = fmaxf(top, l[j]);
     }
-    top = warp_max(top);
     // the error of p grows with the largest p of the row
     float tie = 2e-6f;
     if (softmax) {
+      top = warp_max(top);
       float sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
@@ -366,99 +455,79 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
       }
       if (l[j] == -INFINITY) p = -INFINITY;
       const float c = a.bias ? p : l[j];
-      choice[e] = p;
+      if (grouped) choice[e] = p;
       if (c != -INFINITY) key[j] = ascending(c);
     }
     bad = __any_sync(kAll, bad);
-    bool close = false;
-    if (a.top_groups < a.groups && !bad) {
-      __syncwarp();
-      uint32_t rank[kMaxE / 32];
-      uint32_t kept = 0;
-#pragma unroll
-      for (int j = 0; j < kMaxE / 32; j++) {
-        const int g = lane + 32 * j;
-        rank[j] = 0u;
-        if (g >= a.groups) continue;
-        float v1 = -INFINITY, v2 = -INFINITY;
-        int at = lane % a.size;  // lanes start at different banks
-        for (int i = 0; i < a.size; i++) {
-          const float v = choice[g * a.size + at];
-          at = at + 1 == a.size ? 0 : at + 1;
-          v2 = fmaxf(v2, fminf(v1, v));
-          v1 = fmaxf(v1, v);
-        }
-        rank[j] = ascending(a.size > 1 ? v1 + v2 : v1);
-      }
-      uint32_t last = 0u;
-      for (int n = 0; n <= a.top_groups; n++) {  // the first that is dropped too
-        uint32_t m = 0u;
-#pragma unroll
-        for (int j = 0; j < kMaxE / 32; j++) m = max(m, rank[j]);
-        const uint32_t best = __reduce_max_sync(kAll, m);
-        if (n == a.top_groups) {
-          const float x = from_ascending(last), y = from_ascending(best);
-          close = x - y < 2.0f * tie + 5e-7f * fmaxf(fabsf(x), fabsf(y));
-          break;
-        }
-        uint32_t g = kMaxE;
-#pragma unroll
-        for (int j = kMaxE / 32 - 1; j >= 0; j--)
-          if (rank[j] == best) g = lane + 32 * j;
-        g = __reduce_min_sync(kAll, g);
-#pragma unroll
-        for (int j = 0; j < kMaxE / 32; j++)
-          if (g == lane + 32 * j) {
-            rank[j] = 0u;
-            kept |= 1u << j;
-          }
-        last = best;
-      }
-#pragma unroll
-      for (int j = 0; j < SL; j++) {
-        const int e = ((j / V) * 32 + lane) * V + j % V, g = e < a.E ? e / a.size : 0;
-        const uint32_t k = __shfl_sync(kAll, kept, g & 31);
-        if (!((k >> (g >> 5)) & 1u)) key[j] = 0u;
-      }
-    }
     int mine = -1;
-    if (!bad) {
-      uint32_t before = 0u;
-      int drawn = -1;
+    if (bad) {
+      if (lane == 0) atomicOr(a.status, kBadRoute);
+    } else {
+      bool close = false;
+      if (grouped) {
+        __syncwarp();
+        close = keep_groups<SL, V>(a, choice, reinterpret_cast<uint32_t*>(ranks[warp]), key, tie);
+      }
+      // cut keys: of two neighbours x >= y the true distance is above x - y - 2^-15 |y|
+      uint32_t cut[SL], before = 0u;
+#pragma unroll
+      for (int j = 0; j < SL; j++)
+        cut[j] = key[j] == 0u ? 0u : (key[j] & ~0xFFu) | (0xFFu - (((j / V) * 32 + lane) * V + j % V));
+      sort_keys<SL>(cut);
+      bool whole = false;
       for (int n = 0; n <= a.K; n++) {  // one more than is taken, to see how close it is
-        if (n == a.K && !a.bias) break;
-        uint32_t m = 0u;
-#pragma unroll
-        for (int j = 0; j < SL; j++) m = max(m, key[j]);
-        const uint32_t best = __reduce_max_sync(kAll, m);
+        const uint32_t best = __reduce_max_sync(kAll, cut[0]);
         if (best == 0u) break;
-        uint32_t e = kMaxE;
-#pragma unroll
-        for (int j = SL - 1; j >= 0; j--)
-          if (key[j] == best) e = ((j / V) * 32 + lane) * V + j % V;
-        e = __reduce_min_sync(kAll, e);
-        if (a.bias && n > 0) {
-          const float x = from_ascending(before), y = from_ascending(best);
-          if (x - y < tie + 2.5e-7f * fmaxf(fabsf(x), fabsf(y))) {
-            // the same logit and bias: equal in any precision
-            const bool same = widen<L>(row[e]) == widen<L>(row[drawn]) &&
-                              __ldg(a.bias + e) == __ldg(a.bias + drawn);
-            close |= !same;
-          }
+        if (n > 0) {
+          const float x = from_ascending(before & ~0xFFu), y = from_ascending(best & ~0xFFu);
+          whole |= x - y < (a.bias ? tie : 0.0f) + 3.2e-5f * fmaxf(fabsf(x), fabsf(y));
         }
-        if (n < a.K) {
-          if (lane == n) mine = (int)e;
-          drawn = (int)e;
-          before = best;
+        if (n == a.K) break;
+        before = best;
+        if (lane == n) mine = 0xFF - (int)(best & 0xFFu);
+        if (cut[0] == best) {
 #pragma unroll
-          for (int j = 0; j < SL; j++)
-            if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
+          for (int j = 0; j + 1 < SL; j++) cut[j] = cut[j + 1];
+          cut[SL - 1] = 0u;
+        }
+      }
+      if (whole && !close) {
+        before = 0u;
+        mine = -1;
+        int drawn = -1;
+        for (int n = 0; n <= a.K; n++) {
+          if (n == a.K && !a.bias) break;
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < SL; j++) m = max(m, key[j]);
+          const uint32_t best = __reduce_max_sync(kAll, m);
+          if (best == 0u) break;
+          uint32_t e = kMaxE;
+#pragma unroll
+          for (int j = SL - 1; j >= 0; j--)
+            if (key[j] == best) e = ((j / V) * 32 + lane) * V + j % V;
+          e = __reduce_min_sync(kAll, e);
+          if (a.bias && n > 0) {
+            const float x = from_ascending(before), y = from_ascending(best);
+            if (x - y < tie + 2.5e-7f * fmaxf(fabsf(x), fabsf(y))) {
+              // the same logit and bias: equal in any precision
+              const bool same = widen<L>(row[e]) == widen<L>(row[drawn]) &&
+                                __ldg(a.bias + e) == __ldg(a.bias + drawn);
+              close |= !same;
+            }
+          }
+          if (n < a.K) {
+            if (lane == n) mine = (int)e;
+            drawn = (int)e;
+            before = best;
+#pragma unroll
+            for (int j = 0; j < SL; j++)
+              if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
+          }
         }
       }
       __syncwarp();
       if (close) mine = draw_again<L>(a, softmax, row, values[warp], ranks[warp]);
-    } else if (lane == 0) {
-      atomicOr(a.status, kBadRoute);
     }
     const float x = mine >= 0 ? widen<L>(row[mine]) : 0.0f;
     put_weights(a, softmax, renorm, t, mine, x, top, inv);
