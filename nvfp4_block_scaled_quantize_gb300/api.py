@@ -870,14 +870,18 @@ def nvfp4_gemm_epilogue_backward(grad_out, preact, activation, grad_preact=None,
     grad_preact = _out(grad_preact, "grad_preact", torch.bfloat16, (M, N), dev)
     grad_bias = _out(grad_bias, "grad_bias", torch.float32, (N,), dev)
     amax = _out(amax, "amax", torch.float32, (1,), dev)
+    at, room = None, 0
     if workspace is None:
-        workspace = torch.empty(nvfp4_gemm_epilogue_backward_workspace(M, N), dtype=torch.uint8,
-                                device=dev)
+        room = nvfp4_gemm_epilogue_backward_workspace(M, N)
+        if room:
+            workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+            at = workspace.data_ptr()
     else:
         _check(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        at, room = workspace.data_ptr(), workspace.numel()
     status = L.nvfp4_gemm_epilogue_backward(
         grad_out.data_ptr(), preact.data_ptr(), M, N, _activation(activation), grad_preact.data_ptr(),
-        grad_bias.data_ptr(), amax.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(dev))
+        grad_bias.data_ptr(), amax.data_ptr(), at, room, _stream(dev))
     _raise_if(status, "nvfp4_gemm_epilogue_backward")
     return grad_preact, grad_bias, amax
 

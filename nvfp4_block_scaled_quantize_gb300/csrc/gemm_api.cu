@@ -182,7 +182,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const
 NVFP4_EXPORT nvfp4_status nvfp4_gemm_epilogue_backward_workspace(int64_t M, int64_t N, size_t* bytes) {
   if (bytes == nullptr || M < 0 || N < 0) return NVFP4_ERR_INVALID_ARG;
   if (M > kMaxDim || N > kMaxDim) return NVFP4_ERR_SHAPE;
-  *bytes = (size_t)(M < kEpilogueMaxPartials ? M : kEpilogueMaxPartials) * (size_t)N * 4;
+  *bytes = M <= kEpilogueFewRows ? 0 : (size_t)(M < kEpilogueMaxPartials ? M : kEpilogueMaxPartials) * (size_t)N * 4;
   return NVFP4_OK;
 }
 
@@ -196,10 +196,10 @@ NVFP4_EXPORT nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, con
   if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_SILU) return NVFP4_ERR_INVALID_ARG;
   const bool empty = M == 0 || N == 0;
   if (!empty && (grad_out == nullptr || preact == nullptr || grad_preact == nullptr ||
-                 (grad_bias != nullptr && (workspace == nullptr || workspace_bytes < need))))
+                 (grad_bias != nullptr && need > 0 && (workspace == nullptr || workspace_bytes < need))))
     return NVFP4_ERR_INVALID_ARG;
   if (!aligned(grad_out, 16) || !aligned(preact, 16) || !aligned(grad_preact, 16) ||
-      !aligned(grad_bias, 4) || !aligned(amax, 4) || !aligned(workspace, 16))
+      !aligned(grad_bias, 16) || !aligned(amax, 4) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
   int sms = 0;
   uint32_t* status = nullptr;

@@ -197,14 +197,15 @@ cudaError_t launch_all(K8 kernel8, K4 kernel4, K1 kernel1, const void* grad, con
                        cudaStream_t s) {
   const uintptr_t all = reinterpret_cast<uintptr_t>(grad) | reinterpret_cast<uintptr_t>(z) |
                         reinterpret_cast<uintptr_t>(out);
-  const int64_t joint = (N * 2) % 16 == 0 ? 1 : M >= 8 ? 8 : 0;
+  const bool few = M <= kEpilogueFewRows;  // one range of rows: its sums are the columns'
+  const int64_t joint = (N * 2) % 16 == 0 ? 1 : M >= 8 && !few ? 8 : 0;
   *partials = 0;
   if (joint > 0) {
     const int64_t m = M / joint, n = N * joint;
     const int width = (all | (uintptr_t)(n * 2)) % 32 == 0 ? 16 : 8;
     // ranges of rows: eight CTAs an SM in all, at most the rows of the workspace (one is the last rows')
     int64_t down = (8 * (int64_t)sm_count) / ((n + kThreads * width - 1) / (kThreads * width));
-    const int64_t most = joint == 1 ? kEpilogueMaxPartials : (kEpilogueMaxPartials - 1) / joint;
+    const int64_t most = few ? 1 : joint == 1 ? kEpilogueMaxPartials : (kEpilogueMaxPartials - 1) / joint;
     down = down < 1 ? 1 : down > most ? most : down;
     if (down > m) down = m;
     const int64_t rows = (m + down - 1) / down;
@@ -229,8 +230,9 @@ cudaError_t launch_epilogue_backward(const void* grad, const void* preact, int64
                                      float* partial, int sm_count, cudaStream_t s) {
   int64_t partials = 0;
   auto run = [&](auto kernel8, auto kernel4, auto kernel1) {
-    return launch_all(kernel8, kernel4, kernel1, grad, preact, M, N, grad_z, grad_bias ? partial : nullptr,
-                      &partials, amax, sm_count, s);
+    return launch_all(kernel8, kernel4, kernel1, grad, preact, M, N, grad_z,
+                      grad_bias == nullptr ? nullptr : M <= kEpilogueFewRows ? grad_bias : partial, &partials, amax,
+                      sm_count, s);
   };
   cudaError_t e;
   switch (activation) {
@@ -248,7 +250,7 @@ cudaError_t launch_epilogue_backward(const void* grad, const void* preact, int64
       e = run(epilogue_backward_kernel<NVFP4_ACT_NONE, 8>, epilogue_backward_kernel<NVFP4_ACT_NONE, 4>,
               epilogue_backward_any_kernel<NVFP4_ACT_NONE>);
   }
-  if (e != cudaSuccess || grad_bias == nullptr) return e;
+  if (e != cudaSuccess || grad_bias == nullptr || M <= kEpilogueFewRows) return e;
   return launch_pdl(column_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(32 * kSumWarps), 0, s,
                     (const float*)partial, partials, N, grad_bias);
 }

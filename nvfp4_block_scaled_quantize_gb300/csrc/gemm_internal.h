@@ -36,6 +36,7 @@ cudaError_t prepare_gemm_kernels();
 int64_t gemm_workspace(const GemmArgs& g);
 
 constexpr int64_t kEpilogueMaxPartials = 512;  // rows of the bias gradient's partial sums
+constexpr int64_t kEpilogueFewRows = 32;       // up to which there are none
 cudaError_t launch_epilogue_backward(const void* grad, const void* preact, int64_t M, int64_t N,
                                      int32_t activation, void* grad_z, float* grad_bias, float* amax,
                                      float* partial, int sm_count, cudaStream_t s);

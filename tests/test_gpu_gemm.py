@@ -454,7 +454,7 @@ def test_two_streams_at_once():
 
 @pytest.mark.parametrize("activation", ["none", "relu", "relu2", "gelu", "silu"])
 @pytest.mark.parametrize("M,N", [(1, 8), (3, 2048), (700, 72), (129, 4104), (1030, 1024), (1, 1), (517, 7),
-                                 (90, 1001), (3, 4098), (1003, 999), (4097, 33)])
+                                 (90, 1001), (3, 4098), (1003, 999), (4097, 33), (32, 1000), (33, 1000), (31, 77), (34, 77)])
 def test_epilogue_backward(activation, M, N):
     dev = cuda()
     g = torch.Generator().manual_seed(M + N)

@@ -120,17 +120,18 @@ def test_grouped(L):
 
 def test_epilogue_backward(L):
     n = ctypes.c_size_t()
-    assert L.nvfp4_gemm_epilogue_backward_workspace(3, 16, ctypes.byref(n)) == OK and n.value == 3 * 64
+    assert L.nvfp4_gemm_epilogue_backward_workspace(3, 16, ctypes.byref(n)) == OK and n.value == 0
+    assert L.nvfp4_gemm_epilogue_backward_workspace(33, 16, ctypes.byref(n)) == OK and n.value == 33 * 64
     assert L.nvfp4_gemm_epilogue_backward_workspace(3, 2 ** 31, ctypes.byref(n)) == SHAPE
     assert L.nvfp4_gemm_epilogue_backward_workspace(3, 16, None) == INVALID
 
-    def back(M=3, N=16, act=3, g=FAKE, z=FAKE, out=FAKE, db=FAKE, amax=FAKE, ws=FAKE, size=1 << 20):
+    def back(M=33, N=16, act=3, g=FAKE, z=FAKE, out=FAKE, db=FAKE, amax=FAKE, ws=FAKE, size=1 << 20):
         return L.nvfp4_gemm_epilogue_backward(p(g), p(z), M, N, act, p(out), p(db), p(amax), p(ws), size,
                                               None)
     assert back(N=2 ** 31) == SHAPE and back(M=-1) == INVALID and back(act=5) == INVALID
     for k in ("g", "z", "out", "ws"):
         assert back(**{k: 0}) == INVALID and back(**{k: FAKE + 8}) == ALIGN, k
-    assert back(size=3 * 64 - 1) == INVALID
+    assert back(size=33 * 64 - 1) == INVALID
     assert back(db=FAKE + 2) == ALIGN and back(amax=FAKE + 2) == ALIGN
 
 
