@@ -23,9 +23,9 @@
  * rowwise outputs of x transposed, optionally after a 16-point random Hadamard transform.
  *
  * Execution: every call is asynchronous on the caller's stream (a cudaStream_t passed as
- * void*; NULL is the legacy default stream). The quantize, amax, MX, routing and checkpoint
- * kernels are launched with programmatic dependent launch: each waits for the previous kernel in
- * the stream before it touches memory, and lets the next kernel launched that way start early, so a
+ * void*; NULL is the legacy default stream). The quantize, amax, MX, router, routing, checkpoint,
+ * product and AdamW kernels are launched with programmatic dependent launch: each waits for the
+ * previous kernel in the stream before it touches memory, and lets the next kernel launched that way start early, so a
  * kernel of the caller's launched after them with programmatic dependent launch must wait
  * (cudaGridDependencySynchronize) before it reads their outputs, as that mechanism requires.
  * Pointers marked (device) must be device (or managed) memory, aligned as the declaration says (16
@@ -76,7 +76,8 @@ typedef enum nvfp4_rounding {
 #define NVFP4_DEVICE_TIMEOUT     0x2u  /* the wait for every CTA's amax or a copy wait passed
                                           its limit */
 #define NVFP4_DEVICE_BAD_ROUTE   0x4u  /* an expert id that is not below E, or a plan's row
-                                          outside the packed tensor; the slot was skipped */
+                                          outside the packed tensor; the slot was skipped. Or
+                                          a row of logits without an order (NaN, +inf) */
 
 /* Options of one quantization. Zero-initialise and set what is needed. */
 typedef struct nvfp4_config {
@@ -518,8 +519,8 @@ typedef struct nvfp4_epilogue {
   const void* bias;      /* [N] (grouped: [E][N]) or NULL */
   const void* residual;  /* [M][N] or NULL; may be out itself */
   void* preact;          /* BF16 [M][N] or NULL: receives z, for the backward pass */
-  float* amax;           /* float [1] (grouped: [E]) or NULL: receives max |out| as it is stored, the
-                            amax_row of the next quantization */
+  float* amax;           /* float [1] (grouped: [E]) or NULL: receives max |out| as it is stored (NaN does
+                            not count), the amax_row of the next quantization */
 } nvfp4_epilogue;
 
 /* out [M][N] from a [M][K] and b [N][K] (both with K innermost): a b^T through the epilogue.
@@ -566,10 +567,11 @@ nvfp4_status nvfp4_gemm_grouped_wgrad(const nvfp4_operand* a, const nvfp4_operan
  * column sums of its binary32 values, and its amax: what the quantizations and products of the
  * backward pass take. (The residual's gradient is grad_out.)
  *   grad_out, preact (device) BF16 [M][N], 16-byte aligned; activation; grad_preact (device) BF16
- *   [M][N], 16-byte aligned, may be grad_out; grad_bias (device) float [N] or NULL, its sums in an
- *   order that depends on the sizes and the device alone; amax (device) float [1] or NULL; workspace
- *   (device), 16-byte aligned, of at least nvfp4_gemm_epilogue_backward_workspace bytes where
- *   grad_bias is asked for. Any N (a multiple of 16 is fastest). At z = 0 the derivative of RELU is 0. */
+ *   [M][N], 16-byte aligned, may be grad_out; grad_bias (device) float [N], 16-byte aligned, or NULL,
+ *   its sums in an order that depends on the sizes and the device alone; amax (device) float [1] or
+ *   NULL: max |grad_preact|, NaN not counted; workspace (device), 16-byte aligned, of at least
+ *   nvfp4_gemm_epilogue_backward_workspace bytes where grad_bias is asked for (0 bytes up to 32 rows).
+ *   Any N (a multiple of 16 is fastest). At z = 0 the derivative of RELU is 0. */
 nvfp4_status nvfp4_gemm_epilogue_backward(const void* grad_out, const void* preact, int64_t M,
                                           int64_t N, int32_t activation, void* grad_preact,
                                           float* grad_bias, float* amax, void* workspace,

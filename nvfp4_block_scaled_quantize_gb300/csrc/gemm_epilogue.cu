@@ -1,10 +1,12 @@
 // The gradient through a matrix product's epilogue (declared in include/nvfp4.h): elementwise, with
 // the bias's gradient (column sums) and the amax of what it writes from the same pass. Bound by DRAM:
-// two reads and a write of 2 bytes an element.
+// two reads and a write of 2 bytes an element (8192 x 14336: 111 us, 94% of the copy rate; with 16-byte
+// accesses and the arithmetic element by element, not in packed pairs, 192).
 //
 // A CTA of 128 threads has 2048 columns (1024 where rows do not start on 32-byte boundaries, 128 where
-// not on 16-byte ones), a thread 16 (8, 1) of them, over a range of rows, two at a time so that their loads are under way together. Its
-// column sums go to one row of the partial sums, which a second kernel adds up in order.
+// not on 16-byte ones), a thread 16 (8, 1) of them, over a range of rows, two at a time so that their loads
+// are under way together. Its column sums go to one row of the partial sums, which a second kernel adds up
+// in order; up to 32 rows are one range, whose sums are the gradient.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
