@@ -6,8 +6,8 @@
 // reduction instruction (redux.sync). Binary32 scores are off by a few
 // units in the last place, which can exchange two candidates that are close: where two neighbours of
 // the drawn order (or the last kept and the first dropped group) are closer than that error allows,
-// the row is drawn again from binary64 scores. With normal logits that happens to one row in a few
-// hundred; ranking every row in binary64 would cost more than everything else here.
+// those are ranked by binary64 scores, a candidate a lane. With normal logits that happens to one row in a
+// few hundred; the scores of whole rows in binary64 would cost more than everything else here.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,15 +56,17 @@ __device__ __forceinline__ float from_ascending(uint32_t k) {
   return __uint_as_float((int32_t)k < 0 ? k ^ 0x80000000u : ~k);
 }
 
+// Of `LANES` neighbouring lanes.
+template <int LANES = 32>
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+  for (int o = LANES / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
-template <typename F>
+template <int LANES = 32, typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = v + __shfl_xor_sync(kAll, v, o);
+  for (int o = LANES / 2; o >= 1; o >>= 1) v = v + __shfl_xor_sync(kAll, v, o);
   return v;
 }
 
@@ -165,9 +167,10 @@ __device__ __forceinline__ void put_weights(const RouterArgs& a, bool softmax, b
   const int lane = threadIdx.x & 31;
   float w = 0.0f;
   if (renorm) {
-    const float high = warp_max(mine >= 0 ? x : -INFINITY);
+    const bool few = a.K <= 8;  // lanes behind the eighth have nothing
+    const float mark = mine >= 0 ? x : -INFINITY, high = few ? warp_max<8>(mark) : warp_max(mark);
     if (mine >= 0) w = softmax ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
-    const float sum = warp_sum(w);
+    const float sum = few ? warp_sum<8>(w) : warp_sum(w);
     w = sum > 0.0f ? __fdividef(w, sum) : 0.0f;
   } else if (mine >= 0) {
     w = softmax ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
@@ -337,15 +340,98 @@ __device__ __forceinline__ void sort_keys(uint32_t (&k)[SL]) {
           }
 }
 
-// Keeps the best groups' experts: `choice` (shared, of all experts) ranks the groups, keys of the others
-// become 0. True where binary32 cannot tell the last kept from the first dropped group.
-template <int SL, int V>
-__device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* choice, uint32_t* ranks,
-                                            uint32_t (&key)[SL], float tie) {
+// The two largest of two pairs.
+__device__ __forceinline__ void join_top2(float& v1, float& v2, float w1, float w2) {
+  v2 = fmaxf(fminf(v1, w1), fmaxf(v2, w2));
+  v1 = fmaxf(v1, w1);
+}
+
+// Binary64 ranks of the groups that binary32 may have put on the wrong side: `doubtful` ones, `floor` (lane
+// g: of group g) the least of the values that count, x[j] within its error of that counted again. Sets `kept`
+// right; false where it takes the whole row.
+template <int SL, int V, typename L>
+__device__ __noinline__ bool settle_groups(const RouterArgs& a, bool softmax, const L* row, float top, const float (&x)[SL],
+                                           float floor, float tie, uint32_t doubtful, int* slots, uint32_t& kept) {
   const int lane = threadIdx.x & 31;
-  if (a.groups <= 32) {  // `lanes` lanes a group, each from an element of its own (other banks)
+  if (softmax && a.bias) return false;
+  const uint32_t by_size = (65535u + a.size) / a.size;  // e / size = e * by_size >> 16 for e < 256
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < SL; j++) {
+    const uint32_t e = ((j / V) * 32 + lane) * V + j % V, g = (e * by_size) >> 16;
+    const float f = __shfl_sync(kAll, floor, g & 31);
+    const bool here = x[j] > -INFINITY && doubtful >> (g & 31) & 1u &&
+                      f - x[j] < tie + 2.5e-7f * fmaxf(fabsf(f), fabsf(x[j]));
+    const uint32_t all = __ballot_sync(kAll, here);
+    const int at = count + __popc(all & ((1u << lane) - 1u));
+    if (here && at < 32) slots[at] = (int)e;
+    count += __popc(all);
+  }
+  if (count > 32) return false;
+  __syncwarp();
+  double v = -INFINITY;
+  int g = -1;
+  if (lane < count) {
+    const int e = slots[lane];
+    const double l = (double)widen<L>(row[e]);
+    // (softmax: over the row's sum, which all of them share)
+    v = softmax ? exp(l - (double)top) : 1.0 / (1.0 + exp(-l)) + (a.bias ? (double)__ldg(a.bias + e) : 0.0);
+    g = (int)((e * by_size) >> 16);
+  }
+  __syncwarp();
+  double v1 = -INFINITY, v2 = -INFINITY;
+  for (int m = 0; m < count; m++) {
+    const double w = __shfl_sync(kAll, v, m);
+    if (__shfl_sync(kAll, g, m) != lane) continue;
+    if (w > v1) v2 = v1, v1 = w;
+    else if (w > v2) v2 = w;
+  }
+  const double rank = a.size > 1 ? v1 + v2 : v1;
+  int place = __popc(kept & ~doubtful);
+  for (uint32_t left = doubtful; left != 0u; left &= left - 1u) {
+    const int m = __ffs(left) - 1;
+    const double w = __shfl_sync(kAll, rank, m);
+    place += w > rank || (w == rank && m < lane) ? 1 : 0;
+  }
+  kept = (kept & ~doubtful) | (__ballot_sync(kAll, place < a.top_groups) & doubtful);
+  return true;
+}
+
+// Keeps the best of up to 32 groups: keys of the others become 0. x: this lane's p + bias, -inf where masked.
+// True where the row has to be ranked in binary64.
+template <int SL, int V, typename L>
+__device__ __forceinline__ bool keep_groups(const RouterArgs& a, bool softmax, const L* row, float top,
+                                            const float (&x)[SL], float* choice, int* slots, uint32_t (&key)[SL],
+                                            float tie) {
+  const int lane = threadIdx.x & 31;
+  // Lanes that hold V neighbours of a group each, where they are a power of two: then the two largest of a
+  // group come by shuffles, else from shared memory.
+  const int span = V > 1 && a.size % V == 0 ? a.size / V : 0;
+  const bool near = span > 0 && span <= 32 && (span & (span - 1)) == 0;
+  float v1 = -INFINITY, v2 = -INFINITY;  // lane g: of group g
+  if (near) {
+    const int per = 32 / span;  // groups in 32 V neighbours
+#pragma unroll
+    for (int c = 0; c < SL / V; c++) {
+      float w1 = x[c * V], w2 = -INFINITY;
+#pragma unroll
+      for (int i = 1; i < V; i++) {
+        w2 = fmaxf(w2, fminf(w1, x[c * V + i]));
+        w1 = fmaxf(w1, x[c * V + i]);
+      }
+      for (int o = 1; o < span; o *= 2)
+        join_top2(w1, w2, __shfl_xor_sync(kAll, w1, o), __shfl_xor_sync(kAll, w2, o));
+      const int from = lane % per * span;
+      w1 = __shfl_sync(kAll, w1, from);
+      w2 = __shfl_sync(kAll, w2, from);
+      if (lane / per == c) v1 = w1, v2 = w2;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < SL; j++) choice[((j / V) * 32 + lane) * V + j % V] = x[j];
+    __syncwarp();
+    // `lanes` lanes a group, each from an element of its own (other banks)
     const int lanes = 32 >> (32 - __clz(a.groups - 1)), g = lane / lanes, sub = lane % lanes;
-    float v1 = -INFINITY, v2 = -INFINITY;
     if (g < a.groups) {
       const int count = (a.size - sub + lanes - 1) / lanes;  // elements sub, sub + lanes, ...
       int at = count > 0 ? g % count : 0;
@@ -356,22 +442,66 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ch
         v1 = fmaxf(v1, v);
       }
     }
-    for (int o = 1; o < lanes; o *= 2) {
-      const float w1 = __shfl_xor_sync(kAll, v1, o), w2 = __shfl_xor_sync(kAll, v2, o);
-      v2 = fmaxf(fminf(v1, w1), fmaxf(v2, w2));
-      v1 = fmaxf(v1, w1);
+    for (int o = 1; o < lanes; o *= 2)
+      join_top2(v1, v2, __shfl_xor_sync(kAll, v1, o), __shfl_xor_sync(kAll, v2, o));
+    const int from = lane * lanes;  // beyond the last lane: not used
+    v1 = __shfl_sync(kAll, v1, from);
+    v2 = __shfl_sync(kAll, v2, from);
+  }
+  // a group's place is the number of better ones
+  const bool group = lane < a.groups;
+  const float rank = a.size > 1 ? v1 + v2 : v1;
+  const uint32_t mine = group ? ascending(rank) : 0u;
+  int place = 0;
+#pragma unroll 4
+  for (int o = 0; o < a.groups; o++) {
+    const uint32_t other = __shfl_sync(kAll, mine, o);
+    place += other > mine || (other == mine && o < lane) ? 1 : 0;
+  }
+  uint32_t kept = __ballot_sync(kAll, group && place < a.top_groups);
+  const uint32_t last = __ballot_sync(kAll, group && place == a.top_groups - 1);
+  const uint32_t first = __ballot_sync(kAll, group && place == a.top_groups);
+  const float y = from_ascending(__shfl_sync(kAll, mine, __ffs(last) - 1));
+  const float z = from_ascending(__shfl_sync(kAll, mine, __ffs(first) - 1));
+  auto close = [&](float p, float q) { return p - q < 2.0f * tie + 5e-7f * fmaxf(fabsf(p), fabsf(q)); };
+  if (close(y, z)) {  // the last kept and the first dropped group
+    const uint32_t doubtful = __ballot_sync(kAll, group && (place < a.top_groups ? close(rank, z) : close(y, rank)));
+    if (!settle_groups<SL, V, L>(a, softmax, row, top, x, a.size > 1 ? v2 : v1, tie, doubtful, slots, kept)) return true;
+  }
+  if (near) {
+#pragma unroll
+    for (int c = 0; c < SL / V; c++) {
+      const bool keep = kept >> ((c * 32 + lane) / span & 31) & 1u;
+#pragma unroll
+      for (int i = 0; i < V; i++) key[c * V + i] = keep ? key[c * V + i] : 0u;
     }
-    if (g < a.groups && sub == 0) ranks[g] = ascending(a.size > 1 ? v1 + v2 : v1);
   } else {
-    for (int g = lane; g < a.groups; g += 32) {
-      float v1 = -INFINITY, v2 = -INFINITY;
-      for (int i = 0; i < a.size; i++) {
-        const float v = choice[g * a.size + i];
-        v2 = fmaxf(v2, fminf(v1, v));
-        v1 = fmaxf(v1, v);
-      }
-      ranks[g] = ascending(a.size > 1 ? v1 + v2 : v1);
+    const uint32_t by_size = (65535u + a.size) / a.size;  // e / size = e * by_size >> 16 for e < 256
+#pragma unroll
+    for (int j = 0; j < SL; j++) {
+      const uint32_t g = ((uint32_t)(((j / V) * 32 + lane) * V + j % V) * by_size) >> 16;
+      if (!(kept >> (g & 31) & 1u)) key[j] = 0u;
     }
+  }
+  return false;
+}
+
+// The same for more groups than a warp has lanes.
+template <int SL, int V>
+__device__ __forceinline__ bool keep_many_groups(const RouterArgs& a, const float (&x)[SL], float* choice,
+                                                 uint32_t* ranks, uint32_t (&key)[SL], float tie) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < SL; j++) choice[((j / V) * 32 + lane) * V + j % V] = x[j];
+  __syncwarp();
+  for (int g = lane; g < a.groups; g += 32) {
+    float v1 = -INFINITY, v2 = -INFINITY;
+    for (int i = 0; i < a.size; i++) {
+      const float v = choice[g * a.size + i];
+      v2 = fmaxf(v2, fminf(v1, v));
+      v1 = fmaxf(v1, v);
+    }
+    ranks[g] = ascending(a.size > 1 ? v1 + v2 : v1);
   }
   __syncwarp();
   uint32_t kept = 0, last = 0u;
@@ -382,8 +512,8 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ch
       if (ranks[g] > m) m = ranks[g], at = g;
     const uint32_t best = __reduce_max_sync(kAll, m);
     if (n == a.top_groups) {
-      const float x = from_ascending(last), y = from_ascending(best);
-      close = x - y < 2.0f * tie + 5e-7f * fmaxf(fabsf(x), fabsf(y));
+      const float y = from_ascending(last), z = from_ascending(best);
+      close = y - z < 2.0f * tie + 5e-7f * fmaxf(fabsf(y), fabsf(z));
       break;
     }
     const uint32_t g = __reduce_min_sync(kAll, m == best ? at : (uint32_t)kMaxE);
@@ -400,14 +530,75 @@ __device__ __forceinline__ bool keep_groups(const RouterArgs& a, const float* ch
     const uint32_t k = __shfl_sync(kAll, kept, g & 31);
     if (!((k >> (g >> 5)) & 1u)) key[j] = 0u;
   }
-  __syncwarp();
   return close;
 }
 
-// With a bias or groups. Three ways to the same order, each where the one before cannot tell neighbours
+constexpr uint32_t kNone = 0x00800000u;  // keys below it: masked (-inf) or dropped (0)
+
+// The choice `mine` by whole keys (`taken`; lane n: the n-th; `key`: what is left), put right where binary32
+// cannot tell: two neighbours in it, or the last and some that are left, are closer than its error. Those
+// and the choice, one a lane, are ranked by binary64 sigmoids. (Whole rows in binary64, for the few
+// that need it, took 33 us of 62 at 32768 x 256.) False where that takes the whole row: softmax, or more than 32 of them.
+template <int SL, int V, typename L>
+__device__ __forceinline__ bool settle(const RouterArgs& a, bool softmax, const L* row, const uint32_t (&key)[SL],
+                                       const float (&bias)[SL], uint32_t taken, float tie, int* slots, int& mine) {
+  const int lane = threadIdx.x & 31;
+  auto close = [&](float x, float y) { return x - y < tie + 2.5e-7f * fmaxf(fabsf(x), fabsf(y)); };
+  float l = mine >= 0 ? widen<L>(row[mine]) : 0.0f, b = mine >= 0 ? __ldg(a.bias + mine) : 0.0f;
+  // the same logit and bias: equal in any precision, and the lower index is first already
+  const uint32_t next = __shfl_down_sync(kAll, taken, 1);
+  const float next_l = __shfl_down_sync(kAll, l, 1), next_b = __shfl_down_sync(kAll, b, 1);
+  bool again = lane + 1 < a.K && next >= kNone && close(from_ascending(taken), from_ascending(next)) &&
+               !(l == next_l && b == next_b);
+  const uint32_t last = __shfl_sync(kAll, taken, a.K - 1);
+  const float last_l = __shfl_sync(kAll, l, a.K - 1), last_b = __shfl_sync(kAll, b, a.K - 1);
+  uint32_t others = 0u;
+  if (last >= kNone) {
+#pragma unroll
+    for (int j = 0; j < SL; j++)
+      if (key[j] >= kNone && close(from_ascending(last), from_ascending(key[j]))) {
+        others |= 1u << j;
+        again |= !(bias[j] == last_b && widen<L>(row[((j / V) * 32 + lane) * V + j % V]) == last_l);
+      }
+  }
+  if (!__any_sync(kAll, again)) return true;
+  if (softmax) return false;
+  int count = a.K;
+#pragma unroll
+  for (int j = 0; j < SL; j++) {
+    const bool here = others >> j & 1u;
+    const uint32_t all = __ballot_sync(kAll, here);
+    const int at = count + __popc(all & ((1u << lane) - 1u));
+    if (here && at < 32) slots[at] = ((j / V) * 32 + lane) * V + j % V;
+    count += __popc(all);
+  }
+  if (count > 32) return false;
+  __syncwarp();
+  if (lane >= a.K && lane < count) {
+    mine = slots[lane];
+    l = widen<L>(row[mine]);
+    b = __ldg(a.bias + mine);
+  }
+  const double v = mine >= 0 ? 1.0 / (1.0 + exp(-(double)l)) + (double)b : -INFINITY;
+  int place = 0, chosen = -1;
+  for (int m = 0; m < count; m++) {
+    const double w = __shfl_sync(kAll, v, m);
+    const int e = __shfl_sync(kAll, mine, m);
+    place += w > v || (w == v && e < mine) ? 1 : 0;
+  }
+  for (int m = 0; m < count; m++) {
+    const int at = __shfl_sync(kAll, place, m), e = __shfl_sync(kAll, mine, m);
+    if (at == lane) chosen = e;
+  }
+  mine = lane < a.K ? chosen : -1;
+  return true;
+}
+
+// With a bias or groups. Ways to the same order, each where the one before cannot tell neighbours
 // apart: keys cut to 24 bits beside the expert's number, sorted in each lane, one reduction a draw; whole
-// keys (32768 x 256 with a bias 70 us with these alone, 59 with both; 8 groups too 126 and 103); binary64.
-// Bound by instructions, 1100 a row of 256: its loads and stores would take 5 us.
+// keys; binary64 scores of those that are close; of the whole row. Bound by instructions: its loads and
+// stores would take 5 us at 32768 x 256. There, sigmoid with a bias takes 29 us, with 4 of 8 groups too 40; 5
+// to 7 of these are the second way's.
 template <int SL, int V, typename L>
 __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const RouterArgs a, bool softmax, bool renorm) {
   __shared__ double values[kRouterWarps][kMaxE], ranks[kRouterWarps][kMaxE];
@@ -416,21 +607,32 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
   pdl_allow_next();
   const int64_t step = (int64_t)gridDim.x * kRouterWarps;
   const L* const logits = static_cast<const L*>(a.logits);
-  const bool grouped = a.top_groups < a.groups;
-  for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp; t < a.T; t += step) {
-    float l[SL];
-    uint32_t key[SL];
+  const bool grouped = a.top_groups < a.groups, biased = a.bias != nullptr;
+  int64_t t = (int64_t)blockIdx.x * kRouterWarps + warp;
+  float l[SL], bias[SL];
+  bool bad_bias = false;
+#pragma unroll
+  for (int j = 0; j < SL; j++) {
+    const int e = ((j / V) * 32 + lane) * V + j % V;
+    bias[j] = biased && e < a.E ? __ldg(a.bias + e) : 0.0f;
+    bad_bias |= !(bias[j] < INFINITY);
+  }
+  if (t < a.T) load_row<SL, V, L>(logits + t * a.E, a.E, l);
+  for (; t < a.T; t += step) {
     const L* const row = logits + t * a.E;
-    load_row<SL, V, L>(row, a.E, l);
-    bool bad = false;
+    uint32_t key[SL];
+    bool bad = bad_bias;
     float top = -INFINITY, inv = 1.0f;
 #pragma unroll
     for (int j = 0; j < SL; j++) {
       bad |= !(l[j] < INFINITY);
       top = fmaxf(top, l[j]);
     }
-    // the error of p grows with the largest p of the row
-    float tie = 2e-6f;
+    bad = __any_sync(kAll, bad);
+    // What two values of p are off by together. Sigmoid: p (1 - p) (2 + 1.173 |l|) 2^-23, the exponential's
+    // bound, half a unit of the sum and 2 units of the quotient, below 2.7e-7 each. Softmax: 2 units of the
+    // exponential each and the row's sum, relative to the largest p.
+    float tie = 6e-7f;
     if (softmax) {
       top = warp_max(top);
       float sum = 0.0f;
@@ -438,93 +640,75 @@ __global__ void __launch_bounds__(32 * kRouterWarps, 4) router_kernel(const Rout
       for (int j = 0; j < SL; j++) sum += l[j] == -INFINITY ? 0.0f : __expf(l[j] - top);
       sum = warp_sum(sum);
       inv = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
-      tie *= inv;
+      tie = 2e-6f * inv;
     }
-    float* const choice = reinterpret_cast<float*>(values[warp]);
+    bool close = false;
+    {
+      float x[SL];
 #pragma unroll
-    for (int j = 0; j < SL; j++) {
-      const int e = ((j / V) * 32 + lane) * V + j % V;
-      key[j] = 0u;
-      if (e >= a.E) continue;
-      float p = 0.0f;  // masked (top may be -inf, too)
-      if (l[j] != -INFINITY) p = softmax ? __expf(l[j] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-l[j]));
-      if (a.bias) {
-        const float b = __ldg(a.bias + e);
-        p += b;
-        bad |= !(p < INFINITY) || !(b < INFINITY);
+      for (int j = 0; j < SL; j++) {
+        const float p = softmax ? __expf(l[j] - top) * inv : __fdividef(1.0f, 1.0f + __expf(-l[j]));
+        x[j] = l[j] == -INFINITY ? -INFINITY : p + bias[j];
+        key[j] = ascending(biased ? x[j] : l[j]);
       }
-      if (l[j] == -INFINITY) p = -INFINITY;
-      const float c = a.bias ? p : l[j];
-      if (grouped) choice[e] = p;
-      if (c != -INFINITY) key[j] = ascending(c);
+      // the next row's logits are under way from here on
+      if (t + step < a.T) load_row<SL, V, L>(row + step * a.E, a.E, l);
+      if (grouped) {
+        float* const choice = reinterpret_cast<float*>(values[warp]);
+        close = a.groups <= 32
+                    ? keep_groups<SL, V, L>(a, softmax, row, top, x, choice,
+                                            reinterpret_cast<int*>(ranks[warp]), key, tie)
+                    : keep_many_groups<SL, V>(a, x, choice, reinterpret_cast<uint32_t*>(ranks[warp]), key, tie);
+        __syncwarp();
+      }
     }
-    bad = __any_sync(kAll, bad);
     int mine = -1;
     if (bad) {
       if (lane == 0) atomicOr(a.status, kBadRoute);
     } else {
-      bool close = false;
-      if (grouped) {
-        __syncwarp();
-        close = keep_groups<SL, V>(a, choice, reinterpret_cast<uint32_t*>(ranks[warp]), key, tie);
-      }
-      // cut keys: of two neighbours x >= y the true distance is above x - y - 2^-15 |y|
-      uint32_t cut[SL], before = 0u;
+      uint32_t cut[SL], taken = 0u;  // lane n: the n-th drawn
 #pragma unroll
-      for (int j = 0; j < SL; j++)
-        cut[j] = key[j] == 0u ? 0u : (key[j] & ~0xFFu) | (0xFFu - (((j / V) * 32 + lane) * V + j % V));
+      for (int j = 0; j < SL; j++) cut[j] = (key[j] & ~0xFFu) | (0xFFu - (((j / V) * 32 + lane) * V + j % V));
       sort_keys<SL>(cut);
-      bool whole = false;
-      for (int n = 0; n <= a.K; n++) {  // one more than is taken, to see how close it is
+      for (int n = 0; n < a.K; n++) {
         const uint32_t best = __reduce_max_sync(kAll, cut[0]);
-        if (best == 0u) break;
-        if (n > 0) {
-          const float x = from_ascending(before & ~0xFFu), y = from_ascending(best & ~0xFFu);
-          whole |= x - y < (a.bias ? tie : 0.0f) + 3.2e-5f * fmaxf(fabsf(x), fabsf(y));
-        }
-        if (n == a.K) break;
-        before = best;
-        if (lane == n) mine = 0xFF - (int)(best & 0xFFu);
+        if (lane == n) taken = best;
         if (cut[0] == best) {
 #pragma unroll
           for (int j = 0; j + 1 < SL; j++) cut[j] = cut[j + 1];
           cut[SL - 1] = 0u;
         }
       }
-      if (whole && !close) {
-        before = 0u;
+      // cut keys: of two neighbours x >= y the true distance is above x - y - 2^-15 |y|. One more than is
+      // taken, to see how close it is.
+      uint32_t after = __shfl_down_sync(kAll, taken, 1);
+      const uint32_t dropped = __reduce_max_sync(kAll, cut[0]);
+      if (lane == a.K - 1) after = dropped;
+      const float x = from_ascending(taken & ~0xFFu), y = from_ascending(after & ~0xFFu);
+      const bool near = lane < a.K && after >= kNone &&
+                        x - y < (biased ? tie : 0.0f) + 3.2e-5f * fmaxf(fabsf(x), fabsf(y));
+      if (taken >= kNone) mine = 0xFF - (int)(taken & 0xFFu);
+      // (the cut keys of BF16 logits are whole)
+      if ((biased || sizeof(L) > 2) && __any_sync(kAll, near) && !close) {
+        taken = 0u;
         mine = -1;
-        int drawn = -1;
-        for (int n = 0; n <= a.K; n++) {
-          if (n == a.K && !a.bias) break;
+        for (int n = 0; n < a.K; n++) {
           uint32_t m = 0u;
 #pragma unroll
           for (int j = 0; j < SL; j++) m = max(m, key[j]);
           const uint32_t best = __reduce_max_sync(kAll, m);
-          if (best == 0u) break;
+          if (best < kNone) break;
           uint32_t e = kMaxE;
 #pragma unroll
           for (int j = SL - 1; j >= 0; j--)
             if (key[j] == best) e = ((j / V) * 32 + lane) * V + j % V;
           e = __reduce_min_sync(kAll, e);
-          if (a.bias && n > 0) {
-            const float x = from_ascending(before), y = from_ascending(best);
-            if (x - y < tie + 2.5e-7f * fmaxf(fabsf(x), fabsf(y))) {
-              // the same logit and bias: equal in any precision
-              const bool same = widen<L>(row[e]) == widen<L>(row[drawn]) &&
-                                __ldg(a.bias + e) == __ldg(a.bias + drawn);
-              close |= !same;
-            }
-          }
-          if (n < a.K) {
-            if (lane == n) mine = (int)e;
-            drawn = (int)e;
-            before = best;
+          if (lane == n) taken = best, mine = (int)e;
 #pragma unroll
-            for (int j = 0; j < SL; j++)
-              if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
-          }
+          for (int j = 0; j < SL; j++)
+            if (e == (uint32_t)(((j / V) * 32 + lane) * V + j % V)) key[j] = 0u;
         }
+        if (biased) close = !settle<SL, V, L>(a, softmax, row, key, bias, taken, tie, reinterpret_cast<int*>(ranks[warp]), mine);
       }
       __syncwarp();
       if (close) mine = draw_again<L>(a, softmax, row, values[warp], ranks[warp]);

@@ -8,6 +8,7 @@ import torch
 
 from nvfp4_block_scaled_quantize_gb300 import _lib, api
 from test_gpu_gemm import act, check_product, cuda, operand, values
+from test_gpu_router import check
 
 pytestmark = pytest.mark.gpu
 
@@ -253,3 +254,63 @@ def test_large_tensor_in_a_step(bits):
             else:
                 assert torch.equal(x, y), k
     assert amax.item() == max(w[i:i + (1 << 28)].abs().max().item() for i in range(0, n, 1 << 28))
+
+
+# ---- the router's order among few close scores ------------------------------------------------------
+
+@pytest.mark.parametrize("E,K,groups,top_groups", [(256, 8, 1, 1), (256, 8, 8, 4), (160, 6, 8, 3), (64, 12, 1, 1),
+                                                   (250, 20, 1, 1), (96, 32, 1, 1), (256, 1, 1, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("close", [2, 7, 40])
+def test_few_scores_that_binary32_cannot_tell_apart(E, K, groups, top_groups, score, close):
+    """`close` experts of a row at steps of one unit in the last place, some of them equal, among others that
+    are far: they straddle the last chosen, or are all chosen, or fill every place."""
+    dev = cuda()
+    g = torch.Generator().manual_seed(E + K + close)
+    T = 300
+    x = torch.randn(T, E, generator=g)
+    above = torch.randint(0, K + 1, (T,), generator=g)  # experts that are far above the close ones
+    for t in range(T):
+        order = torch.randperm(E, generator=g)
+        n = int(above[t])
+        x[t, order[:n]] = 5 + 0.125 * torch.arange(n)
+        steps = torch.randint(0, max(2, close // 2), (close,), generator=g)
+        x[t, order[n:n + close]] = 3.5 + steps * 2.0 ** -22
+    bias = (torch.randint(-8, 9, (E,), generator=g) * 2.0 ** -24).float()
+    check(x.to(dev), K, bias.to(dev), score=score, groups=groups, top_groups=top_groups)
+    check(x.to(dev), K, torch.zeros(E, device=dev), score=score, groups=groups, top_groups=top_groups)
+    x[:100, torch.randperm(E, generator=g)[:E - K // 2 - 1]] = -float("inf")  # fewer than K are left
+    check(x.to(dev), K, bias.to(dev), score=score, groups=groups, top_groups=top_groups)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_equal_logits(dtype):
+    dev = cuda()
+    for E, groups, top in ((256, 1, 1), (64, 8, 2), (20, 1, 1)):
+        for bias in (None, torch.zeros(E, device=dev)):
+            ids, w = api.nvfp4_moe_router(torch.zeros(40, E, dtype=dtype, device=dev), 4, score="sigmoid",
+                                          bias=bias, groups=groups, top_groups=top)
+            assert (ids == torch.arange(4, device=dev)).all() and (w == 0.25).all()
+
+
+@pytest.mark.parametrize("E,K,groups,top_groups", [(256, 8, 8, 4), (160, 6, 8, 3), (64, 4, 16, 5), (250, 8, 10, 4),
+                                                   (32, 4, 32, 9), (256, 8, 4, 1)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_groups_that_binary32_cannot_tell_apart(E, K, groups, top_groups, score, biased):
+    """Groups whose two largest are another group's, in another order and up to a unit in the last place."""
+    dev = cuda()
+    g = torch.Generator().manual_seed(E + groups)
+    T, size = 300, E // groups
+    x = torch.randn(T, groups, size, generator=g)
+    for t in range(T):
+        for _ in range(3):
+            i, j = torch.randint(0, groups, (2,), generator=g).tolist()
+            units = torch.randint(-1, 2, (size,), generator=g) * 2.0 ** -23
+            x[t, j] = (x[t, i] * (1 + units))[torch.randperm(size, generator=g)]
+    x = x.view(T, E)
+    bias = torch.zeros(E) + 2.0 ** -20 if biased else None
+    check(x.to(dev), K, None if bias is None else bias.to(dev), score=score, groups=groups, top_groups=top_groups)
+    short = x.to(torch.bfloat16)
+    check(short.to(dev), K, None if bias is None else bias.to(dev), score=score, groups=groups,
+          top_groups=top_groups)
