@@ -464,7 +464,77 @@ struct BoxAt {
   uint32_t buffer;  // the warp's staging; 0: they do not
   uint32_t at;      // of its next buffer
   int32_t x, y, z;
+  int32_t count;  // rows that count
 };
+
+// A row of a warp's in its staging, W words in the swizzle of store_box; element `col` of row `row` there.
+template <int W>
+__device__ __forceinline__ uint32_t staged(uint32_t staging, uint32_t row, uint32_t col) {
+  const uint32_t turn = W == 16 ? (row >> 1) & 3u : row & 7u;
+  const uint32_t byte = col * (W == 16 ? 2 : 4);
+  return staging + row * (W * 4) + (((byte >> 4) ^ turn) << 4) + (byte & 15u);
+}
+// Rows of out that start anywhere: a warp's rows of 32 elements one after the other, a lane's row in w, an
+// element a lane. (6968 x 4133 x 864, GELU, pre-activation: 149 us; each lane its own row, element by
+// element, took 563. 4136 columns, in boxes, take 65.)
+template <int W>
+__device__ __forceinline__ void store_rows(const BoxAt& box, void* p, int64_t at, int64_t pitch, int have,
+                                           const uint32_t (&w)[W]) {
+  const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+  for (uint32_t c = 0; c < W / 4; c++)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(staged<W>(box.buffer, lane, c * (W == 16 ? 8 : 4))),
+                 "r"(w[4 * c]), "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                 : "memory");
+  __syncwarp();
+  const int64_t first = at - (int64_t)lane * pitch + lane;  // at: of this lane's row
+#pragma unroll 8
+  for (int r = 0; r < 32; r++) {
+    if (r < box.count && (int)lane < have) {
+      if constexpr (W == 16) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staged<W>(box.buffer, r, lane)) : "memory");
+        static_cast<uint16_t*>(p)[first + r * pitch] = v;
+      } else {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(staged<W>(box.buffer, r, lane)) : "memory");
+        static_cast<uint32_t*>(p)[first + r * pitch] = v;
+      }
+    }
+  }
+  __syncwarp();
+}
+// The residual's rows, the same way: element `lane` of row r in word r, then turned to this lane's row.
+template <int W>
+__device__ __forceinline__ void load_rows(const BoxAt& box, const void* p, int64_t at, int64_t pitch, int have,
+                                          uint32_t (&w)[32]) {
+  const int lane = threadIdx.x & 31;
+  const int64_t first = at - (int64_t)lane * pitch + lane;
+#pragma unroll
+  for (int r = 0; r < 32; r++) {
+    w[r] = 0u;
+    if (r < box.count && lane < have)
+      w[r] = W == 16 ? static_cast<const uint16_t*>(p)[first + r * pitch]
+                     : static_cast<const uint32_t*>(p)[first + r * pitch];
+  }
+}
+template <int W>
+__device__ __forceinline__ void turn_rows(const BoxAt& box, uint32_t (&w)[32]) {
+  const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < 32; r++) {
+    if (W == 16) asm volatile("st.shared.u16 [%0], %1;" ::"r"(staged<W>(box.buffer, r, lane)), "h"((uint16_t)w[r]) : "memory");
+    else asm volatile("st.shared.u32 [%0], %1;" ::"r"(staged<W>(box.buffer, r, lane)), "r"(w[r]) : "memory");
+  }
+  __syncwarp();
+#pragma unroll
+  for (uint32_t c = 0; c < W / 4; c++)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                 : "r"(staged<W>(box.buffer, lane, c * (W == 16 ? 8 : 4)))
+                 : "memory");
+  __syncwarp();
+}
 
 // A warp's 32 rows of 64 bytes (128 where it has two BOXES, used in turn, and out is binary32) to a box of
 // a map, a lane's row in w, through a staging buffer of the warp's (in the swizzle of that width: the
@@ -500,17 +570,19 @@ __device__ __forceinline__ void store_box(BoxAt& box, const CUtensorMap* map, co
 // `at`, `stride` apart, of which the first `have` count; `whole`: all of them do, side by side and
 // aligned. With BOXES a warp's rows may leave together, `live` or not. Returns the largest |out| as
 // binary32 bits.
-template <int BOXES, int P>
+template <int BOXES, bool ROWS, int P>
 __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], const uint32_t (&residual)[2 * P],
                                            int64_t at, int64_t stride, int have, bool whole, bool live,
                                            BoxAt& box) {
   uint32_t w[P];
   if (a.preact != nullptr) {
     pack_pairs(z, w);
-    if constexpr (BOXES > 0) {
+    if constexpr (ROWS) {
+      store_rows(box, a.preact, at, (int64_t)a.N, have, w);
+    } else if constexpr (BOXES > 0) {
       if (box.buffer) store_box<BOXES>(box, &a.preact_map, w);
     }
-    if ((!BOXES || !box.buffer) && live) store_pairs(a, a.preact, w, at, stride, have, whole);
+    if (!ROWS && (!BOXES || !box.buffer) && live) store_pairs(a, a.preact, w, at, stride, have, whole);
   }
   activate_pairs(a.activation, z);
   if (a.out_bytes == 2) {
@@ -519,10 +591,12 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
       for (int i = 0; i < P; i++) z[i] = f2_add(z[i], f2_from_bf16x2(residual[i]));
     }
     pack_pairs(z, w);
-    if constexpr (BOXES > 0) {
+    if constexpr (ROWS) {
+      store_rows(box, a.out, at, (int64_t)a.N, have, w);
+    } else if constexpr (BOXES > 0) {
       if (box.buffer) store_box<BOXES>(box, &a.out_map, w);
     }
-    if ((!BOXES || !box.buffer) && live) store_pairs(a, a.out, w, at, stride, have, whole);
+    if (!ROWS && (!BOXES || !box.buffer) && live) store_pairs(a, a.out, w, at, stride, have, whole);
     if (a.amax == nullptr || !live) return 0u;
     uint32_t top = 0u;
 #pragma unroll
@@ -547,11 +621,12 @@ __device__ __forceinline__ uint32_t finish(const TcArgs& a, uint64_t (&z)[P], co
     o[2 * i + 1] = __float_as_uint(f.y);
   }
   uint32_t* const to = static_cast<uint32_t*>(a.out) + at;
-  if constexpr (BOXES > 0) {
-    if (BOXES == 2 && box.buffer) store_box<BOXES>(box, &a.out_map, o);
+  if constexpr (BOXES == 2) {
+    if constexpr (ROWS) store_rows(box, a.out, at, (int64_t)a.N, have, o);
+    else if (box.buffer) store_box<BOXES>(box, &a.out_map, o);
   }
   if (!live) return 0u;
-  if (BOXES != 2 || !box.buffer) {
+  if (BOXES != 2 || (!ROWS && !box.buffer)) {
     if (P == 16 && whole) {
 #pragma unroll
       for (int i = 0; i < 2 * P; i += 8) store_words(to + i, a.wide, o + i);
@@ -589,7 +664,9 @@ __device__ __forceinline__ void clear(void* p, int64_t lo, int64_t hi, int64_t a
 
 // ---- the kernel -----------------------------------------------------------------------------------
 
-template <int CTAS, int NT, bool LONG>
+// ROWS: rows of out that do not start on 16-byte boundaries leave row by row, else in boxes. (One kernel for
+// both took 228 us for 217 at 8192 x 14336 x 4096.)
+template <int CTAS, int NT, bool LONG, bool ROWS>
 __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS, NT, LONG>::kPerSm))
     gemm_kernel(const __grid_constant__ TcArgs a, int splits) {
   using S = Shape<CTAS, NT, LONG>;
@@ -783,11 +860,16 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
         const bool counts = live && left > 0 && !(SWAP && splits > 1);
         // an expert's last rows are not stored in boxes, which end with the tensor alone
         const int rows_left = x.p_rows - 128 * half - 32 * quarter;
-        const bool boxes = !SWAP && a.boxes != 0 && rows_left > 0 && left > 0 &&
-                           (a.mode != kGemmGrouped || rows_left >= 32);
-        BoxAt box = {boxes ? staging : 0u, staging_at, col, row - lane, a.mode == kGemmWgrad ? x.e : 0};
+        const bool boxes = !SWAP && (ROWS || a.boxes != 0) && rows_left > 0 && left > 0 &&
+                           (ROWS || a.mode != kGemmGrouped || rows_left >= 32);
+        BoxAt box = {boxes ? staging : 0u, staging_at, col, row - lane, a.mode == kGemmWgrad ? x.e : 0, rows_left};
         uint32_t v[32], residual[32];
-        if (a.residual != nullptr && counts) load_residual<16>(a, residual, at, stride, left, whole);
+        if constexpr (ROWS) {
+          if (boxes && a.residual != nullptr)
+            load_rows<LONG ? 32 : 16>(box, a.residual, at, (int64_t)a.N, left, residual);
+        } else {
+          if (a.residual != nullptr && counts) load_residual<16>(a, residual, at, stride, left, whole);
+        }
         if (!SWAP && a.bias != nullptr) {
           __syncwarp();
           mine[lane] = lane < left ? bias_at(a, (int64_t)x.e * a.N + col + lane) : 0.0f;
@@ -816,6 +898,9 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + j * 512), "r"(v[j]) : "memory");
           continue;
         }
+        if constexpr (ROWS) {
+          if (boxes && a.residual != nullptr) turn_rows<LONG ? 32 : 16>(box, residual);
+        }
         uint64_t z[16];
 #pragma unroll
         for (int j = 0; j < 16; j++)
@@ -833,7 +918,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
             }
           }
         }
-        if (counts || boxes) top = max(top, finish<S::kBoxes, 16>(a, z, residual, at, stride, left, whole, counts, box));
+        if (counts || boxes) top = max(top, finish<S::kBoxes, ROWS, 16>(a, z, residual, at, stride, left, whole, counts, box));
         staging_at = box.at;
       }
       if (splits == 1) report_amax(a, top, x.e);
@@ -879,7 +964,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
             z[j] = f2_mul(z[j], alpha2);
             if (a.bias != nullptr) z[j] = f2_add(z[j], bias2);
           }
-          top = max(top, finish<0, kTurn / 2>(a, z, residual, at, a.N, x.q_rows - c, false, true, none));
+          top = max(top, finish<0, false, kTurn / 2>(a, z, residual, at, a.N, x.q_rows - c, false, true, none));
         }
       }
       report_amax(a, top, x.e);
@@ -893,7 +978,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
   if (warp == S::kEpi + 1) tmem_free<CTAS>(tmem, S::kColumns);
 }
 
-template <int CTAS, int NT, bool LONG>
+template <int CTAS, int NT, bool LONG, bool ROWS = false>
 cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -908,11 +993,11 @@ cudaError_t launch_one(const TcArgs& a, int grid, int splits, cudaStream_t s) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CTAS, NT, LONG>, a, splits);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CTAS, NT, LONG, ROWS>, a, splits);
 }
-template <int CTAS, int NT, bool LONG>
+template <int CTAS, int NT, bool LONG, bool ROWS = false>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(gemm_kernel<CTAS, NT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(gemm_kernel<CTAS, NT, LONG, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Shape<CTAS, NT, LONG>::kSmem);
 }
 
@@ -991,6 +1076,8 @@ bool make_out_maps(TcArgs& t, const GemmArgs& g) {
 cudaError_t prepare_gemm_kernels() {
   cudaError_t e = prepare_one<2, 256, false>(), r;
   if ((r = prepare_one<2, 256, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<2, 256, false, true>()) != cudaSuccess) e = r;
+  if ((r = prepare_one<2, 256, true, true>()) != cudaSuccess) e = r;
   if ((r = prepare_one<1, 32, false>()) != cudaSuccess) e = r;
   if ((r = prepare_one<1, 64, false>()) != cudaSuccess) e = r;
   if ((r = prepare_one<1, 128, false>()) != cudaSuccess) e = r;
@@ -1062,6 +1149,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t s) {
     if (t.boxes && !make_out_maps(t, g)) return cudaErrorInvalidValue;
     const int64_t most = g.mode == kGemmDense ? tiles : sm_count / 2;
     const int grid = (int)(2 * (most < sm_count / 2 ? most : sm_count / 2));
+    if (!t.boxes)
+      return g.out_bytes == 4 ? launch_one<2, 256, true, true>(t, grid, 1, s) : launch_one<2, 256, false, true>(t, grid, 1, s);
     return g.out_bytes == 4 ? launch_one<2, 256, true>(t, grid, 1, s) : launch_one<2, 256, false>(t, grid, 1, s);
   }
   t.q_rows = (int32_t)(g.M < x.rows ? g.M : x.rows);  // out-of-range rows of a box take as long as others
