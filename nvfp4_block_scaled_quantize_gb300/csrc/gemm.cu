@@ -847,6 +847,19 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
         break;
       }
       tc_fence_after();
+      auto release = [&] {  // the accumulator, once a tile
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          uint64_t* const bar = &acc_free[S::kLag == 1 ? 0 : count & 1];
+          if (CTAS == 2) cluster_arrive(cluster_address(smem_u32(bar), 0));
+          else mbar_arrive(bar);
+        }
+      };
+      if (a.mode == kGemmWgrad && a.residual != nullptr && x.kb0 == x.kb1) {
+        release();  // an expert without tokens keeps what it has
+        continue;
+      }
       const uint32_t acc = tmem + lanes + (count & 1) * S::kAccStride;
       uint32_t top = 0u;
 #pragma unroll 1
@@ -878,13 +891,7 @@ __global__ void __launch_bounds__((Shape<CTAS, NT, LONG>::kThreads), (Shape<CTAS
         tmem_load32(acc + 32 * chunk, v);
         tmem_wait_load();
         if (c + kStep >= kFreed && c < kFreed) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            uint64_t* const bar = &acc_free[S::kLag == 1 ? 0 : count & 1];
-            if (CTAS == 2) cluster_arrive(cluster_address(smem_u32(bar), 0));
-            else mbar_arrive(bar);
-          }
+          release();
         }
         if (x.kb0 == x.kb1) {
 #pragma unroll

@@ -314,3 +314,30 @@ def test_groups_that_binary32_cannot_tell_apart(E, K, groups, top_groups, score,
     short = x.to(torch.bfloat16)
     check(short.to(dev), K, None if bias is None else bias.to(dev), score=score, groups=groups,
           top_groups=top_groups)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N", [(40, 72), (520, 776), (2056, 1304), (1031, 1301)])
+def test_experts_without_tokens_keep_their_gradients(dtype, M, N):
+    """With accumulate: bit for bit, whatever is there."""
+    dev = cuda()
+    counts = [0, 40, 0, 0, 7, 0]
+    E, n = len(counts), 64  # 48 + 16 columns of K
+    ends = torch.tensor(counts).cumsum(0).to(torch.int32).to(dev)
+    a = random_bytes(dev, M, n // 2), random_scales(dev, M, n // 16), torch.ones(E, 2, device=dev)
+    b = random_bytes(dev, N, n // 2), random_scales(dev, N, n // 16), torch.ones(E, 2, device=dev)
+    whole = torch.int32 if dtype is torch.float32 else torch.int16
+    bits = torch.iinfo(whole)
+    before = torch.randint(bits.min, bits.max, (E, M, N), dtype=whole, device=dev)
+    out = before.clone().view(dtype)
+    out[1] = 1.0
+    out[4] = 1.0
+    api.nvfp4_gemm_grouped_wgrad(*a, *b, ends, out=out, accumulate=True)
+    for e in (0, 2, 3, 5):
+        assert torch.equal(out[e].view(whole), before[e])
+    for e, lo in ((1, 0), (4, 48)):
+        hi = lo + (counts[e] + 15) // 16 * 16
+        check_product(out[e], values(a[0][:, lo // 2:hi // 2], a[1][:, lo // 16:hi // 16], a[2][e]),
+                      values(b[0][:, lo // 2:hi // 2], b[1][:, lo // 16:hi // 16], b[2][e]),
+                      residual=torch.ones(M, N, device=dev))
+    assert api.nvfp4_get_status() == (0, 0)
