@@ -353,9 +353,10 @@ template <int SL, int V, typename L>
 __device__ __noinline__ bool settle_groups(const RouterArgs& a, bool softmax, const L* row, float top, const float (&x)[SL],
                                            float floor, float tie, uint32_t doubtful, int* slots, uint32_t& kept) {
   const int lane = threadIdx.x & 31;
-  if (softmax && a.bias) return false;
   const uint32_t by_size = (65535u + a.size) / a.size;  // e / size = e * by_size >> 16 for e < 256
   int count = 0;
+  bool some = false, differ = false;
+  float l0 = 0.0f, b0 = 0.0f;
 #pragma unroll
   for (int j = 0; j < SL; j++) {
     const uint32_t e = ((j / V) * 32 + lane) * V + j % V, g = (e * by_size) >> 16;
@@ -366,8 +367,17 @@ __device__ __noinline__ bool settle_groups(const RouterArgs& a, bool softmax, co
     const int at = count + __popc(all & ((1u << lane) - 1u));
     if (here && at < 32) slots[at] = (int)e;
     count += __popc(all);
+    if (here) {
+      const float l = widen<L>(row[e]), b = a.bias ? __ldg(a.bias + e) : 0.0f;
+      if (!some) l0 = l, b0 = b, some = true;
+      differ |= l != l0 || b != b0;
+    }
   }
-  if (count > 32) return false;
+  // All the same, as with a router that has learnt nothing: their groups are equal, the lower first already.
+  const int from = __ffs(__ballot_sync(kAll, some)) - 1;
+  const float l1 = __shfl_sync(kAll, l0, from), b1 = __shfl_sync(kAll, b0, from);
+  if (!__any_sync(kAll, differ || (some && (l0 != l1 || b0 != b1)))) return true;
+  if (count > 32 || (softmax && a.bias)) return false;
   __syncwarp();
   double v = -INFINITY;
   int g = -1;

@@ -288,9 +288,10 @@ def test_rows_of_equal_logits(dtype):
     dev = cuda()
     for E, groups, top in ((256, 1, 1), (64, 8, 2), (20, 1, 1)):
         for bias in (None, torch.zeros(E, device=dev)):
-            ids, w = api.nvfp4_moe_router(torch.zeros(40, E, dtype=dtype, device=dev), 4, score="sigmoid",
-                                          bias=bias, groups=groups, top_groups=top)
-            assert (ids == torch.arange(4, device=dev)).all() and (w == 0.25).all()
+            for score in ("sigmoid", "softmax"):
+                ids, w = api.nvfp4_moe_router(torch.zeros(40, E, dtype=dtype, device=dev), 4, score=score,
+                                              bias=bias, groups=groups, top_groups=top)
+                assert (ids == torch.arange(4, device=dev)).all() and (w == 0.25).all()
 
 
 @pytest.mark.parametrize("E,K,groups,top_groups", [(256, 8, 8, 4), (160, 6, 8, 3), (64, 4, 16, 5), (250, 8, 10, 4),
