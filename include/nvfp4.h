@@ -481,7 +481,8 @@ nvfp4_status nvfp4_moe_router(const void* logits, int32_t logit_bytes, const flo
 
 /* The gradient of the logits, in their type: from grad_weights (device) float [T][K] and the same
  * logits, ids and options. The choice is constant. Slots with an id outside [0, E) have no part (an
- * id >= E sets NVFP4_DEVICE_BAD_ROUTE); an id that stands twice in a row counts twice. */
+ * id >= E sets NVFP4_DEVICE_BAD_ROUTE); an id that stands twice in a row counts twice. With renormalize
+ * a row's only choice has no gradient, exactly. */
 nvfp4_status nvfp4_moe_router_backward(const float* grad_weights, const void* logits,
                                        int32_t logit_bytes, const int32_t* expert_ids, int64_t T,
                                        int32_t E, int32_t K, int32_t score, int32_t renormalize,

@@ -342,3 +342,22 @@ def test_experts_without_tokens_keep_their_gradients(dtype, M, N):
                       values(b[0][:, lo // 2:hi // 2], b[1][:, lo // 16:hi // 16], b[2][e]),
                       residual=torch.ones(M, N, device=dev))
     assert api.nvfp4_get_status() == (0, 0)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("E,K", [(64, 1), (68, 1), (256, 1), (256, 6), (15, 3)])
+def test_a_single_choice_has_weight_one_and_no_gradient(score, dtype, E, K):
+    """With renormalization, exactly: the weight does not depend on the logit. K > 1: the rest is masked."""
+    dev = cuda()
+    g = torch.Generator().manual_seed(E)
+    x = 4 * torch.randn(500, E, generator=g)
+    if K > 1:
+        one = torch.randint(0, E, (500, 1), generator=g)
+        x = torch.full_like(x, -float("inf")).scatter(1, one, x.gather(1, one))
+    x = x.to(dtype).to(dev)
+    for bias in (None, torch.randn(E, generator=g).to(dev)):
+        ids, w = api.nvfp4_moe_router(x, K, score=score, bias=bias, scale=2.5)
+        assert (w[:, 0] == 2.5).all() and not w[:, 1:].any() and (ids[:, 1:] == -1).all()
+        d = api.nvfp4_moe_router_backward(torch.randn(500, K, generator=g).to(dev), x, ids, score=score, scale=2.5)
+        assert not d.any()
