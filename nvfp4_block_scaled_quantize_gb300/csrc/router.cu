@@ -161,6 +161,10 @@ __device__ __noinline__ int draw_again(const RouterArgs& a, bool softmax, const 
   return mine;
 }
 
+// w / sum; exactly 1 for a single choice, which then has no gradient. (Rounded to nearest throughout, the
+// gradient of 16384 x 256 takes 7.5 us for 6.7.)
+__device__ __forceinline__ float part_of(float w, float sum) { return w == sum ? 1.0f : __fdividef(w, sum); }
+
 // The weights of the drawn experts: lane k has the k-th (mine >= 0) and its logit x.
 __device__ __forceinline__ void put_weights(const RouterArgs& a, bool softmax, bool renorm, int64_t t, int mine, float x,
                                             float top, float inv) {
@@ -171,7 +175,7 @@ __device__ __forceinline__ void put_weights(const RouterArgs& a, bool softmax, b
     const float mark = mine >= 0 ? x : -INFINITY, high = few ? warp_max<8>(mark) : warp_max(mark);
     if (mine >= 0) w = softmax ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
     const float sum = few ? warp_sum<8>(w) : warp_sum(w);
-    w = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;  // a single choice has exactly 1
+    w = sum > 0.0f ? part_of(w, sum) : 0.0f;
   } else if (mine >= 0) {
     w = softmax ? __expf(x - top) * inv : sigmoid_over(x, 0.0f);
   }
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_backward_kernel(cons
       if (id >= 0 && high > -INFINITY)
         w = softmax ? __expf(x - high) : sigmoid_over(x, fminf(high, 0.0f));
       const float sum = warp_sum(w);
-      const float r = sum > 0.0f ? __fdiv_rn(w, sum) : 0.0f;  // a single choice: 1, and no gradient
+      const float r = sum > 0.0f ? part_of(w, sum) : 0.0f;
       const float mean = warp_sum(r * g);
       mine = r * (g - mean);
       if (!softmax) mine *= __fdividef(1.0f, 1.0f + __expf(x));  // 1 - p
